@@ -8,6 +8,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libchunkkv.
 
 MAX_BATCH = 1024
 MAX_GATHER_LAYERS = 64
+Q8_PAGE = 64                                   # CHUNKKV_Q8_PAGE
 PROBE_THREADS, PROBE_CHAINS = 256, 16          # CHUNKKV_PROBE_THREADS, CHUNKKV_PROBE_CHAINS
 
 STATUS = {
@@ -33,6 +34,28 @@ class Params(ctypes.Structure):
     ]
 
 
+class PrefillParams(ctypes.Structure):
+    """chunkkv_prefill_params."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("cu_q", ctypes.POINTER(ctypes.c_int32)), ("cu_k", ctypes.POINTER(ctypes.c_int32)),
+        ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("kv_stride_t", ctypes.c_int64), ("kv_stride_h", ctypes.c_int64),
+        ("o_stride_t", ctypes.c_int64), ("o_stride_h", ctypes.c_int64),
+    ]
+
+
+class Q8CacheStruct(ctypes.Structure):
+    """chunkkv_q8_cache."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("ring", ctypes.c_void_p), ("state", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
@@ -41,6 +64,8 @@ def _load():
     P = ctypes.POINTER(Params)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     pp = ctypes.POINTER(ctypes.c_void_p)
+    i64 = ctypes.c_int64
+    PP, Q8 = ctypes.POINTER(PrefillParams), ctypes.POINTER(Q8CacheStruct)
     sigs = {
         "chunkkv_out_capacity": [P, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "chunkkv_workspace_size": [P, i32, i32, ctypes.POINTER(sz)],
@@ -58,6 +83,14 @@ def _load():
         "chunkkv_selftest_wait_timeout": [vp, sz, vp],
         "chunkkv_layer_overlap": [P, i32, vp, vp, vp, vp, vp],
         "chunkkv_probe_ex2": [vp, i32, i32, vp],
+        "chunkkv_prefill_workspace_size": [PP, ctypes.POINTER(sz)],
+        "chunkkv_prefill_path": [PP],
+        "chunkkv_prefill_attention": [PP, vp, vp, vp, vp, vp, sz, vp],
+        "chunkkv_q8_resize": [Q8, vp, vp, i32, vp],
+        "chunkkv_q8_append": [Q8, i32, vp, vp, i64, i64, i64, vp, vp, i32, vp],
+        "chunkkv_q8_load": [Q8, i32, vp, i32, vp, vp, i64, vp],
+        "chunkkv_q8_workspace_size": [Q8, i32, ctypes.POINTER(sz)],
+        "chunkkv_q8_attention": [Q8, i32, i32, ctypes.c_float, vp, i64, i64, vp, i64, i64, vp, sz, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)

@@ -1,0 +1,400 @@
+// The 8-bit paged cache: page tables and slot maps from lengths, writing rows,
+// reading rows back.
+//
+// A cache row is one (sequence, KV head): chunk compression keeps another number of
+// tokens for every head, so every head has a length, pages and scales of its own.
+// A page holds 64 tokens of one row, in the order in which the attention kernel's
+// fragments read it:
+//   keys    [d64 / 64][64 tokens][64 columns]  int8     (d64: d rounded up to 64)
+//   values  [d64][64 tokens]                   int8     (transposed)
+//   scales  [2]                                fp32     keys, values
+#include "serve.cuh"
+
+namespace chunkkv {
+namespace {
+
+// ------------------------------------------------------------ tables and slot maps
+
+constexpr int kResizeThreads = 1024;
+
+__device__ __forceinline__ int pages_of(int n) { return n > 0 ? (n - 1) / kPage + 1 : 0; }
+
+// A ring position below 3 n (head < n, at most n free before the call and after it).
+__device__ __forceinline__ int wrap(long long x, int n) {
+  if (x >= n) x -= n;
+  if (x >= n) x -= n;
+  return (int)x;
+}
+
+// Exclusive scan of (a, b) over the block; totals in ta, tb.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb) {
+  __shared__ long long s[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long xa = a, xb = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long ya = __shfl_up_sync(0xffffffffu, xa, o), yb = __shfl_up_sync(0xffffffffu, xb, o);
+    if (lane >= o) { xa += ya; xb += yb; }
+  }
+  if (lane == 31) { s[0][warp] = xa; s[1][warp] = xb; }
+  __syncthreads();
+  if (warp == 0) {
+    const int nw = blockDim.x >> 5;
+    long long wa = lane < nw ? s[0][lane] : 0, wb = lane < nw ? s[1][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long ya = __shfl_up_sync(0xffffffffu, wa, o), yb = __shfl_up_sync(0xffffffffu, wb, o);
+      if (lane >= o) { wa += ya; wb += yb; }
+    }
+    s[0][lane] = wa;
+    s[1][lane] = wb;
+  }
+  __syncthreads();
+  const long long pa = warp ? s[0][warp - 1] : 0, pb = warp ? s[1][warp - 1] : 0;
+  ta = s[0][31];
+  tb = s[1][31];
+  a = pa + xa - a;
+  b = pb + xb - b;
+}
+
+// Every CTA scans all rows' page counts (a few KB from L2) and then serves its own
+// run of rows: pages that a row gains come from the ring's head in row order, pages
+// that it gives back go behind the ring's free part, and the slots of its new tokens
+// follow from both.  The entries read (free before the call) and those written (not
+// free before it) never meet, so the CTAs need no order among them; the last one to
+// finish writes the lengths and the ring's state, which all of them read before.
+__global__ void __launch_bounds__(kResizeThreads)
+resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restrict__ lens, int32_t* __restrict__ table,
+              int32_t* __restrict__ ring, int32_t* state, int64_t* __restrict__ slots, int n_cap, int rows_per_cta) {
+  extern __shared__ long long s_off[];                      // [2][rows_per_cta] pages gained / given before the row
+  __shared__ bool s_last;
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.x * rows_per_cta, r1 = min(g.rows, r0 + rows_per_cta);
+  const int chunk = (g.rows + kResizeThreads - 1) / kResizeThreads;
+  const int c0 = min(g.rows, tid * chunk), c1 = min(g.rows, c0 + chunk);
+  const int head = ((volatile int32_t*)state)[kRingHead], n_free = ((volatile int32_t*)state)[kRingFree];
+  long long grow = 0, give = 0;
+  bool bad = false;
+  for (int r = c0; r < c1; ++r) {
+    const int n = lens[r], m = new_lens[r];
+    bad |= n < 0 || m < 0 || pages_of(m) > g.max_pages || pages_of(n) > g.max_pages || (slots && m - n > n_cap);
+    const int d = pages_of(m) - pages_of(n);
+    grow += max(d, 0);
+    give += max(-d, 0);
+  }
+  long long grown, given;
+  bad = __syncthreads_or(bad) || head < 0 || head >= g.n_pages || n_free < 0 || n_free > g.n_pages;
+  block_scan2(grow, give, grown, given);
+  const bool ok = !bad && grown <= n_free && n_free - grown + given <= g.n_pages;
+  for (int r = c0; r < c1; ++r) {
+    if (r >= r0 && r < r1) {
+      s_off[r - r0] = grow;
+      s_off[rows_per_cta + r - r0] = give;
+    }
+    const int d = pages_of(new_lens[r]) - pages_of(lens[r]);
+    grow += max(d, 0);
+    give += max(-d, 0);
+  }
+  __syncthreads();
+  if (ok) {
+    // table entries: a warp per row
+    for (int r = r0 + (tid >> 5); r < r1; r += kResizeThreads / 32) {
+      const int have = pages_of(lens[r]), need = pages_of(new_lens[r]);
+      int32_t* row = table + (int64_t)r * g.max_pages;
+      for (int j = have + (tid & 31); j < need; j += 32)
+        row[j] = ring[wrap(head + s_off[r - r0] + (j - have), g.n_pages)];
+      for (int j = need + (tid & 31); j < have; j += 32) {
+        ring[wrap(head + n_free + s_off[rows_per_cta + r - r0] + (j - need), g.n_pages)] = row[j];
+        row[j] = -1;
+      }
+    }
+  }
+  // slots: pages that the row had from the table, the others straight from the ring
+  if (slots) {
+    for (int r = r0; r < r1; ++r) {
+      const int n = lens[r], m = new_lens[r], have = pages_of(n);
+      const int32_t* row = table + (int64_t)r * g.max_pages;
+      for (int i = tid; i < n_cap; i += kResizeThreads) {
+        int64_t slot = -1;
+        if (ok && i < m - n) {
+          const int pos = n + i, j = pos / kPage;
+          const int32_t page = j < have ? row[j] : ring[wrap(head + s_off[r - r0] + (j - have), g.n_pages)];
+          slot = (int64_t)page * kPage + pos % kPage;
+        }
+        slots[(int64_t)r * n_cap + i] = slot;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(&state[kRingTicket], 1) == (int)gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (s_last) {
+    if (ok)
+      for (int r = tid; r < g.rows; r += kResizeThreads) lens[r] = new_lens[r];
+    if (tid == 0) {
+      if (ok) {
+        state[kRingHead] = (int32_t)((head + grown) % g.n_pages);
+        state[kRingFree] = (int32_t)(n_free - grown + given);
+      }
+      state[kRingStatus] = ok ? 0 : bad ? 2 : 1;
+      state[kRingTicket] = 0;
+    }
+  }
+  pdl_trigger();
+}
+
+// ------------------------------------------------------------ writing
+
+constexpr int kIoThreads = 256;
+constexpr float kInv127 = 1.0f / 127.0f;
+constexpr float kSmallest = 7.888609052210118e-31f;          // 2^-100: below it a block counts as zero
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *(const uint4*)p;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
+  *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *(const uint32_t*)&b;
+  }
+  *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rounded to the nearest code, ties to even; NaN (0 x inf of a block with an
+// infinity, whose scale is not finite either) becomes 0.
+__device__ __forceinline__ int code_of(float x) { return max(-127, min(127, __float2int_rn(x))); }
+
+// The codes of a 32-bit word times ratio, rounded again.
+__device__ __forceinline__ uint32_t recode(uint32_t w, float ratio) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o |= ((uint32_t)code_of((float)(int8_t)(w >> (8 * i)) * ratio) & 0xFFu) << (8 * i);
+  return o;
+}
+
+struct AppendArgs {
+  const void* x[2];                // keys, values [B, Hkv, n_cap, d]
+  int8_t* pages[2];
+  int64_t st_b, st_h, st_t;
+  int32_t n_cap;
+};
+
+// One CTA writes the part of one page that a row's new tokens fill, of the keys
+// (blockIdx.z 0) or of the values (1): the tokens into shared memory, their largest
+// magnitude, the page's scale, and the codes.  A page that already holds tokens
+// keeps its scale unless the new tokens are larger; then its codes are rounded again
+// for the new one.
+template <typename T>
+__global__ void __launch_bounds__(kIoThreads)
+append_kernel(Q8Geom g, AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
+              float* __restrict__ scales) {
+  extern __shared__ float tile[];                             // [64][d64 + 1]
+  __shared__ uint32_t s_top[kIoThreads / 32];
+  pdl_wait();
+  const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
+  const int n = min(max(counts[r], 0), a.n_cap);
+  const int64_t* row_slots = slots + (int64_t)r * a.n_cap;
+  const int off0 = n > 0 ? (int)(row_slots[0] & (kPage - 1)) : 0;
+  const int i0 = max(0, (int)blockIdx.x * kPage - off0), i1 = min(n, ((int)blockIdx.x + 1) * kPage - off0);
+  const int64_t slot = i0 < i1 ? row_slots[i0] : -1;
+  const int64_t page = slot >> 6;
+  if (slot >= 0 && page < g.n_pages) {                        // the same for the whole CTA
+    const int t0 = (int)(slot & (kPage - 1)), nt = min(i1 - i0, kPage - t0);
+    const int pitch = g.d64 + 1;
+    const T* x = (const T*)a.x[which] + (r / g.Hkv) * a.st_b + (r % g.Hkv) * a.st_h + i0 * a.st_t;
+    // magnitudes compared as bit patterns: a NaN is above infinity and ends in the scale
+    uint32_t top = 0;
+    const int v8 = g.d64 / 8;
+    for (int i = tid; i < nt * v8; i += kIoThreads) {
+      const int t = i / v8, c = (i % v8) * 8;
+      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < g.d) load8(x + t * a.st_t + c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        top = max(top, __float_as_uint(w[e]) & 0x7FFFFFFFu);
+        tile[t * pitch + c + e] = w[e];
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kIoThreads / 32; ++i) top = max(top, s_top[i]);
+    const float amax = __uint_as_float(top);
+    const float grown = amax < kSmallest ? 0.f : amax * kInv127;
+    const float before = t0 == 0 ? 0.f : scales[page * 2 + which];
+    const float scale = grown > before || grown != grown ? grown : before;   // a NaN scale stays one
+    const float ratio = scale != before ? __fdiv_rn(before, scale) : 1.f;
+    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
+    const bool again = t0 > 0 && ratio != 1.f;                // older codes of the page to be rounded again
+    int8_t* pg = a.pages[which] + page * (int64_t)(g.d64 * kPage);
+    if (which == 0) {
+      if (again)
+        for (int i = tid; i < t0 * (g.d64 / 16); i += kIoThreads) {
+          const int t = i % t0, c = i / t0;                   // 16 columns of an older token
+          uint4* p = (uint4*)(pg + (c / 4) * (kPage * 64) + t * 64 + (c % 4) * 16);
+          uint4 w = *p;
+          w.x = recode(w.x, ratio); w.y = recode(w.y, ratio); w.z = recode(w.z, ratio); w.w = recode(w.w, ratio);
+          *p = w;
+        }
+      const int v16 = g.d64 / 16;
+      for (int i = tid; i < nt * v16; i += kIoThreads) {
+        const int t = i / v16, c = i % v16;
+        const float* src = tile + t * pitch + c * 16;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            w[e] |= ((uint32_t)code_of(src[4 * e + b] * inv) & 0xFFu) << (8 * b);
+        }
+        *(uint4*)(pg + (c / 4) * (kPage * 64) + (t0 + t) * 64 + (c % 4) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      // 16 tokens of a column per thread; vectors that the new tokens fill in part keep their other bytes
+      for (int i = tid; i < g.d64 * 4; i += kIoThreads) {
+        const int c = i >> 2, base = (i & 3) * 16;
+        const bool touched = base < t0 + nt && base + 16 > t0;
+        if (!touched && !(again && base < t0)) continue;
+        uint4* p = (uint4*)(pg + c * kPage + base);
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (base < t0 || base + 16 > t0 + nt) {
+          const uint4 o = *p;
+          w[0] = o.x; w[1] = o.y; w[2] = o.z; w[3] = o.w;
+          if (again && base < t0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = recode(w[e], ratio);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int t = base + e - t0;
+          if (t >= 0 && t < nt) {
+            const uint32_t q = (uint32_t)code_of(tile[t * pitch + c] * inv) & 0xFFu;
+            w[e >> 2] = (w[e >> 2] & ~(0xFFu << (8 * (e & 3)))) | (q << (8 * (e & 3)));
+          }
+        }
+        *p = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if (tid == 0 && scale != before) scales[page * 2 + which] = scale;
+    if (tid == 0 && t0 == 0) scales[page * 2 + which] = scale;
+  }
+  pdl_trigger();
+}
+
+// ------------------------------------------------------------ reading back
+
+struct LoadArgs {
+  const int8_t* pages[2];
+  void* out[2];
+  int64_t st_t;
+  int32_t n_cap;
+};
+
+// One CTA reads one page of a row: codes times the page's scale, rounded once to the
+// output's type.
+template <typename T>
+__global__ void __launch_bounds__(kIoThreads)
+load_kernel(Q8Geom g, LoadArgs a, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
+            const float* __restrict__ scales, const int64_t* __restrict__ start) {
+  extern __shared__ int8_t bytes[];                           // values: [d64][64 + 4]
+  pdl_wait();
+  const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, j = blockIdx.x;
+  const int n = min(safe_len(lens[r], g.max_pages), a.n_cap);
+  const int nt = min(kPage, n - j * kPage);
+  const int64_t at = start[r];
+  if (nt > 0 && at >= 0) {
+    const int64_t page = safe_page(table[(int64_t)r * g.max_pages + j], g.n_pages);
+    const float scale = scales[page * 2 + which];
+    const int8_t* pg = a.pages[which] + page * (int64_t)(g.d64 * kPage);
+    T* out = (T*)a.out[which] + (at + j * kPage) * a.st_t;
+    constexpr int kPitch = kPage + 4;
+    if (which == 1) {
+      for (int i = tid; i < g.d64 * 4; i += kIoThreads) {
+        const uint4 w = *(const uint4*)(pg + i * 16);
+        uint32_t* dst = (uint32_t*)(bytes + (i >> 2) * kPitch + (i & 3) * 16);
+        dst[0] = w.x; dst[1] = w.y; dst[2] = w.z; dst[3] = w.w;
+      }
+      __syncthreads();
+    }
+    const int v8 = g.d / 8;
+    for (int i = tid; i < nt * v8; i += kIoThreads) {
+      const int t = i / v8, c = (i % v8) * 8;
+      float x[8];
+      if (which == 0) {
+        const uint2 w = *(const uint2*)(pg + (c >> 6) * (kPage * 64) + t * 64 + (c & 63));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * scale;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)bytes[(c + e) * kPitch + t] * scale;
+      }
+      store8(out + t * a.st_t + c, x);
+    }
+  }
+  pdl_trigger();
+}
+
+}  // namespace
+
+cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* lens, int32_t* table, int32_t* ring,
+                             int32_t* state, int64_t* slots, int n_cap, int sms, cudaStream_t s) {
+  const int grid = max(1, min(g.rows, sms));
+  const int per = (g.rows + grid - 1) / grid;
+  return launch_pdl(resize_kernel, dim3((g.rows + per - 1) / per), dim3(kResizeThreads),
+                    (size_t)per * 2 * sizeof(long long), s, g, new_lens, lens, table, ring, state, slots, n_cap, per);
+}
+
+cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
+                             int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, int8_t* k_pages,
+                             int8_t* v_pages, float* scales, cudaStream_t s) {
+  AppendArgs a = {{k, v}, {k_pages, v_pages}, st_b, st_h, st_t, n_cap};
+  const size_t smem = (size_t)kPage * (g.d64 + 1) * sizeof(float);
+  // n_cap tokens that begin anywhere in a page touch this many pages
+  const dim3 grid((n_cap + 2 * (kPage - 1)) / kPage, g.rows, 2);
+  auto fn = bf16 ? append_kernel<__nv_bfloat16> : append_kernel<float>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, grid, dim3(kIoThreads), smem, s, g, a, counts, slots, scales);
+}
+
+cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,
+                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, void* k_out,
+                           void* v_out, int64_t st_t, cudaStream_t s) {
+  LoadArgs a = {{k_pages, v_pages}, {k_out, v_out}, st_t, n_cap};
+  const size_t smem = (size_t)g.d64 * (kPage + 4);
+  const dim3 grid((n_cap + kPage - 1) / kPage, g.rows, 2);
+  auto fn = bf16 ? load_kernel<__nv_bfloat16> : load_kernel<float>;
+  return launch_pdl(fn, grid, dim3(kIoThreads), smem, s, g, a, table, lens, scales, start);
+}
+
+}  // namespace chunkkv

@@ -1,0 +1,223 @@
+// C-ABI entry points of the serving operators: argument checks and launch plans.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "serve.cuh"
+
+namespace chunkkv {
+
+int prefill_simt_tile();                                                               // prefill.cu
+template <int MAXB>
+cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q,
+                                const void* k, const void* v, void* out, cudaStream_t s);
+cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* lens, int32_t* table, int32_t* ring,
+                             int32_t* state, int64_t* slots, int n_cap, int sms, cudaStream_t s);   // q8_cache.cu
+cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
+                             int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, int8_t* k_pages,
+                             int8_t* v_pages, float* scales, cudaStream_t s);
+cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,
+                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, void* k_out,
+                           void* v_out, int64_t st_t, cudaStream_t s);
+size_t q8_workspace_bytes(const Q8Geom& g, int G);                                     // q8_attention.cu
+cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
+                                int64_t q_sh, void* out, int64_t o_sb, int64_t o_sh, const int8_t* k_pages,
+                                const int8_t* v_pages, const float* scales, const int32_t* table, const int32_t* lens,
+                                void* ws, int sms, cudaStream_t s);
+
+namespace {
+
+constexpr size_t kServeHeader = 256;            // int32 device error word at offset 0
+constexpr double kLog2e = 1.4426950408889634;
+
+bool aligned(const void* p, uintptr_t n = 16) { return p != nullptr && ((uintptr_t)p & (n - 1)) == 0; }
+chunkkv_status cuda_result(cudaError_t e) { return e == cudaSuccess ? CHUNKKV_OK : CHUNKKV_ERR_CUDA; }
+
+// SMs of the current device (152 where no device is visible, as for the compression's plans).
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  return sms;
+}
+
+bool valid_dtype(int dtype) { return dtype == CHUNKKV_F32 || dtype == CHUNKKV_BF16; }
+int elt_size(int dtype) { return dtype == CHUNKKV_BF16 ? 2 : 4; }
+bool stride_ok(int64_t s, int elt) { return s >= 0 && s < (INT64_MAX >> 32) && (s * elt) % 16 == 0; }
+bool scale_ok(float s) { return s > 0.f && isfinite(s); }
+
+chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
+  if (p == nullptr || p->B < 0 || p->Hq < 1 || p->Hkv < 1 || p->d < 1 || !valid_dtype(p->dtype) || !scale_ok(p->scale) ||
+      p->Hq % p->Hkv != 0)
+    return CHUNKKV_ERR_INVALID_ARG;
+  if (p->B > CHUNKKV_MAX_BATCH || p->d > kMaxD || p->Hq > 65535) return CHUNKKV_ERR_UNSUPPORTED;
+  const int elt = elt_size(p->dtype);
+  if ((p->d * elt) % 16 != 0) return CHUNKKV_ERR_INVALID_ARG;
+  const int64_t st[6] = {p->q_stride_t, p->q_stride_h, p->kv_stride_t, p->kv_stride_h, p->o_stride_t, p->o_stride_h};
+  for (int64_t s : st)
+    if (!stride_ok(s, elt)) return CHUNKKV_ERR_INVALID_ARG;
+  if (p->B > 0) {
+    if (!p->cu_q || !p->cu_k || p->cu_q[0] != 0 || p->cu_k[0] != 0) return CHUNKKV_ERR_INVALID_ARG;
+    for (int b = 0; b < p->B; ++b)
+      if (p->cu_q[b + 1] < p->cu_q[b] || p->cu_k[b + 1] < p->cu_k[b]) return CHUNKKV_ERR_INVALID_ARG;
+  }
+  return CHUNKKV_OK;
+}
+
+// The sequences by descending number of keys (ties in order), with their q tiles of `tile` rows.
+template <int MAXB>
+void fill_table(const chunkkv_prefill_params* p, int tile, PrefillTable<MAXB>& t) {
+  int32_t order[MAXB];
+  t.B = 0;
+  for (int b = 0; b < p->B; ++b)
+    if (p->cu_q[b + 1] > p->cu_q[b]) order[t.B++] = b;
+  const int32_t* ck = p->cu_k;
+  std::sort(order, order + t.B, [ck](int32_t x, int32_t y) {
+    const int32_t nx = ck[x + 1] - ck[x], ny = ck[y + 1] - ck[y];
+    return nx != ny ? nx > ny : x < y;
+  });
+  int32_t u = 0;
+  for (int i = 0; i < t.B; ++i) {
+    const int b = order[i];
+    t.seq[i] = {p->cu_q[b], p->cu_q[b + 1] - p->cu_q[b], ck[b], ck[b + 1] - ck[b]};
+    t.uoff[i] = u;
+    u += (t.seq[i].tq - 1) / tile + 1;
+  }
+  t.uoff[t.B] = u;
+}
+
+template <int MAXB>
+cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, const void* q, const void* k,
+                        const void* v, void* out, cudaStream_t s) {
+  static thread_local PrefillTable<MAXB> tab;
+  fill_table(p, prefill_simt_tile(), tab);
+  return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
+}
+
+// The part of a cache that every call uses; `pages`: the call reads or writes them.
+chunkkv_status check_cache(const chunkkv_q8_cache* c, bool pages, Q8Geom* g) {
+  if (c == nullptr || c->B < 0 || c->Hkv < 1 || c->d < 1 || c->n_pages < 1 || c->max_pages < 1)
+    return CHUNKKV_ERR_INVALID_ARG;
+  if ((int64_t)c->B * c->Hkv > CHUNKKV_Q8_MAX_ROWS || c->d > kMaxD || c->max_pages > INT32_MAX / kPage - 2)
+    return CHUNKKV_ERR_UNSUPPORTED;
+  if (c->d % 8 != 0 || !aligned(c->table, 4) || !aligned(c->lens, 4)) return CHUNKKV_ERR_INVALID_ARG;
+  if (pages && (!aligned(c->k_pages) || !aligned(c->v_pages) || !aligned(c->scales, 8))) return CHUNKKV_ERR_INVALID_ARG;
+  *g = {c->B * c->Hkv, c->Hkv, c->d, (c->d + 63) / 64 * 64, c->n_pages, c->max_pages};
+  return CHUNKKV_OK;
+}
+
+}  // namespace
+}  // namespace chunkkv
+
+using namespace chunkkv;
+
+extern "C" {
+
+chunkkv_status chunkkv_prefill_workspace_size(const chunkkv_prefill_params* p, size_t* bytes) {
+  if (bytes == nullptr) return CHUNKKV_ERR_INVALID_ARG;
+  const chunkkv_status st = check_prefill(p);
+  if (st == CHUNKKV_OK) *bytes = kServeHeader;
+  return st;
+}
+
+int32_t chunkkv_prefill_path(const chunkkv_prefill_params* p) { return check_prefill(p) == CHUNKKV_OK ? 0 : -1; }
+
+chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const void* q, const void* k, const void* v,
+                                         void* out, void* ws, size_t ws_bytes, chunkkv_stream_t stream) {
+  const chunkkv_status st = check_prefill(p);
+  if (st != CHUNKKV_OK) return st;
+  if (p->B == 0 || p->cu_q[p->B] == 0) return CHUNKKV_OK;
+  // k and v may be NULL only where no sequence has a key
+  const bool no_keys = p->cu_k[p->B] == 0;
+  if (!aligned(q) || !aligned(out) || !aligned(ws) || (!no_keys && (!aligned(k) || !aligned(v))))
+    return CHUNKKV_ERR_INVALID_ARG;
+  if (ws_bytes < kServeHeader) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  PrefillGeom g = {p->Hq, p->Hkv, p->Hq / p->Hkv, p->d, (float)(p->scale * kLog2e), p->q_stride_t, p->q_stride_h,
+                   p->kv_stride_t, p->kv_stride_h, p->o_stride_t, p->o_stride_h};
+  const cudaStream_t cs = (cudaStream_t)stream;
+  return cuda_result(p->B <= kSmallBatch ? run_prefill<kSmallBatch>(p, g, q, k, v, out, cs)
+                                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, q, k, v, out, cs));
+}
+
+chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
+                                 chunkkv_stream_t stream) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, false, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (g.rows == 0) return CHUNKKV_OK;
+  if (!aligned(new_lens, 4) || !aligned(c->ring, 4) || !aligned(c->state, 4) || (slots && !aligned(slots, 8)) ||
+      new_lens == c->lens)
+    return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q8_resize(g, new_lens, c->lens, c->table, c->ring, c->state, slots, n_cap, sm_count(),
+                                      (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q8_append(const chunkkv_q8_cache* c, int32_t dtype, const void* k, const void* v, int64_t st_b,
+                                 int64_t st_h, int64_t st_t, const int32_t* counts, const int64_t* slots,
+                                 int32_t n_cap, chunkkv_stream_t stream) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  const int elt = elt_size(dtype);
+  if ((g.d * elt) % 16 != 0 || !stride_ok(st_b, elt) || !stride_ok(st_h, elt) || !stride_ok(st_t, elt))
+    return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0 || n_cap == 0) return CHUNKKV_OK;
+  if (!aligned(k) || !aligned(v) || !aligned(counts, 4) || !aligned(slots, 8)) return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q8_append(g, dtype == CHUNKKV_BF16, k, v, st_b, st_h, st_t, counts, slots, n_cap,
+                                      c->k_pages, c->v_pages, c->scales, (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q8_load(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                               void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  const int elt = elt_size(dtype);
+  if ((g.d * elt) % 16 != 0 || !stride_ok(st_t, elt)) return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0 || n_cap == 0) return CHUNKKV_OK;
+  if (!aligned(start, 8) || !aligned(k_out) || !aligned(v_out)) return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q8_load(g, dtype == CHUNKKV_BF16, c->table, c->lens, c->k_pages, c->v_pages, c->scales,
+                                    start, std::min(n_cap, c->max_pages * kPage), k_out, v_out, st_t,
+                                    (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q8_workspace_size(const chunkkv_q8_cache* c, int32_t G, size_t* bytes) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, false, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (bytes == nullptr || G < 1) return CHUNKKV_ERR_INVALID_ARG;
+  *bytes = q8_workspace_bytes(g, G);
+  return CHUNKKV_OK;
+}
+
+chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, int32_t G, float scale, const void* q,
+                                    int64_t q_stride_b, int64_t q_stride_h, void* out, int64_t o_stride_b,
+                                    int64_t o_stride_h, void* ws, size_t ws_bytes, chunkkv_stream_t stream) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || G < 1 || !scale_ok(scale)) return CHUNKKV_ERR_INVALID_ARG;
+  const int elt = elt_size(dtype);
+  const int64_t strides[4] = {q_stride_b, q_stride_h, o_stride_b, o_stride_h};
+  for (int64_t s : strides)
+    if (!stride_ok(s, elt)) return CHUNKKV_ERR_INVALID_ARG;
+  if ((g.d * elt) % 16 != 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (G > 65535) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0) return CHUNKKV_OK;
+  if (!aligned(q) || !aligned(out) || !aligned(ws)) return CHUNKKV_ERR_INVALID_ARG;
+  if (ws_bytes < q8_workspace_bytes(g, G)) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_result(launch_q8_attention(g, dtype == CHUNKKV_BF16, G, (float)(scale * kLog2e), q, q_stride_b,
+                                         q_stride_h, out, o_stride_b, o_stride_h, c->k_pages, c->v_pages, c->scales,
+                                         c->table, c->lens, ws, sm_count(), (cudaStream_t)stream));
+}
+
+}  // extern "C"

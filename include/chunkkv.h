@@ -309,6 +309,132 @@ chunkkv_status chunkkv_selftest_wait_timeout(void* ws, size_t ws_bytes, chunkkv_
 #define CHUNKKV_PROBE_CHAINS 16
 chunkkv_status chunkkv_probe_ex2(float* sink, int32_t blocks, int32_t iters, chunkkv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving around the compression: attention over the prompt before it, and the
+ * compressed cache held in 8 bits after it (ChunkKV §5.6 keeps the compressed
+ * cache through decoding).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Causal attention over packed prompts with grouped heads:
+ *   out[i][hq] = sum over j <= i + Tk - Tq of softmax_j(scale * q[i][hq] . k[j][hq / G]) * v[j][hq / G]
+ * per sequence (i, j local to it): the last query sits at the last key, so Tq < Tk
+ * continues a sequence whose first Tk - Tq keys are cached, and Tq > Tk leaves the
+ * first Tq - Tk queries without a key; their rows are zeros.  A key that a query
+ * does not see adds nothing to it, whatever k and v hold there (infinities and NaN
+ * included).
+ *   q, out [Tq_total, Hq, d], k, v [Tk_total, Hkv, d]: device memory, dtype's type
+ *   (q, k, v and out start on 16-byte boundaries; every stride is a multiple of 16
+ *   bytes; d is contiguous).  out may not overlap an input.
+ * Sums and softmax statistics are fp32.  For bf16 the products run on the tensor
+ * cores when chunkkv_prefill_path says 1 (probabilities are then rounded to bf16
+ * before they weigh the values), else, and for fp32, in fp32 throughout.
+ */
+typedef struct chunkkv_prefill_params {
+  int32_t B, Hq, Hkv, d;      /* as in chunkkv_params                                       */
+  int32_t dtype;              /* chunkkv_dtype                                               */
+  float scale;                /* > 0 and finite; usually 1 / sqrt(d)                         */
+  const int32_t* cu_q;        /* HOST [B + 1], as chunkkv_params.cu_seqlens, of the queries  */
+  const int32_t* cu_k;        /* HOST [B + 1], of the keys                                   */
+  int64_t q_stride_t, q_stride_h;     /* element strides of q                               */
+  int64_t kv_stride_t, kv_stride_h;   /* element strides of k and of v                      */
+  int64_t o_stride_t, o_stride_h;     /* element strides of out                             */
+} chunkkv_prefill_params;
+
+/* Bytes of device workspace (zero-filled before its first use, like chunkkv_workspace_size's; its first
+ * word is read by chunkkv_status_check).  One workspace must not serve two calls that can overlap. */
+chunkkv_status chunkkv_prefill_workspace_size(const chunkkv_prefill_params* p, size_t* bytes);
+/* Which kernel these shapes take: 0 = fp32 arithmetic, 1 = tensor cores, -1 = invalid parameters. */
+int32_t chunkkv_prefill_path(const chunkkv_prefill_params* p);
+chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const void* q, const void* k, const void* v,
+                                         void* out, void* ws, size_t ws_bytes, chunkkv_stream_t stream);
+
+/*
+ * The compressed cache in 8 bits.  A cache row r = b * Hkv + h is one (sequence, KV
+ * head): chunk compression keeps another number of tokens for every head, so each
+ * has a length, pages and scales of its own.  A page holds CHUNKKV_Q8_PAGE tokens of
+ * one row as int8 codes with one fp32 scale for its keys and one for its values
+ * (value = code * scale).  d64 is d rounded up to a multiple of 64.
+ *   k_pages [n_pages][d64 / 64][CHUNKKV_Q8_PAGE][64], v_pages [n_pages][d64][CHUNKKV_Q8_PAGE]
+ *           int8, device, 16-byte aligned, zero-filled before their first use;
+ *   scales  [n_pages][2] fp32, device (keys, values), zero-filled before its first use;
+ *   table   [B * Hkv][max_pages] int32, device: the page of tokens 64 j .. 64 j + 63;
+ *   lens    [B * Hkv] int32, device: tokens held;
+ *   ring    [n_pages] int32, device: the free pages, state[1] of them from position
+ *           state[0] on, cyclically; at first a permutation of 0 .. n_pages - 1;
+ *   state   [4] int32, device: head, number free, status of the last resize, 0.
+ * table, lens, ring and state belong to one set of lengths; layers whose lengths
+ * agree (one reuse group of ChunkKV §4.2) share them, each layer with its own
+ * k_pages, v_pages and scales.  Calls that use one cache are ordered by their stream.
+ */
+#define CHUNKKV_Q8_PAGE 64
+/* Largest number of cache rows (B * Hkv). */
+#define CHUNKKV_Q8_MAX_ROWS 65535
+typedef struct chunkkv_q8_cache {
+  int32_t B, Hkv, d;
+  int32_t n_pages, max_pages;
+  int8_t* k_pages;
+  int8_t* v_pages;
+  float* scales;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* ring;
+  int32_t* state;
+} chunkkv_q8_cache;
+
+/*
+ * Block tables and slot maps on the GPU: sets every row's length to new_lens[r]
+ * (device [B * Hkv] int32).  Rows that need more pages take them from the ring's
+ * head, in row order; pages that a shorter row no longer needs go behind the ring's
+ * free part, in row order, and their table entries become -1.  slots (NULL, or
+ * device [B * Hkv][n_cap] int64) receives the slots page * CHUNKKV_Q8_PAGE + offset of
+ * tokens lens[r] .. new_lens[r] - 1 and -1 beyond them.
+ * All or nothing: state[2] is 0 when it was done; 1 when the ring has too few pages
+ * and 2 when a length is negative, needs more than max_pages pages, or (with slots)
+ * grows by more than n_cap: then nothing but state[2] and slots (all -1) is written.
+ * Reads and writes table, lens, ring and state only (k_pages, v_pages and scales
+ * may be NULL).
+ */
+chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
+                                 chunkkv_stream_t stream);
+
+/*
+ * Writes new rows into one layer's pages: for r = b * Hkv + h the first
+ * counts[b][h] (device int32) of the n_cap tokens k[b][h][i][:], v[b][h][i][:] (device,
+ * element strides st_b, st_h, st_t; d contiguous) go to slots[r][i], as
+ * chunkkv_q8_resize wrote them for these rows.  A page's scale becomes
+ *   s = max(s_old, m / 127)    m: largest magnitude among its new tokens (zero if below 2^-100)
+ * (s_old = 0 if the new tokens begin the page), its older codes round(code * (s_old / s))
+ * if it grew, and the new codes round(x * (1 / s)), ties to even, in fp32.  A NaN or an
+ * infinity makes the scale of its page NaN or infinite: the page then reads as NaN.
+ */
+chunkkv_status chunkkv_q8_append(const chunkkv_q8_cache* c, int32_t dtype, const void* k, const void* v, int64_t st_b,
+                                 int64_t st_h, int64_t st_t, const int32_t* counts, const int64_t* slots,
+                                 int32_t n_cap, chunkkv_stream_t stream);
+
+/*
+ * Reads rows back: token i < min(lens[r], n_cap) of row r goes to k_out and
+ * v_out[(start[r] + i) * st_t + e] (device, dtype's type; start: device [B * Hkv]
+ * int64, a negative entry skips the row), e.g. as the packed keys of a further
+ * chunkkv_compress_layers or chunkkv_compress_tail call.
+ */
+chunkkv_status chunkkv_q8_load(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                               void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream);
+
+/*
+ * Single-token attention over one layer's cache, G query heads per KV head:
+ *   out[b][h * G + g] = sum_j softmax_j(scale * q[b][h * G + g] . K_j) V_j
+ * over the lens[r] tokens of row r = b * Hkv + h; an empty row gives zeros.
+ *   q, out: device [B, Hkv * G, d] with element strides (b, head), multiples of 16 bytes;
+ *   scale > 0 and finite; sums and softmax statistics in fp32;
+ *   ws: device workspace of chunkkv_q8_workspace_size bytes, zero-filled before its
+ *       first use; not shared by calls that can overlap.
+ */
+chunkkv_status chunkkv_q8_workspace_size(const chunkkv_q8_cache* c, int32_t G, size_t* bytes);
+chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, int32_t G, float scale, const void* q,
+                                    int64_t q_stride_b, int64_t q_stride_h, void* out, int64_t o_stride_b,
+                                    int64_t o_stride_h, void* ws, size_t ws_bytes, chunkkv_stream_t stream);
+
 /* Static description of a status code. */
 const char* chunkkv_status_string(chunkkv_status s);
 

@@ -1,0 +1,540 @@
+"""The serving operators on the GPU, against plain 64-bit implementations written from their formulas.
+
+Tolerances, per output element, with A = sum_j softmax_j |v_j| and E = max_j scale * sum_e |q_e k_je| of its row:
+  logits     fp32 sums of d products: each off by at most (d + 4) 2^-24 E, which moves a probability and the
+             row's sum by that factor each: 2 (d + 4) 2^-24 E A (2^-22 for the 8-bit cache, whose query is
+             held in two 11-bit parts)
+  sums       n terms in fp32 and a few ulp of the exponential: (n + 16) 2^-23 A (2^-22 for the 8-bit cache)
+  bf16       8 significant bits, a unit roundoff of 2^-8: the output's rounding 2^-8 |o|; on the tensor cores the
+             probabilities are rounded too: 2^-8 A
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ckv():
+    import chunk_level_kv_gb300 as m     # fails loudly if the library was not built
+    return m
+
+
+def offsets(ns):
+    out = [0]
+    for n in ns:
+        out.append(out[-1] + n)
+    return out
+
+
+# ------------------------------------------------------------------ prefill attention
+
+def attention64(q, k, v, scale):
+    """(out, A, E) [T, Hq, d], [T, Hq, d], [T, Hq, 1] of one sequence, in 64 bits; hidden keys are cut away."""
+    Tq, Hq, d = q.shape
+    Tk, Hkv, _ = k.shape
+    out = torch.zeros(Tq, Hq, d, dtype=torch.float64, device=q.device)
+    A, E = torch.zeros_like(out), torch.zeros(Tq, Hq, 1, dtype=torch.float64, device=q.device)
+    if Tk == 0:
+        return out, A, E
+    hidden = torch.arange(Tk, device=q.device)[None] > torch.arange(Tq, device=q.device)[:, None] + (Tk - Tq)
+    empty = hidden.all(1)
+    for h in range(Hq):
+        qh, kh, vh = q[:, h].double(), k[:, h * Hkv // Hq].double(), v[:, h * Hkv // Hq].double()
+        s = (qh @ kh.T * scale).masked_fill(hidden, -math.inf)
+        p = torch.softmax(s, -1).masked_fill(hidden, 0.0)
+        p[empty] = 0
+        out[:, h], A[:, h] = p @ vh, p @ vh.abs()
+        E[:, h] = (qh.abs() @ kh.abs().T * scale).masked_fill(hidden, 0).amax(1, keepdim=True)
+    return out, A, E
+
+
+def check_prefill(out, q, k, v, cq, ck, scale, path):
+    d = q.shape[2]
+    for b in range(len(cq) - 1):
+        qs, ks = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+        ref, A, E = attention64(q[qs], k[ks], v[ks], scale)
+        n = ck[b + 1] - ck[b]
+        tol = (2 * (d + 4) * 2.0 ** -24 * E + (n + 16) * 2.0 ** -23) * A + 1e-30
+        if q.dtype == BF:
+            tol = tol + 2.0 ** -8 * ref.abs() + (2.0 ** -8 * A if path else 0)
+        err = (out[qs].double() - ref).abs()
+        assert torch.isfinite(out[qs]).all(), f"sequence {b}"
+        assert bool((err <= tol).all()), f"sequence {b}: {float((err / tol).max())} of the tolerance"
+
+
+def make_qkv(tq, tk, Hq, Hkv, d, dtype, seed, qscale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = (torch.randn(sum(tq), Hq, d, generator=g, device=DEV) * qscale).to(dtype)
+    k = torch.randn(sum(tk), Hkv, d, generator=g, device=DEV).to(dtype)
+    v = torch.randn(sum(tk), Hkv, d, generator=g, device=DEV).to(dtype)
+    return q, k, v
+
+
+LENGTHS = {
+    "one token": ([1], [1]),
+    "tiles": ([128, 256, 64], [128, 256, 64]),
+    "ragged": ([1, 130, 0, 517, 63, 300], [1, 130, 0, 517, 63, 300]),
+    "continued": ([1, 100, 257, 5], [700, 1100, 390, 5]),          # cached keys before the queries
+    "more queries than keys": ([300, 140, 5], [1, 139, 0]),        # the first rows see nothing
+    "long": ([1500], [1500]),
+}
+
+
+@pytest.mark.parametrize("lengths", list(LENGTHS))
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF, 128, 8, 2), (BF, 64, 4, 4), (BF, 128, 7, 1), (BF, 80, 4, 2), (BF, 8, 2, 1),
+                                            (BF, 192, 2, 1), (BF, 256, 4, 2), (F32, 64, 4, 2), (F32, 128, 3, 1),
+                                            (F32, 4, 2, 2), (F32, 100, 2, 1), (F32, 256, 2, 1)])
+def test_prefill_matches_the_formula(ckv, dtype, d, Hq, Hkv, lengths):
+    tq, tk = LENGTHS[lengths]
+    q, k, v = make_qkv(tq, tk, Hq, Hkv, d, dtype, seed=d + Hq)
+    cq, ck = offsets(tq), offsets(tk)
+    out = torch.full_like(q, float("nan"))
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    ckv.prefill_attention(q, k, v, cq, ck, out=out, workspace=ws)
+    ckv.chunkkv_status_check(ws)
+    p, keep = ckv.prefill_params_for(q, k, cq, ck)
+    check_prefill(out, q, k, v, cq, ck, 1 / math.sqrt(d), ckv.chunkkv_prefill_path(p))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_large_batches_use_the_long_table(ckv, dtype):
+    g = torch.Generator().manual_seed(5)
+    tq = [int(x) for x in torch.randint(0, 90, (70,), generator=g)]
+    tk = [n + int(x) for n, x in zip(tq, torch.randint(0, 40, (70,), generator=g))]
+    q, k, v = make_qkv(tq, tk, 4, 2, 64, dtype, seed=9)
+    cq, ck = offsets(tq), offsets(tk)
+    out = ckv.prefill_attention(q, k, v, cq, ck)
+    p, keep = ckv.prefill_params_for(q, k, cq, ck)
+    check_prefill(out, q, k, v, cq, ck, 1 / 8, ckv.chunkkv_prefill_path(p))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_prefill_strided_inputs_and_scale(ckv, dtype, d):
+    # q, k and v as column ranges of one projection, the output into a wider buffer, heads before tokens for q
+    tq = [200, 77]
+    T, Hq, Hkv = sum(tq), 6, 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    qkv = torch.randn(T, Hq + 2 * Hkv, d, generator=g, device=DEV).to(dtype)
+    k, v = qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    q = qkv[:, :Hq].transpose(0, 1).contiguous().transpose(0, 1)
+    wide = torch.full((T, Hq, 2 * d), 7.0, dtype=dtype, device=DEV)
+    out = wide[:, :, :d]
+    ckv.prefill_attention(q, k, v, offsets(tq), scale=0.3, out=out)
+    p, keep = ckv.prefill_params_for(q, k, offsets(tq))
+    check_prefill(out, q, k, v, offsets(tq), offsets(tq), 0.3, ckv.chunkkv_prefill_path(p))
+    assert bool((wide[:, :, d:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128)])
+def test_prefill_growing_logits(ckv, dtype, d):
+    # logits whose maximum grows along the keys (and far beyond the first tile's), and one key that takes all
+    T = 700
+    q, k, v = make_qkv([T], [T], 2, 1, d, dtype, seed=11, qscale=4.0)
+    k = (k.float() * torch.linspace(0.1, 6.0, T, device=DEV)[:, None, None]).to(dtype)
+    k[350] = (q[400:].float().mean((0, 1)) * 40).to(dtype)
+    out = ckv.prefill_attention(q, k, v, [0, T])
+    p, keep = ckv.prefill_params_for(q, k, [0, T])
+    check_prefill(out, q, k, v, [0, T], [0, T], 1 / math.sqrt(d), ckv.chunkkv_prefill_path(p))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_prefill_hidden_keys_may_hold_anything(ckv, dtype, d, bad):
+    # a non-finite key and value at some positions: queries before them, and the other sequences, are untouched
+    tq, spots = [300, 213, 150], [130, 299, 300 + 212]
+    q, k, v = make_qkv(tq, tq, 4, 2, d, dtype, seed=21)
+    cq = offsets(tq)
+    clean = ckv.prefill_attention(q, k, v, cq)
+    kb, vb = k.clone(), v.clone()
+    for s in spots:
+        vb[s, :, ::3] = bad
+        kb[s, :, 1] = bad
+    out = ckv.prefill_attention(q, kb, vb, cq)
+    assert torch.equal(out[:130], clean[:130])
+    assert torch.equal(out[300:300 + 212], clean[300:300 + 212]) and torch.equal(out[513:], clean[513:])
+    # the queries that see them: not finite where the formula is not
+    ref, _, _ = attention64(q[:300], kb[:300], vb[:300], 1 / math.sqrt(d))
+    assert torch.equal(torch.isfinite(ref[130:]), torch.isfinite(out[130:300].double()))
+
+
+def test_prefill_fully_masked_rows_and_empty_calls(ckv):
+    q, k, v = make_qkv([50], [0], 2, 2, 64, BF, seed=1)
+    out = torch.full_like(q, float("nan"))
+    ckv.prefill_attention(q, k, v, [0, 50], [0, 0], out=out)
+    assert bool((out == 0).all())
+    empty = q[:0]
+    assert ckv.prefill_attention(empty, empty, empty, [0, 0]).shape == empty.shape
+    assert ckv.prefill_attention(empty, empty, empty, [0]).shape == empty.shape
+
+
+def test_prefill_on_another_stream_and_in_a_graph(ckv):
+    T = 400
+    q, k, v = make_qkv([T], [T], 4, 2, 128, BF, seed=2)
+    want = ckv.prefill_attention(q, k, v, [0, T])
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ckv.prefill_attention(q, k, v, [0, T], out=out, workspace=ws)
+    side.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ckv.prefill_attention(q, k, v, [0, T], out=out, workspace=ws)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ page tables
+
+class Tables:
+    """chunkkv_q8_resize restated: lists instead of a ring in device memory."""
+
+    def __init__(self, rows, max_pages, n_pages):
+        self.lens, self.max_pages, self.n_pages = [0] * rows, max_pages, n_pages
+        self.table = [[] for _ in range(rows)]
+        self.free = list(range(n_pages))
+
+    def resize(self, new, n_cap):
+        need = [-(-n // 64) for n in new]
+        if any(n < 0 for n in new) or max(need) > self.max_pages or any(n - m > n_cap for n, m in zip(new, self.lens)):
+            return 2, None
+        if sum(max(0, n - len(t)) for n, t in zip(need, self.table)) > len(self.free):
+            return 1, None
+        slots, back = [], []
+        for r, n in enumerate(need):
+            while len(self.table[r]) < n:
+                self.table[r].append(self.free.pop(0))
+            back += self.table[r][n:]
+            del self.table[r][n:]
+            slots.append([self.table[r][p // 64] * 64 + p % 64 for p in range(self.lens[r], new[r])])
+        self.free += back
+        self.lens = list(new)
+        return 0, slots
+
+
+def check_tables(cache, ref, slots, want):
+    torch.cuda.synchronize()
+    head, n_free, _, ticket = cache.state.tolist()
+    assert ticket == 0 and n_free == len(ref.free)
+    ring = cache.ring.tolist()
+    assert [ring[(head + i) % len(ring)] for i in range(n_free)] == ref.free
+    assert cache.lens.tolist() == ref.lens
+    for r, row in enumerate(cache.table.tolist()):
+        assert row == ref.table[r] + [-1] * (ref.max_pages - len(ref.table[r])), r
+    if slots is not None:
+        got = slots.tolist()
+        for r, row in enumerate(got):
+            w = want[r] if want is not None else []
+            assert row == w + [-1] * (len(row) - len(w)), r
+
+
+@pytest.mark.parametrize("rows,max_pages,n_pages,n_cap,calls", [(1, 4, 3, 200, 12), (24, 9, 120, 300, 10),
+                                                                 (1500, 5, 4000, 130, 6), (3000, 3, 9000, 64, 4)])
+def test_resize_matches_the_lists(ckv, rows, max_pages, n_pages, n_cap, calls):
+    g = torch.Generator().manual_seed(rows)
+    cache = ckv.q8_cache(rows, 1, 64, n_pages=n_pages, max_pages=max_pages, n_layers=0)
+    ref = Tables(rows, max_pages, n_pages)
+    slots = torch.full((rows, n_cap), 5, dtype=torch.int64, device=DEV)
+    seen = set()
+    for call in range(calls):
+        grow = torch.randint(0, n_cap + 1, (rows,), generator=g) * (torch.rand(rows, generator=g) < 0.7)
+        new = torch.tensor(ref.lens) + grow
+        cut = torch.rand(rows, generator=g) < 0.4
+        new = torch.where(cut, (new * torch.rand(rows, generator=g)).long(), new).clamp(max=max_pages * 64)
+        new = torch.minimum(new, torch.tensor(ref.lens) + n_cap)
+        status, want = ref.resize(new.tolist(), n_cap)
+        ckv.chunkkv_q8_resize(cache, new.int().to(DEV), slots)
+        assert cache.state[2].item() == status
+        seen.add(status)
+        check_tables(cache, ref, slots, want)
+    ckv.chunkkv_q8_resize(cache, torch.zeros(rows, dtype=torch.int32, device=DEV))       # all leave, no slot map
+    assert ref.resize([0] * rows, 0)[0] == 0
+    check_tables(cache, ref, None, None)
+    assert 0 in seen
+
+
+def test_resize_is_all_or_nothing(ckv):
+    cache = ckv.q8_cache(3, 1, 64, n_pages=5, max_pages=4, n_layers=0)
+    ref = Tables(3, 4, 5)
+    slots = torch.zeros(3, 256, dtype=torch.int64, device=DEV)
+
+    def go(new, status):
+        ckv.chunkkv_q8_resize(cache, torch.tensor(new, dtype=torch.int32, device=DEV), slots)
+        got, want = ref.resize(new, 256)
+        assert got == status == cache.state[2].item()
+        check_tables(cache, ref, slots, want)
+    go([100, 64, 1], 0)
+    go([100, 256, 1], 1)            # one page left, three wanted
+    go([257, 0, 0], 2)              # more than max_pages
+    go([100, -1, 1], 2)
+    go([0, 64, 200], 1)             # pages given back in a call are not yet free for it
+    go([0, 64, 1], 0)
+    go([0, 64, 200], 0)
+    go([2147483647, 64, 200], 2)
+
+
+# ------------------------------------------------------------------ writing and reading back
+
+def fill(ckv, cache, new_lens, k, v, layer=0):
+    """Grows the cache to new_lens with the rows of k, v [B, Hkv, n_cap, d]; returns the counts."""
+    lens = cache.lens.clone()
+    new = torch.tensor(new_lens, dtype=torch.int32, device=DEV)
+    slots = torch.empty(cache.rows, k.shape[2], dtype=torch.int64, device=DEV)
+    ckv.chunkkv_q8_resize(cache, new, slots)
+    assert cache.state[2].item() == 0
+    counts = (new - lens).contiguous()
+    ckv.chunkkv_q8_append(cache, layer, k, v, counts, slots)
+    return counts
+
+
+def read(ckv, cache, dtype, layer=0):
+    lens = cache.lens.tolist()
+    at = offsets(lens)
+    k = torch.full((max(at[-1], 1), cache.d), 9.0, dtype=dtype, device=DEV)
+    v = torch.full_like(k, 9.0)
+    start = torch.tensor(at[:-1], dtype=torch.int64, device=DEV)
+    ckv.chunkkv_q8_load(cache, layer, start, max(max(lens), 1), k, v)
+    return [(k[a:b], v[a:b]) for a, b in zip(at, at[1:])]
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 80), (BF, 8), (BF, 256), (F32, 128), (F32, 72), (F32, 8)])
+def test_append_and_load(ckv, dtype, d):
+    # appends that begin and end inside pages; a value is off by half a step of its page's scale, and by half a
+    # step more for every later append that made the page's scale grow (its codes are rounded again)
+    B, Hkv = 2, 2
+    cache = ckv.q8_cache(B, Hkv, d, n_pages=40, max_pages=8)
+    cache.k_pages[0].fill_(77)                        # stale codes in pages not yet used
+    cache.scales[0].fill_(3.0)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    steps = [[0, 3, 64, 130], [5, 70, 64, 131], [200, 71, 129, 131], [201, 300, 130, 132], [201, 301, 130, 256]]
+    kept = [[[], []] for _ in range(4)]
+    at = [0] * 4
+    for step, lens in enumerate(steps):
+        cap = max(max(n - a for n, a in zip(lens, at)), 1) + 3
+        k = (torch.randn(B, Hkv, cap, d, generator=g, device=DEV) * (1 + step)).to(dtype)
+        v = (torch.randn(B, Hkv, cap, d, generator=g, device=DEV) * (3.0 if step == 1 else 0.5)).to(dtype)
+        fill(ckv, cache, lens, k, v)
+        for r in range(4):
+            for i, x in enumerate((k, v)):
+                kept[r][i].append(x[r // Hkv, r % Hkv, :lens[r] - at[r]])
+        at = lens
+    got = read(ckv, cache, F32)
+    rounded = read(ckv, cache, BF)
+    table = cache.table.tolist()
+    for r in range(4):
+        for i in range(2):
+            x = torch.cat(kept[r][i]).double()
+            y = got[r][i].double()
+            assert y.shape == x.shape
+            for j in range(-(-len(x) // 64)):
+                s = cache.scales[0][table[r][j], i].double()
+                part = slice(64 * j, 64 * j + 64)
+                top = x[part].abs().max()
+                assert abs(s - top / 127) <= 2.0 ** -22 * s
+                # at most len(steps) - 1 roundings after the first, each of at most half a step of the scale then held
+                tol = s * (0.5 + 2.0 ** -10) * len(steps)
+                assert bool(((y[part] - x[part]).abs() <= tol).all())
+                alone = x[part].shape[0] == 64 and r == 2 and j == 0           # written by one append
+                if alone:
+                    assert bool(((y[part] - x[part]).abs() <= s * (0.5 + 2.0 ** -10)).all())
+            assert torch.equal(rounded[r][i], got[r][i].to(BF))
+
+
+def test_append_strides_and_codes(ckv):
+    # one token per row from a [B, Hq + 2 Hkv, d] projection; codes against the formula in 64 bits
+    B, Hkv, d = 3, 2, 128
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(B, 4 + 2 * Hkv, d, generator=g, device=DEV).to(BF)
+    k, v = x[:, 4:4 + Hkv, None], x[:, 4 + Hkv:, None]
+    cache = ckv.q8_cache(B, Hkv, d, n_pages=20, max_pages=3)
+    fill(ckv, cache, [1] * 6, k, v)
+    for (gk, gv), r in zip(read(ckv, cache, F32), range(6)):
+        for y, z in ((gk, k), (gv, v)):
+            z = z[r // Hkv, r % Hkv].double()
+            s = z.abs().max() / 127
+            assert bool(((y.double() - z).abs() <= s * (0.5 + 2.0 ** -10)).all())
+
+
+def test_append_zero_tiny_and_non_finite_blocks(ckv):
+    cache = ckv.q8_cache(1, 4, 64, n_pages=8, max_pages=2)
+    k = torch.zeros(1, 4, 10, 64, device=DEV)
+    v = torch.ones(1, 4, 10, 64, device=DEV)
+    k[0, 1] = 1e-38
+    k[0, 2, 3, 5] = float("nan")
+    k[0, 3, 9, 0] = float("inf")
+    fill(ckv, cache, [10] * 4, k, v)
+    got = read(ckv, cache, F32)
+    assert bool((got[0][0] == 0).all()) and bool((got[1][0] == 0).all())
+    assert bool(got[2][0].isnan().all()) and bool(got[3][0].isnan().any())
+    for r in range(4):
+        assert bool(((got[r][1] - 1).abs() <= 1e-6).all())
+
+
+def test_load_packs_and_skips(ckv):
+    cache = ckv.q8_cache(1, 3, 64, n_pages=9, max_pages=3)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    k = torch.randn(1, 3, 130, 64, generator=g, device=DEV)
+    fill(ckv, cache, [130, 70, 0], k, k)
+    rows = read(ckv, cache, F32)
+    out = torch.full((200, 64), 5.0, device=DEV)
+    start = torch.tensor([100, -1, 3], dtype=torch.int64, device=DEV)
+    ckv.chunkkv_q8_load(cache, 0, start, 40, out, out.clone())
+    assert torch.equal(out[100:140], rows[0][0][:40])
+    assert bool((out[:100] == 5).all()) and bool((out[140:] == 5).all())
+
+
+# ------------------------------------------------------------------ decode attention
+
+def check_decode(ckv, cache, q, out, scale, layer=0):
+    B, Hq, d = q.shape
+    G = Hq // cache.Hkv
+    rows = read(ckv, cache, F32, layer)
+    for r, (k, v) in enumerate(rows):
+        b, h = divmod(r, cache.Hkv)
+        o = out[b, h * G:(h + 1) * G].double()
+        n = len(k)
+        if n == 0:
+            assert bool((o == 0).all()), r
+            continue
+        qr, k, v = q[b, h * G:(h + 1) * G].double(), k.double(), v.double()
+        p = torch.softmax(qr @ k.T * scale, -1)
+        ref, A = p @ v, p @ v.abs()
+        E = (qr.abs() @ k.abs().T * scale).amax(1, keepdim=True)
+        tol = (2 * (d + 4) * 2.0 ** -22 * E + (n + 16) * 2.0 ** -22) * A + 1e-30
+        if q.dtype == BF:
+            tol = tol + 2.0 ** -8 * ref.abs()
+        err = (o - ref).abs()
+        assert torch.isfinite(o).all(), r
+        assert bool((err <= tol).all()), f"row {r} ({n} tokens): {float((err / tol).max())} of the tolerance"
+
+
+def random_cache(ckv, B, Hkv, d, lens, seed, dtype=BF, spread=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    pages = sum(-(-n // 64) for n in lens)
+    cache = ckv.q8_cache(B, Hkv, d, n_pages=pages + 5, max_pages=max(1, max(-(-n // 64) for n in lens)))
+    cache.ring.copy_(torch.randperm(pages + 5, generator=g, device=DEV).int())
+    cache.k_pages[0].fill_(-128)                      # stale codes, and scales that must not be read
+    cache.v_pages[0].fill_(127)
+    cache.scales[0].fill_(float("nan"))
+    n = max(max(lens), 1)
+    grow = torch.exp(spread * torch.randn(1, 1, n, 1, generator=g, device=DEV)) if spread != 1.0 else 1.0
+    k = torch.randn(B, Hkv, n, d, generator=g, device=DEV).to(dtype)
+    v = (torch.randn(B, Hkv, n, d, generator=g, device=DEV) * grow).to(dtype)
+    fill(ckv, cache, lens, k, v)
+    return cache, g
+
+
+DECODE_LENS = {
+    "short": lambda rows: [(i * 37) % 130 for i in range(rows)],                # zero and one among them
+    "one": lambda rows: [1] * rows,
+    "pages": lambda rows: [64 * (i % 4) for i in range(rows)],
+    "long": lambda rows: [3000 + 517 * i if i < 2 else 64 * i + 63 for i in range(rows)],
+}
+
+
+@pytest.mark.parametrize("lens", list(DECODE_LENS))
+@pytest.mark.parametrize("dtype,d,B,Hkv,G", [(BF, 128, 2, 4, 4), (BF, 128, 3, 1, 7), (BF, 64, 4, 2, 1), (BF, 80, 1, 3, 8),
+                                             (BF, 256, 2, 1, 12), (BF, 128, 1, 2, 33), (BF, 192, 1, 2, 3), (BF, 8, 2, 2, 2),
+                                             (F32, 128, 2, 2, 4), (F32, 64, 1, 1, 16), (F32, 96, 2, 2, 5)])
+def test_decode_matches_the_formula(ckv, dtype, d, B, Hkv, G, lens):
+    ls = DECODE_LENS[lens](B * Hkv)
+    cache, g = random_cache(ckv, B, Hkv, d, ls, seed=d + G)
+    q = torch.randn(B, Hkv * G, d, generator=g, device=DEV).to(dtype)
+    out = torch.full_like(q, float("nan"))
+    ws = torch.zeros(ckv.chunkkv_q8_workspace_size(cache, G), dtype=torch.uint8, device=DEV)
+    for call in range(2):                             # the second call finds what the first left in the workspace
+        out.fill_(float("nan"))
+        ckv.chunkkv_q8_attention(cache, 0, q, out, ws)
+        check_decode(ckv, cache, q, out, 1 / math.sqrt(d))
+    again = ckv.q8_attention(cache, 0, q)
+    assert torch.equal(again, out)                    # the same call gives the same bits
+
+
+def test_decode_many_rows(ckv):
+    lens = [int(x) for x in torch.randint(0, 200, (1200,), generator=torch.Generator().manual_seed(1))]
+    cache, g = random_cache(ckv, 300, 4, 64, lens, seed=6)
+    q = torch.randn(300, 8, 64, generator=g, device=DEV).to(BF)
+    check_decode(ckv, cache, q, ckv.q8_attention(cache, 0, q), 1 / 8)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_long_rows_with_uneven_scales_and_sharp_logits(ckv, dtype):
+    # value scales that differ by orders of magnitude between pages, logits with one dominant key, a large query
+    lens = [20000, 0, 1, 9000]
+    cache, g = random_cache(ckv, 2, 2, 128, lens, seed=77, spread=2.0)
+    q = torch.randn(2, 8, 128, generator=g, device=DEV)
+    q[1] *= 30.0
+    q = q.to(dtype)
+    check_decode(ckv, cache, q, ckv.q8_attention(cache, 0, q), 1 / math.sqrt(128))
+    tiny = (q.float() * 1e-30).to(dtype)
+    check_decode(ckv, cache, tiny, ckv.q8_attention(cache, 0, tiny), 1 / math.sqrt(128))
+    zero = torch.zeros_like(q)
+    check_decode(ckv, cache, zero, ckv.q8_attention(cache, 0, zero, scale=0.5), 0.5)
+
+
+def test_decode_strided_queries_layers_and_streams(ckv):
+    B, Hkv, G, d = 2, 2, 4, 128
+    lens = [100, 260, 31, 64]
+    cache = ckv.q8_cache(B, Hkv, d, n_pages=30, max_pages=5, n_layers=2)
+    g = torch.Generator(device=DEV).manual_seed(12)
+    k = torch.randn(B, Hkv, 260, d, generator=g, device=DEV).to(BF)
+    counts = fill(ckv, cache, lens, k, k, layer=0)
+    slots = torch.empty(4, 260, dtype=torch.int64, device=DEV)
+    for r, n in enumerate(lens):                      # the second layer's rows go to the same slots
+        pos = torch.arange(260, device=DEV)
+        page = cache.table[r].long()[(pos // 64).clamp(max=4)]
+        slots[r] = page * 64 + pos % 64
+    ckv.chunkkv_q8_append(cache, 1, 2 * k, -k, counts, slots)
+    qkv = torch.randn(B, Hkv * G + 3, d, generator=g, device=DEV).to(BF)
+    q = qkv[:, 1:1 + Hkv * G]
+    for layer in range(2):
+        wide = torch.full((B, Hkv * G, 2 * d), 3.0, dtype=BF, device=DEV)
+        out = wide[:, :, d:]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            ckv.q8_attention(cache, layer, q, out=out)
+        side.synchronize()
+        check_decode(ckv, cache, q, out, 1 / math.sqrt(d), layer)
+        assert bool((wide[:, :, :d] == 3.0).all())
+
+
+def test_decode_page_with_a_nan_scale(ckv):
+    # a non-finite value in a row's page reaches that row only
+    cache, g = random_cache(ckv, 1, 3, 64, [100, 100, 100], seed=3)
+    q = torch.randn(1, 6, 64, generator=g, device=DEV).to(BF)
+    clean = ckv.q8_attention(cache, 0, q)
+    cache.scales[0][cache.table[1, 1].item(), 1] = float("nan")
+    out = ckv.q8_attention(cache, 0, q)
+    assert torch.equal(out[:, :2], clean[:, :2]) and torch.equal(out[:, 4:], clean[:, 4:])
+    assert bool(out[:, 2:4].isnan().all())
+
+
+def test_decode_in_a_graph_follows_the_lengths(ckv):
+    # one captured call serves later lengths: they are read on the device
+    cache, g = random_cache(ckv, 2, 2, 128, [500, 3, 0, 64], seed=31)
+    q = torch.randn(2, 8, 128, generator=g, device=DEV).to(BF)
+    ws = torch.zeros(ckv.chunkkv_q8_workspace_size(cache, 4), dtype=torch.uint8, device=DEV)
+    out = torch.zeros_like(q)
+    ckv.chunkkv_q8_attention(cache, 0, q, out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ckv.chunkkv_q8_attention(cache, 0, q, out, ws)
+    for new in ([500, 3, 0, 64], [77, 2, 0, 1], [0, 0, 0, 0]):
+        ckv.chunkkv_q8_resize(cache, torch.tensor(new, dtype=torch.int32, device=DEV))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_decode(ckv, cache, q, out, 1 / math.sqrt(128))
