@@ -3,83 +3,532 @@
 //   O_g = sum_j 2^(t_j) s_v V_j / sum_j 2^(t_j),   t_j = scale log2(e) s_k (q_g . K_j)
 //
 // over the tokens j of one cache row, K and V int8 codes, s_k and s_v the scales of
-// the token's page.  One CTA takes one query head and walks its row's pages with a
-// running maximum and sum.
+// the token's page; one pass over the pages with a running maximum of t and sum.
+//
+// What bounds it: every page is read once (2 d bytes a token), HBM.  The arithmetic
+// must keep out of the way: at 6.76 TB/s an SM receives 23 codes a clock, which leaves
+// 5 instruction slots a code.  So both products run on the tensor cores in f16, in
+// which an int8 code is exact (a byte permute and a packed subtraction turn four codes
+// into two operand registers, 1.25 instructions a code), with the G <= 8 query heads of
+// a KV head as the 16-row operand's rows 0-7.  Rows 8-15 carry what f16 cut off: the
+// query is split into two f16 parts (22 bits) and so are the weights, so the products
+// are as good as fp32 ones and cost nothing more than the 16 rows that the
+// instruction computes anyway.  mma.sync and not tcgen05: the operands come from
+// registers after the conversion, and an m128 tile would be 1/16 full.
+//
+// Work split: the pages of all rows in order are cut into one contiguous run per CTA
+// (one CTA per SM), whatever the rows' lengths, which only the device knows: every CTA
+// finds its run by a scan over the lengths.  Inside a CTA the pages go to the warps in
+// turn; each warp has a K and a V slot that bulk copies fill while it works on the
+// other, so about 100 KB per SM are under way.  A row that lies in one CTA is
+// written at once; the CTAs that share a row write (m, l, O) partials, and the last one to
+// arrive adds them in CTA order, so that the result does not depend on the order of
+// arrival.
+#include <cuda_fp16.h>
+
 #include "serve.cuh"
 
 namespace chunkkv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxG = 8;                         // query heads per pass
+constexpr float kWeightScale = 14.f;             // weights are 2^(t - m + 14): f16 keeps them to 2^-38 of the largest
+constexpr size_t kHeader = 256;                  // device error word
 
 struct Q8AttnArgs {
   const void* q;
   void* out;
   int64_t q_sb, q_sh, o_sb, o_sh;
-  float alpha;
+  float alpha;                                   // scale * log2(e)
   int32_t G;
+  int32_t* err;
+  int32_t* arrived;                              // [groups][rows] partials written, zero between calls
+  float* part;                                   // [groups][2 CTAs][8][d64 + 2]
 };
 
+template <int ND>
+constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
+template <int ND>
+constexpr int page_bytes() { return ND * 64 * kPage; }
+template <int ND>
+constexpr int merge_pitch() { return 64 * ND + 2; }         // O, then m and l
+template <int ND>
+constexpr bool q_in_regs() { return ND <= 2; }              // wider heads keep their query fragments in shared memory
+template <int ND>
+constexpr size_t smem_bytes() {
+  return (size_t)warps_of<ND>() * (2 * page_bytes<ND>() + kMaxG * merge_pitch<ND>() * 4 +
+                                   (q_in_regs<ND>() ? 0 : ND * 4 * 32 * 16));
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D (16 x 8, fp32) += A (16 x 16, f16) B (16 x 8, f16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// Four int8 codes as two f16 pairs: a code plus 128 in the low byte of 0x64.. is
+// 1024 + 128 + code, exactly.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 x = __hsub2(*(__half2*)&a, k), y = __hsub2(*(__half2*)&b, k);
+  lo = *(const uint32_t*)&x;
+  hi = *(const uint32_t*)&y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *(const uint32_t*)&h;
+}
+// x = hi + lo in two f16 pairs (lo times up).
+__device__ __forceinline__ void split_half2(float x, float y, float up, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *(const uint32_t*)&h;
+  lo = pack_half2((x - f.x) * up, (y - f.y) * up);
+}
+
+__device__ __forceinline__ void load4f(const float* p, float (&x)[4]) {
+  const float4 v = *(const float4*)p;
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4f(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = *(const uint2*)p;
+  x[0] = __uint_as_float(v.x << 16);
+  x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(v.y << 16);
+  x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, const int8_t* __restrict__ v_pages,
-                    const float* __restrict__ scales, const int32_t* __restrict__ table,
-                    const int32_t* __restrict__ lens) {
-  __shared__ float s_q[kMaxD], s_t[kPage], s_half[2][kPage];
-  pdl_wait();
-  const int r = blockIdx.x, gq = blockIdx.y, tid = threadIdx.x;
-  const int b = r / g.Hkv, hq = (r % g.Hkv) * a.G + gq;
-  const T* q = (const T*)a.q + b * a.q_sb + hq * a.q_sh;
-  for (int e = tid; e < g.d64; e += kThreads) s_q[e] = e < g.d ? to_float(q[e]) : 0.f;
-  const int n = safe_len(lens[r], g.max_pages);
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int j = 0; j * kPage < n; ++j) {
-    const int64_t page = safe_page(table[(int64_t)r * g.max_pages + j], g.n_pages);
-    const float sk = scales[page * 2] * a.alpha, sv = scales[page * 2 + 1];
-    const int8_t* kp = k_pages + page * (int64_t)(g.d64 * kPage);
-    const int8_t* vp = v_pages + page * (int64_t)(g.d64 * kPage);
-    __syncthreads();
-    const int t = tid & 63, half = tid >> 6;
-    float acc = 0.f;
-    for (int c = half * g.d64 / 2; c < (half + 1) * g.d64 / 2; ++c)
-      acc = fmaf(s_q[c], (float)kp[(c >> 6) * (kPage * 64) + t * 64 + (c & 63)], acc);
-    s_half[half][t] = acc;
-    __syncthreads();
-    if (tid < kPage) s_t[tid] = j * kPage + tid < n ? (s_half[0][tid] + s_half[1][tid]) * sk : -INFINITY;
-    __syncthreads();
-    float top = m;
-    for (int i = 0; i < kPage; ++i) top = fmaxf(top, s_t[i]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - ref);
-    m = top;
-    l *= f;
-    for (int i = 0; i < kPage; ++i) l += exp2f(s_t[i] - ref);
-    for (int c = tid, x = 0; c < g.d64; c += kThreads, ++x) {
-      float acc2 = 0.f;
-      for (int i = 0; i < min(kPage, n - j * kPage); ++i)
-        acc2 = fmaf(exp2f(s_t[i] - ref), (float)vp[c * kPage + i], acc2);
-      o[x] = o[x] * f + acc2 * sv;
+__device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
+
+// A bounded wait for one phase of a copy that this warp started.  Nothing but the
+// copy itself completes it, so the limit (seconds) is never met in a healthy run; a
+// warp that meets it records an error, waits no more and lets the kernel end.
+__device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity, bool& dead, int32_t* err) {
+  if (dead) return;
+  for (int i = 0; i < 4096; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+    if (ok) return;
+  }
+  atomicCAS(err, 0, (int)kDevTimeoutTmaProducer);
+  dead = true;
+}
+__device__ __forceinline__ void copy_page(uint32_t dst, const int8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"((uint64_t)src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Where global page x lies: rows are looked up 32 at a time, a lane each.
+struct Cursor {
+  int base;                 // row of lane 0
+  int64_t start;            // pages before it
+  int len;                  // this lane's row's length
+  int64_t end;              // pages up to and with this lane's row
+
+  __device__ void load(const Q8Geom& g, const int32_t* lens, int lane) {
+    const int r = base + lane;
+    len = r < g.rows ? safe_len(lens[r], g.max_pages) : 0;
+    int n = pages_of(len);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += y;
+    }
+    end = start + n;
+  }
+  // Row, page inside the row and length of the row of page x (below the total, not
+  // before an earlier call's).
+  __device__ void locate(const Q8Geom& g, const int32_t* lens, int lane, int64_t x, int& row, int& j, int& n) {
+    while (true) {
+      const uint32_t above = __ballot_sync(0xffffffffu, end > x);
+      if (above || base + 32 >= g.rows) {
+        const int at = above ? __ffs(above) - 1 : 31;
+        row = min(base + at, g.rows - 1);
+        n = __shfl_sync(0xffffffffu, len, at);
+        j = (int)(x - (__shfl_sync(0xffffffffu, end, at) - pages_of(n)));
+        return;
+      }
+      start = __shfl_sync(0xffffffffu, end, 31);
+      base += 32;
+      load(g, lens, lane);
     }
   }
-  T* out = (T*)a.out + b * a.o_sb + hq * a.o_sh;
-  for (int c = tid, x = 0; c < g.d; c += kThreads, ++x) store1(out + c, l == 0.f ? 0.f : o[x] / l);
+};
+
+template <int ND, typename T>
+__global__ void __launch_bounds__(32 * warps_of<ND>(), 1)
+q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, const int8_t* __restrict__ v_pages,
+                    const float2* __restrict__ scales, const int32_t* __restrict__ table,
+                    const int32_t* __restrict__ lens) {
+  constexpr int W = warps_of<ND>(), kThreads = 32 * W, kBytes = page_bytes<ND>(), kPitch = merge_pitch<ND>();
+  constexpr int KS = 4 * ND;                     // k steps of a logit, 16 columns each
+  constexpr int NT = 8 * ND;                     // 8-column tiles of the output
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[2 * W];
+  __shared__ long long s_scan[W];
+  __shared__ int64_t s_start;                    // pages before the CTA's first row
+  __shared__ int s_row, s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+  uint8_t* sK = smem + warp * 2 * kBytes;
+  uint8_t* sV = sK + kBytes;
+  float* sM = (float*)(smem + W * 2 * kBytes);   // [W][8][kPitch]
+  uint4* sQ = (uint4*)(sM + W * kMaxG * kPitch) + warp * KS * 32;
+  const uint32_t kbar = smem_u32(&bars[2 * warp]), vbar = smem_u32(&bars[2 * warp + 1]);
+  if (lane == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(kbar) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(vbar) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
+  // ---- this CTA's run [x0, x1) of the pages of all rows, and the row in which it begins
+  const int chunk = (g.rows + kThreads - 1) / kThreads;
+  const int c0 = min(g.rows, tid * chunk), c1 = min(g.rows, c0 + chunk);
+  long long mine = 0;
+  for (int r = c0; r < c1; ++r) mine += pages_of(safe_len(lens[r], g.max_pages));
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i == warp) before = total;
+    total += s_scan[i];
+  }
+  before += incl - mine;                         // pages before this thread's rows
+  // no more runs than pages: every CTA that shares a row has a part of it
+  const int64_t nc = total < gridDim.x ? total : gridDim.x;
+  const bool busy = blockIdx.x < nc;
+  const int64_t x0 = busy ? total * blockIdx.x / nc : 0, x1 = busy ? total * (blockIdx.x + 1) / nc : 0;
+  if (x0 < x1 && x0 >= before && x0 < before + mine) {
+    int64_t x = before;
+    int r = c0;
+    for (; r < c1 - 1; ++r) {
+      const int n = pages_of(safe_len(lens[r], g.max_pages));
+      if (x + n > x0) break;
+      x += n;
+    }
+    s_row = r;
+    s_start = x;
+  }
+  const int g0 = blockIdx.y * kMaxG, gn = min(kMaxG, a.G - g0);
+  // rows without a token
+  for (int r = blockIdx.x; r < g.rows; r += gridDim.x)
+    if (lens[r] <= 0)
+      for (int i = tid; i < gn * g.d; i += kThreads)
+        store1((T*)a.out + (r / g.Hkv) * a.o_sb + ((r % g.Hkv) * a.G + g0 + i / g.d) * a.o_sh + i % g.d, 0.f);
+  __syncthreads();
+  if (x0 >= x1) {
+    pdl_trigger();
+    return;
+  }
+
+  // ---- pages under way: [x] in the slots, [x + W] known by its index and scales, [x + 2 W] by its index
+  Cursor cur;
+  cur.base = s_row;
+  cur.start = s_start;
+  cur.load(g, lens, lane);
+  int64_t x = x0 + warp;
+  int j0 = 0, n0 = 0, j1 = 0, n1 = 0, row = 0;
+  int64_t page1 = 0;
+  float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
+  bool dead = false;
+  uint32_t phase = 0;
+  if (x < x1) {
+    cur.locate(g, lens, lane, x, row, j0, n0);
+    const int64_t page = safe_page(table[(int64_t)row * g.max_pages + j0], g.n_pages);
+    if (lane == 0) {
+      copy_page(smem_u32(sK), k_pages + page * kBytes, kBytes, kbar);
+      copy_page(smem_u32(sV), v_pages + page * kBytes, kBytes, vbar);
+    }
+    sc0 = scales[page];
+  }
+  if (x + W < x1) {
+    cur.locate(g, lens, lane, x + W, row, j1, n1);
+    page1 = safe_page(table[(int64_t)row * g.max_pages + j1], g.n_pages);
+  }
+
+  int r = s_row;                                 // segment by segment: the CTA's part of row r
+  int64_t xr = s_start;
+  while (true) {
+    const int len = safe_len(lens[r], g.max_pages), np = pages_of(len);
+    const int64_t sa = xr > x0 ? xr : x0, sb = xr + np < x1 ? xr + np : x1;
+    const int b = r / g.Hkv, hq = (r % g.Hkv) * a.G + g0;
+    if (sa < sb) {
+      // the query's fragments: columns 64 p + 16 t + 4 kk .. + 3 are the 16-byte piece of a key that lane t reads
+      float qs = 0.f;
+      uint4 qf[q_in_regs<ND>() ? KS : 1];
+      if (x < sb) {
+        float qv[KS][4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int c = (s >> 2) * 64 + t4 * 16 + (s & 3) * 4;
+          qv[s][0] = qv[s][1] = qv[s][2] = qv[s][3] = 0.f;
+          if (gid < gn && c < g.d) load4f((const T*)a.q + b * a.q_sb + (hq + gid) * a.q_sh + c, qv[s]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(qv[s][e]) & 0x7FFFFFFFu);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // scaled by a power of two into f16's best range, whatever the query's size
+        const int e2 = min(126, max(-126, (int)(top >> 23) - 127));
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        qs = a.alpha * __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint4 f;
+          split_half2(qv[s][0] * down, qv[s][1] * down, 2048.f, f.x, f.y);
+          split_half2(qv[s][2] * down, qv[s][3] * down, 2048.f, f.z, f.w);
+          if constexpr (q_in_regs<ND>()) qf[s] = f; else sQ[s * 32 + lane] = f;
+        }
+      }
+      float m = -INFINITY, l = 0.f, vref = 0.f;
+      float o[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+      while (x < sb) {
+        // indexes and scales of the pages to come
+        const bool more = x + W < x1, more2 = x + 2 * W < x1;
+        if (more) sc1 = scales[page1];
+        int j2 = 0, n2 = 0;
+        int64_t page2 = 0;
+        if (more2) {
+          cur.locate(g, lens, lane, x + 2 * W, row, j2, n2);
+          page2 = safe_page(table[(int64_t)row * g.max_pages + j2], g.n_pages);
+        }
+        wait_copy(kbar, phase, dead, a.err);
+        // S = Q K^T.  Column 2t + e of tile i is token 16 t + 2 i + e of the page: the tokens that lane t's
+        // 16-byte pieces of V hold
+        float s[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+          const int token = 16 * (gid >> 1) + 2 * i + (gid & 1);
+#pragma unroll
+          for (int p = 0; p < ND; ++p) {
+            const uint4 w = *(const uint4*)(sK + p * (kPage * 64) + token * 64 + t4 * 16);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              uint32_t b0, b1;
+              codes_to_f16(ww[kk], b0, b1);
+              uint4 f;
+              if constexpr (q_in_regs<ND>()) f = qf[4 * p + kk]; else f = sQ[(4 * p + kk) * 32 + lane];
+              mma16816(s[i], f, b0, b1);
+            }
+          }
+        }
+        __syncwarp();                            // every lane has read the slot
+        if (more && lane == 0 && !dead) copy_page(smem_u32(sK), k_pages + page1 * kBytes, kBytes, kbar);
+        // t = (high + low 2^-11) s_k scale; the running maximum; weights 2^(t - m + 14)
+        const float ts = sc0.x * qs;
+        const int left = n0 - j0 * kPage - 16 * t4;          // tokens of the row from this lane's first on
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[i][e] = 2 * i + e < left ? fmaf(s[i][2 + e], 1.f / 2048.f, s[i][e]) * ts : -INFINITY;
+            top = fmaxf(top, s[i][e]);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m, top), vn = fmaxf(vref, sc0.y);
+        const float ref = (mn == -INFINITY ? 0.f : mn) - kWeightScale;
+        const float f = ex2(m - mn) * (vref == vn ? 1.f : vref / vn);
+        if (m != -INFINITY) l *= ex2(m - mn);
+        // the values' scale relative to the largest so far goes into the weights
+        const float vr = sc0.y == 0.f ? 0.f : sc0.y / vn;
+        if (__any_sync(0xffffffffu, mn != m || vn != vref)) {
+          const float fo = m == -INFINITY ? 0.f : f;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o[i][0] *= fo;
+            o[i][1] *= fo;
+            o[i][2] *= fo;
+            o[i][3] *= fo;
+          }
+        }
+        m = mn;
+        vref = vn;
+        uint4 pf[4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = ex2(s[2 * kk + (e >> 1)][e & 1] - ref);
+            l += p;
+            w[e] = p * vr;
+          }
+          split_half2(w[0], w[1], 1.f, pf[kk].x, pf[kk].y);
+          split_half2(w[2], w[3], 1.f, pf[kk].z, pf[kk].w);
+        }
+        wait_copy(vbar, phase, dead, a.err);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint4 w = *(const uint4*)(sV + (8 * i + gid) * kPage + t4 * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            uint32_t b0, b1;
+            codes_to_f16(ww[kk], b0, b1);
+            mma16816(o[i], pf[kk], b0, b1);
+          }
+        }
+        __syncwarp();
+        if (more && lane == 0 && !dead) copy_page(smem_u32(sV), v_pages + page1 * kBytes, kBytes, vbar);
+        phase ^= 1;
+        x += W;
+        j0 = j1; n0 = n1; sc0 = sc1;
+        j1 = j2; n1 = n2; page1 = page2;
+      }
+
+      // ---- the warps' parts of the segment together
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      float* mw = sM + (warp * kMaxG + gid) * kPitch;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        mw[8 * i + 2 * t4] = (o[i][0] + o[i][2]) * vref;
+        mw[8 * i + 2 * t4 + 1] = (o[i][1] + o[i][3]) * vref;
+      }
+      if (t4 == 0) {
+        mw[64 * ND] = m;
+        mw[64 * ND + 1] = l;
+      }
+      __syncthreads();
+      const bool whole = sa == xr && sb == xr + np;
+      const int64_t first = ((xr + 1) * nc - 1) / total, last = ((xr + np) * nc - 1) / total;   // CTAs of the row
+      float* part = a.part + (int64_t)blockIdx.y * 2 * nc * kMaxG * kPitch;
+      for (int i = tid; i < gn * 64 * ND; i += kThreads) {
+        const int q = i / (64 * ND), c = i % (64 * ND);
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sM[(w * kMaxG + q) * kPitch + 64 * ND]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float* src = sM + (w * kMaxG + q) * kPitch;
+          const float f = ex2(src[64 * ND] - ref);
+          // a warp without a page of this row holds zeros and m = -inf
+          L += src[64 * ND + 1] * f;
+          acc += src[c] * f;
+        }
+        if (whole) {
+          if (c < g.d) store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L);
+        } else {
+          float* dst = part + ((2 * blockIdx.x + (sa > xr ? 0 : 1)) * kMaxG + q) * kPitch;
+          dst[c] = acc;
+          if (c == 0) {
+            dst[64 * ND] = M;
+            dst[64 * ND + 1] = L;
+          }
+        }
+      }
+      if (!whole) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          int32_t* count = a.arrived + (int64_t)blockIdx.y * g.rows + r;
+          s_last = atomicAdd(count, 1) == (int)(last - first);
+          if (s_last) *count = 0;                // as the next call expects it
+          __threadfence();
+        }
+        __syncthreads();
+        if (s_last) {
+          for (int i = tid; i < gn * g.d; i += kThreads) {
+            const int q = i / g.d, c = i % g.d;
+            float M = -INFINITY, L = 0.f, acc = 0.f;
+            for (int64_t k = first; k <= last; ++k)
+              M = fmaxf(M, __ldcg(part + ((2 * k + (k == first)) * kMaxG + q) * kPitch + 64 * ND));
+            const float ref = M == -INFINITY ? 0.f : M;
+            for (int64_t k = first; k <= last; ++k) {
+              const float* src = part + ((2 * k + (k == first)) * kMaxG + q) * kPitch;
+              const float f = ex2(__ldcg(src + 64 * ND) - ref);
+              L = fmaf(__ldcg(src + 64 * ND + 1), f, L);
+              acc = fmaf(__ldcg(src + c), f, acc);
+            }
+            store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L);
+          }
+        }
+      }
+      __syncthreads();                           // before the merge buffer is written again
+    }
+    xr += np;
+    if (xr >= x1) break;
+    ++r;
+  }
+  if (dead) {                                    // copies still under way land before the CTA's memory is released
+    bool gave_up = false;
+    wait_copy(kbar, phase, gave_up, a.err);
+    wait_copy(vbar, phase, gave_up, a.err);
+  }
   pdl_trigger();
 }
 
+template <int ND, typename T>
+cudaError_t launch(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_pages, const int8_t* v_pages,
+                   const float* scales, const int32_t* table, const int32_t* lens, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(q8_attention_kernel<ND, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem_bytes<ND>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, (a.G + kMaxG - 1) / kMaxG), dim3(32 * warps_of<ND>()),
+                    smem_bytes<ND>(), s, g, a, k_pages, v_pages, (const float2*)scales, table, lens);
+}
+
+template <typename T>
+cudaError_t launch_nd(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_pages, const int8_t* v_pages,
+                      const float* scales, const int32_t* table, const int32_t* lens, int grid, cudaStream_t s) {
+  switch (g.d64 / 64) {
+    case 1: return launch<1, T>(g, a, k_pages, v_pages, scales, table, lens, grid, s);
+    case 2: return launch<2, T>(g, a, k_pages, v_pages, scales, table, lens, grid, s);
+    case 3: return launch<3, T>(g, a, k_pages, v_pages, scales, table, lens, grid, s);
+    default: return launch<4, T>(g, a, k_pages, v_pages, scales, table, lens, grid, s);
+  }
+}
+
+size_t arrived_bytes(const Q8Geom& g, int groups) { return ((size_t)g.rows * groups * 4 + 255) / 256 * 256; }
+
 }  // namespace
 
-size_t q8_workspace_bytes(const Q8Geom& g, int G) { return 256; }
+// [header | arrival counters | partials], for a grid of one CTA per SM.
+size_t q8_workspace_bytes(const Q8Geom& g, int G, int sms) {
+  const int groups = (G + kMaxG - 1) / kMaxG;
+  return kHeader + arrived_bytes(g, groups) + (size_t)groups * 2 * sms * kMaxG * (g.d64 + 2) * 4;
+}
 
 cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
                                 int64_t q_sh, void* out, int64_t o_sb, int64_t o_sh, const int8_t* k_pages,
                                 const int8_t* v_pages, const float* scales, const int32_t* table, const int32_t* lens,
                                 void* ws, int sms, cudaStream_t s) {
-  Q8AttnArgs a = {q, out, q_sb, q_sh, o_sb, o_sh, alpha, G};
-  auto fn = bf16 ? q8_attention_kernel<__nv_bfloat16> : q8_attention_kernel<float>;
-  return launch_pdl(fn, dim3(g.rows, G), dim3(kThreads), 0, s, g, a, k_pages, v_pages, scales, table, lens);
+  char* w = (char*)ws;
+  const int groups = (G + kMaxG - 1) / kMaxG;
+  Q8AttnArgs a = {q, out, q_sb, q_sh, o_sb, o_sh, alpha, G, (int32_t*)w, (int32_t*)(w + kHeader),
+                  (float*)(w + kHeader + arrived_bytes(g, groups))};
+  if (bf16) return launch_nd<__nv_bfloat16>(g, a, k_pages, v_pages, scales, table, lens, sms, s);
+  return launch_nd<float>(g, a, k_pages, v_pages, scales, table, lens, sms, s);
 }
 
 }  // namespace chunkkv

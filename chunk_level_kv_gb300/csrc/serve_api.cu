@@ -20,7 +20,7 @@ cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const vo
 cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,
                            const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, void* k_out,
                            void* v_out, int64_t st_t, cudaStream_t s);
-size_t q8_workspace_bytes(const Q8Geom& g, int G);                                     // q8_attention.cu
+size_t q8_workspace_bytes(const Q8Geom& g, int G, int sms);                                   // q8_attention.cu
 cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
                                 int64_t q_sh, void* out, int64_t o_sb, int64_t o_sh, const int8_t* k_pages,
                                 const int8_t* v_pages, const float* scales, const int32_t* table, const int32_t* lens,
@@ -195,7 +195,7 @@ chunkkv_status chunkkv_q8_workspace_size(const chunkkv_q8_cache* c, int32_t G, s
   const chunkkv_status st = check_cache(c, false, &g);
   if (st != CHUNKKV_OK) return st;
   if (bytes == nullptr || G < 1) return CHUNKKV_ERR_INVALID_ARG;
-  *bytes = q8_workspace_bytes(g, G);
+  *bytes = q8_workspace_bytes(g, G, sm_count());
   return CHUNKKV_OK;
 }
 
@@ -214,7 +214,7 @@ chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, in
   if (G > 65535) return CHUNKKV_ERR_UNSUPPORTED;
   if (g.rows == 0) return CHUNKKV_OK;
   if (!aligned(q) || !aligned(out) || !aligned(ws)) return CHUNKKV_ERR_INVALID_ARG;
-  if (ws_bytes < q8_workspace_bytes(g, G)) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < q8_workspace_bytes(g, G, sm_count())) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
   return cuda_result(launch_q8_attention(g, dtype == CHUNKKV_BF16, G, (float)(scale * kLog2e), q, q_stride_b,
                                          q_stride_h, out, o_stride_b, o_stride_h, c->k_pages, c->v_pages, c->scales,
                                          c->table, c->lens, ws, sm_count(), (cudaStream_t)stream));
