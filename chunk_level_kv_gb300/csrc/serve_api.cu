@@ -12,6 +12,11 @@ int prefill_simt_tile();                                                        
 template <int MAXB>
 cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q,
                                 const void* k, const void* v, void* out, cudaStream_t s);
+int prefill_tc_rows();                                                                 // prefill_tc.cu
+template <int MAXB>
+cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int rows, int q_total, int k_total,
+                              const void* q, const void* k, const void* v, void* out, int32_t* err, int sms,
+                              cudaStream_t s);
 cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* lens, int32_t* table, int32_t* ring,
                              int32_t* state, int64_t* slots, int n_cap, int sms, cudaStream_t s);   // q8_cache.cu
 cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
@@ -64,6 +69,8 @@ chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
     if (!p->cu_q || !p->cu_k || p->cu_q[0] != 0 || p->cu_k[0] != 0) return CHUNKKV_ERR_INVALID_ARG;
     for (int b = 0; b < p->B; ++b)
       if (p->cu_q[b + 1] < p->cu_q[b] || p->cu_k[b + 1] < p->cu_k[b]) return CHUNKKV_ERR_INVALID_ARG;
+    // work items (at most one per 64 query rows, plus one per sequence, of each head) are counted in 32 bits
+    if (((int64_t)p->cu_q[p->B] / 64 + p->B) * p->Hq > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
   }
   return CHUNKKV_OK;
 }
@@ -90,12 +97,42 @@ void fill_table(const chunkkv_prefill_params* p, int tile, PrefillTable<MAXB>& t
   t.uoff[t.B] = u;
 }
 
+// The tensor-core kernel: bf16 rows of up to 128 columns that tensor maps can address (no axis
+// longer than 1 with stride 0, strides below 2^40 bytes), and a key to attend to.
+bool prefill_on_tc(const chunkkv_prefill_params* p) {
+  const int64_t most = (int64_t)1 << 39;
+  auto axis = [most](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < most); };
+  return p->dtype == CHUNKKV_BF16 && p->d <= 128 && p->B > 0 && p->cu_k[p->B] > 0 &&
+         axis(p->q_stride_t, p->cu_q[p->B]) && axis(p->q_stride_h, p->Hq) && axis(p->kv_stride_t, p->cu_k[p->B]) &&
+         axis(p->kv_stride_h, p->Hkv);
+}
+
+// Tensor maps address device memory only.
+bool device_pointer(const void* p) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return a.type == cudaMemoryTypeDevice;
+}
+
 template <int MAXB>
 cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, const void* q, const void* k,
-                        const void* v, void* out, cudaStream_t s) {
+                        const void* v, void* out, int32_t* err, cudaStream_t s) {
   static thread_local PrefillTable<MAXB> tab;
-  fill_table(p, prefill_simt_tile(), tab);
-  return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
+  if (!prefill_on_tc(p)) {
+    fill_table(p, prefill_simt_tile(), tab);
+    return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
+  }
+  const int sms = sm_count();
+  int rows = prefill_tc_rows();
+  fill_table(p, rows, tab);
+  if ((int64_t)tab.uoff[tab.B] * p->Hq < sms) {
+    rows /= 2;
+    fill_table(p, rows, tab);
+  }
+  return launch_prefill_tc(tab, g, rows, p->cu_q[p->B], p->cu_k[p->B], q, k, v, out, err, sms, s);
 }
 
 // The part of a cache that every call uses; `pages`: the call reads or writes them.
@@ -124,7 +161,10 @@ chunkkv_status chunkkv_prefill_workspace_size(const chunkkv_prefill_params* p, s
   return st;
 }
 
-int32_t chunkkv_prefill_path(const chunkkv_prefill_params* p) { return check_prefill(p) == CHUNKKV_OK ? 0 : -1; }
+int32_t chunkkv_prefill_path(const chunkkv_prefill_params* p) {
+  if (check_prefill(p) != CHUNKKV_OK) return -1;
+  return prefill_on_tc(p) ? 1 : 0;
+}
 
 chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const void* q, const void* k, const void* v,
                                          void* out, void* ws, size_t ws_bytes, chunkkv_stream_t stream) {
@@ -136,11 +176,12 @@ chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const 
   if (!aligned(q) || !aligned(out) || !aligned(ws) || (!no_keys && (!aligned(k) || !aligned(v))))
     return CHUNKKV_ERR_INVALID_ARG;
   if (ws_bytes < kServeHeader) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  if (prefill_on_tc(p) && !(device_pointer(q) && device_pointer(k) && device_pointer(v))) return CHUNKKV_ERR_INVALID_ARG;
   PrefillGeom g = {p->Hq, p->Hkv, p->Hq / p->Hkv, p->d, (float)(p->scale * kLog2e), p->q_stride_t, p->q_stride_h,
                    p->kv_stride_t, p->kv_stride_h, p->o_stride_t, p->o_stride_h};
   const cudaStream_t cs = (cudaStream_t)stream;
-  return cuda_result(p->B <= kSmallBatch ? run_prefill<kSmallBatch>(p, g, q, k, v, out, cs)
-                                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, q, k, v, out, cs));
+  return cuda_result(p->B <= kSmallBatch ? run_prefill<kSmallBatch>(p, g, q, k, v, out, (int32_t*)ws, cs)
+                                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, q, k, v, out, (int32_t*)ws, cs));
 }
 
 chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
