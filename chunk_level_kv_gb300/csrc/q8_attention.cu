@@ -32,6 +32,7 @@ namespace chunkkv {
 namespace {
 
 constexpr int kMaxG = 8;                         // query heads per pass
+constexpr int kMaxGrid = 256;                    // CTAs of a pass (one per SM)
 constexpr float kWeightScale = 14.f;             // weights are 2^(t - m + 14): f16 keeps them to 2^-38 of the largest
 constexpr size_t kHeader = 256;                  // device error word
 
@@ -43,8 +44,13 @@ struct Q8AttnArgs {
   int32_t G;
   int32_t* err;
   int32_t* arrived;                              // [groups][rows] partials written, zero between calls
-  float* part;                                   // [groups][2 CTAs][8][d64 + 2]
+  float* part;                                   // [groups][2 CTAs][8][d64 + 4]: O, m, l
 };
+
+// Rows of up to this many pages are not cut: a row in two pieces costs the CTAs that
+// share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's
+// share of the bandwidth, and the eight warps take eight pages at once.
+constexpr int kWholeRow = 8;
 
 template <int ND>
 constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
@@ -52,6 +58,8 @@ template <int ND>
 constexpr int page_bytes() { return ND * 64 * kPage; }
 template <int ND>
 constexpr int merge_pitch() { return 64 * ND + 2; }         // O, then m and l
+template <int ND>
+constexpr int part_pitch() { return 64 * ND + 4; }          // the same in the workspace, in 16-byte rows
 template <int ND>
 constexpr bool q_in_regs() { return ND <= 2; }              // wider heads keep their query fragments in shared memory
 template <int ND>
@@ -107,6 +115,12 @@ __device__ __forceinline__ void load4f(const __nv_bfloat16* p, float (&x)[4]) {
 }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *(float4*)p = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+  *(uint2*)p = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+}
 
 __device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
 
@@ -174,13 +188,14 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
                     const float2* __restrict__ scales, const int32_t* __restrict__ table,
                     const int32_t* __restrict__ lens) {
   constexpr int W = warps_of<ND>(), kThreads = 32 * W, kBytes = page_bytes<ND>(), kPitch = merge_pitch<ND>();
+  constexpr int kPart = part_pitch<ND>();
   constexpr int KS = 4 * ND;                     // k steps of a logit, 16 columns each
   constexpr int NT = 8 * ND;                     // 8-column tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[2 * W];
   __shared__ long long s_scan[W];
-  __shared__ int64_t s_start;                    // pages before the CTA's first row
-  __shared__ int s_row, s_last;
+  __shared__ int64_t s_cut[2], s_start[2];       // the run's ends, and the pages before the rows that they lie in
+  __shared__ int s_row[2], s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
   uint8_t* sK = smem + warp * 2 * kBytes;
   uint8_t* sV = sK + kBytes;
@@ -217,17 +232,23 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
   // no more runs than pages: every CTA that shares a row has a part of it
   const int64_t nc = total < gridDim.x ? total : gridDim.x;
   const bool busy = blockIdx.x < nc;
-  const int64_t x0 = busy ? total * blockIdx.x / nc : 0, x1 = busy ? total * (blockIdx.x + 1) / nc : 0;
-  if (x0 < x1 && x0 >= before && x0 < before + mine) {
-    int64_t x = before;
-    int r = c0;
-    for (; r < c1 - 1; ++r) {
-      const int n = pages_of(safe_len(lens[r], g.max_pages));
-      if (x + n > x0) break;
-      x += n;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t cut = busy ? total * (blockIdx.x + k) / nc : total;
+    if (cut == total) {
+      if (tid == 0) s_cut[k] = total;
+    } else if (cut >= before && cut < before + mine) {
+      int64_t x = before;
+      int r = c0, n = 0;
+      for (; r < c1; ++r) {
+        n = pages_of(safe_len(lens[r], g.max_pages));
+        if (x + n > cut) break;
+        x += n;
+      }
+      s_cut[k] = n <= kWholeRow ? x : cut;       // short rows stay in one piece
+      s_row[k] = r;
+      s_start[k] = x;
     }
-    s_row = r;
-    s_start = x;
   }
   const int g0 = blockIdx.y * kMaxG, gn = min(kMaxG, a.G - g0);
   // rows without a token
@@ -236,6 +257,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       for (int i = tid; i < gn * g.d; i += kThreads)
         store1((T*)a.out + (r / g.Hkv) * a.o_sb + ((r % g.Hkv) * a.G + g0 + i / g.d) * a.o_sh + i % g.d, 0.f);
   __syncthreads();
+  const int64_t x0 = s_cut[0], x1 = s_cut[1];
   if (x0 >= x1) {
     pdl_trigger();
     return;
@@ -243,8 +265,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
 
   // ---- pages under way: [x] in the slots, [x + W] known by its index and scales, [x + 2 W] by its index
   Cursor cur;
-  cur.base = s_row;
-  cur.start = s_start;
+  cur.base = s_row[0];
+  cur.start = s_start[0];
   cur.load(g, lens, lane);
   int64_t x = x0 + warp;
   int j0 = 0, n0 = 0, j1 = 0, n1 = 0, row = 0;
@@ -266,8 +288,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
     page1 = safe_page(table[(int64_t)row * g.max_pages + j1], g.n_pages);
   }
 
-  int r = s_row;                                 // segment by segment: the CTA's part of row r
-  int64_t xr = s_start;
+  int r = s_row[0];                              // segment by segment: the CTA's part of row r
+  int64_t xr = s_start[0];
   while (true) {
     const int len = safe_len(lens[r], g.max_pages), np = pages_of(len);
     const int64_t sa = xr > x0 ? xr : x0, sb = xr + np < x1 ? xr + np : x1;
@@ -420,7 +442,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       __syncthreads();
       const bool whole = sa == xr && sb == xr + np;
       const int64_t first = ((xr + 1) * nc - 1) / total, last = ((xr + np) * nc - 1) / total;   // CTAs of the row
-      float* part = a.part + (int64_t)blockIdx.y * 2 * nc * kMaxG * kPitch;
+      float* part = a.part + (int64_t)blockIdx.y * 2 * nc * kMaxG * kPart;
       for (int i = tid; i < gn * 64 * ND; i += kThreads) {
         const int q = i / (64 * ND), c = i % (64 * ND);
         float M = -INFINITY;
@@ -439,7 +461,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         if (whole) {
           if (c < g.d) store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L);
         } else {
-          float* dst = part + ((2 * blockIdx.x + (sa > xr ? 0 : 1)) * kMaxG + q) * kPitch;
+          float* dst = part + ((2 * blockIdx.x + (sa > xr ? 0 : 1)) * kMaxG + q) * kPart;
           dst[c] = acc;
           if (c == 0) {
             dst[64 * ND] = M;
@@ -458,19 +480,66 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         }
         __syncthreads();
         if (s_last) {
-          for (int i = tid; i < gn * g.d; i += kThreads) {
-            const int q = i / g.d, c = i % g.d;
-            float M = -INFINITY, L = 0.f, acc = 0.f;
-            for (int64_t k = first; k <= last; ++k)
-              M = fmaxf(M, __ldcg(part + ((2 * k + (k == first)) * kMaxG + q) * kPitch + 64 * ND));
+          // factors 2^(m - M) of the parts and the sums, then O: 16 bytes of a part per thread and step, the
+          // parts dealt to as many groups of threads as there are, the groups' sums added in order
+          const int np2 = (int)(last - first) + 1, ne = gn * (16 * ND);
+          float* sF = sM;                        // [np2][kMaxG]
+          float4* sA = (float4*)(sM + (size_t)W * kMaxG * kPitch - 4 * kThreads);   // [groups][ne]
+          static_assert(W * kMaxG * kPitch - 4 * kThreads >= kMaxG * kMaxGrid, "a factor for every part");
+          auto src = [&](int k, int q) { return part + ((2 * (first + k) + (k == 0)) * kMaxG + q) * kPart; };
+          __shared__ float s_sum[kMaxG];
+          for (int q = warp; q < gn; q += W) {
+            float M = -INFINITY;
+            for (int k = lane; k < np2; k += 32) M = fmaxf(M, __ldcg(src(k, q) + 64 * ND));
+#pragma unroll
+            for (int o2 = 16; o2; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
             const float ref = M == -INFINITY ? 0.f : M;
-            for (int64_t k = first; k <= last; ++k) {
-              const float* src = part + ((2 * k + (k == first)) * kMaxG + q) * kPitch;
-              const float f = ex2(__ldcg(src + 64 * ND) - ref);
-              L = fmaf(__ldcg(src + 64 * ND + 1), f, L);
-              acc = fmaf(__ldcg(src + c), f, acc);
+            float L = 0.f;
+            for (int k = lane; k < np2; k += 32) {
+              const float f = ex2(__ldcg(src(k, q) + 64 * ND) - ref);
+              sF[k * kMaxG + q] = f;
+              L = fmaf(__ldcg(src(k, q) + 64 * ND + 1), f, L);
             }
-            store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L);
+#pragma unroll
+            for (int o2 = 16; o2; o2 >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o2);
+            if (lane == 0) s_sum[q] = L;
+          }
+          __syncthreads();
+          const int ng = max(1, kThreads / ne);
+          for (int i = tid; i < ne * ng; i += kThreads) {
+            const int e = i % ne, grp = i / ne, q = e / (16 * ND), c = (e % (16 * ND)) * 4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = grp; k < np2; k += ng) {
+              const float4 v = __ldcg((const float4*)(src(k, q) + c));
+              const float f = sF[k * kMaxG + q];
+              acc.x = fmaf(v.x, f, acc.x);
+              acc.y = fmaf(v.y, f, acc.y);
+              acc.z = fmaf(v.z, f, acc.z);
+              acc.w = fmaf(v.w, f, acc.w);
+            }
+            if (ng > 1) {
+              sA[i] = acc;
+            } else {
+              T* dst = (T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c;
+              const float L = s_sum[q];
+              if (c < g.d) store4(dst, make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L));
+            }
+          }
+          if (ng > 1) {
+            __syncthreads();
+            if (tid < ne) {
+              float4 acc = sA[tid];
+              for (int grp = 1; grp < ng; ++grp) {
+                const float4 v = sA[grp * ne + tid];
+                acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+              }
+              const int q = tid / (16 * ND), c = (tid % (16 * ND)) * 4;
+              const float L = s_sum[q];
+              if (c < g.d)
+                store4((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c,
+                       make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L));
+            }
           }
         }
       }
@@ -516,7 +585,7 @@ size_t arrived_bytes(const Q8Geom& g, int groups) { return ((size_t)g.rows * gro
 // [header | arrival counters | partials], for a grid of one CTA per SM.
 size_t q8_workspace_bytes(const Q8Geom& g, int G, int sms) {
   const int groups = (G + kMaxG - 1) / kMaxG;
-  return kHeader + arrived_bytes(g, groups) + (size_t)groups * 2 * sms * kMaxG * (g.d64 + 2) * 4;
+  return kHeader + arrived_bytes(g, groups) + (size_t)groups * 2 * (sms < kMaxGrid ? sms : kMaxGrid) * kMaxG * (g.d64 + 4) * 4;
 }
 
 cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
@@ -524,6 +593,7 @@ cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, 
                                 const int8_t* v_pages, const float* scales, const int32_t* table, const int32_t* lens,
                                 void* ws, int sms, cudaStream_t s) {
   char* w = (char*)ws;
+  sms = sms < kMaxGrid ? sms : kMaxGrid;
   const int groups = (G + kMaxG - 1) / kMaxG;
   Q8AttnArgs a = {q, out, q_sb, q_sh, o_sb, o_sh, alpha, G, (int32_t*)w, (int32_t*)(w + kHeader),
                   (float*)(w + kHeader + arrived_bytes(g, groups))};
