@@ -180,8 +180,8 @@ prefill_simt_kernel(const __grid_constant__ PrefillTable<MAXB> tab, PrefillGeom 
 template <int ND, typename T, int MAXB>
 cudaError_t launch(const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q, const void* k, const void* v,
                    void* out, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<ND, T, MAXB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem_bytes<ND>());
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(prefill_simt_kernel<ND, T, MAXB>, (int)smem_bytes<ND>(), done);
   if (e != cudaSuccess) return e;
   return launch_pdl(prefill_simt_kernel<ND, T, MAXB>, dim3(tab.uoff[tab.B], g.Hq), dim3(kThreads), smem_bytes<ND>(), s,
                     tab, g, (const T*)q, (const T*)k, (const T*)v, (T*)out);

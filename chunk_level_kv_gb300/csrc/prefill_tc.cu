@@ -551,8 +551,8 @@ bool encode(EncodeFn enc, CUtensorMap* map, const void* base, int d, int heads, 
 template <int D, int MAXB>
 cudaError_t launch(const TcMaps& maps, const TcGeom& g, const PrefillTable<MAXB>& tab, const void* v, void* out,
                    int32_t* err, int sms, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<D, MAXB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem_bytes<D>());
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(prefill_tc_kernel<D, MAXB>, smem_bytes<D>(), done);
   if (e != cudaSuccess) return e;
   return launch_pdl(prefill_tc_kernel<D, MAXB>, dim3(std::min(g.n_items, sms)), dim3(kThreads), (size_t)smem_bytes<D>(), s,
                     maps, g, tab, (const __nv_bfloat16*)v, (__nv_bfloat16*)out, err, err + kSchedWord);

@@ -50,7 +50,11 @@ struct Q8AttnArgs {
 // Rows of up to this many pages are not cut: a row in two pieces costs the CTAs that
 // share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's
 // share of the bandwidth, and the eight warps take eight pages at once.
+// A cut within kNearEnd pages of a long row's begin or end moves there, so that a CTA
+// seldom has a second row for a few pages.
 constexpr int kWholeRow = 8;
+constexpr int kNearEnd = 3;
+static_assert(kWholeRow > 2 * kNearEnd, "a row's two ends do not meet");
 
 template <int ND>
 constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
@@ -245,7 +249,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         if (x + n > cut) break;
         x += n;
       }
-      s_cut[k] = n <= kWholeRow ? x : cut;       // short rows stay in one piece
+      // short rows stay in one piece, and a long one's end is no place to cut either
+      s_cut[k] = n <= kWholeRow || cut - x <= kNearEnd ? x : x + n - cut <= kNearEnd ? x + n : cut;
       s_row[k] = r;
       s_start[k] = x;
     }
@@ -441,7 +446,9 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       }
       __syncthreads();
       const bool whole = sa == xr && sb == xr + np;
-      const int64_t first = ((xr + 1) * nc - 1) / total, last = ((xr + np) * nc - 1) / total;   // CTAs of the row
+      // the CTAs of a row that is cut: from the last one whose cut is at its begin or moves there, to the last
+      // one whose cut does not move to its end
+      const int64_t first = ((xr + kNearEnd + 1) * nc - 1) / total, last = ((xr + np - kNearEnd) * nc - 1) / total;
       float* part = a.part + (int64_t)blockIdx.y * 2 * nc * kMaxG * kPart;
       for (int i = tid; i < gn * 64 * ND; i += kThreads) {
         const int q = i / (64 * ND), c = i % (64 * ND);
@@ -560,8 +567,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
 template <int ND, typename T>
 cudaError_t launch(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_pages, const int8_t* v_pages,
                    const float* scales, const int32_t* table, const int32_t* lens, int grid, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(q8_attention_kernel<ND, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem_bytes<ND>());
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(q8_attention_kernel<ND, T>, (int)smem_bytes<ND>(), done);
   if (e != cudaSuccess) return e;
   return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, (a.G + kMaxG - 1) / kMaxG), dim3(32 * warps_of<ND>()),
                     smem_bytes<ND>(), s, g, a, k_pages, v_pages, (const float2*)scales, table, lens);

@@ -16,6 +16,7 @@ namespace {
 // ------------------------------------------------------------ tables and slot maps
 
 constexpr int kResizeThreads = 1024;
+constexpr int kSlotRun = 1024;                  // tokens of a row that a warp maps: 17 pages at most, a lane each
 
 __device__ __forceinline__ int pages_of(int n) { return n > 0 ? (n - 1) / kPage + 1 : 0; }
 
@@ -110,19 +111,24 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
       }
     }
   }
-  // slots: pages that the row had from the table, the others straight from the ring
+  // slots: a warp per run of kSlotRun tokens of a row.  Its lanes hold the run's pages (those that the row had
+  // from the table, the others straight from the ring), and every step writes 64 slots.
   if (slots) {
-    for (int r = r0; r < r1; ++r) {
+    const int runs = (n_cap + kSlotRun - 1) / kSlotRun, lane = tid & 31;
+    for (int w = tid >> 5; w < (r1 - r0) * runs; w += kResizeThreads / 32) {
+      const int r = r0 + w / runs, i0 = w % runs * kSlotRun, i1 = min(n_cap, i0 + kSlotRun);
       const int n = lens[r], m = new_lens[r], have = pages_of(n);
-      const int32_t* row = table + (int64_t)r * g.max_pages;
-      for (int i = tid; i < n_cap; i += kResizeThreads) {
-        int64_t slot = -1;
-        if (ok && i < m - n) {
-          const int pos = n + i, j = pos / kPage;
-          const int32_t page = j < have ? row[j] : ring[wrap(head + s_off[r - r0] + (j - have), g.n_pages)];
-          slot = (int64_t)page * kPage + pos % kPage;
-        }
-        slots[(int64_t)r * n_cap + i] = slot;
+      const int added = ok ? m - n : 0;
+      int64_t* row_slots = slots + (int64_t)r * n_cap;
+      int32_t page = -1;
+      const int first = (n + i0) / kPage, j = first + lane;     // i0 < added makes these positions of the row
+      if (i0 < added && j < pages_of(m))
+        page = j < have ? table[(int64_t)r * g.max_pages + j] : ring[wrap(head + s_off[r - r0] + (j - have), g.n_pages)];
+#pragma unroll 2
+      for (int i = i0 + lane; i - lane < i1; i += 32) {
+        const int pos = n + i;
+        const int32_t p = __shfl_sync(0xffffffffu, page, i < added ? pos / kPage - first : 0);
+        if (i < i1) row_slots[i] = i < added ? (int64_t)p * kPage + pos % kPage : -1;
       }
     }
   }
@@ -154,24 +160,32 @@ constexpr int kIoThreads = 256;
 constexpr float kInv127 = 1.0f / 127.0f;
 constexpr float kSmallest = 7.888609052210118e-31f;          // 2^-100: below it a block counts as zero
 
+// Eight elements of a row as they lie in memory, and one of them as fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+struct Vec8;
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *(const uint4*)p;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Vec8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) { a = ((const float4*)p)[0]; b = ((const float4*)p)[1]; }
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
-}
+};
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 v;
+  __device__ void load(const __nv_bfloat16* p) { v = *(const uint4*)p; }
+  __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
   *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -184,6 +198,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     w[i] = *(const uint32_t*)&b;
   }
   *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 4 x 4 bytes of four words transposed: byte b of word i goes to byte i of word b.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, b, 0x5410);
+  w[1] = __byte_perm(a, b, 0x7632);
+  w[2] = __byte_perm(c, d, 0x5410);
+  w[3] = __byte_perm(c, d, 0x7632);
 }
 
 // Rounded to the nearest code, ties to even; NaN (0 x inf of a block with an
@@ -207,40 +231,47 @@ struct AppendArgs {
 };
 
 // One CTA writes the part of one page that a row's new tokens fill, of the keys
-// (blockIdx.z 0) or of the values (1): the tokens into shared memory, their largest
-// magnitude, the page's scale, and the codes.  A page that already holds tokens
-// keeps its scale unless the new tokens are larger; then its codes are rounded again
-// for the new one.
-template <typename T>
+// (blockIdx.z 0) or of the values (1).  Its threads hold the tokens in registers while
+// the largest magnitude, and from it the page's scale, is found; a page that already
+// holds tokens keeps its scale unless the new ones are larger, else its codes are
+// rounded again for the new one.  Keys are written as they were read, 8 bytes a
+// vector; values go through shared memory as codes and leave in 16-token pieces of a
+// column, the bytes transposed 4 x 4 in registers.
+template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 append_kernel(Q8Geom g, AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
               float* __restrict__ scales) {
-  extern __shared__ float tile[];                             // [64][d64 + 1]
+  constexpr int kV8 = 8 * ND, kVecs = kPage * kV8 / kIoThreads;      // vectors of a row, and of a thread
+  constexpr int kPitch = 64 * ND + 4;                                // bytes of a token's codes in shared memory
   __shared__ uint32_t s_top[kIoThreads / 32];
+  __shared__ __align__(16) uint8_t s_code[kPage * kPitch];
   pdl_wait();
   const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
-  const int n = min(max(counts[r], 0), a.n_cap);
   const int64_t* row_slots = slots + (int64_t)r * a.n_cap;
-  const int off0 = n > 0 ? (int)(row_slots[0] & (kPage - 1)) : 0;
+  const int n = min(max(counts[r], 0), a.n_cap);
+  const int off0 = (int)(row_slots[0] & (kPage - 1));
   const int i0 = max(0, (int)blockIdx.x * kPage - off0), i1 = min(n, ((int)blockIdx.x + 1) * kPage - off0);
-  const int64_t slot = i0 < i1 ? row_slots[i0] : -1;
-  const int64_t page = slot >> 6;
-  if (slot >= 0 && page < g.n_pages) {                        // the same for the whole CTA
+  if (i0 < i1) {                                                     // the same for the whole CTA
+    const int64_t slot = row_slots[i0];
+    const T* x = (const T*)(which ? a.x[1] : a.x[0]) + (r / g.Hkv) * a.st_b + (r % g.Hkv) * a.st_h + i0 * a.st_t;
     const int t0 = (int)(slot & (kPage - 1)), nt = min(i1 - i0, kPage - t0);
-    const int pitch = g.d64 + 1;
-    const T* x = (const T*)a.x[which] + (r / g.Hkv) * a.st_b + (r % g.Hkv) * a.st_h + i0 * a.st_t;
+    const int64_t page = slot >> 6;
+    Vec8<T> raw[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int t = (i * kIoThreads + tid) / kV8, c = (i * kIoThreads + tid) % kV8 * 8;
+      if (t < nt && c < g.d) raw[i].load(x + t * a.st_t + c); else raw[i].zero();
+    }
+    const bool inside = slot >= 0 && page < g.n_pages;
+    const float before = t0 == 0 || !inside ? 0.f : scales[page * 2 + which];
     // magnitudes compared as bit patterns: a NaN is above infinity and ends in the scale
     uint32_t top = 0;
-    const int v8 = g.d64 / 8;
-    for (int i = tid; i < nt * v8; i += kIoThreads) {
-      const int t = i / v8, c = (i % v8) * 8;
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < g.d) load8(x + t * a.st_t + c, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        top = max(top, __float_as_uint(w[e]) & 0x7FFFFFFFu);
-        tile[t * pitch + c + e] = w[e];
-      }
+    for (int i = 0; i < kVecs; ++i) {
+      float w[8];
+      raw[i].get(w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(w[e]) & 0x7FFFFFFFu);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((tid & 31) == 0) s_top[tid >> 5] = top;
@@ -249,64 +280,73 @@ append_kernel(Q8Geom g, AppendArgs a, const int32_t* __restrict__ counts, const 
     for (int i = 0; i < kIoThreads / 32; ++i) top = max(top, s_top[i]);
     const float amax = __uint_as_float(top);
     const float grown = amax < kSmallest ? 0.f : amax * kInv127;
-    const float before = t0 == 0 ? 0.f : scales[page * 2 + which];
     const float scale = grown > before || grown != grown ? grown : before;   // a NaN scale stays one
     const float ratio = scale != before ? __fdiv_rn(before, scale) : 1.f;
     const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-    const bool again = t0 > 0 && ratio != 1.f;                // older codes of the page to be rounded again
-    int8_t* pg = a.pages[which] + page * (int64_t)(g.d64 * kPage);
-    if (which == 0) {
-      if (again)
-        for (int i = tid; i < t0 * (g.d64 / 16); i += kIoThreads) {
-          const int t = i % t0, c = i / t0;                   // 16 columns of an older token
+    const bool again = t0 > 0 && ratio != 1.f;                       // older codes of the page to be rounded again
+    int8_t* pg = (which ? a.pages[1] : a.pages[0]) + page * (int64_t)(64 * ND * kPage);
+    if (inside) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int t = (i * kIoThreads + tid) / kV8, c = (i * kIoThreads + tid) % kV8 * 8;
+        float w[8];
+        raw[i].get(w);
+        uint32_t q[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e >> 2] |= ((uint32_t)code_of(w[e] * inv) & 0xFFu) << (8 * (e & 3));
+        if (which == 0) {
+          if (t < nt) *(uint2*)(pg + (c >> 6) * (kPage * 64) + (t0 + t) * 64 + (c & 63)) = make_uint2(q[0], q[1]);
+        } else if (t < nt) {
+          uint32_t* dst = (uint32_t*)(s_code + (t0 + t) * kPitch + c);
+          dst[0] = q[0];
+          dst[1] = q[1];
+        }
+      }
+      if (which == 0 && again)
+        for (int i = tid; i < t0 * (4 * ND); i += kIoThreads) {
+          const int t = i % t0, c = i / t0;                          // 16 columns of an older token
           uint4* p = (uint4*)(pg + (c / 4) * (kPage * 64) + t * 64 + (c % 4) * 16);
           uint4 w = *p;
           w.x = recode(w.x, ratio); w.y = recode(w.y, ratio); w.z = recode(w.z, ratio); w.w = recode(w.w, ratio);
           *p = w;
         }
-      const int v16 = g.d64 / 16;
-      for (int i = tid; i < nt * v16; i += kIoThreads) {
-        const int t = i / v16, c = i % v16;
-        const float* src = tile + t * pitch + c * 16;
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            w[e] |= ((uint32_t)code_of(src[4 * e + b] * inv) & 0xFFu) << (8 * b);
-        }
-        *(uint4*)(pg + (c / 4) * (kPage * 64) + (t0 + t) * 64 + (c % 4) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      // 16 tokens of a column per thread; vectors that the new tokens fill in part keep their other bytes
-      for (int i = tid; i < g.d64 * 4; i += kIoThreads) {
-        const int c = i >> 2, base = (i & 3) * 16;
+      if (tid == 0 && (scale != before || t0 == 0)) scales[page * 2 + which] = scale;
+    }
+    if (which == 1) {
+      __syncthreads();
+      for (int i = tid; inside && i < 16 * ND * 4; i += kIoThreads) {
+        const int c = (i >> 2) * 4, base = (i & 3) * 16;             // 4 columns, 16 tokens
         const bool touched = base < t0 + nt && base + 16 > t0;
         if (!touched && !(again && base < t0)) continue;
-        uint4* p = (uint4*)(pg + c * kPage + base);
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (base < t0 || base + 16 > t0 + nt) {
-          const uint4 o = *p;
-          w[0] = o.x; w[1] = o.y; w[2] = o.z; w[3] = o.w;
-          if (again && base < t0) {
+        const bool part = base < t0 || base + 16 > t0 + nt;          // other tokens' bytes are kept
+        uint32_t w[4][4];                                            // [4 tokens each][word: 4 columns, then 4 tokens]
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = recode(w[e], ratio);
-          }
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) w[e][b] = *(const uint32_t*)(s_code + (base + 4 * e + b) * kPitch + c);
+          transpose4(w[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = base + e - t0;
-          if (t >= 0 && t < nt) {
-            const uint32_t q = (uint32_t)code_of(tile[t * pitch + c] * inv) & 0xFFu;
-            w[e >> 2] = (w[e >> 2] & ~(0xFFu << (8 * (e & 3)))) | (q << (8 * (e & 3)));
+        for (int b = 0; b < 4; ++b) {
+          uint4* p = (uint4*)(pg + (c + b) * kPage + base);
+          uint32_t o[4] = {w[0][b], w[1][b], w[2][b], w[3][b]};
+          if (part) {
+            const uint4 old4 = *p;
+            uint32_t old[4] = {old4.x, old4.y, old4.z, old4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (again) old[e] = recode(old[e], ratio);
+              uint32_t keep = 0;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (base + 4 * e + z < t0 || base + 4 * e + z >= t0 + nt) keep |= 0xFFu << (8 * z);
+              o[e] = (o[e] & ~keep) | (old[e] & keep);
+            }
           }
+          *p = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *p = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    if (tid == 0 && scale != before) scales[page * 2 + which] = scale;
-    if (tid == 0 && t0 == 0) scales[page * 2 + which] = scale;
   }
   pdl_trigger();
 }
@@ -326,7 +366,8 @@ template <typename T>
 __global__ void __launch_bounds__(kIoThreads)
 load_kernel(Q8Geom g, LoadArgs a, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
             const float* __restrict__ scales, const int64_t* __restrict__ start) {
-  extern __shared__ int8_t bytes[];                           // values: [d64][64 + 4]
+  constexpr int kPitch = kPage + 4;                           // bytes of a column in shared memory
+  extern __shared__ __align__(16) uint8_t bytes[];            // values: [d64][kPitch]
   pdl_wait();
   const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, j = blockIdx.x;
   const int n = min(safe_len(lens[r], g.max_pages), a.n_cap);
@@ -335,33 +376,60 @@ load_kernel(Q8Geom g, LoadArgs a, const int32_t* __restrict__ table, const int32
   if (nt > 0 && at >= 0) {
     const int64_t page = safe_page(table[(int64_t)r * g.max_pages + j], g.n_pages);
     const float scale = scales[page * 2 + which];
-    const int8_t* pg = a.pages[which] + page * (int64_t)(g.d64 * kPage);
-    T* out = (T*)a.out[which] + (at + j * kPage) * a.st_t;
-    constexpr int kPitch = kPage + 4;
-    if (which == 1) {
+    const int8_t* pg = (which ? a.pages[1] : a.pages[0]) + page * (int64_t)(g.d64 * kPage);
+    T* out = (T*)(which ? a.out[1] : a.out[0]) + (at + j * kPage) * a.st_t;
+    const int v8 = g.d / 8;
+    if (which == 0) {
+#pragma unroll 4
+      for (int i = tid; i < nt * v8; i += kIoThreads) {
+        const int t = i / v8, c = (i % v8) * 8;
+        const uint2 w = *(const uint2*)(pg + (c >> 6) * (kPage * 64) + t * 64 + (c & 63));
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * scale;
+        store8(out + t * a.st_t + c, x);
+      }
+    } else {
+#pragma unroll 2
       for (int i = tid; i < g.d64 * 4; i += kIoThreads) {
         const uint4 w = *(const uint4*)(pg + i * 16);
         uint32_t* dst = (uint32_t*)(bytes + (i >> 2) * kPitch + (i & 3) * 16);
         dst[0] = w.x; dst[1] = w.y; dst[2] = w.z; dst[3] = w.w;
       }
       __syncthreads();
-    }
-    const int v8 = g.d / 8;
-    for (int i = tid; i < nt * v8; i += kIoThreads) {
-      const int t = i / v8, c = (i % v8) * 8;
-      float x[8];
-      if (which == 0) {
-        const uint2 w = *(const uint2*)(pg + (c >> 6) * (kPage * 64) + t * 64 + (c & 63));
+      for (int i = tid; i < v8 * 16; i += kIoThreads) {
+        const int c = i % v8 * 8, t = i / v8 * 4;             // 8 columns, 4 tokens
+        if (t >= nt) continue;
+        uint32_t w[2][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * scale;
-      } else {
+        for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = *(const uint32_t*)(bytes + (c + e) * kPitch + t);
+        transpose4(w[0]);
+        transpose4(w[1]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)bytes[(c + e) * kPitch + t] * scale;
+        for (int k = 0; k < 4; ++k) {
+          if (t + k >= nt) break;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)(w[e >> 2][k] >> (8 * (e & 3))) * scale;
+          store8(out + (t + k) * a.st_t + c, x);
+        }
       }
-      store8(out + t * a.st_t + c, x);
     }
   }
   pdl_trigger();
+}
+
+template <typename T>
+cudaError_t launch_append(const Q8Geom& g, const AppendArgs& a, const int32_t* counts, const int64_t* slots,
+                          float* scales, cudaStream_t s) {
+  // n_cap tokens that begin anywhere in a page touch this many pages
+  const dim3 grid((a.n_cap + 2 * (kPage - 1)) / kPage, g.rows, 2);
+  switch (g.d64 / 64) {
+    case 1: return launch_pdl(append_kernel<1, T>, grid, dim3(kIoThreads), 0, s, g, a, counts, slots, scales);
+    case 2: return launch_pdl(append_kernel<2, T>, grid, dim3(kIoThreads), 0, s, g, a, counts, slots, scales);
+    case 3: return launch_pdl(append_kernel<3, T>, grid, dim3(kIoThreads), 0, s, g, a, counts, slots, scales);
+    default: return launch_pdl(append_kernel<4, T>, grid, dim3(kIoThreads), 0, s, g, a, counts, slots, scales);
+  }
 }
 
 }  // namespace
@@ -378,13 +446,8 @@ cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const vo
                              int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, int8_t* k_pages,
                              int8_t* v_pages, float* scales, cudaStream_t s) {
   AppendArgs a = {{k, v}, {k_pages, v_pages}, st_b, st_h, st_t, n_cap};
-  const size_t smem = (size_t)kPage * (g.d64 + 1) * sizeof(float);
-  // n_cap tokens that begin anywhere in a page touch this many pages
-  const dim3 grid((n_cap + 2 * (kPage - 1)) / kPage, g.rows, 2);
-  auto fn = bf16 ? append_kernel<__nv_bfloat16> : append_kernel<float>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fn, grid, dim3(kIoThreads), smem, s, g, a, counts, slots, scales);
+  return bf16 ? launch_append<__nv_bfloat16>(g, a, counts, slots, scales, s)
+              : launch_append<float>(g, a, counts, slots, scales, s);
 }
 
 cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,

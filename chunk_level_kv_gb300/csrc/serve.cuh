@@ -62,4 +62,18 @@ __device__ __forceinline__ int safe_len(int32_t n, int max_pages) {
 // The ring's state words (chunkkv_q8_cache.state).
 enum { kRingHead = 0, kRingFree = 1, kRingStatus = 2, kRingTicket = 3 };
 
+// Raises a kernel's dynamic shared-memory limit once per device (`done`: a bit per
+// device, one word per kernel instance).
+template <typename F>
+cudaError_t raise_smem(F* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 }  // namespace chunkkv

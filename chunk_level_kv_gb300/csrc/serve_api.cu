@@ -41,12 +41,15 @@ chunkkv_status cuda_result(cudaError_t e) { return e == cudaSuccess ? CHUNKKV_OK
 
 // SMs of the current device (152 where no device is visible, as for the compression's plans).
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
     cudaGetLastError();
     return 152;
   }
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

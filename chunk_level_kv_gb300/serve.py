@@ -12,7 +12,7 @@ from dataclasses import dataclass, field
 import torch
 
 from ._lib import LIB, Q8_PAGE, PrefillParams, Q8CacheStruct
-from .api import _check, _DT, _ptr, _stream
+from .api import _check, _DT
 
 
 def _host_i32(xs):
@@ -21,6 +21,11 @@ def _host_i32(xs):
 
 def _bytes(t):
     return t.numel() * t.element_size()
+
+
+def _stream(t) -> int:
+    """The current stream of the tensor's device, as the integer that ctypes passes on."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index or 0)
 
 
 # ------------------------------------------------------------------ prefill attention
@@ -65,8 +70,8 @@ def chunkkv_prefill_path(p: PrefillParams) -> int:
 
 def chunkkv_prefill_attention(p: PrefillParams, q, k, v, out, ws) -> None:
     _check("chunkkv_prefill_attention",
-           LIB.chunkkv_prefill_attention(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(ws), _bytes(ws),
-                                         _stream(q.device)))
+           LIB.chunkkv_prefill_attention(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), ws.data_ptr(), _bytes(ws),
+                                         _stream(q)))
 
 
 def prefill_attention(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, out=None, workspace=None):
@@ -165,8 +170,8 @@ def chunkkv_q8_resize(cache: Q8Cache, new_lens, slots=None) -> None:
         if slots.dtype != torch.int64 or slots.dim() != 2 or slots.shape[0] != cache.rows or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
         n_cap = slots.shape[1]
-    _check("chunkkv_q8_resize", LIB.chunkkv_q8_resize(cache.layer(0), _ptr(new_lens), _ptr(slots), n_cap,
-                                                      _stream(cache.device)))
+    _check("chunkkv_q8_resize", LIB.chunkkv_q8_resize(cache.layer(0), new_lens.data_ptr(), None if slots is None else slots.data_ptr(), n_cap,
+                                                      _stream(cache.lens)))
 
 
 def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
@@ -180,8 +185,8 @@ def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
     if slots.dtype != torch.int64 or slots.shape != (cache.rows, n_cap) or not slots.is_contiguous():
         raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
     _check("chunkkv_q8_append",
-           LIB.chunkkv_q8_append(cache.layer(layer), _DT[k.dtype], _ptr(k), _ptr(v), k.stride(0), k.stride(1),
-                                 k.stride(2), _ptr(counts), _ptr(slots), n_cap, _stream(cache.device)))
+           LIB.chunkkv_q8_append(cache.layer(layer), _DT[k.dtype], k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                                 k.stride(2), counts.data_ptr(), slots.data_ptr(), n_cap, _stream(cache.lens)))
 
 
 def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out) -> None:
@@ -192,8 +197,8 @@ def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out)
             or k_out.dtype not in _DT or k_out.dim() != 2 or k_out.shape[1] != cache.d or k_out.stride(1) != 1):
         raise ValueError("k_out, v_out [tokens, d] of one type and layout, the head dimension contiguous")
     _check("chunkkv_q8_load",
-           LIB.chunkkv_q8_load(cache.layer(layer), _DT[k_out.dtype], _ptr(start), n_cap, _ptr(k_out), _ptr(v_out),
-                               k_out.stride(0), _stream(cache.device)))
+           LIB.chunkkv_q8_load(cache.layer(layer), _DT[k_out.dtype], start.data_ptr(), n_cap, k_out.data_ptr(), v_out.data_ptr(),
+                               k_out.stride(0), _stream(cache.lens)))
 
 
 def chunkkv_q8_workspace_size(cache: Q8Cache, G: int) -> int:
@@ -211,9 +216,9 @@ def chunkkv_q8_attention(cache: Q8Cache, layer: int, q, out, ws, scale: float | 
         raise ValueError("q and out [B, Hkv * G, d], the head dimension contiguous")
     _check("chunkkv_q8_attention",
            LIB.chunkkv_q8_attention(cache.layer(layer), _DT[q.dtype], q.shape[1] // cache.Hkv,
-                                    1.0 / math.sqrt(cache.d) if scale is None else scale, _ptr(q), q.stride(0),
-                                    q.stride(1), _ptr(out), out.stride(0), out.stride(1), _ptr(ws), _bytes(ws),
-                                    _stream(cache.device)))
+                                    1.0 / math.sqrt(cache.d) if scale is None else scale, q.data_ptr(), q.stride(0),
+                                    q.stride(1), out.data_ptr(), out.stride(0), out.stride(1), ws.data_ptr(), _bytes(ws),
+                                    _stream(cache.lens)))
 
 
 def q8_attention(cache: Q8Cache, layer: int, q, *, scale: float | None = None, out=None, workspace=None):
