@@ -8,16 +8,21 @@
 // first) walks the keys in blocks of 128 and keeps for both tiles S = Q K^T (fp32, 128
 // columns) and O (fp32, D columns) in TMEM: 512 columns.  Per block and tile:
 //   S = Q K^T                  8 products of K = 16, operands in shared memory
-//   P = 2^(S alpha - m)        one thread per row: the row maximum, the exponentials, their
-//                              sum, P rounded to bf16 into the columns of S that it replaces
+//   P = 2^(S alpha - m)        one thread per row: the exponentials and their sum, P rounded
+//                              to bf16 into the columns of S that it replaces
 //   O += P V                   A operand P in TMEM, V as it lies ([keys][d], outer-major)
 // While the threads of one tile work on its S, the tensor cores do the other tile's two
 // products: 2 x 512 cycles at full rate, in which 128 threads have 128 x 128
-// exponentials (512 cycles of the exponential unit) and about 450 other instructions
+// exponentials (512 cycles of the exponential unit) and about 200 other instructions
 // each to do.  So the tensor cores bound it as long as the softmax keeps up.
 //
-// The running maximum is kept until a block's maximum passes it by 2^8: only then are
-// O and the sum rescaled (fp32 holds the range; the final division removes it).
+// The reference m of a row is the maximum of the first block in which it sees a key, and
+// stays while the row's sum is below 2^24: a common factor of P, O and the sum costs no
+// precision (bf16 and fp32 have the same exponents) and the final division removes it.
+// So a block has no maximum to find before its exponentials, and they need no more
+// than 64 logits in registers at a time.  A block that passes the bound is done over
+// with its maximum as the reference, O and the sum rescaled; S is still there, since
+// P replaces it only after that test.
 //
 // The blocks are taken from the last one down: the masked ones come first.  P is zero
 // where a key is hidden, but 0 x inf is NaN, and the values of hidden keys (later
@@ -47,7 +52,7 @@ constexpr int kThreads = 384;                     // 12 warps (the last one idle
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register shares within the launch's");
 constexpr int kMaxChecked = 4;                    // masked blocks of an item: 256 rows' limits span at most three
-constexpr float kRescale = 8.f;                   // growth of the maximum (base-2 exponent) that is let pass
+constexpr float kBig = 16777216.f;                // bound of a row's sum under its reference
 
 template <int D> constexpr int block_bytes() { return kTile * D * 2; }
 constexpr int kPanel = kTile * 128;               // 128 rows x 64 elements
@@ -99,8 +104,72 @@ __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<
   return it;
 }
 
-// max of three
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// The first of the row's 32 columns at `first` that are hidden, and those after it.
+template <bool MASK>
+__device__ __forceinline__ float chunk_max(const float (&s)[32], int first, int seen, float m) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float a = !MASK || first + i <= seen ? s[i] : -INFINITY, b = !MASK || first + i + 1 <= seen ? s[i + 1] : -INFINITY;
+    m = fmaxf(m, fmaxf(a, b));
+  }
+  return m;
+}
+// Row maximum over the columns 0 .. seen of S.
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t tS, int seen) {
+  float ra[32], rb[32], m = -INFINITY;
+  tmem_ld32(tS, ra);
+  tmem_wait(ra);
+  tmem_ld32(tS + 32, rb);
+  m = chunk_max<MASK>(ra, 0, seen, m);
+  tmem_wait(rb);
+  tmem_ld32(tS + 64, ra);
+  m = chunk_max<MASK>(rb, 32, seen, m);
+  tmem_wait(ra);
+  tmem_ld32(tS + 96, rb);
+  m = chunk_max<MASK>(ra, 64, seen, m);
+  tmem_wait(rb);
+  return chunk_max<MASK>(rb, 96, seen, m);
+}
+
+// 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
+// and a packed conversion.
+template <bool MASK, int C>
+__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
+                                          uint32_t (&p)[64]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), a2, n2);
+    float2 w = make_float2(ex2(e.x), ex2(e.y));
+    if (MASK) {                                               // whatever a hidden logit is
+      w.x = 32 * C + 2 * i <= seen ? w.x : 0.f;
+      w.y = 32 * C + 2 * i + 1 <= seen ? w.y : 0.f;
+    }
+    sum[i & 1] = __fadd2_rn(sum[i & 1], w);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
+    p[16 * C + i] = *(const uint32_t*)&b;
+  }
+}
+// A row's P under the reference -neg, and its sum.
+template <bool MASK>
+__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, uint32_t (&p)[64]) {
+  float ra[32], rb[32];
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 a2 = make_float2(alpha, alpha), n2 = make_float2(neg, neg);
+  tmem_ld32(tS, ra);
+  tmem_wait(ra);
+  tmem_ld32(tS + 32, rb);
+  chunk_exp<MASK, 0>(ra, a2, n2, seen, sum, p);
+  tmem_wait(rb);
+  tmem_ld32(tS + 64, ra);
+  chunk_exp<MASK, 1>(rb, a2, n2, seen, sum, p);
+  tmem_wait(ra);
+  tmem_ld32(tS + 96, rb);
+  chunk_exp<MASK, 2>(ra, a2, n2, seen, sum, p);
+  tmem_wait(rb);
+  chunk_exp<MASK, 3>(rb, a2, n2, seen, sum, p);
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
 
 template <int D, int MAXB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -171,46 +240,36 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       const Item it = decode_item(g, tab, item);
       const int nb = t ? it.nb1 : it.nb0;
       const int limit = it.limit + t * kTile + row;           // last key that this row sees
-      float m = -INFINITY, neg = 0.f;                         // the row's reference and -m alpha
-      float2 l2 = make_float2(0.f, 0.f);
+      float m = -INFINITY, neg = 0.f, l = 0.f;                // the row's reference, -m alpha, and its sum
       bool ok = true;
       for (int j = nb - 1; j >= 0; --j) {
         if (!wait_bar(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
         ++sc;
         fence_after();
-        float s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait(s[c]);
-        // a block with a key that the warp's first row does not see
-        if (j * kTile + kTile - 1 > limit - lane) {
-          const int seen = limit - j * kTile;                 // columns 0 .. seen
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[c][i] = 32 * c + i <= seen ? s[c][i] : -INFINITY;
-        }
-        float top[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
-#pragma unroll
-        for (int i = 1; i < 31; i += 2)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top[c] = max3(top[c], s[c][i], s[c][i + 1]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], s[c][31]);
-        const float bm = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        const bool grow = (bm - m) * g.alpha > kRescale || (m == -INFINITY && bm != -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2((m - bm) * g.alpha) : 1.f;
-          if (grow) {
+        const int seen = limit - j * kTile;                   // columns 0 .. seen
+        const bool masked = kTile - 1 > seen - lane;          // some key is hidden to the warp's first row
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+          const float bm = masked ? row_max<true>(tS, seen) : row_max<false>(tS, seen);
+          if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
             neg = -m * g.alpha;
           }
-          l2.x *= f;
-          l2.y *= f;
-          if (j < nb - 1) {                                   // O holds something
-            // the block before is done: its product was issued before the one that s_full follows
-#pragma unroll
+        }
+        uint32_t p[64];
+        float sum = masked ? row_exp<true>(tS, g.alpha, neg, seen, p) : row_exp<false>(tS, g.alpha, neg, seen, p);
+        const bool over = !(l + sum <= kBig);                 // a NaN too
+        if (__any_sync(0xffffffffu, over)) {
+          const float bm = masked ? row_max<true>(tS, seen) : row_max<false>(tS, seen);
+          const float mn = fmaxf(m, bm);
+          const float f = over ? ex2((m - mn) * g.alpha) : 1.f;
+          if (over) {
+            m = mn;
+            neg = -m * g.alpha;
+          }
+          l *= f;
+          if (j < nb - 1) {
+            // O holds the blocks before, all of them done: their products were issued before this S
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
               tmem_ld32(tO + 32 * c, o);
@@ -220,28 +279,17 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
               tmem_st32(tO + 32 * c, o);
             }
           }
+          sum = masked ? row_exp<true>(tS, g.alpha, neg, seen, p) : row_exp<false>(tS, g.alpha, neg, seen, p);
         }
-        const float2 a2 = make_float2(g.alpha, g.alpha), n2 = make_float2(neg, neg);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(s[c][2 * i], s[c][2 * i + 1]), a2, n2);
-            const float2 w = make_float2(ex2(e.x), ex2(e.y));
-            l2 = __fadd2_rn(l2, w);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
-            p[i] = *(const uint32_t*)&b;
-          }
-          tmem_st16(tS + 16 * c, p);
-        }
+        l += sum;
+        tmem_st32<0>(tS, p);
+        tmem_st32<32>(tS + 32, p);
         tmem_st_wait();
         fence_before();
         mbar_arrive(p_full + 8 * t);
       }
       if (!ok) break;
       // ---- the item's rows
-      const float l = l2.x + l2.y;
       const float inv = l == 0.f ? 0.f : 1.f / l;             // no visible key: zeros
       const bool live = t * kTile + row < it.rows;
       __nv_bfloat16* po = out + (int64_t)(it.q0 + t * kTile + row) * g.o_st + it.h * g.o_sh;

@@ -16,7 +16,7 @@ namespace {
 // ------------------------------------------------------------ tables and slot maps
 
 constexpr int kResizeThreads = 1024;
-constexpr int kSlotRun = 1024;                  // tokens of a row that a warp maps: 17 pages at most, a lane each
+constexpr int kSlotRun = 256;                   // tokens of a row that a warp maps: 5 pages at most, a lane each
 
 __device__ __forceinline__ int pages_of(int n) { return n > 0 ? (n - 1) / kPage + 1 : 0; }
 

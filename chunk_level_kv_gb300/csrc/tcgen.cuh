@@ -123,12 +123,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&r)[32]) {
       "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]),
       "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31]) : "memory");
 }
-// 16 columns (32 bf16 of P).
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+// 32 columns of packed pairs, registers N .. N + 31 of r.
+template <int N, int M>
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[M]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(addr), "r"(r[N]), "r"(r[N + 1]), "r"(r[N + 2]), "r"(r[N + 3]), "r"(r[N + 4]), "r"(r[N + 5]), "r"(r[N + 6]),
+      "r"(r[N + 7]), "r"(r[N + 8]), "r"(r[N + 9]), "r"(r[N + 10]), "r"(r[N + 11]), "r"(r[N + 12]), "r"(r[N + 13]),
+      "r"(r[N + 14]), "r"(r[N + 15]), "r"(r[N + 16]), "r"(r[N + 17]), "r"(r[N + 18]), "r"(r[N + 19]), "r"(r[N + 20]),
+      "r"(r[N + 21]), "r"(r[N + 22]), "r"(r[N + 23]), "r"(r[N + 24]), "r"(r[N + 25]), "r"(r[N + 26]), "r"(r[N + 27]),
+      "r"(r[N + 28]), "r"(r[N + 29]), "r"(r[N + 30]), "r"(r[N + 31]) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
