@@ -197,7 +197,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);                    // [kItemRing][kMaxChecked][4] keys, a bit each
   static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked <= 1024, "control block");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(drained, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
@@ -220,7 +220,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Ctl ctl{err, abort_flag, g.timeout};
   uint32_t loaded = 0, q_loaded = 0;              // copies that the producer armed (for the teardown)
 
@@ -232,9 +232,9 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const uint32_t tS = lanes + t * kTile, tO = lanes + 256 + t * kTile;
     uint32_t sc = 0, oc = 0, cc = 0;              // phases of s_full, o_full and (a bit per slot) checked
     pdl_wait();
-    for (uint32_t n = 0; !*abort_flag; ++n) {
+    for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
-      if (!wait_bar(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+      if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
       const int item = s_items[slot];
       if (item < 0) break;
       const Item it = decode_item(g, tab, item);
@@ -243,7 +243,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       float m = -INFINITY, neg = 0.f, l = 0.f;                // the row's reference, -m alpha, and its sum
       bool ok = true;
       for (int j = nb - 1; j >= 0; --j) {
-        if (!wait_bar(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
+        if (!wait_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
         ++sc;
         fence_after();
         const int seen = limit - j * kTile;                   // columns 0 .. seen
@@ -295,12 +295,12 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       __nv_bfloat16* po = out + (int64_t)(it.q0 + t * kTile + row) * g.o_st + it.h * g.o_sh;
       bool flagged = false;
       if (it.nb > 0 && t * kTile < it.rows) {
-        if (!wait_bar(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
+        if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
         for (int c = 0; c < kMaxChecked * 4; ++c) flagged |= s_bad[slot * kMaxChecked * 4 + c] != 0;
       }
       if (it.nb > 0) cc ^= 1u << slot;
       if (nb > 0) {
-        if (!wait_bar(ctl, o_full + 8 * t, oc & 1, kDevTimeoutEpilogue)) break;
+        if (!wait_warp(ctl, o_full + 8 * t, oc & 1, kDevTimeoutEpilogue)) break;
         ++oc;
         fence_after();
       }
@@ -393,82 +393,90 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           ++q_loaded;
         }
       }
-    } else if (warp == 9 && lane == 0) {
-      // ------------------------------------------------ MMA issuer
-      uint32_t kv = 0, qc = 0, okc = 0;           // stages used, query loads, parity of v_ok (a bit per stage)
-      uint32_t pc[2] = {0, 0};
+    } else if (warp == 9) {
+      // ------------------------------------------------ MMA issuer (the whole warp, one elected lane at each issue)
+      uint32_t kv = 0, qc = 0, okc = 0, pc = 0;   // stages used, query loads; parities of v_ok (a bit per stage) and p_full
       const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
-      for (uint32_t n = 0; !*abort_flag; ++n) {
-        const int slot = n % kItemRing;
-        if (!wait_bar(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
-        const int item = s_items[slot];
-        mbar_arrive(item_empty + 8 * slot);
-        if (item < 0) break;
-        const Item it = decode_item(g, tab, item);
-        if (it.nb == 0) continue;
-        if (!wait_bar(ctl, q_full, qc & 1, kDevTimeoutMma)) break;
-        ++qc;
-        bool ok = true;
-        // S of tile t for the K block in stage st
-        auto scores = [&](int t, int st) {
-          const uint64_t kd = sw128_desc(smem_u32(sKV) + st * kBlock, 16, 1024);
+      const uint64_t kdesc = sw128_desc(smem_u32(sKV), 16, 1024), vdesc = sw128_desc(smem_u32(sKV), kPanel, 1024);
+      // S of tile t for the K block in stage st
+      auto scores = [&](int t, int st) {
+        if (elect_one()) {
+          const uint64_t kd = kdesc + st * (kBlock >> 4), qd = qdesc + t * (kBlock >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + t * kTile, qdesc + ((t * kBlock) >> 4) + off, kd + off, idesc<kTile>(), kk > 0);
+            mma_ss(tmem + t * kTile, qd + off, kd + off, idesc<kTile>(), kk > 0);
           }
           commit(s_full + 8 * t);
-        };
+        }
+        __syncwarp();
+      };
+      // O of tile t += P of the tile times the V block in stage st
+      auto values = [&](int t, int st, bool add, bool last) {
+        if (elect_one()) {
+          const uint64_t vd = vdesc + st * (kBlock >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + 8 * kk, vd + ((kk * 2048) >> 4), idesc<D>() | kOuterMajorB,
+                   add || kk > 0);
+          if (last) commit(o_full + 8 * t);
+        }
+        __syncwarp();
+      };
+      auto release = [&](uint32_t bar) {
+        if (elect_one()) commit(bar);
+        __syncwarp();
+      };
+      for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
+        const int slot = n % kItemRing;
+        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
+        const int item = __shfl_sync(0xffffffffu, s_items[slot], 0);
+        if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+        if (item < 0) break;
+        const Item it = decode_item(g, tab, item);
+        if (it.nb == 0) continue;
+        if (!wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma)) break;
+        ++qc;
         int st = kv % kStages;
-        if (!wait_bar(ctl, kv_full + 8 * st, (kv / kStages) & 1, kDevTimeoutMma)) break;
+        if (!wait_warp(ctl, kv_full + 8 * st, (kv / kStages) & 1, kDevTimeoutMma)) break;
         fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (it.nb - 1 < (t ? it.nb1 : it.nb0)) scores(t, st);
-        commit(kv_empty + 8 * st);
+        if (it.nb - 1 < it.nb0) scores(0, st);
+        if (it.nb - 1 < it.nb1) scores(1, st);
+        release(kv_empty + 8 * st);
         ++kv;
-        if (it.nb == 1) commit(q_empty);
-        for (int j = it.nb - 1; j >= 0 && ok; --j) {
+        if (it.nb == 1) release(q_empty);
+        bool ok = true;
+        for (int j = it.nb - 1; j >= 0; --j) {
           const int sv = kv % kStages, sk = (kv + 1) % kStages;
-          bool have_v = false, have_k = false;
-          for (int t = 0; t < 2 && ok; ++t) {
+          ok = wait_warp(ctl, kv_full + 8 * sv, (kv / kStages) & 1, kDevTimeoutMma);
+          if (ok && j >= it.low) {
+            ok = wait_warp(ctl, v_ok + 8 * sv, (okc >> sv) & 1, kDevTimeoutMma);
+            okc ^= 1u << sv;
+          }
+          if (ok && j >= 1) ok = wait_warp(ctl, kv_full + 8 * sk, ((kv + 1) / kStages) & 1, kDevTimeoutMma);
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
             const int nb = t ? it.nb1 : it.nb0;
             if (j < nb) {
-              if (!have_v) {
-                ok = wait_bar(ctl, kv_full + 8 * sv, (kv / kStages) & 1, kDevTimeoutMma);
-                if (ok && j >= it.low) {
-                  ok = wait_bar(ctl, v_ok + 8 * sv, (okc >> sv) & 1, kDevTimeoutMma);
-                  okc ^= 1u << sv;
-                }
-                have_v = true;
-              }
-              ok = ok && wait_bar(ctl, p_full + 8 * t, pc[t] & 1, kDevTimeoutMma);
+              ok = wait_warp(ctl, p_full + 8 * t, (pc >> t) & 1, kDevTimeoutMma);
               if (!ok) break;
-              ++pc[t];
+              pc ^= 1u << t;
               fence_after();
-              const uint64_t vd = sw128_desc(smem_u32(sKV) + sv * kBlock, kPanel, 1024);
-#pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + 8 * kk, vd + ((kk * 2048) >> 4),
-                       idesc<D>() | kOuterMajorB, j < nb - 1 || kk > 0);
-              if (j == 0) commit(o_full + 8 * t);
+              values(t, sv, j < nb - 1, j == 0);
             }
             if (j >= 1 && j - 1 < nb) {
-              if (!have_k) {
-                ok = wait_bar(ctl, kv_full + 8 * sk, ((kv + 1) / kStages) & 1, kDevTimeoutMma);
-                if (!ok) break;
-                fence_after();
-                have_k = true;
-              }
+              fence_after();
               scores(t, sk);
             }
           }
           if (!ok) break;
-          commit(kv_empty + 8 * sv);
+          release(kv_empty + 8 * sv);
           ++kv;
           if (j >= 1) {
-            commit(kv_empty + 8 * sk);
+            release(kv_empty + 8 * sk);
             ++kv;
-            if (j == 1) commit(q_empty);
+            if (j == 1) release(q_empty);
           }
         }
         if (!ok) break;
@@ -476,9 +484,9 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     } else if (warp == 10) {
       // ------------------------------------------------ check of the values that some row must not see
       uint32_t kv = 0;
-      for (uint32_t n = 0; !*abort_flag; ++n) {
+      for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
-        if (!wait_bar(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
         const int item = s_items[slot];
         if (item < 0) break;
         const Item it = decode_item(g, tab, item);
@@ -488,7 +496,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         for (int j = it.nb - 1; j >= it.low && ok; --j) {
           const uint32_t use = kv + 2 * (it.nb - 1 - j) + 1;
           const int st = use % kStages;
-          ok = wait_bar(ctl, kv_full + 8 * st, (use / kStages) & 1, kDevTimeoutEpilogue);
+          ok = wait_warp(ctl, kv_full + 8 * st, (use / kStages) & 1, kDevTimeoutEpilogue);
           if (!ok) break;
           uint4* blk = (uint4*)(sKV + st * kBlock);
           uint32_t top = 0;
@@ -552,8 +560,9 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         landed &= drain_phase(kv_full + 8 * (i % kStages), (i / kStages) & 1);
       if (q_loaded > 0) landed &= drain_phase(q_full, (q_loaded - 1) & 1);
     }
-    if (warp == 9 && lane == 0) {
-      commit(drained);
+    if (warp == 9) {
+      if (elect_one()) commit(drained);
+      __syncwarp();
       landed &= drain_phase(drained, 0);
     }
     if (!landed) {

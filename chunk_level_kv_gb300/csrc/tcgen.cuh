@@ -48,6 +48,11 @@ __device__ __forceinline__ bool wait_bar(const Ctl& ctl, uint32_t bar, uint32_t 
     }
   }
 }
+// The same for a converged warp, with one answer for all its lanes: a role that goes on
+// to warp-wide instructions may not lose some of them to a give-up.
+__device__ __forceinline__ bool wait_warp(const Ctl& ctl, uint32_t bar, uint32_t parity, int code) {
+  return __all_sync(0xffffffffu, wait_bar(ctl, bar, parity, code));
+}
 // After a give-up: a bounded wait for an operation of this CTA that is still in
 // flight, which must land before the memory that it writes is released.
 constexpr long long kDrainCycles = 100000000LL;
@@ -62,6 +67,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint3
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(dst), "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+
+// True in one lane of a converged warp, always the same one.  A role whose loop is
+// uniform over the warp and that elects a lane only around the issue keeps its
+// descriptors in uniform registers; inside `if (lane == 0)` each product took several
+// times the instructions and, next to busy softmax warps, twice its time to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
