@@ -26,12 +26,12 @@
 //
 // The blocks are taken from the last one down: the masked ones come first.  P is zero
 // where a key is hidden, but 0 x inf is NaN, and the values of hidden keys (later
-// positions, the next sequence's rows) may hold anything.  So a checking warp looks
-// through the V of the masked blocks before the product and replaces non-finite
+// positions, the next sequence's rows) may hold anything.  So two checking warps look
+// through the V of the masked blocks before the product and replace non-finite
 // elements by zero; rows that do see such a key get the element added at the end.
 //
-// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 MMA issuer, 10 V
-// check.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 MMA issuer, 10 and
+// 11 V check.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,7 +48,7 @@ using namespace tcgen;
 constexpr int kTile = 128;                        // query rows of a tile, keys of a block
 constexpr int kStages = 5;                        // K and V blocks in shared memory
 constexpr int kItemRing = 2;
-constexpr int kThreads = 384;                     // 12 warps (the last one idle: register shares go by warpgroup)
+constexpr int kThreads = 384;                     // 12 warps, three warpgroups
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register shares within the launch's");
 constexpr int kMaxChecked = 4;                    // masked blocks of an item: 256 rows' limits span at most three
@@ -68,6 +68,7 @@ struct TcGeom {
   int32_t n_items;
   float alpha;
   int64_t v_st, v_sh, o_st, o_sh;                 // element strides of v and out
+  int32_t wide;                                   // out's rows are 32-byte aligned and d a multiple of 32
   long long timeout;
 };
 struct TcMaps { CUtensorMap q, k, v; };
@@ -194,17 +195,17 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* s_items = abort_flag + 1;                                                  // [kItemRing]
-  uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);                    // [kItemRing][kMaxChecked][4] keys, a bit each
-  static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked <= 1024, "control block");
+  uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);     // [kItemRing][two warps][kMaxChecked][4] keys, a bit each
+  static_assert(8 * kBars + 8 + 4 * kItemRing + 32 * kItemRing * kMaxChecked <= 1024, "control block");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(drained, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
-    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 1); mbar_init(v_ok + 8 * i, 1); }
-    // an item's slot is released by the MMA issuer, the checking warp and each softmax warp
+    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 1); mbar_init(v_ok + 8 * i, 2); }
+    // an item's slot is released by the MMA issuer, the checking warps and each softmax warp
     for (int i = 0; i < kItemRing; ++i) {
-      mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 10); mbar_init(checked + 8 * i, 1);
+      mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11); mbar_init(checked + 8 * i, 2);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -296,7 +297,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       bool flagged = false;
       if (it.nb > 0 && t * kTile < it.rows) {
         if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
-        for (int c = 0; c < kMaxChecked * 4; ++c) flagged |= s_bad[slot * kMaxChecked * 4 + c] != 0;
+        for (int c = 0; c < kMaxChecked * 8; ++c) flagged |= s_bad[slot * kMaxChecked * 8 + c] != 0;
       }
       if (it.nb > 0) cc ^= 1u << slot;
       if (nb > 0) {
@@ -319,7 +320,8 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           for (int k = 0; k < min(it.nb - it.low, kMaxChecked); ++k)
             for (int r = 0; r < kTile; ++r) {
               const int key = (it.low + k) * kTile + r;
-              if (key > limit || key >= it.tk || !(s_bad[(slot * kMaxChecked + k) * 4 + (r >> 5)] >> (r & 31) & 1)) continue;
+              const uint32_t* bad = s_bad + slot * kMaxChecked * 8 + k * 4 + (r >> 5);
+              if (key > limit || key >= it.tk || !((bad[0] | bad[kMaxChecked * 4]) >> (r & 31) & 1)) continue;
               const __nv_bfloat16* pv = v + (int64_t)(it.k0 + key) * g.v_st + it.hk * g.v_sh + 32 * c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
@@ -330,15 +332,21 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         }
         if (live) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (32 * c + i >= g.d) break;
-            uint32_t w[4];
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const __nv_bfloat162 b = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
               w[e] = *(const uint32_t*)&b;
             }
-            *(uint4*)(po + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            // a lane per row: whole 32-byte sectors where the rows' alignment allows it
+            if (g.wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(po + 32 * c + i), "r"(w[0]), "r"(w[1]),
+                           "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+            } else {
+              if (32 * c + i < g.d) *(uint4*)(po + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              if (32 * c + i + 8 < g.d) *(uint4*)(po + 32 * c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
@@ -481,7 +489,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         }
         if (!ok) break;
       }
-    } else if (warp == 10) {
+    } else if (warp >= 10) {
       // ------------------------------------------------ check of the values that some row must not see
       uint32_t kv = 0;
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
@@ -490,7 +498,8 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         const int item = s_items[slot];
         if (item < 0) break;
         const Item it = decode_item(g, tab, item);
-        for (int i = lane; i < kMaxChecked * 4; i += 32) s_bad[slot * kMaxChecked * 4 + i] = 0;
+        uint32_t* bad_keys = s_bad + (slot * 2 + warp - 10) * kMaxChecked * 4;
+        for (int i = lane; i < kMaxChecked * 4; i += 32) bad_keys[i] = 0;
         __syncwarp();
         bool ok = true;
         for (int j = it.nb - 1; j >= it.low && ok; --j) {
@@ -498,17 +507,18 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           const int st = use % kStages;
           ok = wait_warp(ctl, kv_full + 8 * st, (use / kStages) & 1, kDevTimeoutEpilogue);
           if (!ok) break;
-          uint4* blk = (uint4*)(sKV + st * kBlock);
+          uint4* blk = (uint4*)(sKV + st * kBlock);           // a half for each of the two warps
+          const int i0 = (warp - 10) * (kBlock / 32) + lane, i1 = (warp - 9) * (kBlock / 32);
           uint32_t top = 0;
 #pragma unroll 8
-          for (int i = lane; i < kBlock / 16; i += 32) {
+          for (int i = i0; i < i1; i += 32) {
             const uint4 w = blk[i];
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
                                          __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
           }
           const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
           if (__any_sync(0xffffffffu, bad)) {
-            for (int i = lane; i < kBlock / 16; i += 32) {
+            for (int i = i0; i < i1; i += 32) {
               uint4 w = blk[i];
               uint32_t* x = (uint32_t*)&w;
               bool hit = false;
@@ -520,7 +530,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
               if (hit) {
                 blk[i] = w;
                 const int r = (i / 8) & (kTile - 1);          // rows of 128 bytes, whatever the swizzle
-                atomicOr(&s_bad[(slot * kMaxChecked + (j - it.low)) * 4 + (r >> 5)], 1u << (r & 31));
+                atomicOr(&bad_keys[(j - it.low) * 4 + (r >> 5)], 1u << (r & 31));
               }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it next
@@ -631,7 +641,8 @@ cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& 
       !encode(enc, &maps.k, k, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh) ||
       !encode(enc, &maps.v, v, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh))
     return cudaErrorInvalidValue;
-  TcGeom g = {p.Hq, p.G, p.d, rows, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL};
+  TcGeom g = {p.Hq, p.G, p.d, rows, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh,
+              p.d % 32 == 0 && p.o_st % 16 == 0 && p.o_sh % 16 == 0 && (uintptr_t)out % 32 == 0, 4000000000LL};
   if (p.d <= 64) return launch<64, MAXB>(maps, g, tab, v, out, err, sms, s);
   return launch<128, MAXB>(maps, g, tab, v, out, err, sms, s);
 }
