@@ -26,12 +26,13 @@
 //
 // The blocks are taken from the last one down: the masked ones come first.  P is zero
 // where a key is hidden, but 0 x inf is NaN, and the values of hidden keys (later
-// positions, the next sequence's rows) may hold anything.  So two checking warps look
-// through the V of the masked blocks before the product and replace non-finite
+// positions, the next sequence's rows) may hold anything.  So a checking warp looks
+// through the V of the masked blocks before the product and replaces non-finite
 // elements by zero; rows that do see such a key get the element added at the end.
 //
-// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 MMA issuer, 10 and
-// 11 V check.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 and 10 MMA
+// issuers of tile 0 and 1 (with one issuer for both, its waits for one tile kept the
+// other's products back: a block pair took 3250 cycles), 11 V check.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -46,7 +47,7 @@ namespace {
 using namespace tcgen;
 
 constexpr int kTile = 128;                        // query rows of a tile, keys of a block
-constexpr int kStages = 5;                        // K and V blocks in shared memory
+constexpr int kStages = 4;                        // K and V blocks in shared memory (five were no faster)
 constexpr int kItemRing = 2;
 constexpr int kThreads = 384;                     // 12 warps, three warpgroups
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -56,7 +57,8 @@ constexpr float kBig = 16777216.f;                // bound of a row's sum under 
 
 template <int D> constexpr int block_bytes() { return kTile * D * 2; }
 constexpr int kPanel = kTile * 128;               // 128 rows x 64 elements
-template <int D> constexpr int smem_bytes() { return (2 + kStages) * block_bytes<D>() + 1024; }
+constexpr int kStageOut = 32 * 128;               // a softmax warp's 32 rows x 64 output columns
+template <int D> constexpr int smem_bytes() { return (2 + kStages) * block_bytes<D>() + 1024 + 8 * kStageOut; }
 template <int N> constexpr uint32_t idesc() {     // fp32 D, bf16 A and B, M = 128
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
@@ -68,7 +70,6 @@ struct TcGeom {
   int32_t n_items;
   float alpha;
   int64_t v_st, v_sh, o_st, o_sh;                 // element strides of v and out
-  int32_t wide;                                   // out's rows are 32-byte aligned and d a multiple of 32
   long long timeout;
 };
 struct TcMaps { CUtensorMap q, k, v; };
@@ -105,38 +106,43 @@ __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<
   return it;
 }
 
-// The first of the row's 32 columns at `first` that are hidden, and those after it.
-template <bool MASK>
-__device__ __forceinline__ float chunk_max(const float (&s)[32], int first, int seen, float m) {
+// A 32-column chunk of a warp's rows at column `first`: all of it visible, some, or none
+// to any of them (`seen` - lane: what the warp's first row sees, 31 more for the last).
+__device__ __forceinline__ bool chunk_full(int first, int seen, int lane) { return first + 31 <= seen - lane; }
+__device__ __forceinline__ bool chunk_none(int first, int seen, int lane) { return first > seen - lane + 31; }
+
+template <int C>
+__device__ __forceinline__ float chunk_max(const float (&s)[32], int seen, int lane, float m) {
+  if (chunk_full(32 * C, seen, lane)) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
-    const float a = !MASK || first + i <= seen ? s[i] : -INFINITY, b = !MASK || first + i + 1 <= seen ? s[i + 1] : -INFINITY;
-    m = fmaxf(m, fmaxf(a, b));
+    for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
+  } else if (!chunk_none(32 * C, seen, lane)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, 32 * C + i <= seen ? s[i] : -INFINITY);
   }
   return m;
 }
 // Row maximum over the columns 0 .. seen of S.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t tS, int seen) {
+__device__ __forceinline__ float row_max(uint32_t tS, int seen, int lane) {
   float ra[32], rb[32], m = -INFINITY;
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  m = chunk_max<MASK>(ra, 0, seen, m);
+  m = chunk_max<0>(ra, seen, lane, m);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  m = chunk_max<MASK>(rb, 32, seen, m);
+  m = chunk_max<1>(rb, seen, lane, m);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  m = chunk_max<MASK>(ra, 64, seen, m);
+  m = chunk_max<2>(ra, seen, lane, m);
   tmem_wait(rb);
-  return chunk_max<MASK>(rb, 96, seen, m);
+  return chunk_max<3>(rb, seen, lane, m);
 }
 
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
 // and a packed conversion.
 template <bool MASK, int C>
-__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
+__device__ __forceinline__ void exp_pairs(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
                                           uint32_t (&p)[64]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -151,25 +157,84 @@ __device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float
     p[16 * C + i] = *(const uint32_t*)&b;
   }
 }
-// A row's P under the reference -neg, and its sum.
+template <bool MASK, int C>
+__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, int lane,
+                                          float2 (&sum)[2], uint32_t (&p)[64]) {
+  if (!MASK || chunk_full(32 * C, seen, lane)) {
+    exp_pairs<false, C>(s, a2, n2, seen, sum, p);
+  } else if (!chunk_none(32 * C, seen, lane)) {
+    exp_pairs<true, C>(s, a2, n2, seen, sum, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[16 * C + i] = 0;
+  }
+}
+// A row's P under the reference -neg, and its sum.  Without MASK it is straight-line
+// code: a branch per chunk cost 400 cycles of a block's 1000.
 template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, uint32_t (&p)[64]) {
+__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, int lane, uint32_t (&p)[64]) {
   float ra[32], rb[32];
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 a2 = make_float2(alpha, alpha), n2 = make_float2(neg, neg);
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  chunk_exp<MASK, 0>(ra, a2, n2, seen, sum, p);
+  chunk_exp<MASK, 0>(ra, a2, n2, seen, lane, sum, p);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  chunk_exp<MASK, 1>(rb, a2, n2, seen, sum, p);
+  chunk_exp<MASK, 1>(rb, a2, n2, seen, lane, sum, p);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  chunk_exp<MASK, 2>(ra, a2, n2, seen, sum, p);
+  chunk_exp<MASK, 2>(ra, a2, n2, seen, lane, sum, p);
   tmem_wait(rb);
-  chunk_exp<MASK, 3>(rb, a2, n2, seen, sum, p);
+  chunk_exp<MASK, 3>(rb, a2, n2, seen, lane, sum, p);
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// A block whose sum passed the bound, done over: rows that are `over` move their
+// reference to the block's maximum, and what O (at tO, unless it is still empty) and l
+// hold goes with it.  Returns (m, -m alpha, l); P is written.  Out of line, as the next
+// function: the loop around it has to stay in the instruction cache.
+template <int D>
+__device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, int seen, int lane,
+                                           bool over) {
+  const float bm = row_max(tS, seen, lane);
+  const float mn = fmaxf(m, bm);
+  const float f = over ? ex2((m - mn) * alpha) : 1.f;
+  if (over) m = mn;
+  const float neg = m == -INFINITY ? 0.f : -m * alpha;
+  if (tO != 0xFFFFFFFFu) {
+    // the blocks before are done: their products were issued before this S
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      tmem_ld32(tO + 32 * c, o);
+      tmem_wait(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] *= f;
+      tmem_st32(tO + 32 * c, o);
+    }
+  }
+  uint32_t p[64];
+  const float sum = row_exp<true>(tS, alpha, neg, seen, lane, p);
+  tmem_st32<0>(tS, p);
+  tmem_st32<32>(tS + 32, p);
+  return make_float3(m, neg, l * f + sum);
+}
+
+// Adds to 32 staged output columns (from c0 on; piece k of the row at k ^ x) of a row the
+// non-finite values of the keys that it sees, which the check took out of the products.
+__device__ __noinline__ void add_non_finite(uint8_t* row, int piece, int x, const uint32_t* bad, int blocks, int keys,
+                                            const __nv_bfloat16* v, int64_t v_st, int columns) {
+  for (int k = 0; k < blocks * kTile && k < keys; ++k) {
+    if (!(bad[k >> 5] >> (k & 31) & 1)) continue;
+    for (int i = 0; i < columns; ++i) {
+      const __nv_bfloat16 y = v[k * v_st + i];
+      if ((__bfloat16_as_ushort(y) & 0x7F80u) != 0x7F80u) continue;
+      __nv_bfloat16* o = (__nv_bfloat16*)(row + ((piece + (i >> 3)) ^ x) * 16) + (i & 7);
+      *o = __float2bfloat16_rn(__bfloat162float(*o) + __bfloat162float(y));
+    }
+  }
 }
 
 template <int D, int MAXB>
@@ -186,26 +251,28 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   uint8_t* sQ = smem;                             // two tiles
   uint8_t* sKV = smem + 2 * kBlock;               // kStages blocks: K, V, K, V ... of descending blocks
   uint64_t* bars = (uint64_t*)(sKV + kStages * kBlock);
-  const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;
-  const uint32_t s_full = q_full + 24, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
+  const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;      // drained: [2]
+  const uint32_t turn = q_full + 32, s_full = q_full + 48, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
   const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages, v_ok = kv_empty + 8 * kStages;
   const uint32_t item_full = v_ok + 8 * kStages, item_empty = item_full + 8 * kItemRing;
   const uint32_t checked = item_empty + 8 * kItemRing;                                     // [kItemRing]
-  constexpr int kBars = 3 + 6 + 3 * kStages + 3 * kItemRing;
+  constexpr int kBars = 6 + 6 + 3 * kStages + 3 * kItemRing;
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* s_items = abort_flag + 1;                                                  // [kItemRing]
-  uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);     // [kItemRing][two warps][kMaxChecked][4] keys, a bit each
-  static_assert(8 * kBars + 8 + 4 * kItemRing + 32 * kItemRing * kMaxChecked <= 1024, "control block");
+  uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);     // [kItemRing][kMaxChecked][4] keys, a bit each
+  static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked <= 1024, "control block");
 
+  uint8_t* sOut = (uint8_t*)bars + 1024;           // [8][kStageOut]
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(drained, 1);
+    mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
+    mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
-    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 1); mbar_init(v_ok + 8 * i, 2); }
-    // an item's slot is released by the MMA issuer, the checking warps and each softmax warp
+    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 2); mbar_init(v_ok + 8 * i, 1); }
+    // an item's slot is released by the MMA issuers, the checking warp and each softmax warp
     for (int i = 0; i < kItemRing; ++i) {
-      mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11); mbar_init(checked + 8 * i, 2);
+      mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11); mbar_init(checked + 8 * i, 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -248,43 +315,27 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         ++sc;
         fence_after();
         const int seen = limit - j * kTile;                   // columns 0 .. seen
-        const bool masked = kTile - 1 > seen - lane;          // some key is hidden to the warp's first row
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float bm = masked ? row_max<true>(tS, seen) : row_max<false>(tS, seen);
+          const float bm = row_max(tS, seen, lane);
           if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
             neg = -m * g.alpha;
           }
         }
         uint32_t p[64];
-        float sum = masked ? row_exp<true>(tS, g.alpha, neg, seen, p) : row_exp<false>(tS, g.alpha, neg, seen, p);
+        const float sum = kTile - 1 > seen - lane ? row_exp<true>(tS, g.alpha, neg, seen, lane, p)      // a hidden key in the warp
+                                                  : row_exp<false>(tS, g.alpha, neg, seen, lane, p);
         const bool over = !(l + sum <= kBig);                 // a NaN too
-        if (__any_sync(0xffffffffu, over)) {
-          const float bm = masked ? row_max<true>(tS, seen) : row_max<false>(tS, seen);
-          const float mn = fmaxf(m, bm);
-          const float f = over ? ex2((m - mn) * g.alpha) : 1.f;
-          if (over) {
-            m = mn;
-            neg = -m * g.alpha;
-          }
-          l *= f;
-          if (j < nb - 1) {
-            // O holds the blocks before, all of them done: their products were issued before this S
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(tO + 32 * c, o);
-              tmem_wait(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tmem_st32(tO + 32 * c, o);
-            }
-          }
-          sum = masked ? row_exp<true>(tS, g.alpha, neg, seen, p) : row_exp<false>(tS, g.alpha, neg, seen, p);
+        if (!__any_sync(0xffffffffu, over)) {
+          l += sum;
+          tmem_st32<0>(tS, p);
+          tmem_st32<32>(tS + 32, p);
+        } else {
+          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, seen, lane, over);
+          m = r.x;
+          neg = r.y;
+          l = r.z;
         }
-        l += sum;
-        tmem_st32<0>(tS, p);
-        tmem_st32<32>(tS + 32, p);
         tmem_st_wait();
         fence_before();
         mbar_arrive(p_full + 8 * t);
@@ -293,11 +344,10 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       // ---- the item's rows
       const float inv = l == 0.f ? 0.f : 1.f / l;             // no visible key: zeros
       const bool live = t * kTile + row < it.rows;
-      __nv_bfloat16* po = out + (int64_t)(it.q0 + t * kTile + row) * g.o_st + it.h * g.o_sh;
       bool flagged = false;
       if (it.nb > 0 && t * kTile < it.rows) {
         if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
-        for (int c = 0; c < kMaxChecked * 8; ++c) flagged |= s_bad[slot * kMaxChecked * 8 + c] != 0;
+        for (int c = 0; c < kMaxChecked * 4; ++c) flagged |= s_bad[slot * kMaxChecked * 4 + c] != 0;
       }
       if (it.nb > 0) cc ^= 1u << slot;
       if (nb > 0) {
@@ -305,9 +355,12 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         ++oc;
         fence_after();
       }
+      // 64 columns at a time through the warp's own staging rows, so that the stores are whole lines of a row:
+      // 16-byte piece k of row r lies at k ^ (r & 7)
+      uint8_t* stage = sOut + warp * kStageOut;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
-        if (t * kTile >= it.rows || 32 * c >= g.d) break;     // the same for the whole warp
+        if (t * kTile + (warp & 3) * 32 >= it.rows || 32 * c >= g.d) break;     // the same for the whole warp
         float o[32];
         if (nb > 0) {
           tmem_ld32(tO + 32 * c, o);
@@ -315,39 +368,30 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = nb > 0 ? o[i] * inv : 0.f;
-        if (flagged && live) {
-          // non-finite values of visible keys, which the check took out of the products
-          for (int k = 0; k < min(it.nb - it.low, kMaxChecked); ++k)
-            for (int r = 0; r < kTile; ++r) {
-              const int key = (it.low + k) * kTile + r;
-              const uint32_t* bad = s_bad + slot * kMaxChecked * 8 + k * 4 + (r >> 5);
-              if (key > limit || key >= it.tk || !((bad[0] | bad[kMaxChecked * 4]) >> (r & 31) & 1)) continue;
-              const __nv_bfloat16* pv = v + (int64_t)(it.k0 + key) * g.v_st + it.hk * g.v_sh + 32 * c;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = 32 * c + i < g.d ? __bfloat162float(pv[i]) : 0.f;
-                if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) o[i] += x;
-              }
-            }
-        }
-        if (live) {
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
-              w[e] = *(const uint32_t*)&b;
-            }
-            // a lane per row: whole 32-byte sectors where the rows' alignment allows it
-            if (g.wide) {
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(po + 32 * c + i), "r"(w[0]), "r"(w[1]),
-                           "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-            } else {
-              if (32 * c + i < g.d) *(uint4*)(po + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-              if (32 * c + i + 8 < g.d) *(uint4*)(po + 32 * c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
+            w[e] = *(const uint32_t*)&b;
           }
+          *(uint4*)(stage + lane * 128 + (((c & 1) * 4 + i) ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (flagged && live)
+          add_non_finite(stage + lane * 128, (c & 1) * 4, lane & 7, s_bad + slot * kMaxChecked * 4,
+                         min(it.nb - it.low, kMaxChecked), min(limit + 1, it.tk) - it.low * kTile,
+                         v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh + 32 * c, g.v_st, min(32, g.d - 32 * c));
+        if ((c & 1) || 32 * (c + 1) >= g.d) {                 // both halves of the 64 columns are there, or the last ones
+          __syncwarp();
+          const int k = lane & 7, col = (c >> 1) * 64 + k * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), qr = t * kTile + (warp & 3) * 32 + r;
+            const uint4 w = *(const uint4*)(stage + r * 128 + (k ^ (r & 7)) * 16);
+            if (qr < it.rows && col < g.d) *(uint4*)(out + (int64_t)(it.q0 + qr) * g.o_st + it.h * g.o_sh + col) = w;
+          }
+          __syncwarp();
         }
       }
       fence_before();
@@ -401,40 +445,39 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           ++q_loaded;
         }
       }
-    } else if (warp == 9) {
-      // ------------------------------------------------ MMA issuer (the whole warp, one elected lane at each issue)
-      uint32_t kv = 0, qc = 0, okc = 0, pc = 0;   // stages used, query loads; parities of v_ok (a bit per stage) and p_full
-      const uint64_t qdesc = sw128_desc(smem_u32(sQ), 16, 1024);
+    } else if (warp == 9 || warp == 10) {
+      // ------------------------------------------------ MMA issuer of one tile (the whole warp, one elected lane at an issue)
+      const int t = warp - 9;
+      uint32_t qc = 0, pc = 0, tc = 0, okc = 0;   // query loads, P tiles, turns, and the parity of v_ok (a bit per stage)
+      int st = 0;                                 // stage in turn and its parity
+      uint32_t ph = 0;
+      const uint32_t tS = tmem + t * kTile, tO = tmem + 256 + t * kTile;
+      const uint64_t qdesc = sw128_desc(smem_u32(sQ) + t * kBlock, 16, 1024);
       const uint64_t kdesc = sw128_desc(smem_u32(sKV), 16, 1024), vdesc = sw128_desc(smem_u32(sKV), kPanel, 1024);
-      // S of tile t for the K block in stage st
-      auto scores = [&](int t, int st) {
-        if (elect_one()) {
-          const uint64_t kd = kdesc + st * (kBlock >> 4), qd = qdesc + t * (kBlock >> 4);
+      // S = Q K^T for the K block in stage sk, O += P V for the V block in stage sv; the stages are released
+      // with the products that read them
+      auto scores = [&](int sk, bool pass) {
+        const uint64_t kd = kdesc + sk * (kBlock >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + t * kTile, qd + off, kd + off, idesc<kTile>(), kk > 0);
-          }
-          commit(s_full + 8 * t);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+          mma_ss(tS, qdesc + off, kd + off, idesc<kTile>(), kk > 0);
+          if (kk == D / 16 - 3 && pass) mbar_arrive(turn + 8 * (t ^ 1));
         }
-        __syncwarp();
+        commit(s_full + 8 * t);
+        commit(kv_empty + 8 * sk);
       };
-      // O of tile t += P of the tile times the V block in stage st
-      auto values = [&](int t, int st, bool add, bool last) {
-        if (elect_one()) {
-          const uint64_t vd = vdesc + st * (kBlock >> 4);
+      auto values = [&](int sv, bool add) {
+        const uint64_t vd = vdesc + sv * (kBlock >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + 8 * kk, vd + ((kk * 2048) >> 4), idesc<D>() | kOuterMajorB,
-                   add || kk > 0);
-          if (last) commit(o_full + 8 * t);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tO, tS + 8 * kk, vd + ((kk * 2048) >> 4), idesc<D>() | kOuterMajorB, add || kk > 0);
+        commit(kv_empty + 8 * sv);
       };
-      auto release = [&](uint32_t bar) {
-        if (elect_one()) commit(bar);
-        __syncwarp();
-      };
+      // a block that this tile does not need: released only once it is there, so that the
+      // release counts for this use of the stage
+      auto skip = [&](int sx) { if (lane == 0) mbar_arrive(kv_empty + 8 * sx); };
+      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1; } };
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
         if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
@@ -443,53 +486,74 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         if (item < 0) break;
         const Item it = decode_item(g, tab, item);
         if (it.nb == 0) continue;
-        if (!wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma)) break;
+        const int nb = t ? it.nb1 : it.nb0;
+        bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma);
+        if (!ok) break;
         ++qc;
-        int st = kv % kStages;
-        if (!wait_warp(ctl, kv_full + 8 * st, (kv / kStages) & 1, kDevTimeoutMma)) break;
         fence_after();
-        if (it.nb - 1 < it.nb0) scores(0, st);
-        if (it.nb - 1 < it.nb1) scores(1, st);
-        release(kv_empty + 8 * st);
-        ++kv;
-        if (it.nb == 1) release(q_empty);
-        bool ok = true;
-        for (int j = it.nb - 1; j >= 0; --j) {
-          const int sv = kv % kStages, sk = (kv + 1) % kStages;
-          ok = wait_warp(ctl, kv_full + 8 * sv, (kv / kStages) & 1, kDevTimeoutMma);
-          if (ok && j >= it.low) {
-            ok = wait_warp(ctl, v_ok + 8 * sv, (okc >> sv) & 1, kDevTimeoutMma);
-            okc ^= 1u << sv;
+        if (it.nb - 1 < nb) {
+          if (elect_one()) {
+            scores(st, false);
+            if (it.nb == 1) commit(q_empty);
           }
-          if (ok && j >= 1) ok = wait_warp(ctl, kv_full + 8 * sk, ((kv + 1) / kStages) & 1, kDevTimeoutMma);
+        } else {
+          skip(st);
+        }
+        __syncwarp();
+        next();
+        for (int j = it.nb - 1; j >= 0; --j) {
+          // V of this block and K of the one below it, and then P: nothing is waited for between the products
+          const int sv = st;
+          ok = wait_warp(ctl, kv_full + 8 * sv, ph, kDevTimeoutMma);
+          if (ok && j < nb && j >= it.low) ok = wait_warp(ctl, v_ok + 8 * sv, (okc >> sv) & 1, kDevTimeoutMma);
+          if (j >= it.low) okc ^= 1u << sv;
+          next();
+          const int sk = st;
+          if (ok && j >= 1) {
+            ok = wait_warp(ctl, kv_full + 8 * sk, ph, kDevTimeoutMma);
+            next();
+          }
           if (!ok) break;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nb = t ? it.nb1 : it.nb0;
-            if (j < nb) {
-              ok = wait_warp(ctl, p_full + 8 * t, (pc >> t) & 1, kDevTimeoutMma);
-              if (!ok) break;
-              pc ^= 1u << t;
-              fence_after();
-              values(t, sv, j < nb - 1, j == 0);
+          if (j < nb) {
+            // the two tiles take turns, tile 0 first
+            const bool both = j < min(it.nb0, it.nb1);
+            if (both) {
+              ok = wait_warp(ctl, turn + 8 * t, (tc & 1) ^ (t ^ 1), kDevTimeoutMma);
+              ++tc;
             }
+            ok = ok && wait_warp(ctl, p_full + 8 * t, pc & 1, kDevTimeoutMma);
+            if (!ok) break;
+            ++pc;
+            fence_after();
+            if (elect_one()) {
+              values(sv, j < nb - 1);
+              if (j >= 1) {
+                scores(sk, both);
+              } else {
+                if (both) mbar_arrive(turn + 8 * (t ^ 1));
+                commit(o_full + 8 * t);
+              }
+              if (j == 1) commit(q_empty);        // the queries have been read
+            }
+          } else {
+            skip(sv);
             if (j >= 1 && j - 1 < nb) {
               fence_after();
-              scores(t, sk);
+              if (elect_one()) {
+                scores(sk, false);
+                if (j == 1) commit(q_empty);
+              }
+            } else if (j >= 1) {
+              skip(sk);
             }
           }
-          if (!ok) break;
-          release(kv_empty + 8 * sv);
-          ++kv;
-          if (j >= 1) {
-            release(kv_empty + 8 * sk);
-            ++kv;
-            if (j == 1) release(q_empty);
-          }
+          __syncwarp();
         }
         if (!ok) break;
+        if (nb == 0 && lane == 0) mbar_arrive(q_empty);
+        __syncwarp();
       }
-    } else if (warp >= 10) {
+    } else if (warp == 11) {
       // ------------------------------------------------ check of the values that some row must not see
       uint32_t kv = 0;
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
@@ -498,7 +562,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         const int item = s_items[slot];
         if (item < 0) break;
         const Item it = decode_item(g, tab, item);
-        uint32_t* bad_keys = s_bad + (slot * 2 + warp - 10) * kMaxChecked * 4;
+        uint32_t* bad_keys = s_bad + slot * kMaxChecked * 4;
         for (int i = lane; i < kMaxChecked * 4; i += 32) bad_keys[i] = 0;
         __syncwarp();
         bool ok = true;
@@ -507,18 +571,22 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           const int st = use % kStages;
           ok = wait_warp(ctl, kv_full + 8 * st, (use / kStages) & 1, kDevTimeoutEpilogue);
           if (!ok) break;
-          uint4* blk = (uint4*)(sKV + st * kBlock);           // a half for each of the two warps
-          const int i0 = (warp - 10) * (kBlock / 32) + lane, i1 = (warp - 9) * (kBlock / 32);
-          uint32_t top = 0;
+          uint4* blk = (uint4*)(sKV + st * kBlock);
+          // 0 x + sum stays zero as long as every x is finite
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
 #pragma unroll 8
-          for (int i = i0; i < i1; i += 32) {
+          for (int i = lane; i < kBlock / 16; i += 32) {
             const uint4 w = blk[i];
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                         __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+            sum[0] = __hfma2(*(const __nv_bfloat162*)&w.x, zero, sum[0]);
+            sum[1] = __hfma2(*(const __nv_bfloat162*)&w.y, zero, sum[1]);
+            sum[2] = __hfma2(*(const __nv_bfloat162*)&w.z, zero, sum[2]);
+            sum[3] = __hfma2(*(const __nv_bfloat162*)&w.w, zero, sum[3]);
           }
-          const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
+          const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+          const bool bad = (*(const uint32_t*)&all & 0x7FFF7FFFu) != 0;
           if (__any_sync(0xffffffffu, bad)) {
-            for (int i = i0; i < i1; i += 32) {
+            for (int i = lane; i < kBlock / 16; i += 32) {
               uint4 w = blk[i];
               uint32_t* x = (uint32_t*)&w;
               bool hit = false;
@@ -570,10 +638,11 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         landed &= drain_phase(kv_full + 8 * (i % kStages), (i / kStages) & 1);
       if (q_loaded > 0) landed &= drain_phase(q_full, (q_loaded - 1) & 1);
     }
-    if (warp == 9) {
-      if (elect_one()) commit(drained);
+    if (warp == 9 || warp == 10) {
+      const uint32_t bar = drained + 8 * (warp - 9);
+      if (elect_one()) commit(bar);
       __syncwarp();
-      landed &= drain_phase(drained, 0);
+      landed &= drain_phase(bar, 0);
     }
     if (!landed) {
       const long long t0 = clock64();
@@ -641,8 +710,7 @@ cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& 
       !encode(enc, &maps.k, k, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh) ||
       !encode(enc, &maps.v, v, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh))
     return cudaErrorInvalidValue;
-  TcGeom g = {p.Hq, p.G, p.d, rows, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh,
-              p.d % 32 == 0 && p.o_st % 16 == 0 && p.o_sh % 16 == 0 && (uintptr_t)out % 32 == 0, 4000000000LL};
+  TcGeom g = {p.Hq, p.G, p.d, rows, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL};
   if (p.d <= 64) return launch<64, MAXB>(maps, g, tab, v, out, err, sms, s);
   return launch<128, MAXB>(maps, g, tab, v, out, err, sms, s);
 }
