@@ -16,9 +16,9 @@
 // exponentials (512 cycles of the exponential unit) and about 200 other instructions
 // each to do.  So the tensor cores bound it as long as the softmax keeps up.
 //
-// The reference m of a row is the maximum of the first block in which it sees a key, and
-// stays while the row's sum is below 2^24: a common factor of P, O and the sum costs no
-// precision (bf16 and fp32 have the same exponents) and the final division removes it.
+// The reference m of a row is the maximum of some of its first logits and stays while
+// the row's sum is below 2^24: a common factor of P, O and the sum costs no precision
+// (bf16 and fp32 have the same exponents) and the final division removes it.
 // So a block has no maximum to find before its exponentials, and they need no more
 // than 64 logits in registers at a time.  A block that passes the bound is done over
 // with its maximum as the reference, O and the sum rescaled; S is still there, since
@@ -139,6 +139,19 @@ __device__ __forceinline__ float row_max(uint32_t tS, int seen, int lane) {
   return chunk_max<3>(rb, seen, lane, m);
 }
 
+// A first reference: the maximum over the last 32 columns that all of the warp's rows
+// reach into (any of a row's logits would do), or over all where a row sees none.
+__device__ __noinline__ float first_reference(uint32_t tS, int seen, int lane) {
+  if (seen - lane < 0) return row_max(tS, seen, lane);
+  const int first = min((seen - lane) >> 5, 3) * 32;
+  float r[32], m = -INFINITY;
+  tmem_ld32(tS + first, r);
+  tmem_wait(r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = fmaxf(m, first + i <= seen ? r[i] : -INFINITY);
+  return m;
+}
+
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
 // and a packed conversion.
 template <bool MASK, int C>
@@ -222,16 +235,16 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
   return make_float3(m, neg, l * f + sum);
 }
 
-// Adds to 32 staged output columns (from c0 on; piece k of the row at k ^ x) of a row the
-// non-finite values of the keys that it sees, which the check took out of the products.
-__device__ __noinline__ void add_non_finite(uint8_t* row, int piece, int x, const uint32_t* bad, int blocks, int keys,
+// Adds to the staged columns of a row (16-byte piece k at k ^ x) the non-finite values of
+// the keys that it sees, which the check took out of the products.
+__device__ __noinline__ void add_non_finite(uint8_t* row, int x, const uint32_t* bad, int blocks, int keys,
                                             const __nv_bfloat16* v, int64_t v_st, int columns) {
   for (int k = 0; k < blocks * kTile && k < keys; ++k) {
     if (!(bad[k >> 5] >> (k & 31) & 1)) continue;
     for (int i = 0; i < columns; ++i) {
       const __nv_bfloat16 y = v[k * v_st + i];
       if ((__bfloat16_as_ushort(y) & 0x7F80u) != 0x7F80u) continue;
-      __nv_bfloat16* o = (__nv_bfloat16*)(row + ((piece + (i >> 3)) ^ x) * 16) + (i & 7);
+      __nv_bfloat16* o = (__nv_bfloat16*)(row + ((i >> 3) ^ x) * 16) + (i & 7);
       *o = __float2bfloat16_rn(__bfloat162float(*o) + __bfloat162float(y));
     }
   }
@@ -316,7 +329,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         fence_after();
         const int seen = limit - j * kTile;                   // columns 0 .. seen
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float bm = row_max(tS, seen, lane);
+          const float bm = first_reference(tS, seen, lane);
           if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
             neg = -m * g.alpha;
@@ -358,38 +371,45 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       // 64 columns at a time through the warp's own staging rows, so that the stores are whole lines of a row:
       // 16-byte piece k of row r lies at k ^ (r & 7)
       uint8_t* stage = sOut + warp * kStageOut;
+      const int wr = t * kTile + (warp & 3) * 32;             // the warp's first row of the item
+      if (wr < it.rows) {
+        __nv_bfloat16* po = out + (int64_t)(it.q0 + wr + (lane >> 3)) * g.o_st + it.h * g.o_sh + (lane & 7) * 8;
+        const int64_t step = 4 * g.o_st;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        if (t * kTile + (warp & 3) * 32 >= it.rows || 32 * c >= g.d) break;     // the same for the whole warp
-        float o[32];
-        if (nb > 0) {
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait(o);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = nb > 0 ? o[i] * inv : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
-            w[e] = *(const uint32_t*)&b;
+        for (int c = 0; c < D / 64 && 64 * c < g.d; ++c) {
+          float oa[32], ob[32];
+          if (nb > 0) {
+            tmem_ld32(tO + 64 * c, oa);
+            tmem_ld32(tO + 64 * c + 32, ob);
+            tmem_wait(oa);
+            tmem_wait(ob);
           }
-          *(uint4*)(stage + lane * 128 + (((c & 1) * 4 + i) ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (flagged && live)
-          add_non_finite(stage + lane * 128, (c & 1) * 4, lane & 7, s_bad + slot * kMaxChecked * 4,
-                         min(it.nb - it.low, kMaxChecked), min(limit + 1, it.tk) - it.low * kTile,
-                         v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh + 32 * c, g.v_st, min(32, g.d - 32 * c));
-        if ((c & 1) || 32 * (c + 1) >= g.d) {                 // both halves of the 64 columns are there, or the last ones
-          __syncwarp();
-          const int k = lane & 7, col = (c >> 1) * 64 + k * 8;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), qr = t * kTile + (warp & 3) * 32 + r;
-            const uint4 w = *(const uint4*)(stage + r * 128 + (k ^ (r & 7)) * 16);
-            if (qr < it.rows && col < g.d) *(uint4*)(out + (int64_t)(it.q0 + qr) * g.o_st + it.h * g.o_sh + col) = w;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = (i & 3) * 8 + 2 * e;
+              const __nv_bfloat162 b = i < 4 ? __floats2bfloat162_rn(oa[k] * inv, oa[k + 1] * inv)
+                                             : __floats2bfloat162_rn(ob[k] * inv, ob[k + 1] * inv);
+              w[e] = nb > 0 ? *(const uint32_t*)&b : 0u;
+            }
+            *(uint4*)(stage + lane * 128 + (i ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (flagged && live)
+            add_non_finite(stage + lane * 128, lane & 7, s_bad + slot * kMaxChecked * 4, min(it.nb - it.low, kMaxChecked),
+                           min(limit + 1, it.tk) - it.low * kTile,
+                           v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh + 64 * c, g.v_st,
+                           min(64, g.d - 64 * c));
+          __syncwarp();
+          const bool inside = 64 * c + (lane & 7) * 8 < g.d;
+          __nv_bfloat16* pr = po + 64 * c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const uint4 w = *(const uint4*)(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+            if (inside && wr + r < it.rows) *(uint4*)pr = w;
+            pr += step;
           }
           __syncwarp();
         }
