@@ -3,7 +3,10 @@
 //
 //   O_i = sum_{j <= i + Tk - Tq} softmax_j(scale q_i . k_j) v_j
 //
-// A work item is one head's run of 256 query rows (two tiles of 128) of one sequence.
+// A work item is one head's run of 256 query rows (two tiles of 128) of one sequence, or
+// of its keys' part of kb blocks where whole items would leave SMs idle (few query rows
+// against many keys): then the parts' (m, l, O) go to the workspace, and the last one of a
+// tile to arrive adds them in order.
 // The CTA (one per SM, claiming items from a counter in the workspace, the longest
 // first) walks the keys in blocks of 128 and keeps for both tiles S = Q K^T (fp32, 128
 // columns) and O (fp32, D columns) in TMEM: 512 columns.  Per block and tile:
@@ -47,6 +50,7 @@ namespace {
 using namespace tcgen;
 
 constexpr int kTile = 128;                        // query rows of a tile, keys of a block
+constexpr int kRows = 2 * kTile;                  // query rows of an item
 constexpr int kStages = 4;                        // K and V blocks in shared memory (five were no faster)
 constexpr int kItemRing = 2;
 constexpr int kThreads = 384;                     // 12 warps, three warpgroups
@@ -59,6 +63,8 @@ template <int D> constexpr int block_bytes() { return kTile * D * 2; }
 constexpr int kPanel = kTile * 128;               // 128 rows x 64 elements
 constexpr int kStageOut = 32 * 128;               // a softmax warp's 32 rows x 64 output columns
 template <int D> constexpr int smem_bytes() { return (2 + kStages) * block_bytes<D>() + 1024 + 8 * kStageOut; }
+// A tile's part: O as [4 warps][D columns][32 lanes], then the rows' m and l.
+template <int D> constexpr int part_floats() { return kTile * (D + 2); }
 template <int N> constexpr uint32_t idesc() {     // fp32 D, bf16 A and B, M = 128
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
@@ -66,11 +72,13 @@ constexpr uint32_t kOuterMajorB = 1u << 16;
 
 struct TcGeom {
   int32_t Hq, G, d;
-  int32_t rows;                                   // query rows of an item: 256, or 128 for few items
+  int32_t kb;                                     // key blocks of an item at most (0: items are whole)
   int32_t n_items;
   float alpha;
   int64_t v_st, v_sh, o_st, o_sh;                 // element strides of v and out
   long long timeout;
+  int32_t* arrived;                               // [n_items][2] parts of a tile that have arrived, zero between calls
+  float* part;                                    // [n_items][2][part_floats<D>()]
 };
 struct TcMaps { CUtensorMap q, k, v; };
 
@@ -82,9 +90,10 @@ struct Item {
   int nb0, nb1;                                   // key blocks of the two tiles
   int nb;                                         // blocks walked
   int low;                                        // blocks low .. nb - 1 hold keys hidden to some row
+  int s, parts0, parts1;                          // the item's part, and how many each tile has (SPLIT)
 };
 
-template <int MAXB>
+template <bool SPLIT, int MAXB>
 __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<MAXB>& tab, int item) {
   Item it;
   const int u = item / g.Hq;
@@ -92,15 +101,29 @@ __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<
   it.hk = it.h / g.G;
   const int i = find_seq(tab, u);
   const PrefillSeq sq = tab.seq[i];
-  const int r0 = (tab.uoff[i + 1] - 1 - u) * g.rows;        // later rows see more keys: they come first
+  const int unit = tab.uoff[i + 1] - 1 - u, ns = SPLIT ? sq.ns : 1;
+  const int r0 = unit / ns * kRows;               // later rows see more keys: they come first
+  it.s = SPLIT ? ns - 1 - unit % ns : 0;          // item - s Hq is the tile's first part
   it.q0 = sq.q0 + r0;
+  it.rows = min(kRows, sq.tq - r0);
   it.k0 = sq.k0;
   it.tk = sq.tk;
-  it.rows = min(g.rows, sq.tq - r0);
-  it.limit = r0 + sq.tk - sq.tq;
+  it.limit = r0 + sq.tk - sq.tq;                  // last key that the first row sees
   const int last0 = it.limit + min(it.rows, kTile) - 1, last1 = it.limit + it.rows - 1;
   it.nb0 = last0 < 0 ? 0 : last0 / kTile + 1;
   it.nb1 = it.rows <= kTile || last1 < 0 ? 0 : last1 / kTile + 1;
+  it.parts0 = it.parts1 = 1;
+  if (SPLIT) {
+    it.parts0 = (it.nb0 + g.kb - 1) / g.kb;
+    it.parts1 = (it.nb1 + g.kb - 1) / g.kb;
+    // from here on counted from the part's first key
+    const int b0 = it.s * g.kb;
+    it.k0 += b0 * kTile;
+    it.tk -= b0 * kTile;
+    it.limit -= b0 * kTile;
+    it.nb0 = min(max(it.nb0 - b0, 0), g.kb);
+    it.nb1 = min(max(it.nb1 - b0, 0), g.kb);
+  }
   it.nb = max(it.nb0, it.nb1);
   it.low = max(it.limit + 1, 0) / kTile;
   return it;
@@ -250,7 +273,71 @@ __device__ __noinline__ void add_non_finite(uint8_t* row, int x, const uint32_t*
   }
 }
 
-template <int D, int MAXB>
+// The same for a part in the workspace (a lane's columns 32 floats apart).
+__device__ __noinline__ void add_non_finite_part(float* o, const uint32_t* bad, int blocks, int keys,
+                                                 const __nv_bfloat16* v, int64_t v_st, int columns) {
+  for (int k = 0; k < blocks * kTile && k < keys; ++k) {
+    if (!(bad[k >> 5] >> (k & 31) & 1)) continue;
+    for (int i = 0; i < columns; ++i) {
+      const __nv_bfloat16 y = v[k * v_st + i];
+      if ((__bfloat16_as_ushort(y) & 0x7F80u) == 0x7F80u) o[32 * i] += __bfloat162float(y);
+    }
+  }
+}
+
+// A warp's rows of a tile's part to the workspace, a lane per row: whole lines per column.
+template <int D>
+__device__ __noinline__ void store_part(float* part, uint32_t tO, float m, float l, int row) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(tO + 32 * c, o);
+    tmem_wait(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * 32, o[i]);
+  }
+  float* ml = part - (row >> 5) * (D * 32) - (row & 31) + kTile * D;
+  __stcg(ml + row, m);
+  __stcg(ml + kTile + row, l);
+}
+
+// Eight output columns as they are written, to a 16-byte piece.
+__device__ __forceinline__ void put8(uint8_t* piece, const float* o) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+    w[e] = *(const uint32_t*)&b;
+  }
+  *(uint4*)piece = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 64 columns of a row from the parts of its tile, added in their order, to the row's
+// staging pieces.  at: the columns' place in a part.
+template <int D>
+__device__ __noinline__ void join_parts(const float* p0, int64_t next, int parts, int at, int row, float alpha,
+                                        uint8_t* stage_row, int x) {
+  float M = -INFINITY, L = 0.f, o[64];
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(p0 + k * next + kTile * D + row));
+  const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < 64; ++i) o[i] = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < parts; ++k) {
+    const float* p = p0 + k * next;
+    const float f = ex2((__ldcg(p + kTile * D + row) - ref) * alpha);
+    L = fmaf(__ldcg(p + kTile * D + kTile + row), f, L);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) o[i] = fmaf(__ldcg(p + at + 32 * i), f, o[i]);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int i = 0; i < 64; ++i) o[i] *= inv;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) put8(stage_row + (i ^ x) * 16, o + 8 * i);
+}
+
+template <int D, bool SPLIT, int MAXB>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcGeom g,
                   const __grid_constant__ PrefillTable<MAXB> tab, const __nv_bfloat16* __restrict__ v,
@@ -265,22 +352,23 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   uint8_t* sKV = smem + 2 * kBlock;               // kStages blocks: K, V, K, V ... of descending blocks
   uint64_t* bars = (uint64_t*)(sKV + kStages * kBlock);
   const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;      // drained: [2]
-  const uint32_t turn = q_full + 32, s_full = q_full + 48, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
+  const uint32_t turn = q_full + 32, joined = q_full + 48, s_full = q_full + 64, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
   const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages, v_ok = kv_empty + 8 * kStages;
   const uint32_t item_full = v_ok + 8 * kStages, item_empty = item_full + 8 * kItemRing;
   const uint32_t checked = item_empty + 8 * kItemRing;                                     // [kItemRing]
-  constexpr int kBars = 6 + 6 + 3 * kStages + 3 * kItemRing;
+  constexpr int kBars = 8 + 6 + 3 * kStages + 3 * kItemRing;
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* s_items = abort_flag + 1;                                                  // [kItemRing]
   uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);     // [kItemRing][kMaxChecked][4] keys, a bit each
-  static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked <= 1024, "control block");
+  static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked + 8 <= 1024, "control block");
 
   uint8_t* sOut = (uint8_t*)bars + 1024;           // [8][kStageOut]
+  volatile int* s_last = (volatile int*)(s_bad + kItemRing * kMaxChecked * 4);           // [2]
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
-    mbar_init(turn, 1); mbar_init(turn + 8, 1);
+    mbar_init(turn, 1); mbar_init(turn + 8, 1); mbar_init(joined, 128); mbar_init(joined + 8, 128);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
     for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 2); mbar_init(v_ok + 8 * i, 1); }
     // an item's slot is released by the MMA issuers, the checking warp and each softmax warp
@@ -311,14 +399,14 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = lanes + t * kTile, tO = lanes + 256 + t * kTile;
-    uint32_t sc = 0, oc = 0, cc = 0;              // phases of s_full, o_full and (a bit per slot) checked
+    uint32_t sc = 0, oc = 0, cc = 0, jc = 0;      // phases of s_full, o_full, (a bit per slot) checked and joined
     pdl_wait();
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
       if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
       const int item = s_items[slot];
       if (item < 0) break;
-      const Item it = decode_item(g, tab, item);
+      const Item it = decode_item<SPLIT>(g, tab, item);
       const int nb = t ? it.nb1 : it.nb0;
       const int limit = it.limit + t * kTile + row;           // last key that this row sees
       float m = -INFINITY, neg = 0.f, l = 0.f;                // the row's reference, -m alpha, and its sum
@@ -372,31 +460,61 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       // 16-byte piece k of row r lies at k ^ (r & 7)
       uint8_t* stage = sOut + warp * kStageOut;
       const int wr = t * kTile + (warp & 3) * 32;             // the warp's first row of the item
-      if (wr < it.rows) {
+      // one part: straight from O; several: this part's (m, l, O) to the workspace, and once all are there, their sum
+      const int parts = t ? it.parts1 : it.parts0;
+      float* part = g.part + ((int64_t)item * 2 + t) * part_floats<D>() + (warp & 3) * (D * 32) + lane;
+      bool write = wr < it.rows && (!SPLIT || (parts > 1 ? nb > 0 : it.s == 0));
+      if (SPLIT && parts > 1 && nb > 0 && t * kTile < it.rows) {
+        store_part<D>(part, tO, m, l, row);
+        if (flagged && live)
+          add_non_finite_part(part, s_bad + slot * kMaxChecked * 4, min(it.nb - it.low, kMaxChecked),
+                              min(limit + 1, it.tk) - it.low * kTile,
+                              v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh, g.v_st, g.d);
+        __threadfence();
+        mbar_arrive(joined + 8 * t);              // this thread's part is out
+        if (!wait_warp(ctl, joined + 8 * t, jc & 1, kDevTimeoutEpilogue)) break;
+        if (row == 0) {
+          int32_t* count = g.arrived + ((int64_t)(item - it.s * g.Hq) * 2 + t);
+          const bool last = atomicAdd(count, 1) == parts - 1;
+          if (last) *count = 0;                   // as the next call expects it
+          s_last[t] = last;
+          __threadfence();
+        }
+        __syncwarp();
+        mbar_arrive(joined + 8 * t);
+        if (!wait_warp(ctl, joined + 8 * t, (jc + 1) & 1, kDevTimeoutEpilogue)) break;
+        jc += 2;
+        write = write && s_last[t];
+      }
+      if (write) {
         __nv_bfloat16* po = out + (int64_t)(it.q0 + wr + (lane >> 3)) * g.o_st + it.h * g.o_sh + (lane & 7) * 8;
         const int64_t step = 4 * g.o_st;
 #pragma unroll 1
         for (int c = 0; c < D / 64 && 64 * c < g.d; ++c) {
-          float oa[32], ob[32];
-          if (nb > 0) {
-            tmem_ld32(tO + 64 * c, oa);
-            tmem_ld32(tO + 64 * c + 32, ob);
-            tmem_wait(oa);
-            tmem_wait(ob);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = (i & 3) * 8 + 2 * e;
-              const __nv_bfloat162 b = i < 4 ? __floats2bfloat162_rn(oa[k] * inv, oa[k + 1] * inv)
-                                             : __floats2bfloat162_rn(ob[k] * inv, ob[k + 1] * inv);
-              w[e] = nb > 0 ? *(const uint32_t*)&b : 0u;
+          if (SPLIT && parts > 1) {
+            join_parts<D>(g.part + ((int64_t)(item - it.s * g.Hq) * 2 + t) * part_floats<D>(),
+                          (int64_t)g.Hq * 2 * part_floats<D>(), parts, (warp & 3) * (D * 32) + 64 * c * 32 + lane, row, g.alpha,
+                          stage + lane * 128, lane & 7);
+          } else {
+            float oa[32], ob[32];
+            if (nb > 0) {
+              tmem_ld32(tO + 64 * c, oa);
+              tmem_ld32(tO + 64 * c + 32, ob);
+              tmem_wait(oa);
+              tmem_wait(ob);
             }
-            *(uint4*)(stage + lane * 128 + (i ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              oa[i] = nb > 0 ? oa[i] * inv : 0.f;             // no key at all: zeros
+              ob[i] = nb > 0 ? ob[i] * inv : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              put8(stage + lane * 128 + (i ^ (lane & 7)) * 16, oa + 8 * i);
+              put8(stage + lane * 128 + ((4 + i) ^ (lane & 7)) * 16, ob + 8 * i);
+            }
           }
-          if (flagged && live)
+          if (flagged && live && (!SPLIT || parts <= 1))
             add_non_finite(stage + lane * 128, lane & 7, s_bad + slot * kMaxChecked * 4, min(it.nb - it.low, kMaxChecked),
                            min(limit + 1, it.tk) - it.low * kTile,
                            v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh + 64 * c, g.v_st,
@@ -432,7 +550,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         s_items[slot] = item;
         mbar_arrive(item_full + 8 * slot);
         if (item < 0) break;
-        const Item it = decode_item(g, tab, item);
+        const Item it = decode_item<SPLIT>(g, tab, item);
         for (int b = 0; b < 2 * it.nb && ok; ++b) {
           if (b == 2) {
             // the queries after the first K and V blocks: the last item's products still read the old ones
@@ -504,7 +622,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         const int item = __shfl_sync(0xffffffffu, s_items[slot], 0);
         if (lane == 0) mbar_arrive(item_empty + 8 * slot);
         if (item < 0) break;
-        const Item it = decode_item(g, tab, item);
+        const Item it = decode_item<SPLIT>(g, tab, item);
         if (it.nb == 0) continue;
         const int nb = t ? it.nb1 : it.nb0;
         bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma);
@@ -581,7 +699,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
         const int item = s_items[slot];
         if (item < 0) break;
-        const Item it = decode_item(g, tab, item);
+        const Item it = decode_item<SPLIT>(g, tab, item);
         uint32_t* bad_keys = s_bad + slot * kMaxChecked * 4;
         for (int i = lane; i < kMaxChecked * 4; i += 32) bad_keys[i] = 0;
         __syncwarp();
@@ -704,25 +822,32 @@ bool encode(EncodeFn enc, CUtensorMap* map, const void* base, int d, int heads, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MAXB>
+template <int D, bool SPLIT, int MAXB>
 cudaError_t launch(const TcMaps& maps, const TcGeom& g, const PrefillTable<MAXB>& tab, const void* v, void* out,
                    int32_t* err, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = raise_smem(prefill_tc_kernel<D, MAXB>, smem_bytes<D>(), done);
+  const cudaError_t e = raise_smem(prefill_tc_kernel<D, SPLIT, MAXB>, smem_bytes<D>(), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_tc_kernel<D, MAXB>, dim3(std::min(g.n_items, sms)), dim3(kThreads), (size_t)smem_bytes<D>(), s,
+  return launch_pdl(prefill_tc_kernel<D, SPLIT, MAXB>, dim3(std::min(g.n_items, sms)), dim3(kThreads), (size_t)smem_bytes<D>(), s,
                     maps, g, tab, (const __nv_bfloat16*)v, (__nv_bfloat16*)out, err, err + kSchedWord);
 }
 
 }  // namespace
 
-// Query rows of a work item.
-int prefill_tc_rows() { return 2 * kTile; }
+// Query rows of a work item and keys of a block.
+int prefill_tc_rows() { return kRows; }
+int prefill_tc_block() { return kTile; }
+
+// The workspace that split items need: counters, then parts.
+size_t prefill_tc_counter_bytes(int64_t n_items) { return (size_t)(n_items * 2 * 4 + 255) / 256 * 256; }
+size_t prefill_tc_part_bytes(int64_t n_items, int d) {
+  return (size_t)n_items * 2 * (d <= 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
+}
 
 template <int MAXB>
-cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int rows, int q_total, int k_total,
-                              const void* q, const void* k, const void* v, void* out, int32_t* err, int sms,
-                              cudaStream_t s) {
+cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int kb, int q_total, int k_total,
+                              const void* q, const void* k, const void* v, void* out, int32_t* err, int32_t* arrived,
+                              float* part, int sms, cudaStream_t s) {
   const EncodeFn enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
   static thread_local TcMaps maps;
@@ -730,15 +855,17 @@ cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& 
       !encode(enc, &maps.k, k, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh) ||
       !encode(enc, &maps.v, v, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh))
     return cudaErrorInvalidValue;
-  TcGeom g = {p.Hq, p.G, p.d, rows, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL};
-  if (p.d <= 64) return launch<64, MAXB>(maps, g, tab, v, out, err, sms, s);
-  return launch<128, MAXB>(maps, g, tab, v, out, err, sms, s);
+  TcGeom g = {p.Hq, p.G, p.d, kb, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL,
+              arrived, part};
+  if (kb > 0)
+    return p.d <= 64 ? launch<64, true>(maps, g, tab, v, out, err, sms, s) : launch<128, true>(maps, g, tab, v, out, err, sms, s);
+  return p.d <= 64 ? launch<64, false>(maps, g, tab, v, out, err, sms, s) : launch<128, false>(maps, g, tab, v, out, err, sms, s);
 }
 template cudaError_t launch_prefill_tc<kSmallBatch>(const PrefillTable<kSmallBatch>&, const PrefillGeom&, int, int, int,
-                                                    const void*, const void*, const void*, void*, int32_t*, int,
-                                                    cudaStream_t);
+                                                    const void*, const void*, const void*, void*, int32_t*,
+                                                    int32_t*, float*, int, cudaStream_t);
 template cudaError_t launch_prefill_tc<CHUNKKV_MAX_BATCH>(const PrefillTable<CHUNKKV_MAX_BATCH>&, const PrefillGeom&,
                                                           int, int, int, const void*, const void*, const void*, void*,
-                                                          int32_t*, int, cudaStream_t);
+                                                          int32_t*, int32_t*, float*, int, cudaStream_t);
 
 }  // namespace chunkkv

@@ -12,15 +12,16 @@ namespace chunkkv {
 // first, so that the last items to start are short), with the q tile offsets.
 struct PrefillSeq {
   int32_t q0, tq, k0, tk;          // first packed row and length of its queries and of its keys
+  int32_t ns;                      // parts into which the keys of its q tiles are split (1: whole)
 };
 template <int MAXB>
 struct PrefillTable {
   int32_t B;
-  int32_t uoff[MAXB + 1];          // q tiles before sequence i
+  int32_t uoff[MAXB + 1];          // units (q tiles x parts) before sequence i
   PrefillSeq seq[MAXB];
 };
-// Two sizes of the table, which travels as a kernel argument: 0.7 KB for batches of
-// up to 32 sequences and 20 KB above (a launch copies its arguments).
+// Two sizes of the table, which travels as a kernel argument: 0.8 KB for batches of
+// up to 32 sequences and 24 KB above (a launch copies its arguments).
 constexpr int kSmallBatch = 32;
 
 struct PrefillGeom {
@@ -29,7 +30,7 @@ struct PrefillGeom {
   int64_t q_st, q_sh, kv_st, kv_sh, o_st, o_sh;   // element strides (token, head)
 };
 
-// Sequence index of q tile u.
+// Sequence index of unit u.
 template <int MAXB>
 __device__ __forceinline__ int find_seq(const PrefillTable<MAXB>& t, int u) {
   int lo = 0, hi = t.B;            // uoff[lo] <= u < uoff[hi]

@@ -13,10 +13,13 @@ template <int MAXB>
 cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q,
                                 const void* k, const void* v, void* out, cudaStream_t s);
 int prefill_tc_rows();                                                                 // prefill_tc.cu
+int prefill_tc_block();
+size_t prefill_tc_counter_bytes(int64_t n_items);
+size_t prefill_tc_part_bytes(int64_t n_items, int d);
 template <int MAXB>
-cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int rows, int q_total, int k_total,
-                              const void* q, const void* k, const void* v, void* out, int32_t* err, int sms,
-                              cudaStream_t s);
+cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int kb, int q_total, int k_total,
+                              const void* q, const void* k, const void* v, void* out, int32_t* err, int32_t* arrived,
+                              float* part, int sms, cudaStream_t s);
 cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* lens, int32_t* table, int32_t* ring,
                              int32_t* state, int64_t* slots, int n_cap, int sms, cudaStream_t s);   // q8_cache.cu
 cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
@@ -78,9 +81,10 @@ chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
   return CHUNKKV_OK;
 }
 
-// The sequences by descending number of keys (ties in order), with their q tiles of `tile` rows.
+// The sequences by descending number of keys (ties in order), with their units: q tiles of `tile` rows, times the
+// parts of at most kb key blocks that the last tile's keys make (kb = 0: whole).
 template <int MAXB>
-void fill_table(const chunkkv_prefill_params* p, int tile, PrefillTable<MAXB>& t) {
+void fill_table(const chunkkv_prefill_params* p, int tile, int kb, PrefillTable<MAXB>& t) {
   int32_t order[MAXB];
   t.B = 0;
   for (int b = 0; b < p->B; ++b)
@@ -93,11 +97,45 @@ void fill_table(const chunkkv_prefill_params* p, int tile, PrefillTable<MAXB>& t
   int32_t u = 0;
   for (int i = 0; i < t.B; ++i) {
     const int b = order[i];
-    t.seq[i] = {p->cu_q[b], p->cu_q[b + 1] - p->cu_q[b], ck[b], ck[b + 1] - ck[b]};
+    const int32_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = ck[b + 1] - ck[b];
+    const int32_t blocks = (int32_t)(((int64_t)tk + prefill_tc_block() - 1) / prefill_tc_block());
+    const int32_t ns = kb > 0 && blocks > kb ? (blocks - 1) / kb + 1 : 1;
+    t.seq[i] = {p->cu_q[b], tq, ck[b], tk, ns};
     t.uoff[i] = u;
-    u += (t.seq[i].tq - 1) / tile + 1;
+    u += ((tq - 1) / tile + 1) * ns;
   }
   t.uoff[t.B] = u;
+}
+
+// Key blocks of a work item at most (0: items are not split), and the number of items.
+//
+// Whole items keep partial results out of memory (128 KB a part, written and read again, against 64 KB of keys
+// and values a block).  But where few query rows meet many keys, the longest item takes much longer than an even
+// share of the work for every SM; then the keys are split into parts of about that share.
+constexpr int64_t kMinPart = 8;                 // blocks of a part at least
+
+void plan_items(const chunkkv_prefill_params* p, int sms, int* kb, int64_t* n_items) {
+  const int64_t rows = prefill_tc_rows(), block = prefill_tc_block();
+  int64_t work = 0, longest = 0, units = 0;
+  for (int b = 0; b < p->B; ++b) {
+    const int64_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = p->cu_k[b + 1] - p->cu_k[b];
+    for (int64_t r = 0; r < tq; r += rows, ++units) {
+      const int64_t last = std::min(r + rows, tq) - 1 + tk - tq, n = last < 0 ? 0 : last / block + 1;
+      work += n;
+      longest = std::max(longest, n);
+    }
+  }
+  const int64_t share = work * p->Hq / sms;
+  *kb = 0;
+  *n_items = units * p->Hq;
+  if (longest < 2 * share + kMinPart) return;
+  *kb = (int)std::max<int64_t>(kMinPart, share + 1);
+  units = 0;
+  for (int b = 0; b < p->B; ++b) {
+    const int64_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = p->cu_k[b + 1] - p->cu_k[b];
+    units += (tq + rows - 1) / rows * std::max<int64_t>(1, ((tk + block - 1) / block + *kb - 1) / *kb);
+  }
+  *n_items = units * p->Hq;
 }
 
 // The tensor-core kernel: bf16 rows of up to 128 columns that tensor maps can address (no axis
@@ -121,21 +159,30 @@ bool device_pointer(const void* p) {
 }
 
 template <int MAXB>
-cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, const void* q, const void* k,
-                        const void* v, void* out, int32_t* err, cudaStream_t s) {
+cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, bool tc, int kb, int64_t n_items, const void* q,
+                        const void* k, const void* v, void* out, char* ws, cudaStream_t s) {
   static thread_local PrefillTable<MAXB> tab;
-  if (!prefill_on_tc(p)) {
-    fill_table(p, prefill_simt_tile(), tab);
+  if (!tc) {
+    fill_table(p, prefill_simt_tile(), 0, tab);
     return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
   }
-  const int sms = sm_count();
-  int rows = prefill_tc_rows();
-  fill_table(p, rows, tab);
-  if ((int64_t)tab.uoff[tab.B] * p->Hq < sms) {
-    rows /= 2;
-    fill_table(p, rows, tab);
-  }
-  return launch_prefill_tc(tab, g, rows, p->cu_q[p->B], p->cu_k[p->B], q, k, v, out, err, sms, s);
+  fill_table(p, prefill_tc_rows(), kb, tab);
+  return launch_prefill_tc(tab, g, kb, p->cu_q[p->B], p->cu_k[p->B], q, k, v, out, (int32_t*)ws,
+                           (int32_t*)(ws + kServeHeader),
+                           (float*)(ws + kServeHeader + (kb > 0 ? prefill_tc_counter_bytes(n_items) : 0)), sm_count(), s);
+}
+
+// How a call runs: on the tensor cores, in items of kb blocks (0: whole), and its workspace.
+chunkkv_status plan_prefill(const chunkkv_prefill_params* p, bool* tc, int* kb, int64_t* n_items, size_t* bytes) {
+  *tc = prefill_on_tc(p);
+  *kb = 0;
+  *n_items = 0;
+  *bytes = kServeHeader;
+  if (!*tc) return CHUNKKV_OK;
+  plan_items(p, sm_count(), kb, n_items);
+  if (*n_items > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
+  if (*kb > 0) *bytes += prefill_tc_counter_bytes(*n_items) + prefill_tc_part_bytes(*n_items, p->d);
+  return CHUNKKV_OK;
 }
 
 // The part of a cache that every call uses; `pages`: the call reads or writes them.
@@ -160,8 +207,11 @@ extern "C" {
 chunkkv_status chunkkv_prefill_workspace_size(const chunkkv_prefill_params* p, size_t* bytes) {
   if (bytes == nullptr) return CHUNKKV_ERR_INVALID_ARG;
   const chunkkv_status st = check_prefill(p);
-  if (st == CHUNKKV_OK) *bytes = kServeHeader;
-  return st;
+  if (st != CHUNKKV_OK) return st;
+  bool tc;
+  int kb;
+  int64_t n_items;
+  return plan_prefill(p, &tc, &kb, &n_items, bytes);
 }
 
 int32_t chunkkv_prefill_path(const chunkkv_prefill_params* p) {
@@ -178,13 +228,20 @@ chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const 
   const bool no_keys = p->cu_k[p->B] == 0;
   if (!aligned(q) || !aligned(out) || !aligned(ws) || (!no_keys && (!aligned(k) || !aligned(v))))
     return CHUNKKV_ERR_INVALID_ARG;
-  if (ws_bytes < kServeHeader) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
-  if (prefill_on_tc(p) && !(device_pointer(q) && device_pointer(k) && device_pointer(v))) return CHUNKKV_ERR_INVALID_ARG;
+  bool tc;
+  int kb;
+  int64_t n_items;
+  size_t need;
+  const chunkkv_status plan = plan_prefill(p, &tc, &kb, &n_items, &need);
+  if (plan != CHUNKKV_OK) return plan;
+  if (ws_bytes < need) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  if (tc && !(device_pointer(q) && device_pointer(k) && device_pointer(v))) return CHUNKKV_ERR_INVALID_ARG;
   PrefillGeom g = {p->Hq, p->Hkv, p->Hq / p->Hkv, p->d, (float)(p->scale * kLog2e), p->q_stride_t, p->q_stride_h,
                    p->kv_stride_t, p->kv_stride_h, p->o_stride_t, p->o_stride_h};
   const cudaStream_t cs = (cudaStream_t)stream;
-  return cuda_result(p->B <= kSmallBatch ? run_prefill<kSmallBatch>(p, g, q, k, v, out, (int32_t*)ws, cs)
-                                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, q, k, v, out, (int32_t*)ws, cs));
+  return cuda_result(p->B <= kSmallBatch
+                         ? run_prefill<kSmallBatch>(p, g, tc, kb, n_items, q, k, v, out, (char*)ws, cs)
+                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, tc, kb, n_items, q, k, v, out, (char*)ws, cs));
 }
 
 chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,

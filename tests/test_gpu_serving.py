@@ -94,10 +94,10 @@ def test_prefill_matches_the_formula(ckv, dtype, d, Hq, Hkv, lengths):
     q, k, v = make_qkv(tq, tk, Hq, Hkv, d, dtype, seed=d + Hq)
     cq, ck = offsets(tq), offsets(tk)
     out = torch.full_like(q, float("nan"))
-    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    p, keep = ckv.prefill_params_for(q, k, cq, ck)
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
     ckv.prefill_attention(q, k, v, cq, ck, out=out, workspace=ws)
     ckv.chunkkv_status_check(ws)
-    p, keep = ckv.prefill_params_for(q, k, cq, ck)
     check_prefill(out, q, k, v, cq, ck, 1 / math.sqrt(d), ckv.chunkkv_prefill_path(p))
 
 
@@ -162,6 +162,43 @@ def test_prefill_hidden_keys_may_hold_anything(ckv, dtype, d, bad):
     assert torch.equal(torch.isfinite(ref[130:]), torch.isfinite(out[130:300].double()))
 
 
+@pytest.mark.parametrize("tq,tk,Hq,Hkv,d", [([1], [9000], 8, 2, 128), ([37, 300, 3], [5000, 3001, 0], 4, 1, 64),
+                                            ([130, 1, 600], [4096, 130, 2600], 7, 7, 128), ([256], [8192], 2, 1, 80)])
+def test_prefill_few_rows_against_many_keys(ckv, tq, tk, Hq, Hkv, d):
+    # the keys of a tile in parts that different CTAs take and one of them joins; twice on one workspace
+    q, k, v = make_qkv(tq, tk, Hq, Hkv, d, BF, seed=17)
+    cq, ck = offsets(tq), offsets(tk)
+    p, keep = ckv.prefill_params_for(q, k, cq, ck)
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 256                                      # parts
+    outs = []
+    for _ in range(2):
+        out = torch.full_like(q, float("nan"))
+        ckv.chunkkv_prefill_attention(p, q, k, v, out, ws)
+        ckv.chunkkv_status_check(ws)
+        outs.append(out)
+    check_prefill(outs[0], q, k, v, cq, ck, 1 / math.sqrt(d), 1)
+    assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefill_hidden_keys_of_split_rows(ckv, bad):
+    # the last part holds the keys that some rows must not see
+    tq, tk = [200, 64], [6000, 3000]
+    q, k, v = make_qkv(tq, tk, 4, 2, 128, BF, seed=19)
+    cq, ck = offsets(tq), offsets(tk)
+    clean = ckv.prefill_attention(q, k, v, cq, ck)
+    vb, kb = v.clone(), k.clone()
+    spot = 6000 - 200 + 120                                      # first seen by query 120
+    vb[spot, :, 5] = bad
+    kb[6000 + 2999] = bad                                        # seen by the very last query alone
+    vb[6000 + 2999] = bad
+    out = ckv.prefill_attention(q, kb, vb, cq, ck)
+    assert torch.equal(out[:120], clean[:120]) and torch.equal(out[200:263], clean[200:263])
+    assert not torch.isfinite(out[120:200, :, 5]).any() and torch.isfinite(out[120:200, :, 6:]).all()
+    assert not torch.isfinite(out[263]).any()
+
+
 def test_prefill_fully_masked_rows_and_empty_calls(ckv):
     q, k, v = make_qkv([50], [0], 2, 2, 64, BF, seed=1)
     out = torch.full_like(q, float("nan"))
@@ -176,7 +213,8 @@ def test_prefill_on_another_stream_and_in_a_graph(ckv):
     T = 400
     q, k, v = make_qkv([T], [T], 4, 2, 128, BF, seed=2)
     want = ckv.prefill_attention(q, k, v, [0, T])
-    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    p, keep = ckv.prefill_params_for(q, k, [0, T])
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
     out = torch.zeros_like(q)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
