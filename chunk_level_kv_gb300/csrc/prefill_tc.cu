@@ -3,10 +3,12 @@
 //
 //   O_i = sum_{j <= i + Tk - Tq} softmax_j(scale q_i . k_j) v_j
 //
-// A work item is one head's run of 256 query rows (two tiles of 128) of one sequence, or
-// of its keys' part of kb blocks where whole items would leave SMs idle (few query rows
-// against many keys): then the parts' (m, l, O) go to the workspace, and the last one of a
-// tile to arrive adds them in order.
+// A work item is two tiles of 128 query rows of one sequence.  A tile's rows are the gp
+// query heads of a KV head (or of a part of its group) at 128 / gp consecutive positions,
+// row = position * gp + head, so that short prompts fill their tiles and a block of keys
+// and values serves every head of its group.  Where whole items would leave SMs idle
+// (few query rows against many keys), an item takes a part of the keys, kb blocks: the
+// parts' (m, l, O) go to the workspace, and a second launch adds them in order.
 // The CTA (one per SM, claiming items from a counter in the workspace, the longest
 // first) walks the keys in blocks of 128 and keeps for both tiles S = Q K^T (fp32, 128
 // columns) and O (fp32, D columns) in TMEM: 512 columns.  Per block and tile:
@@ -50,7 +52,6 @@ namespace {
 using namespace tcgen;
 
 constexpr int kTile = 128;                        // query rows of a tile, keys of a block
-constexpr int kRows = 2 * kTile;                  // query rows of an item
 constexpr int kStages = 4;                        // K and V blocks in shared memory (five were no faster)
 constexpr int kItemRing = 2;
 constexpr int kThreads = 384;                     // 12 warps, three warpgroups
@@ -71,22 +72,27 @@ template <int N> constexpr uint32_t idesc() {     // fp32 D, bf16 A and B, M = 1
 constexpr uint32_t kOuterMajorB = 1u << 16;
 
 struct TcGeom {
-  int32_t Hq, G, d;
+  int32_t groups;                                 // head groups of gp query heads
+  int32_t per_kv;                                 // of them per KV head
+  int32_t gp, inv_gp;                             // inv_gp: ceil(65536 / gp), to divide a row by gp
+  int32_t pos;                                    // positions of a tile, 128 / gp
+  int32_t d;
   int32_t kb;                                     // key blocks of an item at most (0: items are whole)
   int32_t n_items;
   float alpha;
   int64_t v_st, v_sh, o_st, o_sh;                 // element strides of v and out
   long long timeout;
-  int32_t* arrived;                               // [n_items][2] parts of a tile that have arrived, zero between calls
   float* part;                                    // [n_items][2][part_floats<D>()]
 };
 struct TcMaps { CUtensorMap q, k, v; };
 
+// The producer decodes an item once and hands it to the other roles in shared memory.
 struct Item {
-  int h, hk;
+  int item;                                       // -1: no more
+  int h, hk;                                      // its first query head, its KV head
   int q0, k0, tk;                                 // packed rows where the item's queries and the sequence's keys begin
-  int rows;                                       // query rows that exist
-  int limit;                                      // last key that the item's first row sees (may be negative)
+  int rows;                                       // positions that exist
+  int limit;                                      // last key that the item's first position sees (may be negative)
   int nb0, nb1;                                   // key blocks of the two tiles
   int nb;                                         // blocks walked
   int low;                                        // blocks low .. nb - 1 hold keys hidden to some row
@@ -96,22 +102,23 @@ struct Item {
 template <bool SPLIT, int MAXB>
 __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<MAXB>& tab, int item) {
   Item it;
-  const int u = item / g.Hq;
-  it.h = item - u * g.Hq;
-  it.hk = it.h / g.G;
+  it.item = item;
+  const int u = item / g.groups, hg = item - u * g.groups;
+  it.h = hg * g.gp;
+  it.hk = hg / g.per_kv;
   const int i = find_seq(tab, u);
   const PrefillSeq sq = tab.seq[i];
   const int unit = tab.uoff[i + 1] - 1 - u, ns = SPLIT ? sq.ns : 1;
-  const int r0 = unit / ns * kRows;               // later rows see more keys: they come first
-  it.s = SPLIT ? ns - 1 - unit % ns : 0;          // item - s Hq is the tile's first part
+  const int r0 = unit / ns * 2 * g.pos;           // later positions see more keys: they come first
+  it.s = SPLIT ? ns - 1 - unit % ns : 0;          // item - s groups is the tile's first part
   it.q0 = sq.q0 + r0;
-  it.rows = min(kRows, sq.tq - r0);
+  it.rows = min(2 * g.pos, sq.tq - r0);
   it.k0 = sq.k0;
   it.tk = sq.tk;
   it.limit = r0 + sq.tk - sq.tq;                  // last key that the first row sees
-  const int last0 = it.limit + min(it.rows, kTile) - 1, last1 = it.limit + it.rows - 1;
+  const int last0 = it.limit + min(it.rows, g.pos) - 1, last1 = it.limit + it.rows - 1;
   it.nb0 = last0 < 0 ? 0 : last0 / kTile + 1;
-  it.nb1 = it.rows <= kTile || last1 < 0 ? 0 : last1 / kTile + 1;
+  it.nb1 = it.rows <= g.pos || last1 < 0 ? 0 : last1 / kTile + 1;
   it.parts0 = it.parts1 = 1;
   if (SPLIT) {
     it.parts0 = (it.nb0 + g.kb - 1) / g.kb;
@@ -129,44 +136,34 @@ __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<
   return it;
 }
 
-// A 32-column chunk of a warp's rows at column `first`: all of it visible, some, or none
-// to any of them (`seen` - lane: what the warp's first row sees, 31 more for the last).
-__device__ __forceinline__ bool chunk_full(int first, int seen, int lane) { return first + 31 <= seen - lane; }
-__device__ __forceinline__ bool chunk_none(int first, int seen, int lane) { return first > seen - lane + 31; }
-
+// Row maximum over the columns 0 .. seen of S.
 template <int C>
-__device__ __forceinline__ float chunk_max(const float (&s)[32], int seen, int lane, float m) {
-  if (chunk_full(32 * C, seen, lane)) {
+__device__ __forceinline__ float chunk_max(const float (&s)[32], int seen, float m) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
-  } else if (!chunk_none(32 * C, seen, lane)) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m = fmaxf(m, 32 * C + i <= seen ? s[i] : -INFINITY);
-  }
+  for (int i = 0; i < 32; ++i) m = fmaxf(m, 32 * C + i <= seen ? s[i] : -INFINITY);
   return m;
 }
-// Row maximum over the columns 0 .. seen of S.
-__device__ __forceinline__ float row_max(uint32_t tS, int seen, int lane) {
+__device__ __forceinline__ float row_max(uint32_t tS, int seen) {
   float ra[32], rb[32], m = -INFINITY;
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  m = chunk_max<0>(ra, seen, lane, m);
+  m = chunk_max<0>(ra, seen, m);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  m = chunk_max<1>(rb, seen, lane, m);
+  m = chunk_max<1>(rb, seen, m);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  m = chunk_max<2>(ra, seen, lane, m);
+  m = chunk_max<2>(ra, seen, m);
   tmem_wait(rb);
-  return chunk_max<3>(rb, seen, lane, m);
+  return chunk_max<3>(rb, seen, m);
 }
-
 // A first reference: the maximum over the last 32 columns that all of the warp's rows
-// reach into (any of a row's logits would do), or over all where a row sees none.
-__device__ __noinline__ float first_reference(uint32_t tS, int seen, int lane) {
-  if (seen - lane < 0) return row_max(tS, seen, lane);
-  const int first = min((seen - lane) >> 5, 3) * 32;
+// reach into (any of a row's logits would do; lo: what the first of them sees), or over
+// all where a row sees none.
+__device__ __noinline__ float first_reference(uint32_t tS, int seen, int lo) {
+  if (lo < 0) return row_max(tS, seen);
+  const int first = min(lo >> 5, 3) * 32;
   float r[32], m = -INFINITY;
   tmem_ld32(tS + first, r);
   tmem_wait(r);
@@ -178,7 +175,7 @@ __device__ __noinline__ float first_reference(uint32_t tS, int seen, int lane) {
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
 // and a packed conversion.
 template <bool MASK, int C>
-__device__ __forceinline__ void exp_pairs(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
+__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
                                           uint32_t (&p)[64]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -193,37 +190,25 @@ __device__ __forceinline__ void exp_pairs(const float (&s)[32], float2 a2, float
     p[16 * C + i] = *(const uint32_t*)&b;
   }
 }
-template <bool MASK, int C>
-__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, int lane,
-                                          float2 (&sum)[2], uint32_t (&p)[64]) {
-  if (!MASK || chunk_full(32 * C, seen, lane)) {
-    exp_pairs<false, C>(s, a2, n2, seen, sum, p);
-  } else if (!chunk_none(32 * C, seen, lane)) {
-    exp_pairs<true, C>(s, a2, n2, seen, sum, p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[16 * C + i] = 0;
-  }
-}
-// A row's P under the reference -neg, and its sum.  Without MASK it is straight-line
-// code: a branch per chunk cost 400 cycles of a block's 1000.
+// A row's P under the reference -neg, and its sum.  Straight-line code: a branch per
+// chunk cost 400 cycles of a block's 1000.
 template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, int lane, uint32_t (&p)[64]) {
+__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, uint32_t (&p)[64]) {
   float ra[32], rb[32];
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 a2 = make_float2(alpha, alpha), n2 = make_float2(neg, neg);
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  chunk_exp<MASK, 0>(ra, a2, n2, seen, lane, sum, p);
+  chunk_exp<MASK, 0>(ra, a2, n2, seen, sum, p);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  chunk_exp<MASK, 1>(rb, a2, n2, seen, lane, sum, p);
+  chunk_exp<MASK, 1>(rb, a2, n2, seen, sum, p);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  chunk_exp<MASK, 2>(ra, a2, n2, seen, lane, sum, p);
+  chunk_exp<MASK, 2>(ra, a2, n2, seen, sum, p);
   tmem_wait(rb);
-  chunk_exp<MASK, 3>(rb, a2, n2, seen, lane, sum, p);
+  chunk_exp<MASK, 3>(rb, a2, n2, seen, sum, p);
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
@@ -232,9 +217,8 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, in
 // hold goes with it.  Returns (m, -m alpha, l); P is written.  Out of line, as the next
 // function: the loop around it has to stay in the instruction cache.
 template <int D>
-__device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, int seen, int lane,
-                                           bool over) {
-  const float bm = row_max(tS, seen, lane);
+__device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, int seen, bool over) {
+  const float bm = row_max(tS, seen);
   const float mn = fmaxf(m, bm);
   const float f = over ? ex2((m - mn) * alpha) : 1.f;
   if (over) m = mn;
@@ -252,53 +236,10 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
     }
   }
   uint32_t p[64];
-  const float sum = row_exp<true>(tS, alpha, neg, seen, lane, p);
+  const float sum = row_exp<true>(tS, alpha, neg, seen, p);
   tmem_st32<0>(tS, p);
   tmem_st32<32>(tS + 32, p);
   return make_float3(m, neg, l * f + sum);
-}
-
-// Adds to the staged columns of a row (16-byte piece k at k ^ x) the non-finite values of
-// the keys that it sees, which the check took out of the products.
-__device__ __noinline__ void add_non_finite(uint8_t* row, int x, const uint32_t* bad, int blocks, int keys,
-                                            const __nv_bfloat16* v, int64_t v_st, int columns) {
-  for (int k = 0; k < blocks * kTile && k < keys; ++k) {
-    if (!(bad[k >> 5] >> (k & 31) & 1)) continue;
-    for (int i = 0; i < columns; ++i) {
-      const __nv_bfloat16 y = v[k * v_st + i];
-      if ((__bfloat16_as_ushort(y) & 0x7F80u) != 0x7F80u) continue;
-      __nv_bfloat16* o = (__nv_bfloat16*)(row + ((i >> 3) ^ x) * 16) + (i & 7);
-      *o = __float2bfloat16_rn(__bfloat162float(*o) + __bfloat162float(y));
-    }
-  }
-}
-
-// The same for a part in the workspace (a lane's columns 32 floats apart).
-__device__ __noinline__ void add_non_finite_part(float* o, const uint32_t* bad, int blocks, int keys,
-                                                 const __nv_bfloat16* v, int64_t v_st, int columns) {
-  for (int k = 0; k < blocks * kTile && k < keys; ++k) {
-    if (!(bad[k >> 5] >> (k & 31) & 1)) continue;
-    for (int i = 0; i < columns; ++i) {
-      const __nv_bfloat16 y = v[k * v_st + i];
-      if ((__bfloat16_as_ushort(y) & 0x7F80u) == 0x7F80u) o[32 * i] += __bfloat162float(y);
-    }
-  }
-}
-
-// A warp's rows of a tile's part to the workspace, a lane per row: whole lines per column.
-template <int D>
-__device__ __noinline__ void store_part(float* part, uint32_t tO, float m, float l, int row) {
-#pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    float o[32];
-    tmem_ld32(tO + 32 * c, o);
-    tmem_wait(o);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * 32, o[i]);
-  }
-  float* ml = part - (row >> 5) * (D * 32) - (row & 31) + kTile * D;
-  __stcg(ml + row, m);
-  __stcg(ml + kTile + row, l);
 }
 
 // Eight output columns as they are written, to a 16-byte piece.
@@ -312,29 +253,86 @@ __device__ __forceinline__ void put8(uint8_t* piece, const float* o) {
   *(uint4*)piece = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 64 columns of a row from the parts of its tile, added in their order, to the row's
-// staging pieces.  at: the columns' place in a part.
-template <int D>
-__device__ __noinline__ void join_parts(const float* p0, int64_t next, int parts, int at, int row, float alpha,
-                                        uint8_t* stage_row, int x) {
-  float M = -INFINITY, L = 0.f, o[64];
-  for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(p0 + k * next + kTile * D + row));
-  const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-  for (int i = 0; i < 64; ++i) o[i] = 0.f;
-#pragma unroll 1
-  for (int k = 0; k < parts; ++k) {
-    const float* p = p0 + k * next;
-    const float f = ex2((__ldcg(p + kTile * D + row) - ref) * alpha);
-    L = fmaf(__ldcg(p + kTile * D + kTile + row), f, L);
-#pragma unroll
-    for (int i = 0; i < 64; ++i) o[i] = fmaf(__ldcg(p + at + 32 * i), f, o[i]);
+// The keys with non-finite values that a row sees: a bit per key (null: none), their
+// number, and the values of the first.
+struct Bad {
+  const uint32_t* keys;
+  int n;
+  const __nv_bfloat16* v;
+};
+// Calls add(column, value) for each such value in columns c0 .. c1 - 1.
+template <typename F>
+__device__ __forceinline__ void each_bad(const Bad& bad, int64_t v_st, int c0, int c1, F add) {
+  for (int k = 0; k < bad.n; ++k) {
+    if (!(bad.keys[k >> 5] >> (k & 31) & 1)) continue;
+    for (int i = c0; i < c1; ++i) {
+      const __nv_bfloat16 y = bad.v[k * v_st + i];
+      if ((__bfloat16_as_ushort(y) & 0x7F80u) == 0x7F80u) add(i, __bfloat162float(y));
+    }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+}
+
+// A warp's rows of the output, 64 columns at a time through the warp's own staging rows,
+// so that the stores are whole lines of a row: 16-byte piece k of row r lies at k ^ (r & 7).
+// out: the tile's first position and head; left: positions of it that exist; tO:
+// 0xFFFFFFFF for rows without any key.  Out of line: its registers would be taken from
+// the loop over the blocks (1320 cycles a block for 1020).
+template <int D>
+__device__ __noinline__ void write_rows(const TcGeom& g, __nv_bfloat16* out, int left, uint32_t tO, float inv, uint8_t* stage,
+                                        int row, Bad bad) {
+  const int lane = row & 31;
+  out += (lane & 7) * 8;
+#pragma unroll 1
+  for (int c = 0; c < D / 64 && 64 * c < g.d; ++c) {
+    float oa[32], ob[32];
+    if (tO != 0xFFFFFFFFu) {
+      tmem_ld32(tO + 64 * c, oa);
+      tmem_ld32(tO + 64 * c + 32, ob);
+      tmem_wait(oa);
+      tmem_wait(ob);
+    }
 #pragma unroll
-  for (int i = 0; i < 64; ++i) o[i] *= inv;
+    for (int i = 0; i < 32; ++i) {
+      oa[i] = tO != 0xFFFFFFFFu ? oa[i] * inv : 0.f;
+      ob[i] = tO != 0xFFFFFFFFu ? ob[i] * inv : 0.f;
+    }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) put8(stage_row + (i ^ x) * 16, o + 8 * i);
+    for (int i = 0; i < 4; ++i) {
+      put8(stage + lane * 128 + (i ^ (lane & 7)) * 16, oa + 8 * i);
+      put8(stage + lane * 128 + ((4 + i) ^ (lane & 7)) * 16, ob + 8 * i);
+    }
+    if (bad.keys)
+      each_bad(bad, g.v_st, 64 * c, min(64 * c + 64, g.d), [&](int i, float y) {
+        __nv_bfloat16* o = (__nv_bfloat16*)(stage + lane * 128 + (((i >> 3) & 7) ^ (lane & 7)) * 16) + (i & 7);
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + y);
+      });
+    __syncwarp();
+    const bool inside = 64 * c + (lane & 7) * 8 < g.d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3), tr = row - lane + r, pos = (tr * g.inv_gp) >> 16;
+      const uint4 w = *(const uint4*)(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+      if (inside && pos < left) *(uint4*)(out + pos * g.o_st + (tr - pos * g.gp) * g.o_sh + 64 * c) = w;
+    }
+    __syncwarp();
+  }
+}
+
+// A warp's rows of a tile's part to the workspace, a lane per row: whole lines per column.
+template <int D>
+__device__ __noinline__ void store_part(const TcGeom& g, float* part, uint32_t tO, float m, float l, int row, Bad bad) {
+  float* po = part + (row >> 5) * (D * 32) + (row & 31);
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(tO + 32 * c, o);
+    tmem_wait(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) __stcg(po + (32 * c + i) * 32, o[i]);
+  }
+  if (bad.keys) each_bad(bad, g.v_st, 0, g.d, [&](int i, float y) { po[32 * i] += y; });
+  __stcg(part + kTile * D + row, m);
+  __stcg(part + kTile * D + kTile + row, l);
 }
 
 template <int D, bool SPLIT, int MAXB>
@@ -352,23 +350,23 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
   uint8_t* sKV = smem + 2 * kBlock;               // kStages blocks: K, V, K, V ... of descending blocks
   uint64_t* bars = (uint64_t*)(sKV + kStages * kBlock);
   const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;      // drained: [2]
-  const uint32_t turn = q_full + 32, joined = q_full + 48, s_full = q_full + 64, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
+  const uint32_t turn = q_full + 32, s_full = q_full + 48, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
   const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages, v_ok = kv_empty + 8 * kStages;
   const uint32_t item_full = v_ok + 8 * kStages, item_empty = item_full + 8 * kItemRing;
   const uint32_t checked = item_empty + 8 * kItemRing;                                     // [kItemRing]
-  constexpr int kBars = 8 + 6 + 3 * kStages + 3 * kItemRing;
+  constexpr int kBars = 6 + 6 + 3 * kStages + 3 * kItemRing;
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  volatile int* s_items = abort_flag + 1;                                                  // [kItemRing]
+  volatile Item* s_items = (volatile Item*)(abort_flag + 1);                               // [kItemRing]
   uint32_t* s_bad = (uint32_t*)(s_items + kItemRing);     // [kItemRing][kMaxChecked][4] keys, a bit each
-  static_assert(8 * kBars + 8 + 4 * kItemRing + 16 * kItemRing * kMaxChecked + 8 <= 1024, "control block");
+  static_assert(8 * kBars + 8 + (sizeof(Item) + 4) * kItemRing + 16 * kItemRing * kMaxChecked <= 1024, "control block");
 
+  volatile int* s_any = (volatile int*)(s_bad + kItemRing * kMaxChecked * 4);              // [kItemRing] any of them
   uint8_t* sOut = (uint8_t*)bars + 1024;           // [8][kStageOut]
-  volatile int* s_last = (volatile int*)(s_bad + kItemRing * kMaxChecked * 4);           // [2]
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
-    mbar_init(turn, 1); mbar_init(turn + 8, 1); mbar_init(joined, 128); mbar_init(joined + 8, 128);
+    mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
     for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 2); mbar_init(v_ok + 8 * i, 1); }
     // an item's slot is released by the MMA issuers, the checking warp and each softmax warp
@@ -397,42 +395,45 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------ softmax: one query row per thread
     const int t = warp >> 2, row = threadIdx.x & 127;
+    // positions of this row and of the warp's first row
+    const int my_pos = (row * g.inv_gp) >> 16, pos_lo = ((row - lane) * g.inv_gp) >> 16;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = lanes + t * kTile, tO = lanes + 256 + t * kTile;
-    uint32_t sc = 0, oc = 0, cc = 0, jc = 0;      // phases of s_full, o_full, (a bit per slot) checked and joined
+    uint32_t sc = 0, oc = 0, cc = 0;              // phases of s_full, o_full and (a bit per slot) checked
     pdl_wait();
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
       if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
-      const int item = s_items[slot];
-      if (item < 0) break;
-      const Item it = decode_item<SPLIT>(g, tab, item);
+      const volatile Item& it = s_items[slot];                // read where it is used: registers are short
+      if (it.item < 0) break;
       const int nb = t ? it.nb1 : it.nb0;
-      const int limit = it.limit + t * kTile + row;           // last key that this row sees
-      float m = -INFINITY, neg = 0.f, l = 0.f;                // the row's reference, -m alpha, and its sum
+      const int limit = it.limit + t * g.pos + my_pos;        // last key that this row sees
+      const bool live = my_pos < g.pos && t * g.pos + my_pos < it.rows;
+      // the row's reference, -m alpha, and its sum; rows of the tile that do not exist never look for one
+      float m = live ? -INFINITY : 0.f, neg = 0.f, l = 0.f;
       bool ok = true;
       for (int j = nb - 1; j >= 0; --j) {
         if (!wait_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
         ++sc;
         fence_after();
-        const int seen = limit - j * kTile;                   // columns 0 .. seen
+        const int seen = limit - j * kTile, lo = seen - (my_pos - pos_lo);       // columns 0 .. seen; the warp's first row's
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float bm = first_reference(tS, seen, lane);
+          const float bm = first_reference(tS, seen, lo);
           if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
             neg = -m * g.alpha;
           }
         }
         uint32_t p[64];
-        const float sum = kTile - 1 > seen - lane ? row_exp<true>(tS, g.alpha, neg, seen, lane, p)      // a hidden key in the warp
-                                                  : row_exp<false>(tS, g.alpha, neg, seen, lane, p);
-        const bool over = !(l + sum <= kBig);                 // a NaN too
+        const float sum = kTile - 1 > lo ? row_exp<true>(tS, g.alpha, neg, seen, p)      // a hidden key in the warp
+                                       : row_exp<false>(tS, g.alpha, neg, seen, p);
+        const bool over = live && !(l + sum <= kBig);         // a NaN too
         if (!__any_sync(0xffffffffu, over)) {
           l += sum;
           tmem_st32<0>(tS, p);
           tmem_st32<32>(tS + 32, p);
         } else {
-          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, seen, lane, over);
+          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, seen, over);
           m = r.x;
           neg = r.y;
           l = r.z;
@@ -444,11 +445,10 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       if (!ok) break;
       // ---- the item's rows
       const float inv = l == 0.f ? 0.f : 1.f / l;             // no visible key: zeros
-      const bool live = t * kTile + row < it.rows;
       bool flagged = false;
-      if (it.nb > 0 && t * kTile < it.rows) {
+      if (it.nb > 0 && t * g.pos < it.rows) {
         if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
-        for (int c = 0; c < kMaxChecked * 4; ++c) flagged |= s_bad[slot * kMaxChecked * 4 + c] != 0;
+        flagged = s_any[slot] != 0;
       }
       if (it.nb > 0) cc ^= 1u << slot;
       if (nb > 0) {
@@ -456,81 +456,16 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         ++oc;
         fence_after();
       }
-      // 64 columns at a time through the warp's own staging rows, so that the stores are whole lines of a row:
-      // 16-byte piece k of row r lies at k ^ (r & 7)
-      uint8_t* stage = sOut + warp * kStageOut;
-      const int wr = t * kTile + (warp & 3) * 32;             // the warp's first row of the item
-      // one part: straight from O; several: this part's (m, l, O) to the workspace, and once all are there, their sum
-      const int parts = t ? it.parts1 : it.parts0;
-      float* part = g.part + ((int64_t)item * 2 + t) * part_floats<D>() + (warp & 3) * (D * 32) + lane;
-      bool write = wr < it.rows && (!SPLIT || (parts > 1 ? nb > 0 : it.s == 0));
-      if (SPLIT && parts > 1 && nb > 0 && t * kTile < it.rows) {
-        store_part<D>(part, tO, m, l, row);
-        if (flagged && live)
-          add_non_finite_part(part, s_bad + slot * kMaxChecked * 4, min(it.nb - it.low, kMaxChecked),
-                              min(limit + 1, it.tk) - it.low * kTile,
-                              v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh, g.v_st, g.d);
-        __threadfence();
-        mbar_arrive(joined + 8 * t);              // this thread's part is out
-        if (!wait_warp(ctl, joined + 8 * t, jc & 1, kDevTimeoutEpilogue)) break;
-        if (row == 0) {
-          int32_t* count = g.arrived + ((int64_t)(item - it.s * g.Hq) * 2 + t);
-          const bool last = atomicAdd(count, 1) == parts - 1;
-          if (last) *count = 0;                   // as the next call expects it
-          s_last[t] = last;
-          __threadfence();
-        }
-        __syncwarp();
-        mbar_arrive(joined + 8 * t);
-        if (!wait_warp(ctl, joined + 8 * t, (jc + 1) & 1, kDevTimeoutEpilogue)) break;
-        jc += 2;
-        write = write && s_last[t];
-      }
-      if (write) {
-        __nv_bfloat16* po = out + (int64_t)(it.q0 + wr + (lane >> 3)) * g.o_st + it.h * g.o_sh + (lane & 7) * 8;
-        const int64_t step = 4 * g.o_st;
-#pragma unroll 1
-        for (int c = 0; c < D / 64 && 64 * c < g.d; ++c) {
-          if (SPLIT && parts > 1) {
-            join_parts<D>(g.part + ((int64_t)(item - it.s * g.Hq) * 2 + t) * part_floats<D>(),
-                          (int64_t)g.Hq * 2 * part_floats<D>(), parts, (warp & 3) * (D * 32) + 64 * c * 32 + lane, row, g.alpha,
-                          stage + lane * 128, lane & 7);
-          } else {
-            float oa[32], ob[32];
-            if (nb > 0) {
-              tmem_ld32(tO + 64 * c, oa);
-              tmem_ld32(tO + 64 * c + 32, ob);
-              tmem_wait(oa);
-              tmem_wait(ob);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              oa[i] = nb > 0 ? oa[i] * inv : 0.f;             // no key at all: zeros
-              ob[i] = nb > 0 ? ob[i] * inv : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              put8(stage + lane * 128 + (i ^ (lane & 7)) * 16, oa + 8 * i);
-              put8(stage + lane * 128 + ((4 + i) ^ (lane & 7)) * 16, ob + 8 * i);
-            }
-          }
-          if (flagged && live && (!SPLIT || parts <= 1))
-            add_non_finite(stage + lane * 128, lane & 7, s_bad + slot * kMaxChecked * 4, min(it.nb - it.low, kMaxChecked),
-                           min(limit + 1, it.tk) - it.low * kTile,
-                           v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh + 64 * c, g.v_st,
-                           min(64, g.d - 64 * c));
-          __syncwarp();
-          const bool inside = 64 * c + (lane & 7) * 8 < g.d;
-          __nv_bfloat16* pr = po + 64 * c;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            const uint4 w = *(const uint4*)(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
-            if (inside && wr + r < it.rows) *(uint4*)pr = w;
-            pr += step;
-          }
-          __syncwarp();
-        }
+      // non-finite values that the check took out of the products (if any) for the rows that see them
+      const Bad bad = {flagged && live ? s_bad + slot * kMaxChecked * 4 : nullptr,
+                       min(min(it.nb - it.low, kMaxChecked) * kTile, min(limit + 1, it.tk) - it.low * kTile),
+                       v + (int64_t)(it.k0 + it.low * kTile) * g.v_st + it.hk * g.v_sh};
+      if (SPLIT) {
+        // the part's (m, l, O) to the workspace; join_kernel adds a tile's parts
+        if (nb > 0) store_part<D>(g, g.part + ((int64_t)it.item * 2 + t) * part_floats<D>(), tO, m, l, row, bad);
+      } else if (pos_lo < g.pos && t * g.pos + pos_lo < it.rows) {
+        write_rows<D>(g, out + (int64_t)(it.q0 + t * g.pos) * g.o_st + it.h * g.o_sh, min(g.pos, it.rows - t * g.pos),
+                      nb > 0 ? tO : 0xFFFFFFFFu, inv, sOut + warp * kStageOut, row, bad);
       }
       fence_before();
       __syncwarp();
@@ -541,27 +476,36 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------ TMA producer
       pdl_wait();
+      // a tile's rows: gp heads at each of its positions (rows past the box keep what they held)
+      auto load_q = [&](const Item& it) {
+        const int tiles = it.rows > g.pos ? 2 : 1;
+        mbar_expect_tx(q_full, tiles * kPanels * g.gp * g.pos * 128);
+        for (int x = 0; x < tiles * kPanels; ++x)
+          tma_load_3d(smem_u32(sQ) + x * kPanel, &maps.q, q_full, 64 * (x % kPanels), it.h, it.q0 + x / kPanels * g.pos);
+        ++q_loaded;
+      };
       bool ok = true;
       for (uint32_t n = 0; ok && !*abort_flag; ++n) {
         const int slot = n % kItemRing;
         if (!wait_bar(ctl, item_empty + 8 * slot, ((n / kItemRing) & 1) ^ 1, kDevTimeoutTmaProducer)) break;
-        int item = atomicAdd(&sched[0], 1);
-        if (item >= g.n_items) item = -1;
-        s_items[slot] = item;
-        mbar_arrive(item_full + 8 * slot);
-        if (item < 0) break;
+        const int item = atomicAdd(&sched[0], 1);
+        if (item >= g.n_items) {
+          s_items[slot].item = -1;
+          mbar_arrive(item_full + 8 * slot);
+          break;
+        }
         const Item it = decode_item<SPLIT>(g, tab, item);
+        const int* from = (const int*)&it;
+        volatile int* to = (volatile int*)&s_items[slot];
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = from[i];
+        mbar_arrive(item_full + 8 * slot);
         for (int b = 0; b < 2 * it.nb && ok; ++b) {
           if (b == 2) {
             // the queries after the first K and V blocks: the last item's products still read the old ones
             ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
             if (!ok) break;
-            const int tiles = it.rows > kTile ? 2 : 1;
-            mbar_expect_tx(q_full, tiles * kBlock);
-            for (int x = 0; x < tiles * kPanels; ++x)
-              tma_load_3d(smem_u32(sQ) + x * kPanel, &maps.q, q_full, 64 * (x % kPanels), it.h,
-                          it.q0 + x / kPanels * kTile);
-            ++q_loaded;
+            load_q(it);
           }
           const int st = loaded % kStages;
           ok = wait_bar(ctl, kv_empty + 8 * st, ((loaded / kStages) & 1) ^ 1, kDevTimeoutTmaProducer);
@@ -576,11 +520,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         if (ok && it.nb == 1) {                   // an item of one block: its queries come last
           ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
           if (!ok) break;
-          const int tiles = it.rows > kTile ? 2 : 1;
-          mbar_expect_tx(q_full, tiles * kBlock);
-          for (int x = 0; x < tiles * kPanels; ++x)
-            tma_load_3d(smem_u32(sQ) + x * kPanel, &maps.q, q_full, 64 * (x % kPanels), it.h, it.q0 + x / kPanels * kTile);
-          ++q_loaded;
+          load_q(it);
         }
       }
     } else if (warp == 9 || warp == 10) {
@@ -619,10 +559,14 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
         if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
-        const int item = __shfl_sync(0xffffffffu, s_items[slot], 0);
+        struct { int item, nb, nb0, nb1, low; } it;
+        it.item = __shfl_sync(0xffffffffu, s_items[slot].item, 0);
+        it.nb = __shfl_sync(0xffffffffu, s_items[slot].nb, 0);
+        it.nb0 = __shfl_sync(0xffffffffu, s_items[slot].nb0, 0);
+        it.nb1 = __shfl_sync(0xffffffffu, s_items[slot].nb1, 0);
+        it.low = __shfl_sync(0xffffffffu, s_items[slot].low, 0);
         if (lane == 0) mbar_arrive(item_empty + 8 * slot);
-        if (item < 0) break;
-        const Item it = decode_item<SPLIT>(g, tab, item);
+        if (it.item < 0) break;
         if (it.nb == 0) continue;
         const int nb = t ? it.nb1 : it.nb0;
         bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma);
@@ -697,13 +641,14 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
         if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
-        const int item = s_items[slot];
-        if (item < 0) break;
-        const Item it = decode_item<SPLIT>(g, tab, item);
+        struct { int nb, low; } it;
+        if (s_items[slot].item < 0) break;
+        it.nb = s_items[slot].nb;
+        it.low = s_items[slot].low;
         uint32_t* bad_keys = s_bad + slot * kMaxChecked * 4;
         for (int i = lane; i < kMaxChecked * 4; i += 32) bad_keys[i] = 0;
         __syncwarp();
-        bool ok = true;
+        bool ok = true, any = false;
         for (int j = it.nb - 1; j >= it.low && ok; --j) {
           const uint32_t use = kv + 2 * (it.nb - 1 - j) + 1;
           const int st = use % kStages;
@@ -724,6 +669,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
           const bool bad = (*(const uint32_t*)&all & 0x7FFF7FFFu) != 0;
           if (__any_sync(0xffffffffu, bad)) {
+            any = true;
             for (int i = lane; i < kBlock / 16; i += 32) {
               uint4 w = blk[i];
               uint32_t* x = (uint32_t*)&w;
@@ -748,6 +694,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         kv += 2 * it.nb;
         __syncwarp();
         if (lane == 0) {
+          s_any[slot] = any;
           if (it.nb > 0) mbar_arrive(checked + 8 * slot);
           mbar_arrive(item_empty + 8 * slot);
         }
@@ -795,6 +742,54 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
+// The parts of a tile together: 32 columns of its 128 rows per CTA, two warps for 32 rows
+// (16 columns each), a lane per row; the parts are added in order.
+template <int D, int MAXB>
+__global__ void __launch_bounds__(256)
+join_kernel(const __grid_constant__ TcGeom g, const __grid_constant__ PrefillTable<MAXB> tab,
+            __nv_bfloat16* __restrict__ out) {
+  __shared__ __align__(16) uint8_t rows[kTile * 80];          // 64 bytes a row, 80 apart
+  const int item = blockIdx.x >> 1, t = blockIdx.x & 1, c0 = blockIdx.y * 32;
+  const Item it = decode_item<true>(g, tab, item);
+  pdl_wait();
+  if (it.s == 0 && t * g.pos < it.rows) {
+    const int parts = t ? it.parts1 : it.parts0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, c = c0 + (warp >> 2) * 16;
+    const int64_t next = (int64_t)g.groups * 2 * part_floats<D>();
+    const float* p0 = g.part + ((int64_t)item * 2 + t) * part_floats<D>();
+    const float* ml = p0 + kTile * D + row;
+    float M = -INFINITY, L = 0.f, o[16];
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(ml + k * next));
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+      const float f = ex2((__ldcg(ml + k * next) - ref) * g.alpha);
+      const float* p = p0 + k * next + (warp & 3) * (D * 32) + c * 32 + lane;
+      L = fmaf(__ldcg(ml + k * next + kTile), f, L);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i), f, o[i]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;               // no visible key: zeros
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= inv;
+    put8(rows + row * 80 + (warp >> 2) * 32, o);
+    put8(rows + row * 80 + (warp >> 2) * 32 + 16, o + 8);
+    __syncthreads();
+    const int left = min(g.pos, it.rows - t * g.pos);         // positions of the tile that exist
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 64 + (threadIdx.x >> 2), k = threadIdx.x & 3, pos = (r * g.inv_gp) >> 16;
+      if (pos < left && c0 + k * 8 < g.d)
+        *(uint4*)(out + (int64_t)(it.q0 + t * g.pos + pos) * g.o_st + (it.h + r - pos * g.gp) * g.o_sh + c0 + k * 8) =
+            *(const uint4*)(rows + r * 80 + k * 16);
+    }
+  }
+  pdl_trigger();
+}
+
 // ---------------------------------------------------------------- host side
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
 EncodeFn encode_fn() {
@@ -810,12 +805,13 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// [rows][heads][d] bf16 in boxes of 128 rows x 64 columns of one head; columns past d
+// [rows][heads][d] bf16 in boxes of 64 columns of some heads and rows; columns past d
 // and rows past the end read as zeros.  The stride of an axis of extent 1 is unused.
-bool encode(EncodeFn enc, CUtensorMap* map, const void* base, int d, int heads, int rows, int64_t st, int64_t sh) {
+bool encode(EncodeFn enc, CUtensorMap* map, const void* base, int d, int heads, int rows, int64_t st, int64_t sh,
+            int box_heads, int box_rows) {
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {heads == 1 ? 16 : (cuuint64_t)sh * 2, rows == 1 ? 16 : (cuuint64_t)st * 2};
-  cuuint32_t box[3] = {64, 1, kTile};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -828,44 +824,58 @@ cudaError_t launch(const TcMaps& maps, const TcGeom& g, const PrefillTable<MAXB>
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = raise_smem(prefill_tc_kernel<D, SPLIT, MAXB>, smem_bytes<D>(), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_tc_kernel<D, SPLIT, MAXB>, dim3(std::min(g.n_items, sms)), dim3(kThreads), (size_t)smem_bytes<D>(), s,
-                    maps, g, tab, (const __nv_bfloat16*)v, (__nv_bfloat16*)out, err, err + kSchedWord);
+  const cudaError_t run = launch_pdl(prefill_tc_kernel<D, SPLIT, MAXB>, dim3(std::min(g.n_items, sms)), dim3(kThreads),
+                                     (size_t)smem_bytes<D>(), s, maps, g, tab, (const __nv_bfloat16*)v,
+                                     (__nv_bfloat16*)out, err, err + kSchedWord);
+  if (!SPLIT || run != cudaSuccess) return run;
+  return launch_pdl(join_kernel<D, MAXB>, dim3(g.n_items * 2, (g.d + 31) / 32), dim3(256), 0, s, g, tab, (__nv_bfloat16*)out);
 }
 
 }  // namespace
 
-// Query rows of a work item and keys of a block.
-int prefill_tc_rows() { return kRows; }
+// Query heads that share a tile, of the G of a KV head: the divisor of G that leaves the
+// fewest of the tile's 128 rows empty, the largest one of those.
+int prefill_tc_heads(int G) {
+  int best = 1;
+  for (int gp = 2; gp <= std::min(G, kTile); ++gp)
+    if (G % gp == 0 && kTile / gp * gp >= kTile / best * best) best = gp;
+  // a few empty rows are worth the sharing of keys and values
+  for (int gp = best + 1; gp <= std::min(G, kTile); ++gp)
+    if (G % gp == 0 && kTile / gp * gp >= 120) best = gp;
+  return best;
+}
+// Positions of a work item (two tiles) and keys of a block.
+int prefill_tc_rows(int G) { return 2 * (kTile / prefill_tc_heads(G)); }
 int prefill_tc_block() { return kTile; }
 
-// The workspace that split items need: counters, then parts.
-size_t prefill_tc_counter_bytes(int64_t n_items) { return (size_t)(n_items * 2 * 4 + 255) / 256 * 256; }
+// The workspace that split items need.
 size_t prefill_tc_part_bytes(int64_t n_items, int d) {
   return (size_t)n_items * 2 * (d <= 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
 }
 
 template <int MAXB>
 cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int kb, int q_total, int k_total,
-                              const void* q, const void* k, const void* v, void* out, int32_t* err, int32_t* arrived,
-                              float* part, int sms, cudaStream_t s) {
+                              const void* q, const void* k, const void* v, void* out, int32_t* err, float* part,
+                              int sms, cudaStream_t s) {
   const EncodeFn enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
+  const int gp = prefill_tc_heads(p.G);
   static thread_local TcMaps maps;
-  if (!encode(enc, &maps.q, q, p.d, p.Hq, q_total, p.q_st, p.q_sh) ||
-      !encode(enc, &maps.k, k, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh) ||
-      !encode(enc, &maps.v, v, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh))
+  if (!encode(enc, &maps.q, q, p.d, p.Hq, q_total, p.q_st, p.q_sh, gp, kTile / gp) ||
+      !encode(enc, &maps.k, k, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh, 1, kTile) ||
+      !encode(enc, &maps.v, v, p.d, p.Hkv, k_total, p.kv_st, p.kv_sh, 1, kTile))
     return cudaErrorInvalidValue;
-  TcGeom g = {p.Hq, p.G, p.d, kb, tab.uoff[tab.B] * p.Hq, p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL,
-              arrived, part};
+  TcGeom g = {p.Hq / gp, p.G / gp, gp, (65536 + gp - 1) / gp, kTile / gp, p.d, kb, tab.uoff[tab.B] * (p.Hq / gp), p.alpha, p.kv_st, p.kv_sh, p.o_st, p.o_sh, 4000000000LL,
+              part};
   if (kb > 0)
     return p.d <= 64 ? launch<64, true>(maps, g, tab, v, out, err, sms, s) : launch<128, true>(maps, g, tab, v, out, err, sms, s);
   return p.d <= 64 ? launch<64, false>(maps, g, tab, v, out, err, sms, s) : launch<128, false>(maps, g, tab, v, out, err, sms, s);
 }
 template cudaError_t launch_prefill_tc<kSmallBatch>(const PrefillTable<kSmallBatch>&, const PrefillGeom&, int, int, int,
                                                     const void*, const void*, const void*, void*, int32_t*,
-                                                    int32_t*, float*, int, cudaStream_t);
+                                                    float*, int, cudaStream_t);
 template cudaError_t launch_prefill_tc<CHUNKKV_MAX_BATCH>(const PrefillTable<CHUNKKV_MAX_BATCH>&, const PrefillGeom&,
                                                           int, int, int, const void*, const void*, const void*, void*,
-                                                          int32_t*, int32_t*, float*, int, cudaStream_t);
+                                                          int32_t*, float*, int, cudaStream_t);
 
 }  // namespace chunkkv

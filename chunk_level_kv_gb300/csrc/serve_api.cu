@@ -12,14 +12,14 @@ int prefill_simt_tile();                                                        
 template <int MAXB>
 cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q,
                                 const void* k, const void* v, void* out, cudaStream_t s);
-int prefill_tc_rows();                                                                 // prefill_tc.cu
+int prefill_tc_heads(int G);                                                           // prefill_tc.cu
+int prefill_tc_rows(int G);
 int prefill_tc_block();
-size_t prefill_tc_counter_bytes(int64_t n_items);
 size_t prefill_tc_part_bytes(int64_t n_items, int d);
 template <int MAXB>
 cudaError_t launch_prefill_tc(const PrefillTable<MAXB>& tab, const PrefillGeom& p, int kb, int q_total, int k_total,
-                              const void* q, const void* k, const void* v, void* out, int32_t* err, int32_t* arrived,
-                              float* part, int sms, cudaStream_t s);
+                              const void* q, const void* k, const void* v, void* out, int32_t* err, float* part,
+                              int sms, cudaStream_t s);
 cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* lens, int32_t* table, int32_t* ring,
                              int32_t* state, int64_t* slots, int n_cap, int sms, cudaStream_t s);   // q8_cache.cu
 cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
@@ -75,8 +75,8 @@ chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
     if (!p->cu_q || !p->cu_k || p->cu_q[0] != 0 || p->cu_k[0] != 0) return CHUNKKV_ERR_INVALID_ARG;
     for (int b = 0; b < p->B; ++b)
       if (p->cu_q[b + 1] < p->cu_q[b] || p->cu_k[b + 1] < p->cu_k[b]) return CHUNKKV_ERR_INVALID_ARG;
-    // work items (at most one per 64 query rows, plus one per sequence, of each head) are counted in 32 bits
-    if (((int64_t)p->cu_q[p->B] / 64 + p->B) * p->Hq > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
+    // work items (at most one per 2 query positions, plus one per sequence, of each head) are counted in 32 bits
+    if (((int64_t)p->cu_q[p->B] / 2 + p->B) * p->Hq > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
   }
   return CHUNKKV_OK;
 }
@@ -115,7 +115,8 @@ void fill_table(const chunkkv_prefill_params* p, int tile, int kb, PrefillTable<
 constexpr int64_t kMinPart = 8;                 // blocks of a part at least
 
 void plan_items(const chunkkv_prefill_params* p, int sms, int* kb, int64_t* n_items) {
-  const int64_t rows = prefill_tc_rows(), block = prefill_tc_block();
+  const int G = p->Hq / p->Hkv, groups = p->Hq / prefill_tc_heads(G);
+  const int64_t rows = prefill_tc_rows(G), block = prefill_tc_block();
   int64_t work = 0, longest = 0, units = 0;
   for (int b = 0; b < p->B; ++b) {
     const int64_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = p->cu_k[b + 1] - p->cu_k[b];
@@ -125,17 +126,23 @@ void plan_items(const chunkkv_prefill_params* p, int sms, int* kb, int64_t* n_it
       longest = std::max(longest, n);
     }
   }
-  const int64_t share = work * p->Hq / sms;
+  const int64_t share = work * groups / sms;
   *kb = 0;
-  *n_items = units * p->Hq;
+  *n_items = units * groups;
   if (longest < 2 * share + kMinPart) return;
-  *kb = (int)std::max<int64_t>(kMinPart, share + 1);
-  units = 0;
-  for (int b = 0; b < p->B; ++b) {
-    const int64_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = p->cu_k[b + 1] - p->cu_k[b];
-    units += (tq + rows - 1) / rows * std::max<int64_t>(1, ((tk + block - 1) / block + *kb - 1) / *kb);
+  // the shortest parts that still make one wave of items, where there are such
+  for (int64_t n = std::max(kMinPart, share + 1);; n += std::max<int64_t>(1, n / 8)) {
+    units = 0;
+    for (int b = 0; b < p->B; ++b) {
+      const int64_t tq = p->cu_q[b + 1] - p->cu_q[b], tk = p->cu_k[b + 1] - p->cu_k[b];
+      units += (tq + rows - 1) / rows * std::max<int64_t>(1, ((tk + block - 1) / block + n - 1) / n);
+    }
+    if (units * groups > sms && n < longest) continue;
+    if (n >= longest) return;
+    *kb = (int)n;
+    *n_items = units * groups;
+    return;
   }
-  *n_items = units * p->Hq;
 }
 
 // The tensor-core kernel: bf16 rows of up to 128 columns that tensor maps can address (no axis
@@ -159,17 +166,16 @@ bool device_pointer(const void* p) {
 }
 
 template <int MAXB>
-cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, bool tc, int kb, int64_t n_items, const void* q,
-                        const void* k, const void* v, void* out, char* ws, cudaStream_t s) {
+cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, bool tc, int kb, const void* q, const void* k,
+                        const void* v, void* out, char* ws, cudaStream_t s) {
   static thread_local PrefillTable<MAXB> tab;
   if (!tc) {
     fill_table(p, prefill_simt_tile(), 0, tab);
     return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
   }
-  fill_table(p, prefill_tc_rows(), kb, tab);
+  fill_table(p, prefill_tc_rows(p->Hq / p->Hkv), kb, tab);
   return launch_prefill_tc(tab, g, kb, p->cu_q[p->B], p->cu_k[p->B], q, k, v, out, (int32_t*)ws,
-                           (int32_t*)(ws + kServeHeader),
-                           (float*)(ws + kServeHeader + (kb > 0 ? prefill_tc_counter_bytes(n_items) : 0)), sm_count(), s);
+                           (float*)(ws + kServeHeader), sm_count(), s);
 }
 
 // How a call runs: on the tensor cores, in items of kb blocks (0: whole), and its workspace.
@@ -181,7 +187,7 @@ chunkkv_status plan_prefill(const chunkkv_prefill_params* p, bool* tc, int* kb, 
   if (!*tc) return CHUNKKV_OK;
   plan_items(p, sm_count(), kb, n_items);
   if (*n_items > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
-  if (*kb > 0) *bytes += prefill_tc_counter_bytes(*n_items) + prefill_tc_part_bytes(*n_items, p->d);
+  if (*kb > 0) *bytes += prefill_tc_part_bytes(*n_items, p->d);
   return CHUNKKV_OK;
 }
 
@@ -240,8 +246,8 @@ chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const 
                    p->kv_stride_t, p->kv_stride_h, p->o_stride_t, p->o_stride_h};
   const cudaStream_t cs = (cudaStream_t)stream;
   return cuda_result(p->B <= kSmallBatch
-                         ? run_prefill<kSmallBatch>(p, g, tc, kb, n_items, q, k, v, out, (char*)ws, cs)
-                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, tc, kb, n_items, q, k, v, out, (char*)ws, cs));
+                         ? run_prefill<kSmallBatch>(p, g, tc, kb, q, k, v, out, (char*)ws, cs)
+                         : run_prefill<CHUNKKV_MAX_BATCH>(p, g, tc, kb, q, k, v, out, (char*)ws, cs));
 }
 
 chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
