@@ -136,55 +136,57 @@ __device__ __forceinline__ Item decode_item(const TcGeom& g, const PrefillTable<
   return it;
 }
 
-// Row maximum over the columns 0 .. seen of S.
-template <int C>
-__device__ __forceinline__ float chunk_max(const float (&s)[32], int seen, float m) {
+// What a row runs once per item or less is kept out of the loop over the blocks, in small
+// loops of its own: at one pass an item, straight-line code costs its instruction fetches
+// (an unrolled write of the output rows took 6000 cycles an item).
+
+// -inf into the columns of S that the row does not see (those after `seen`), whatever
+// they hold.  lo: what the warp's first row sees; columns up to there are left alone.
+__device__ __noinline__ void hide(uint32_t tS, int seen, int lo) {
+#pragma unroll 1
+  for (int c = max(lo + 1, 0) & ~31; c < kTile; c += 32) {
+    float s[32];
+    tmem_ld32(tS + c, s);
+    tmem_wait(s);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, 32 * C + i <= seen ? s[i] : -INFINITY);
+    for (int i = 0; i < 32; ++i) s[i] = c + i <= seen ? s[i] : -INFINITY;
+    tmem_st32(tS + c, s);
+  }
+  tmem_st_wait();
+}
+// Row maximum of S.
+__device__ __forceinline__ float row_max(uint32_t tS) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 32) {
+    float s[32];
+    tmem_ld32(tS + c, s);
+    tmem_wait(s);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
+  }
   return m;
 }
-__device__ __forceinline__ float row_max(uint32_t tS, int seen) {
-  float ra[32], rb[32], m = -INFINITY;
-  tmem_ld32(tS, ra);
-  tmem_wait(ra);
-  tmem_ld32(tS + 32, rb);
-  m = chunk_max<0>(ra, seen, m);
-  tmem_wait(rb);
-  tmem_ld32(tS + 64, ra);
-  m = chunk_max<1>(rb, seen, m);
-  tmem_wait(ra);
-  tmem_ld32(tS + 96, rb);
-  m = chunk_max<2>(ra, seen, m);
-  tmem_wait(rb);
-  return chunk_max<3>(rb, seen, m);
-}
 // A first reference: the maximum over the last 32 columns that all of the warp's rows
-// reach into (any of a row's logits would do; lo: what the first of them sees), or over
-// all where a row sees none.
-__device__ __noinline__ float first_reference(uint32_t tS, int seen, int lo) {
-  if (lo < 0) return row_max(tS, seen);
-  const int first = min(lo >> 5, 3) * 32;
-  float r[32], m = -INFINITY;
-  tmem_ld32(tS + first, r);
-  tmem_wait(r);
+// reach into (any of a row's logits would do), or over all where a row sees none.
+__device__ __noinline__ float first_reference(uint32_t tS, int lo) {
+  if (lo < 0) return row_max(tS);
+  float s[32], m = -INFINITY;
+  tmem_ld32(tS + min(lo >> 5, 3) * 32, s);
+  tmem_wait(s);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, first + i <= seen ? r[i] : -INFINITY);
+  for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
   return m;
 }
 
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
 // and a packed conversion.
-template <bool MASK, int C>
-__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, int seen, float2 (&sum)[2],
-                                          uint32_t (&p)[64]) {
+template <int C>
+__device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, float2 (&sum)[2], uint32_t (&p)[64]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), a2, n2);
-    float2 w = make_float2(ex2(e.x), ex2(e.y));
-    if (MASK) {                                               // whatever a hidden logit is
-      w.x = 32 * C + 2 * i <= seen ? w.x : 0.f;
-      w.y = 32 * C + 2 * i + 1 <= seen ? w.y : 0.f;
-    }
+    const float2 w = make_float2(ex2(e.x), ex2(e.y));
     sum[i & 1] = __fadd2_rn(sum[i & 1], w);
     const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
     p[16 * C + i] = *(const uint32_t*)&b;
@@ -192,33 +194,31 @@ __device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float
 }
 // A row's P under the reference -neg, and its sum.  Straight-line code: a branch per
 // chunk cost 400 cycles of a block's 1000.
-template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, int seen, uint32_t (&p)[64]) {
+__device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, uint32_t (&p)[64]) {
   float ra[32], rb[32];
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 a2 = make_float2(alpha, alpha), n2 = make_float2(neg, neg);
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  chunk_exp<MASK, 0>(ra, a2, n2, seen, sum, p);
+  chunk_exp<0>(ra, a2, n2, sum, p);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  chunk_exp<MASK, 1>(rb, a2, n2, seen, sum, p);
+  chunk_exp<1>(rb, a2, n2, sum, p);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  chunk_exp<MASK, 2>(ra, a2, n2, seen, sum, p);
+  chunk_exp<2>(ra, a2, n2, sum, p);
   tmem_wait(rb);
-  chunk_exp<MASK, 3>(rb, a2, n2, seen, sum, p);
+  chunk_exp<3>(rb, a2, n2, sum, p);
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // A block whose sum passed the bound, done over: rows that are `over` move their
 // reference to the block's maximum, and what O (at tO, unless it is still empty) and l
-// hold goes with it.  Returns (m, -m alpha, l); P is written.  Out of line, as the next
-// function: the loop around it has to stay in the instruction cache.
+// hold goes with it.  Returns (m, -m alpha, l); P is written.
 template <int D>
-__device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, int seen, bool over) {
-  const float bm = row_max(tS, seen);
+__device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, bool over) {
+  const float bm = row_max(tS);
   const float mn = fmaxf(m, bm);
   const float f = over ? ex2((m - mn) * alpha) : 1.f;
   if (over) m = mn;
@@ -236,7 +236,7 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
     }
   }
   uint32_t p[64];
-  const float sum = row_exp<true>(tS, alpha, neg, seen, p);
+  const float sum = row_exp(tS, alpha, neg, p);
   tmem_st32<0>(tS, p);
   tmem_st32<32>(tS + 32, p);
   return make_float3(m, neg, l * f + sum);
@@ -275,44 +275,36 @@ __device__ __forceinline__ void each_bad(const Bad& bad, int64_t v_st, int c0, i
 // A warp's rows of the output, 64 columns at a time through the warp's own staging rows,
 // so that the stores are whole lines of a row: 16-byte piece k of row r lies at k ^ (r & 7).
 // out: the tile's first position and head; left: positions of it that exist; tO:
-// 0xFFFFFFFF for rows without any key.  Out of line: its registers would be taken from
-// the loop over the blocks (1320 cycles a block for 1020).
+// 0xFFFFFFFF for rows without any key.
 template <int D>
 __device__ __noinline__ void write_rows(const TcGeom& g, __nv_bfloat16* out, int left, uint32_t tO, float inv, uint8_t* stage,
                                         int row, Bad bad) {
   const int lane = row & 31;
+  uint8_t* mine = stage + lane * 128;
   out += (lane & 7) * 8;
 #pragma unroll 1
-  for (int c = 0; c < D / 64 && 64 * c < g.d; ++c) {
-    float oa[32], ob[32];
-    if (tO != 0xFFFFFFFFu) {
-      tmem_ld32(tO + 64 * c, oa);
-      tmem_ld32(tO + 64 * c + 32, ob);
-      tmem_wait(oa);
-      tmem_wait(ob);
-    }
+  for (int c = 0; c < D && c < g.d; c += 64) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      float o[16];
+      if (tO != 0xFFFFFFFFu) tmem_get16(tO + c + 16 * k, o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      oa[i] = tO != 0xFFFFFFFFu ? oa[i] * inv : 0.f;
-      ob[i] = tO != 0xFFFFFFFFu ? ob[i] * inv : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      put8(stage + lane * 128 + (i ^ (lane & 7)) * 16, oa + 8 * i);
-      put8(stage + lane * 128 + ((4 + i) ^ (lane & 7)) * 16, ob + 8 * i);
+      for (int i = 0; i < 16; ++i) o[i] = tO != 0xFFFFFFFFu ? o[i] * inv : 0.f;
+      put8(mine + ((2 * k) ^ (lane & 7)) * 16, o);
+      put8(mine + ((2 * k + 1) ^ (lane & 7)) * 16, o + 8);
     }
     if (bad.keys)
-      each_bad(bad, g.v_st, 64 * c, min(64 * c + 64, g.d), [&](int i, float y) {
-        __nv_bfloat16* o = (__nv_bfloat16*)(stage + lane * 128 + (((i >> 3) & 7) ^ (lane & 7)) * 16) + (i & 7);
+      each_bad(bad, g.v_st, c, min(c + 64, g.d), [&](int i, float y) {
+        __nv_bfloat16* o = (__nv_bfloat16*)(mine + (((i >> 3) & 7) ^ (lane & 7)) * 16) + (i & 7);
         *o = __float2bfloat16_rn(__bfloat162float(*o) + y);
       });
     __syncwarp();
-    const bool inside = 64 * c + (lane & 7) * 8 < g.d;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3), tr = row - lane + r, pos = (tr * g.inv_gp) >> 16;
+    const bool inside = c + (lane & 7) * 8 < g.d;
+#pragma unroll 1
+    for (int r = lane >> 3; r < 32; r += 4) {
+      const int tr = row - lane + r, pos = (tr * g.inv_gp) >> 16;
       const uint4 w = *(const uint4*)(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
-      if (inside && pos < left) *(uint4*)(out + pos * g.o_st + (tr - pos * g.gp) * g.o_sh + 64 * c) = w;
+      if (inside && pos < left) *(uint4*)(out + pos * g.o_st + (tr - pos * g.gp) * g.o_sh + c) = w;
     }
     __syncwarp();
   }
@@ -323,12 +315,11 @@ template <int D>
 __device__ __noinline__ void store_part(const TcGeom& g, float* part, uint32_t tO, float m, float l, int row, Bad bad) {
   float* po = part + (row >> 5) * (D * 32) + (row & 31);
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    float o[32];
-    tmem_ld32(tO + 32 * c, o);
-    tmem_wait(o);
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    tmem_get16(tO + c, o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) __stcg(po + (32 * c + i) * 32, o[i]);
+    for (int i = 0; i < 16; ++i) __stcg(po + (c + i) * 32, o[i]);
   }
   if (bad.keys) each_bad(bad, g.v_st, 0, g.d, [&](int i, float y) { po[32 * i] += y; });
   __stcg(part + kTile * D + row, m);
@@ -417,23 +408,23 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         ++sc;
         fence_after();
         const int seen = limit - j * kTile, lo = seen - (my_pos - pos_lo);       // columns 0 .. seen; the warp's first row's
+        if (kTile - 1 > lo) hide(tS, seen, lo);               // a hidden key in the warp
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float bm = first_reference(tS, seen, lo);
+          const float bm = first_reference(tS, lo);
           if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
             neg = -m * g.alpha;
           }
         }
         uint32_t p[64];
-        const float sum = kTile - 1 > lo ? row_exp<true>(tS, g.alpha, neg, seen, p)      // a hidden key in the warp
-                                       : row_exp<false>(tS, g.alpha, neg, seen, p);
+        const float sum = row_exp(tS, g.alpha, neg, p);
         const bool over = live && !(l + sum <= kBig);         // a NaN too
         if (!__any_sync(0xffffffffu, over)) {
           l += sum;
           tmem_st32<0>(tS, p);
           tmem_st32<32>(tS + 32, p);
         } else {
-          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, seen, over);
+          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, over);
           m = r.x;
           neg = r.y;
           l = r.z;
@@ -444,7 +435,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       }
       if (!ok) break;
       // ---- the item's rows
-      const float inv = l == 0.f ? 0.f : 1.f / l;             // no visible key: zeros
+      const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);  // no visible key: zeros (else l is 1 or more, from its reference)
       bool flagged = false;
       if (it.nb > 0 && t * g.pos < it.rows) {
         if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;

@@ -129,6 +129,15 @@ __device__ __forceinline__ void tmem_wait(float (&r)[32]) {
   // an asm statement takes at most 30 read-write operands: the last two are tied here
   asm volatile("" : "+f"(r[30]), "+f"(r[31])::"memory");
 }
+// 16 columns, and the wait for them.
+__device__ __forceinline__ void tmem_get16(uint32_t addr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
