@@ -282,9 +282,17 @@ __device__ __noinline__ void write_rows(const TcGeom& g, __nv_bfloat16* out, int
   const int lane = row & 31;
   uint8_t* mine = stage + lane * 128;
   out += (lane & 7) * 8;
+  // of the rows that this lane writes pieces of, -1: none (the plan keeps a tile's rows within 2^31 elements)
+  int where[8];
+  const int o_st = (int)g.o_st, o_sh = (int)g.o_sh;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int tr = row - lane + 4 * i + (lane >> 3), pos = (tr * g.inv_gp) >> 16;
+    where[i] = pos < left ? pos * o_st + (tr - pos * g.gp) * o_sh : -1;
+  }
 #pragma unroll 1
   for (int c = 0; c < D && c < g.d; c += 64) {
-#pragma unroll 1
+#pragma unroll 2
     for (int k = 0; k < 4; ++k) {
       float o[16];
       if (tO != 0xFFFFFFFFu) tmem_get16(tO + c + 16 * k, o);
@@ -300,11 +308,11 @@ __device__ __noinline__ void write_rows(const TcGeom& g, __nv_bfloat16* out, int
       });
     __syncwarp();
     const bool inside = c + (lane & 7) * 8 < g.d;
-#pragma unroll 1
-    for (int r = lane >> 3; r < 32; r += 4) {
-      const int tr = row - lane + r, pos = (tr * g.inv_gp) >> 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
       const uint4 w = *(const uint4*)(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
-      if (inside && pos < left) *(uint4*)(out + pos * g.o_st + (tr - pos * g.gp) * g.o_sh + c) = w;
+      if (inside && where[i] >= 0) *(uint4*)(out + where[i] + c) = w;
     }
     __syncwarp();
   }

@@ -146,13 +146,14 @@ void plan_items(const chunkkv_prefill_params* p, int sms, int* kb, int64_t* n_it
 }
 
 // The tensor-core kernel: bf16 rows of up to 128 columns that tensor maps can address (no axis
-// longer than 1 with stride 0, strides below 2^40 bytes), and a key to attend to.
+// longer than 1 with stride 0, strides below 2^40 bytes), a tile of the output within 2^31 elements,
+// and a key to attend to.
 bool prefill_on_tc(const chunkkv_prefill_params* p) {
   const int64_t most = (int64_t)1 << 39;
   auto axis = [most](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < most); };
   return p->dtype == CHUNKKV_BF16 && p->d <= 128 && p->B > 0 && p->cu_k[p->B] > 0 &&
          axis(p->q_stride_t, p->cu_q[p->B]) && axis(p->q_stride_h, p->Hq) && axis(p->kv_stride_t, p->cu_k[p->B]) &&
-         axis(p->kv_stride_h, p->Hkv);
+         axis(p->kv_stride_h, p->Hkv) && p->o_stride_t < (1 << 22) && p->o_stride_h < (1 << 22);
 }
 
 // Tensor maps address device memory only.
