@@ -8,9 +8,9 @@
 
 namespace chunkkv {
 
-int prefill_simt_tile();                                                               // prefill.cu
+int prefill_simt_rows(int64_t ctas, int sms);                                          // prefill.cu
 template <int MAXB>
-cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, const void* q,
+cudaError_t launch_prefill_simt(bool bf16, const PrefillTable<MAXB>& tab, const PrefillGeom& g, int rows, const void* q,
                                 const void* k, const void* v, void* out, cudaStream_t s);
 int prefill_tc_heads(int G);                                                           // prefill_tc.cu
 int prefill_tc_rows(int G);
@@ -171,8 +171,10 @@ cudaError_t run_prefill(const chunkkv_prefill_params* p, const PrefillGeom& g, b
                         const void* v, void* out, char* ws, cudaStream_t s) {
   static thread_local PrefillTable<MAXB> tab;
   if (!tc) {
-    fill_table(p, prefill_simt_tile(), 0, tab);
-    return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, q, k, v, out, s);
+    fill_table(p, 64, 0, tab);
+    const int rows = prefill_simt_rows((int64_t)tab.uoff[tab.B] * p->Hq, sm_count());
+    if (rows != 64) fill_table(p, rows, 0, tab);
+    return launch_prefill_simt(p->dtype == CHUNKKV_BF16, tab, g, rows, q, k, v, out, s);
   }
   fill_table(p, prefill_tc_rows(p->Hq / p->Hkv), kb, tab);
   return launch_prefill_tc(tab, g, kb, p->cu_q[p->B], p->cu_k[p->B], q, k, v, out, (int32_t*)ws,
