@@ -106,13 +106,38 @@ prefill_simt_kernel(const __grid_constant__ PrefillTable<MAXB> tab, PrefillGeom 
 #pragma unroll
     for (int c = 0; c < 4 * ND; ++c) o[r][c] = 0.f;
   }
+  // heads of up to 128 columns: a tile's keys and values are read into registers while the one before is in use
+  constexpr bool kAhead = ND <= 2;
+  constexpr int kVecs = kAhead ? kTile * 16 * ND / kThreads : 1;
+  float4 rk[kVecs], rv[kVecs];
+  auto read_ahead = [&](int j0) {
+    const int64_t koff = (int64_t)(sq.k0 + j0) * g.kv_st + hk * g.kv_sh;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int x = i * kThreads + threadIdx.x, r = x / (16 * ND), c = (x % (16 * ND)) * 4;
+      const bool in = r < sq.tk - j0 && c < g.d;
+      rk[i] = in ? load4(k + koff + r * g.kv_st + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      rv[i] = in ? load4(v + koff + r * g.kv_st + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  if (kAhead && n_keys > 0) read_ahead(0);
   for (int j0 = 0; j0 < n_keys; j0 += kTile) {
     __syncthreads();                                         // the previous tile's readers are done
     const int nk = min(kTile, sq.tk - j0);
-    const int64_t koff = (int64_t)(sq.k0 + j0) * g.kv_st + hk * g.kv_sh;
-    load_tile<kTile, ND>(sK, kPitch, k + koff, g.kv_st, nk, g.d);
-    load_tile<kTile, ND>(sV, 64 * ND, v + koff, g.kv_st, nk, g.d);
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int x = i * kThreads + threadIdx.x, r = x / (16 * ND), c = (x % (16 * ND)) * 4;
+        *(float4*)(sK + r * kPitch + c) = rk[i];
+        *(float4*)(sV + r * 64 * ND + c) = rv[i];
+      }
+    } else {
+      const int64_t koff = (int64_t)(sq.k0 + j0) * g.kv_st + hk * g.kv_sh;
+      load_tile<kTile, ND>(sK, kPitch, k + koff, g.kv_st, nk, g.d);
+      load_tile<kTile, ND>(sV, 64 * ND, v + koff, g.kv_st, nk, g.d);
+    }
     __syncthreads();
+    if (kAhead && j0 + kTile < n_keys) read_ahead(j0 + kTile);
     float s[RM][4];
 #pragma unroll
     for (int r = 0; r < RM; ++r)
