@@ -15,7 +15,7 @@ namespace {
 
 // ------------------------------------------------------------ tables and slot maps
 
-constexpr int kResizeThreads = 1024;
+constexpr int kResizeThreads = 512;
 constexpr int kSlotRun = 256;                   // tokens of a row that a warp maps: 5 pages at most, a lane each
 
 __device__ __forceinline__ int pages_of(int n) { return n > 0 ? (n - 1) / kPage + 1 : 0; }
@@ -77,6 +77,7 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
   const int head = ((volatile int32_t*)state)[kRingHead], n_free = ((volatile int32_t*)state)[kRingFree];
   long long grow = 0, give = 0;
   bool bad = false;
+#pragma unroll 4
   for (int r = c0; r < c1; ++r) {
     const int n = lens[r], m = new_lens[r];
     bad |= n < 0 || m < 0 || pages_of(m) > g.max_pages || pages_of(n) > g.max_pages || (slots && m - n > n_cap);
@@ -134,9 +135,8 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
   }
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
+    // no fence: the last CTA changes what the others have read by now, and reads nothing that they wrote
     s_last = atomicAdd(&state[kRingTicket], 1) == (int)gridDim.x - 1;
-    __threadfence();
   }
   __syncthreads();
   if (s_last) {
