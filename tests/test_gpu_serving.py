@@ -576,3 +576,21 @@ def test_decode_in_a_graph_follows_the_lengths(ckv):
         graph.replay()
         torch.cuda.synchronize()
         check_decode(ckv, cache, q, out, 1 / math.sqrt(128))
+
+
+# ------------------------------------------------------------------ together
+
+def test_the_example_serves_a_layer(ckv):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import serve_layer
+    r = serve_layer.serve()
+    after, before, again, end = r["lengths"]
+    assert all(0 < n <= 200 + 16 for n in after) and before == [n + 24 for n in after]
+    assert all(0 < n <= 200 + 16 for n in again) and end == [n + 16 for n in again]
+    # a code is off by at most half a step of 1/127 of its page's largest value (about 4 standard deviations), so
+    # uniformly distributed by 4 / 127 / sqrt(12) = 0.9 % of a standard deviation, in keys and values, and a few
+    # roundings more while a page grows; bf16 adds 0.2 %: within 5 % with a wide margin
+    assert len(r["errors"]) == 40 and max(r["errors"]) < 0.05
+    assert bool(torch.isfinite(r["hidden"]).all())
