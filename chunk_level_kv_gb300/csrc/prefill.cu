@@ -11,6 +11,12 @@
 // RM = 4 where its CTAs fill the GPU; RM = 1 where they do not (four times as many CTAs,
 // each of which reads more shared memory per product).
 // A query row without any key (Tq > Tk) gives zeros.
+//
+// What bounds it: the FMA pipes and the shared-memory reads that feed them.  4 d products
+// a visible pair on 152 x 128 lanes would take 2 us for 512 tokens, 4 query heads of 64
+// columns; there its CTAs' latency decides, tile after tile: 26 us (16-row CTAs and the
+// next tile read ahead; 54 us with 64-row CTAs).  8192 bf16 tokens of 32 heads take it
+// 16.9 ms (33 TFLOP/s), against 0.31 ms on the tensor cores.
 #include "serve.cuh"
 
 namespace chunkkv {

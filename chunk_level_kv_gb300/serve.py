@@ -25,6 +25,8 @@ def _bytes(t):
 
 def _stream(t) -> int:
     """The current stream of the tensor's device, as the integer that ctypes passes on."""
+    if not t.is_cuda:
+        raise ValueError("the tensors live in GPU memory")
     return torch._C._cuda_getCurrentRawStream(t.device.index or 0)
 
 

@@ -77,6 +77,7 @@ class Layer:
 
 
 def serve(seqlens=(700, 1500, 333), Hkv=2, G=4, d=128, w=16, c=10, budget=200, steps=40, again_at=24, seed=0) -> dict:
+    assert again_at >= w, "the second compression scores with the last w decoded queries"
     dev = torch.device("cuda:0")
     g = torch.Generator(device=dev).manual_seed(seed)
 
