@@ -45,7 +45,8 @@
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 and 10 MMA
 // issuers of tile 0 and 1 (with one issuer for both, its waits for one tile kept the
-// other's products back: a block pair took 3250 cycles), 11 V check.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+// other's products back: a block pair took 3250 cycles), 11 V check.
+// Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -67,6 +68,7 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register shares within the launch's");
 constexpr int kMaxChecked = 4;                    // masked blocks of an item: 256 rows' limits span at most three
 constexpr float kBig = 16777216.f;                // bound of a row's sum under its reference
+constexpr float kHuge = 4194304.f;                // references (in base-2 exponents) up to which one rounding will do
 
 template <int D> constexpr int block_bytes() { return kTile * D * 2; }
 constexpr int kPanel = kTile * 128;               // 128 rows x 64 elements
@@ -176,7 +178,8 @@ __device__ __forceinline__ float row_max(uint32_t tS) {
   return m;
 }
 // A first reference: the maximum over the last 32 columns that all of the warp's rows
-// reach into (any of a row's logits would do), or over all where a row sees none.
+// reach into (any of a row's finite logits would do), or over all where a row has none
+// there.
 __device__ __noinline__ float first_reference(uint32_t tS, int lo) {
   if (lo < 0) return row_max(tS);
   float s[32], m = -INFINITY;
@@ -184,7 +187,7 @@ __device__ __noinline__ float first_reference(uint32_t tS, int lo) {
   tmem_wait(s);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
-  return m;
+  return __any_sync(0xffffffffu, m == -INFINITY) ? row_max(tS) : m;
 }
 
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
@@ -221,9 +224,30 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, ui
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// A block whose sum passed the bound, done over: rows that are `over` move their
+// The same, of (S - base) alpha + neg.
+__device__ __forceinline__ float row_exp_from(uint32_t tS, float base, float alpha, float neg, uint32_t (&p)[64]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float s[32];
+    tmem_ld32(tS + 32 * c, s);
+    tmem_wait(s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = ex2(fmaf(s[2 * i] - base, alpha, neg)), b = ex2(fmaf(s[2 * i + 1] - base, alpha, neg));
+      sum += a + b;
+      const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
+      p[16 * c + i] = *(const uint32_t*)&w;
+    }
+  }
+  return sum;
+}
+
+// A block whose sum passed the bound, or whose reference is huge, done over: rows that are `over` move their
 // reference to the block's maximum, and what O (at tO, unless it is still empty) and l
-// hold goes with it.  Returns (m, -m alpha, l); P is written.
+// hold goes with it.  Under a huge reference S alpha - m alpha in one rounding is off by
+// more than an exponential bears (half a unit of m alpha in its last place), so there the
+// difference comes first.  Returns (m, -m alpha, l); P is written.
 template <int D>
 __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, bool over) {
   const float bm = row_max(tS);
@@ -244,7 +268,8 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
     }
   }
   uint32_t p[64];
-  const float sum = row_exp(tS, alpha, neg, p);
+  const bool huge = !(fabsf(neg) <= kHuge);
+  const float sum = row_exp_from(tS, huge ? m : 0.f, alpha, huge ? 0.f : neg, p);
   tmem_st32<0>(tS, p);
   tmem_st32<32>(tS + 32, p);
   return make_float3(m, neg, l * f + sum);
@@ -434,7 +459,7 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         }
         uint32_t p[64];
         const float sum = row_exp(tS, g.alpha, neg, p);
-        const bool over = live && !(l + sum <= kBig);         // a NaN too
+        const bool over = live && !(l + sum <= kBig && fabsf(neg) <= kHuge);         // a NaN too
         if (!__any_sync(0xffffffffu, over)) {
           l += sum;
           tmem_st32<0>(tS, p);

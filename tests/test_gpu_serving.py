@@ -142,6 +142,42 @@ def test_prefill_growing_logits(ckv, dtype, d):
     check_prefill(out, q, k, v, [0, T], [0, T], 1 / math.sqrt(d), ckv.chunkkv_prefill_path(p))
 
 
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 1), (BF, 64, 4), (F32, 64, 2)])
+def test_prefill_huge_logits_pick_one_key(ckv, dtype, d, G):
+    # exactly representable logits whose differences are 2^25 and more: the largest visible one takes all
+    T = 240
+    q = torch.zeros(T, G, d, dtype=dtype, device=DEV)
+    k = torch.zeros(T, 1, d, dtype=dtype, device=DEV)
+    q[:, :, 0] = 2.0 ** 14
+    size = torch.arange(T, device=DEV) * 7919 % 251
+    k[:, 0, 0] = (2.0 ** 14 * (1 + size)).to(dtype)
+    v = torch.randn(T, 1, d, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
+    out = ckv.prefill_attention(q, k, v, [0, T], scale=0.3)
+    best = torch.stack([size[:i + 1].argmax() for i in range(T)])
+    assert torch.equal(out, v[best].expand(T, G, d))
+
+
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 1), (BF, 64, 4), (F32, 64, 1)])
+def test_prefill_runs_of_minus_infinite_logits(ckv, dtype, d, G):
+    # whole runs of 32 visible keys whose logits are -inf take no weight, wherever a block's runs begin
+    T = 420
+    q, k, v = make_qkv([T], [T], G, 1, d, dtype, seed=23)
+    q = q.abs() + 0.01
+    gone = torch.zeros(T, dtype=torch.bool, device=DEV)
+    for a, b in ((32, 64), (128, 160), (224, 256), (300, 416)):
+        gone[a:b] = True
+    k[gone, :, 0] = -float("inf")
+    out = ckv.prefill_attention(q, k, v, [0, T])
+    s = torch.einsum("ihd,jd->hij", q.double(), torch.where(gone[:, None], 0, k[:, 0]).double()) / math.sqrt(d)
+    hide = gone[None] | (torch.arange(T, device=DEV)[None] > torch.arange(T, device=DEV)[:, None])
+    w = torch.softmax(s.masked_fill(hide, -math.inf), -1)
+    ref = torch.einsum("hij,jd->ihd", w, v[:, 0].double())
+    A = torch.einsum("hij,jd->ihd", w, v[:, 0].double().abs())
+    # logits of a few units off by (d + 4) 2^-24 of at most 64, the sums as above
+    tol = (2 * (d + 4) * 2.0 ** -24 * 64 + (T + 16) * 2.0 ** -23) * A + (2.0 ** -8 * (ref.abs() + A) if dtype == BF else 0)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
 def test_prefill_hidden_keys_may_hold_anything(ckv, dtype, d, bad):
