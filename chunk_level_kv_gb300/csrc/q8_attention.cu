@@ -386,7 +386,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float mn = fmaxf(m, top), vn = fmaxf(vref, sc0.y);
-        const float ref = (mn == -INFINITY ? 0.f : mn) - kWeightScale;
+        const float ref = mn == -INFINITY ? 0.f : mn;
         const float f = ex2(m - mn) * (vref == vn ? 1.f : vref / vn);
         if (m != -INFINITY) l *= ex2(m - mn);
         // the values' scale relative to the largest so far goes into the weights
@@ -409,7 +409,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p = ex2(s[2 * kk + (e >> 1)][e & 1] - ref);
+            const float p = ex2((s[2 * kk + (e >> 1)][e & 1] - ref) + kWeightScale);
             l += p;
             w[e] = p * vr;
           }

@@ -138,7 +138,7 @@ class Q8Cache:
         return self.B * self.Hkv
 
     def layer(self, i: int):
-        """The chunkkv_q8_cache of layer i, by reference."""
+        """The chunkkv_q8_cache of layer i, by reference (the tensors' addresses as they were at construction)."""
         return ctypes.byref(self._c[i])
 
 
@@ -178,17 +178,17 @@ def chunkkv_q8_resize(cache: Q8Cache, new_lens, slots=None) -> None:
 
 def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
     """Writes the first counts[b][h] of k, v [B, Hkv, n_cap, d] (any strides, d contiguous) to their slots."""
-    if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.dtype not in _DT:
+    shape, st, dt = k.shape, k.stride(), _DT.get(k.dtype)
+    if dt is None or v.shape != shape or v.stride() != st or v.dtype != k.dtype:
         raise ValueError("k and v of one shape, type (float32 or bfloat16) and strides")
-    if k.dim() != 4 or k.shape[0] != cache.B or k.shape[1] != cache.Hkv or k.shape[3] != cache.d or k.stride(3) != 1:
+    if len(shape) != 4 or shape[0] != cache.B or shape[1] != cache.Hkv or shape[3] != cache.d or st[3] != 1:
         raise ValueError("k, v [B, Hkv, n_cap, d], the head dimension contiguous")
-    n_cap = k.shape[2]
     _rows_i32(cache, counts, "counts")
-    if slots.dtype != torch.int64 or slots.shape != (cache.rows, n_cap) or not slots.is_contiguous():
+    if slots.dtype != torch.int64 or slots.shape != (cache.rows, shape[2]) or not slots.is_contiguous():
         raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
     _check("chunkkv_q8_append",
-           LIB.chunkkv_q8_append(cache.layer(layer), _DT[k.dtype], k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                                 k.stride(2), counts.data_ptr(), slots.data_ptr(), n_cap, _stream(cache.lens)))
+           LIB.chunkkv_q8_append(cache.layer(layer), dt, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2],
+                                 counts.data_ptr(), slots.data_ptr(), shape[2], _stream(cache.lens)))
 
 
 def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out) -> None:
@@ -211,16 +211,15 @@ def chunkkv_q8_workspace_size(cache: Q8Cache, G: int) -> int:
 
 def chunkkv_q8_attention(cache: Q8Cache, layer: int, q, out, ws, scale: float | None = None) -> None:
     """out [B, Hkv * G, d] = attention of q over the rows of one layer's cache."""
-    if q.dim() != 3 or q.shape != out.shape or q.dtype != out.dtype or q.dtype not in _DT:
+    shape, qs, os_, dt = q.shape, q.stride(), out.stride(), _DT.get(q.dtype)
+    if dt is None or len(shape) != 3 or out.shape != shape or out.dtype != q.dtype:
         raise ValueError("q and out [B, Hq, d] of one type, float32 or bfloat16")
-    if (q.shape[0] != cache.B or q.shape[2] != cache.d or q.shape[1] % cache.Hkv or q.stride(2) != 1
-            or out.stride(2) != 1):
+    if shape[0] != cache.B or shape[2] != cache.d or shape[1] % cache.Hkv or qs[2] != 1 or os_[2] != 1:
         raise ValueError("q and out [B, Hkv * G, d], the head dimension contiguous")
     _check("chunkkv_q8_attention",
-           LIB.chunkkv_q8_attention(cache.layer(layer), _DT[q.dtype], q.shape[1] // cache.Hkv,
-                                    1.0 / math.sqrt(cache.d) if scale is None else scale, q.data_ptr(), q.stride(0),
-                                    q.stride(1), out.data_ptr(), out.stride(0), out.stride(1), ws.data_ptr(), _bytes(ws),
-                                    _stream(cache.lens)))
+           LIB.chunkkv_q8_attention(cache.layer(layer), dt, shape[1] // cache.Hkv,
+                                    1.0 / math.sqrt(cache.d) if scale is None else scale, q.data_ptr(), qs[0], qs[1],
+                                    out.data_ptr(), os_[0], os_[1], ws.data_ptr(), _bytes(ws), _stream(cache.lens)))
 
 
 def q8_attention(cache: Q8Cache, layer: int, q, *, scale: float | None = None, out=None, workspace=None):
