@@ -26,8 +26,8 @@
 // Measured (one layer, 128 columns): 16384 tokens of 28 / 4 heads 1.03 ms, 1.87 PFLOP/s of
 // the visible pairs; 8192 tokens of 32 / 8 heads 0.31 ms, 1.76 PFLOP/s; 16 prompts of 100
 // to 2000 tokens packed 0.18 ms, 1.12 PFLOP/s (an item there has 6 block pairs, and its
-// begin and end cost as much as three more); 700 + 500 new tokens on 5 to 9 thousand
-// cached ones 0.09 ms; 64 new tokens on 9000 26 us.
+// begin and end cost as much as three more); 420 and 455 new tokens on 5.3 and 7.7
+// thousand cached ones 0.09 ms; 64 new tokens on 9000 26 us.
 //
 // The reference m of a row is the maximum of some of its first logits and stays while
 // the row's sum is below 2^24: a common factor of P, O and the sum costs no precision
