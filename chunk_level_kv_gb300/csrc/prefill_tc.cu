@@ -62,6 +62,7 @@ using namespace tcgen;
 
 constexpr int kTile = 128;                        // query rows of a tile, keys of a block
 constexpr int kStages = 4;                        // K and V blocks in shared memory (five were no faster)
+static_assert(kStages % 2 == 0, "K blocks lie in even stages, V blocks in odd ones");
 constexpr int kItemRing = 2;
 constexpr int kThreads = 384;                     // 12 warps, three warpgroups
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -400,7 +401,8 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
     mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
-    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 2); mbar_init(v_ok + 8 * i, 1); }
+    // a stage is released by the MMA issuers, one that holds V by the checking warp too
+    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 1); mbar_init(kv_empty + 8 * i, 2 + (i & 1)); mbar_init(v_ok + 8 * i, 1); }
     // an item's slot is released by the MMA issuers, the checking warp and each softmax warp
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11); mbar_init(checked + 8 * i, 1);
@@ -681,11 +683,18 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         for (int i = lane; i < kMaxChecked * 4; i += 32) bad_keys[i] = 0;
         __syncwarp();
         bool ok = true, any = false;
-        for (int j = it.nb - 1; j >= it.low && ok; --j) {
+        // Every V block is waited for and released, checked or not: a phase that was left out could still be open
+        // when a later one of its stage is waited for by parity, and one that this warp did not hold could be two
+        // phases gone.
+        for (int j = it.nb - 1; j >= 0 && ok; --j) {
           const uint32_t use = kv + 2 * (it.nb - 1 - j) + 1;
           const int st = use % kStages;
           ok = wait_warp(ctl, kv_full + 8 * st, (use / kStages) & 1, kDevTimeoutEpilogue);
           if (!ok) break;
+          if (j < it.low) {
+            if (lane == 0) mbar_arrive(kv_empty + 8 * st);
+            continue;
+          }
           uint4* blk = (uint4*)(sKV + st * kBlock);
           // 0 x + sum stays zero as long as every x is finite
           const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
@@ -720,7 +729,10 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it next
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(v_ok + 8 * st);
+          if (lane == 0) {
+            mbar_arrive(v_ok + 8 * st);
+            mbar_arrive(kv_empty + 8 * st);
+          }
         }
         if (!ok) break;
         kv += 2 * it.nb;
