@@ -111,7 +111,8 @@ enum DeviceError : int32_t {
 // The workspace header (256 bytes, zero-filled before the workspace's first use):
 // int32 word 0 is the device error word; words kSchedWord and kSchedWord + 1 are
 // the tensor-core scoring launch's item counter and count of finished CTAs, which
-// the launch's last CTA sets back to zero.
+// the launch's last CTA sets back to zero.  Decode attention (q8_attention.cu) counts
+// in the bytes from 32 on, back to zero as well.
 constexpr int kSchedWord = 4;
 
 // Decode a global unit id into (b, h, u).

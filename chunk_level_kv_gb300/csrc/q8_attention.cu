@@ -37,19 +37,24 @@ namespace chunkkv {
 namespace {
 
 constexpr int kMaxG = 8;                         // query heads per pass
-constexpr int kMaxGrid = 256;                    // CTAs of a pass (one per SM)
+constexpr int kMaxGrid = 224;                    // CTAs of a pass (one per SM): a count for each in the header
 constexpr float kWeightScale = 14.f;             // weights are 2^(t - m + 14): f16 keeps them to 2^-38 of the largest
-constexpr size_t kHeader = 256;                  // device error word
+constexpr int kMaxGroups = 16;                   // passes of kMaxG heads in one launch
+// Parts of a cut row that have arrived, 8 bits for each CTA (the row's first) and pass, zero between calls.  They lie
+// at a place that no shape moves and that no serving call writes otherwise; the first pass's in the header proper.
+constexpr int kCountByte = 32;
+static_assert(kCountByte > 4 * (kSchedWord + 1) && kCountByte % 4 == 0 && kMaxGrid % 4 == 0, "behind the other words");
+static_assert(kCountByte + kMaxGrid <= 256 && kMaxGrid < 256, "the first pass's counts lie in the header proper");
+static_assert(kCountByte + kMaxGrid * kMaxGroups <= kServeHeader, "the counts lie in the serving header");
 
 struct Q8AttnArgs {
   const void* q;
   void* out;
   int64_t q_sb, q_sh, o_sb, o_sh;
   float alpha;                                   // scale * log2(e)
-  int32_t G;
-  int32_t* err;
-  int32_t* arrived;                              // [groups][rows] partials written, zero between calls
-  float* part;                                   // [groups][2 CTAs][8][d64 + 4]: O, m, l
+  int32_t G, g0;                                 // query heads per KV head, and the first of this launch
+  int32_t* err;                                  // the workspace header: error word, counts of arrived parts
+  float* part;                                   // [passes][2 CTAs][8][d64 + 4]: O, m, l
 };
 
 // Rows of up to this many pages are not cut: a row in two pieces costs the CTAs that
@@ -260,7 +265,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       s_start[k] = x;
     }
   }
-  const int g0 = blockIdx.y * kMaxG, gn = min(kMaxG, a.G - g0);
+  const int g0 = a.g0 + blockIdx.y * kMaxG, gn = min(kMaxG, a.G - g0);
   // rows without a token
   for (int r = blockIdx.x; r < g.rows; r += gridDim.x)
     if (lens[r] <= 0)
@@ -485,9 +490,11 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         __threadfence();
         __syncthreads();
         if (tid == 0) {
-          int32_t* count = a.arrived + (int64_t)blockIdx.y * g.rows + r;
-          s_last = atomicAdd(count, 1) == (int)(last - first);
-          if (s_last) *count = 0;                // as the next call expects it
+          // a CTA is the first of one cut row at most: its byte counts that row's parts
+          const int at = kCountByte + blockIdx.y * kMaxGrid + (int)first, shift = 8 * (at & 3);
+          uint32_t* count = (uint32_t*)a.err + (at >> 2);
+          s_last = (int)(atomicAdd(count, 1u << shift) >> shift & 0xFFu) == (int)(last - first);
+          if (s_last) atomicSub(count, (uint32_t)(last - first + 1) << shift);   // as the next call expects it
           __threadfence();
         }
         __syncthreads();
@@ -575,7 +582,7 @@ cudaError_t launch(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_pages, 
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = raise_smem(q8_attention_kernel<ND, T>, (int)smem_bytes<ND>(), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, (a.G + kMaxG - 1) / kMaxG), dim3(32 * warps_of<ND>()),
+  return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, min(kMaxGroups, (a.G - a.g0 + kMaxG - 1) / kMaxG)), dim3(32 * warps_of<ND>()),
                     smem_bytes<ND>(), s, g, a, k_pages, v_pages, (const float2*)scales, table, lens);
 }
 
@@ -590,14 +597,12 @@ cudaError_t launch_nd(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_page
   }
 }
 
-size_t arrived_bytes(const Q8Geom& g, int groups) { return ((size_t)g.rows * groups * 4 + 255) / 256 * 256; }
-
 }  // namespace
 
-// [header | arrival counters | partials], for a grid of one CTA per SM.
+// [serving header | partials], for a grid of one CTA per SM.
 size_t q8_workspace_bytes(const Q8Geom& g, int G, int sms) {
-  const int groups = (G + kMaxG - 1) / kMaxG;
-  return kHeader + arrived_bytes(g, groups) + (size_t)groups * 2 * (sms < kMaxGrid ? sms : kMaxGrid) * kMaxG * (g.d64 + 4) * 4;
+  const int groups = min(kMaxGroups, (G + kMaxG - 1) / kMaxG);
+  return kServeHeader + (size_t)groups * 2 * (sms < kMaxGrid ? sms : kMaxGrid) * kMaxG * (g.d64 + 4) * 4;
 }
 
 cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
@@ -606,11 +611,14 @@ cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, 
                                 void* ws, int sms, cudaStream_t s) {
   char* w = (char*)ws;
   sms = sms < kMaxGrid ? sms : kMaxGrid;
-  const int groups = (G + kMaxG - 1) / kMaxG;
-  Q8AttnArgs a = {q, out, q_sb, q_sh, o_sb, o_sh, alpha, G, (int32_t*)w, (int32_t*)(w + kHeader),
-                  (float*)(w + kHeader + arrived_bytes(g, groups))};
-  if (bf16) return launch_nd<__nv_bfloat16>(g, a, k_pages, v_pages, scales, table, lens, sms, s);
-  return launch_nd<float>(g, a, k_pages, v_pages, scales, table, lens, sms, s);
+  // a pass for every 8 query heads of a KV head; launches of more passes than there are counts for share them
+  for (int g0 = 0; g0 < G; g0 += kMaxG * kMaxGroups) {
+    Q8AttnArgs a = {q, out, q_sb, q_sh, o_sb, o_sh, alpha, G, g0, (int32_t*)w, (float*)(w + kServeHeader)};
+    const cudaError_t e = bf16 ? launch_nd<__nv_bfloat16>(g, a, k_pages, v_pages, scales, table, lens, sms, s)
+                               : launch_nd<float>(g, a, k_pages, v_pages, scales, table, lens, sms, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace chunkkv

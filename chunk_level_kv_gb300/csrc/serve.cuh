@@ -6,6 +6,10 @@
 
 namespace chunkkv {
 
+// The start of a serving workspace: the header that all calls share (common.cuh), and behind it decode attention's
+// counts (q8_attention.cu), which partial results of any call leave alone.
+constexpr size_t kHeader = 256, kServeHeader = 3840;
+
 // ------------------------------------------------------------ prefill attention
 
 // Sequences of a packed batch in the order in which their work is taken (longest

@@ -36,7 +36,6 @@ cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, 
 
 namespace {
 
-constexpr size_t kServeHeader = 256;            // int32 device error word at offset 0
 constexpr double kLog2e = 1.4426950408889634;
 
 bool aligned(const void* p, uintptr_t n = 16) { return p != nullptr && ((uintptr_t)p & (n - 1)) == 0; }
@@ -186,11 +185,11 @@ chunkkv_status plan_prefill(const chunkkv_prefill_params* p, bool* tc, int* kb, 
   *tc = prefill_on_tc(p);
   *kb = 0;
   *n_items = 0;
-  *bytes = kServeHeader;
+  *bytes = kHeader;
   if (!*tc) return CHUNKKV_OK;
   plan_items(p, sm_count(), kb, n_items);
   if (*n_items > INT32_MAX / 2) return CHUNKKV_ERR_UNSUPPORTED;
-  if (*kb > 0) *bytes += prefill_tc_part_bytes(*n_items, p->d);
+  if (*kb > 0) *bytes = kServeHeader + prefill_tc_part_bytes(*n_items, p->d);
   return CHUNKKV_OK;
 }
 

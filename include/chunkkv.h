@@ -428,7 +428,10 @@ chunkkv_status chunkkv_q8_load(const chunkkv_q8_cache* c, int32_t dtype, const i
  *   q, out: device [B, Hkv * G, d] with element strides (b, head), multiples of 16 bytes;
  *   scale > 0 and finite; sums and softmax statistics in fp32;
  *   ws: device workspace of chunkkv_q8_workspace_size bytes, zero-filled before its
- *       first use; not shared by calls that can overlap.
+ *       first use; not shared by calls that can overlap.  One workspace may serve
+ *       caches and G of any kind and chunkkv_prefill_attention in turn; while G <= 8, the
+ *       compression's calls too (for G > 8 they would write over counts that have to be
+ *       zero).
  */
 chunkkv_status chunkkv_q8_workspace_size(const chunkkv_q8_cache* c, int32_t G, size_t* bytes);
 chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, int32_t G, float scale, const void* q,

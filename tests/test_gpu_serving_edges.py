@@ -7,7 +7,9 @@ import math
 import pytest
 import torch
 
-from test_gpu_serving import BF, DEV, F32, check_prefill, ckv, make_qkv, offsets  # noqa: F401
+from test_gpu_serving import (  # noqa: F401
+    BF, DEV, check_decode, check_prefill, ckv, make_qkv, offsets, random_cache,
+)
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,37 @@ def test_prefill_masked_items_after_unmasked_ones(ckv, Hq, Hkv, d, long):  # noq
             vb[ck[i]:ck[i + 1]] = bad
         for _ in range(20):
             assert torch.equal(ckv.prefill_attention(q, k, vb, cq, ck), clean)
+
+
+# ------------------------------------------------------------------ decode attention
+
+@pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])
+def test_decode_workspace_serves_any_calls_in_turn(ckv, between, heads):  # noqa: F811
+    # one workspace for caches of other shapes, other numbers of heads, and a split prompt (or, for up to 8 heads,
+    # the compression's scoring) between them
+    d = 128
+    small, g = random_cache(ckv, 2, 4, d, [6000 + 100 * i for i in range(8)], seed=51)
+    large, _ = random_cache(ckv, 64, 8, d, [600 + (i * 97) % 700 for i in range(512)], seed=52)
+    narrow, _ = random_cache(ckv, 3, 1, 64, [5000, 40, 2000], seed=53)
+    pq, pk, pv = make_qkv([20], [9000], 8, 2, d, BF, seed=54)
+    p, keep = ckv.prefill_params_for(pq, pk, [0, 20], [0, 9000])
+    want = ckv.prefill_attention(pq, pk, pv, [0, 20], [0, 9000])
+    window, sk, _ = make_qkv([16], [3000], 8, 2, d, BF, seed=55)
+    sp, keep_s = ckv.params_for(window[None], sk, [0, 3000], Hkv=2, w=16, c=10, L_max=100)
+    scores = torch.zeros(1, 2, ckv.chunkkv_out_capacity(sp)[1], device=DEV)
+    ws = torch.zeros(max([ckv.chunkkv_q8_workspace_size(c, G) for c in (small, large, narrow) for G in heads]
+                         + [ckv.chunkkv_prefill_workspace_size(p), ckv.chunkkv_workspace_size(sp)]),
+                     dtype=torch.uint8, device=DEV)
+    for G in heads:
+        for cache in (small, large, narrow, large):
+            q = torch.randn(cache.B, cache.Hkv * G, cache.d, generator=g, device=DEV).to(BF)
+            out = torch.full_like(q, float("nan"))
+            ckv.chunkkv_q8_attention(cache, 0, q, out, ws)
+            ckv.chunkkv_status_check(ws)
+            check_decode(ckv, cache, q, out, 1 / math.sqrt(cache.d))
+            if between == "prompt":
+                prompt = torch.full_like(pq, float("nan"))
+                ckv.chunkkv_prefill_attention(p, pq, pk, pv, prompt, ws)
+                assert torch.equal(prompt, want)
+            else:
+                ckv.chunkkv_score(sp, window, sk, scores, ws)
