@@ -21,7 +21,7 @@
 // finds its run by a scan over the lengths.  Inside a CTA the pages go to the warps in
 // turn; each warp has a K and a V slot that bulk copies fill while it works on the
 // other, so about 100 KB per SM are under way.  A row that lies in one CTA is
-// written at once; the CTAs that share a row write (m, l, O) partials, and the last one to
+// written at once; the CTAs that share a row write partials (O, l, references), and the last one to
 // arrive adds them in CTA order, so that the result does not depend on the order of
 // arrival.
 //
@@ -38,7 +38,8 @@ namespace {
 
 constexpr int kMaxG = 8;                         // query heads per pass
 constexpr int kMaxGrid = 224;                    // CTAs of a pass (one per SM): a count for each in the header
-constexpr float kWeightScale = 14.f;             // weights are 2^(t - m + 14): f16 keeps them to 2^-38 of the largest
+constexpr float kWeightScale = 14.f;             // weights are times 2^14: f16 keeps them to 2^-38 of the largest
+constexpr float kMostScale = 8.5e37f;            // about 2^126
 constexpr int kMaxGroups = 16;                   // passes of kMaxG heads in one launch
 // Parts of a cut row that have arrived, 8 bits for each CTA (the row's first) and pass, zero between calls.  They lie
 // at a place that no shape moves and that no serving call writes otherwise; the first pass's in the header proper.
@@ -54,7 +55,7 @@ struct Q8AttnArgs {
   float alpha;                                   // scale * log2(e)
   int32_t G, g0;                                 // query heads per KV head, and the first of this launch
   int32_t* err;                                  // the workspace header: error word, counts of arrived parts
-  float* part;                                   // [passes][2 CTAs][8][d64 + 4]: O, m, l
+  float* part;                                   // [passes][2 CTAs][8][d64 + 4]: O, m, l, O's reference
 };
 
 // Rows of up to this many pages are not cut: a row in two pieces costs the CTAs that
@@ -71,7 +72,7 @@ constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
 template <int ND>
 constexpr int page_bytes() { return ND * 64 * kPage; }
 template <int ND>
-constexpr int merge_pitch() { return 64 * ND + 2; }         // O, then m and l
+constexpr int merge_pitch() { return 64 * ND + 3; }         // O, then m, l and O's reference
 template <int ND>
 constexpr int part_pitch() { return 64 * ND + 4; }          // the same in the workspace, in 16-byte rows
 template <int ND>
@@ -86,6 +87,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)_
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // D (16 x 8, fp32) += A (16 x 16, f16) B (16 x 8, f16)
@@ -134,6 +140,11 @@ __device__ __forceinline__ void store4(float* p, float4 v) { *(float4*)p = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
   *(uint2*)p = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+}
+
+// O over the sum, from O's reference to the sum's.
+__device__ __forceinline__ float4 finish(float4 o, float sum, float up) {
+  return make_float4(o.x / sum * up, o.y / sum * up, o.z / sum * up, o.w / sum * up);
 }
 
 __device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
@@ -338,7 +349,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
           if constexpr (q_in_regs<ND>()) qf[s] = f; else sQ[s * 32 + lane] = f;
         }
       }
-      float m = -INFINITY, l = 0.f, vref = 0.f;
+      float m = -INFINITY, l = 0.f, mo = -INFINITY;
       float o[NT][4];
 #pragma unroll
       for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -390,14 +401,15 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m, top), vn = fmaxf(vref, sc0.y);
+        const float mn = fmaxf(m, top);
         const float ref = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - mn) * (vref == vn ? 1.f : vref / vn);
         if (m != -INFINITY) l *= ex2(m - mn);
-        // the values' scale relative to the largest so far goes into the weights
-        const float vr = sc0.y == 0.f ? 0.f : sc0.y / vn;
-        if (__any_sync(0xffffffffu, mn != m || vn != vref)) {
-          const float fo = m == -INFINITY ? 0.f : f;
+        m = mn;
+        // O has a reference of its own, the maximum of t + log2 s_v: how large a page's values are counts only with
+        // the weight that they have, and f16 keeps every weight times s_v to 2^-38 of the largest
+        const float on = fmaxf(mo, top + lg2(fabsf(sc0.y)));
+        if (__any_sync(0xffffffffu, on != mo)) {
+          const float fo = mo == -INFINITY ? 0.f : ex2(mo - on);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             o[i][0] *= fo;
@@ -406,8 +418,12 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
             o[i][3] *= fo;
           }
         }
-        m = mn;
-        vref = vn;
+        mo = on;
+        // 2^(t - ref) vr = 2^(t - on) s_v.  The power in two halves, since it alone may pass fp32's range, and the
+        // product bounded, since 0 x inf is NaN (the bound meets weights below 2^-112 of the largest)
+        const float half = ex2(0.5f * (ref - (on == -INFINITY ? 0.f : on)));
+        float vr = sc0.y == 0.f ? 0.f : sc0.y * half * half;
+        vr = vr > kMostScale ? kMostScale : vr;
         uint4 pf[4];
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -447,12 +463,13 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       float* mw = sM + (warp * kMaxG + gid) * kPitch;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        mw[8 * i + 2 * t4] = (o[i][0] + o[i][2]) * vref;
-        mw[8 * i + 2 * t4 + 1] = (o[i][1] + o[i][3]) * vref;
+        mw[8 * i + 2 * t4] = o[i][0] + o[i][2];
+        mw[8 * i + 2 * t4 + 1] = o[i][1] + o[i][3];
       }
       if (t4 == 0) {
         mw[64 * ND] = m;
         mw[64 * ND + 1] = l;
+        mw[64 * ND + 2] = mo;
       }
       __syncthreads();
       const bool whole = sa == xr && sb == xr + np;
@@ -462,27 +479,30 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       float* part = a.part + (int64_t)blockIdx.y * 2 * nc * kMaxG * kPart;
       for (int i = tid; i < gn * 64 * ND; i += kThreads) {
         const int q = i / (64 * ND), c = i % (64 * ND);
-        float M = -INFINITY;
+        float M = -INFINITY, MO = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, sM[(w * kMaxG + q) * kPitch + 64 * ND]);
-        const float ref = M == -INFINITY ? 0.f : M;
+        for (int w = 0; w < W; ++w) {
+          M = fmaxf(M, sM[(w * kMaxG + q) * kPitch + 64 * ND]);
+          MO = fmaxf(MO, sM[(w * kMaxG + q) * kPitch + 64 * ND + 2]);
+        }
+        const float ref = M == -INFINITY ? 0.f : M, oref = MO == -INFINITY ? 0.f : MO;
         float L = 0.f, acc = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float* src = sM + (w * kMaxG + q) * kPitch;
-          const float f = ex2(src[64 * ND] - ref);
-          // a warp without a page of this row holds zeros and m = -inf
-          L += src[64 * ND + 1] * f;
-          acc += src[c] * f;
+          // a warp without a page of this row holds zeros and -inf
+          L += src[64 * ND + 1] * ex2(src[64 * ND] - ref);
+          acc += src[c] * ex2(src[64 * ND + 2] - oref);
         }
         if (whole) {
-          if (c < g.d) store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L);
+          if (c < g.d) store1((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, acc / L * ex2(MO - M));
         } else {
           float* dst = part + ((2 * blockIdx.x + (sa > xr ? 0 : 1)) * kMaxG + q) * kPart;
           dst[c] = acc;
           if (c == 0) {
             dst[64 * ND] = M;
             dst[64 * ND + 1] = L;
+            dst[64 * ND + 2] = MO;
           }
         }
       }
@@ -499,29 +519,37 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
         }
         __syncthreads();
         if (s_last) {
-          // factors 2^(m - M) of the parts and the sums, then O: 16 bytes of a part per thread and step, the
+          // factors of the parts' O and the sums, then O: 16 bytes of a part per thread and step, the
           // parts dealt to as many groups of threads as there are, the groups' sums added in order
           const int np2 = (int)(last - first) + 1, ne = gn * (16 * ND);
           float* sF = sM;                        // [np2][kMaxG]
           float4* sA = (float4*)(sM + (size_t)W * kMaxG * kPitch - 4 * kThreads);   // [groups][ne]
           static_assert(W * kMaxG * kPitch - 4 * kThreads >= kMaxG * kMaxGrid, "a factor for every part");
           auto src = [&](int k, int q) { return part + ((2 * (first + k) + (k == 0)) * kMaxG + q) * kPart; };
-          __shared__ float s_sum[kMaxG];
+          __shared__ float s_sum[kMaxG], s_up[kMaxG];
           for (int q = warp; q < gn; q += W) {
-            float M = -INFINITY;
-            for (int k = lane; k < np2; k += 32) M = fmaxf(M, __ldcg(src(k, q) + 64 * ND));
+            float M = -INFINITY, MO = -INFINITY;
+            for (int k = lane; k < np2; k += 32) {
+              M = fmaxf(M, __ldcg(src(k, q) + 64 * ND));
+              MO = fmaxf(MO, __ldcg(src(k, q) + 64 * ND + 2));
+            }
 #pragma unroll
-            for (int o2 = 16; o2; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
-            const float ref = M == -INFINITY ? 0.f : M;
+            for (int o2 = 16; o2; o2 >>= 1) {
+              M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+              MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o2));
+            }
+            const float ref = M == -INFINITY ? 0.f : M, oref = MO == -INFINITY ? 0.f : MO;
             float L = 0.f;
             for (int k = lane; k < np2; k += 32) {
-              const float f = ex2(__ldcg(src(k, q) + 64 * ND) - ref);
-              sF[k * kMaxG + q] = f;
-              L = fmaf(__ldcg(src(k, q) + 64 * ND + 1), f, L);
+              sF[k * kMaxG + q] = ex2(__ldcg(src(k, q) + 64 * ND + 2) - oref);
+              L = fmaf(__ldcg(src(k, q) + 64 * ND + 1), ex2(__ldcg(src(k, q) + 64 * ND) - ref), L);
             }
 #pragma unroll
             for (int o2 = 16; o2; o2 >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o2);
-            if (lane == 0) s_sum[q] = L;
+            if (lane == 0) {
+              s_sum[q] = L;
+              s_up[q] = ex2(MO - M);
+            }
           }
           __syncthreads();
           const int ng = max(1, kThreads / ne);
@@ -541,8 +569,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
               sA[i] = acc;
             } else {
               T* dst = (T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c;
-              const float L = s_sum[q];
-              if (c < g.d) store4(dst, make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L));
+              if (c < g.d) store4(dst, finish(acc, s_sum[q], s_up[q]));
             }
           }
           if (ng > 1) {
@@ -554,10 +581,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
                 acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
               }
               const int q = tid / (16 * ND), c = (tid % (16 * ND)) * 4;
-              const float L = s_sum[q];
-              if (c < g.d)
-                store4((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c,
-                       make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L));
+              if (c < g.d) store4((T*)a.out + b * a.o_sb + (hq + q) * a.o_sh + c, finish(acc, s_sum[q], s_up[q]));
             }
           }
         }

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from test_gpu_serving import (  # noqa: F401
-    BF, DEV, check_decode, check_prefill, ckv, make_qkv, offsets, random_cache,
+    BF, DEV, F32, check_decode, check_prefill, ckv, fill, make_qkv, offsets, random_cache, read,
 )
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +73,35 @@ def test_decode_workspace_serves_any_calls_in_turn(ckv, between, heads):  # noqa
                 assert torch.equal(prompt, want)
             else:
                 ckv.chunkkv_score(sp, window, sk, scores, ws)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,G", [(128, 4), (256, 2)])
+def test_decode_value_scales_far_apart(ckv, dtype, d, G):  # noqa: F811
+    # Half of a row's pages hold values 2^r times the others' under weights below 2^-190 of theirs; the pages of a
+    # kind lie together (so that a warp has both kinds), in either order.  Tolerance as in check_decode with the
+    # logits of the keys that count.
+    rows, n = 320, 16 * 64
+    g = torch.Generator(device=DEV).manual_seed(61)
+    cache = ckv.q8_cache(rows, 1, d, n_pages=rows * 16, max_pages=16)
+    k = torch.randn(rows, 1, n, d, generator=g, device=DEV)
+    k[..., 0] = torch.rand(rows, 1, n, generator=g, device=DEV)
+    v = torch.randn(rows, 1, n, d, generator=g, device=DEV)
+    r = torch.tensor([0.0, 20.0, 30.0, 40.0, 60.0, 90.0], device=DEV)[torch.arange(rows, device=DEV) // 2 % 6]
+    far = (torch.arange(n, device=DEV)[None] < n // 2) ^ (torch.arange(rows, device=DEV) % 2 == 1)[:, None]
+    k[:, 0, :, 0] = torch.where(far, -140.0, k[:, 0, :, 0])
+    v *= torch.where(far, 2.0 ** r[:, None], 1.0)[:, None, :, None]
+    fill(ckv, cache, [n] * rows, k, v)
+    q = torch.zeros(rows, G, d, device=DEV)
+    q[:, :, 0] = 1 + torch.arange(G, device=DEV) / 4
+    q = q.to(dtype)
+    out = ckv.q8_attention(cache, 0, q, scale=1.0)
+    for i, (kr, vr) in enumerate(read(ckv, cache, F32)):
+        near = ~far[i]
+        qi, ki, vi = q[i].double(), kr.double(), vr.double()
+        p = torch.softmax(qi @ ki.T, -1)
+        ref, A = p @ vi, p @ vi.abs()
+        E = (qi.abs() @ ki[near].abs().T).amax(1, keepdim=True)
+        tol = (2 * (d + 4) * 2.0 ** -22 * E + (n + 16) * 2.0 ** -22) * A + (2.0 ** -8 * ref.abs() if dtype == BF else 0)
+        err = (out[i].double() - ref).abs()
+        assert bool((err <= tol).all()), f"2^{int(r[i])}, row {i}: {float((err / tol).max())} of the tolerance"
