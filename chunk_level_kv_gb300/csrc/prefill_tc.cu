@@ -244,6 +244,13 @@ __device__ __forceinline__ float row_exp_from(uint32_t tS, float base, float alp
   return sum;
 }
 
+// What the rounding of -m alpha took from a row's reference: its terms are 2^(S alpha - (m alpha - residual)).  Terms
+// under two references are comparable only with it (near kHuge -m alpha is rounded to multiples of 1/4).
+__device__ __forceinline__ float residual(float m, float alpha) {
+  const float neg = -m * alpha;
+  return fabsf(neg) <= kHuge ? fmaf(m, alpha, neg) : 0.f;     // huge references: see block_again
+}
+
 // A block whose sum passed the bound, or whose reference is huge, done over: rows that are `over` move their
 // reference to the block's maximum, and what O (at tO, unless it is still empty) and l
 // hold goes with it.  Under a huge reference S alpha - m alpha in one rounding is off by
@@ -253,8 +260,11 @@ template <int D>
 __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha, float m, float l, bool over) {
   const float bm = row_max(tS);
   const float mn = fmaxf(m, bm);
-  const float f = over ? ex2((m - mn) * alpha) : 1.f;
-  if (over) m = mn;
+  float f = 1.f;
+  if (over) {
+    f = m == -INFINITY ? 0.f : ex2((m - mn) * alpha - residual(m, alpha) + residual(mn, alpha));
+    m = mn;
+  }
   const float neg = m == -INFINITY ? 0.f : -m * alpha;
   if (tO != 0xFFFFFFFFu) {
     // the blocks before are done: their products were issued before this S
@@ -810,7 +820,7 @@ join_kernel(const __grid_constant__ TcGeom g, const __grid_constant__ PrefillTab
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
 #pragma unroll 2
     for (int k = 0; k < parts; ++k) {
-      const float f = ex2((__ldcg(ml + k * next) - ref) * g.alpha);
+      const float m = __ldcg(ml + k * next), f = ex2((m - ref) * g.alpha - residual(m, g.alpha));
       const float* p = p0 + k * next + (warp & 3) * (D * 32) + c * 32 + lane;
       L = fmaf(__ldcg(ml + k * next + kTile), f, L);
 #pragma unroll

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from test_gpu_serving import (  # noqa: F401
-    BF, DEV, F32, check_decode, check_prefill, ckv, fill, make_qkv, offsets, random_cache, read,
+    BF, DEV, F32, attention64, check_decode, check_prefill, ckv, fill, make_qkv, offsets, random_cache, read,
 )
 
 pytestmark = pytest.mark.gpu
@@ -39,6 +39,38 @@ def test_prefill_masked_items_after_unmasked_ones(ckv, Hq, Hkv, d, long):  # noq
             vb[ck[i]:ck[i + 1]] = bad
         for _ in range(20):
             assert torch.equal(ckv.prefill_attention(q, k, vb, cq, ck), clean)
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("d,size", [(128, 4), (64, 4), (128, 8)])
+def test_prefill_references_far_from_zero(ckv, d, size, split):  # noqa: F811
+    # Exactly representable logits near size * 2^20 that differ by a few units between blocks of keys, so that
+    # several blocks, and parts, of a row share the weight under references of their own.  In a row's last block
+    # the last 32 keys lie 39 units lower (2^16.9 in weight), so a first reference taken there has to move.
+    # Tolerance: logits exact, exponents below 40 in fp32 (2^-18 of a weight), sums and bf16 as elsewhere.
+    T, rows, scale = 6000 if split else 960, 128, 0.3
+    g = torch.Generator(device=DEV).manual_seed(size + d)
+    q = torch.zeros(rows, 1, d, dtype=BF, device=DEV)
+    k = torch.zeros(T, 1, d, dtype=BF, device=DEV)
+    q[:, 0, 0] = 1024.0 * (1 + torch.arange(rows, device=DEV) / 128)
+    q[:, 0, 1] = 1.0
+    k[:, 0, 0] = 1024.0 * size
+    blocks = (torch.arange(T, device=DEV) - (T - rows)).div(128, rounding_mode="floor") + T // 128 + 1
+    up = torch.randint(0, 4, (T // 128 + 2,), generator=g, device=DEV)[blocks] + 40
+    up[-32 - rows:] = 1
+    k[:, 0, 1] = up.to(BF)
+    v = torch.where(torch.rand(T // 128 + 2, 1, d, generator=g, device=DEV) < 0.5, -1.0, 1.0)[blocks].to(BF)
+    cq, ck = [0, rows], [0, T]
+    p, keep = ckv.prefill_params_for(q, k, cq, ck, scale=scale)
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
+    assert (ws.numel() > 1 << 16) == split
+    out = torch.full_like(q, float("nan"))
+    ckv.chunkkv_prefill_attention(p, q, k, v, out, ws)
+    ckv.chunkkv_status_check(ws)
+    ref, A, _ = attention64(q, k, v, scale)
+    tol = (2.0 ** -18 + (T + 16) * 2.0 ** -23 + 2.0 ** -8) * A + 2.0 ** -8 * ref.abs()
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
 
 
 # ------------------------------------------------------------------ decode attention
