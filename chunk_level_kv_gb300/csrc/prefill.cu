@@ -200,7 +200,8 @@ prefill_simt_kernel(const __grid_constant__ PrefillTable<MAXB> tab, PrefillGeom 
   for (int r = 0; r < RM; ++r) {
     const int row = ty * RM + r;
     if (row >= rows) continue;
-    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];        // l is 0 only where no key is visible
+    // no visible key: zeros; logits that are all -inf: NaN (else l is 1 or more, from the maximum)
+    const float inv = l[r] != 0.f ? 1.f / l[r] : last0 + r < 0 ? 0.f : NAN;
     T* po = out + (int64_t)(sq.q0 + r0 + row) * g.o_st + h * g.o_sh;
 #pragma unroll
     for (int c = 0; c < ND; ++c)

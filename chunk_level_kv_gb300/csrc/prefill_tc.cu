@@ -488,7 +488,8 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
       }
       if (!ok) break;
       // ---- the item's rows
-      const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);  // no visible key: zeros (else l is 1 or more, from its reference)
+      // no visible key: zeros; logits that are all -inf: NaN (else l is 1 or more, from its reference)
+      const float inv = l != 0.f ? __fdividef(1.f, l) : limit < 0 ? 0.f : NAN;
       bool flagged = false;
       if (it.nb > 0 && t * g.pos < it.rows) {
         if (!wait_warp(ctl, checked + 8 * slot, (cc >> slot) & 1, kDevTimeoutEpilogue)) break;
@@ -826,7 +827,8 @@ join_kernel(const __grid_constant__ TcGeom g, const __grid_constant__ PrefillTab
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i), f, o[i]);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;               // no visible key: zeros
+    // no visible key: zeros; logits that are all -inf: NaN
+    const float inv = L != 0.f ? 1.f / L : it.limit + t * g.pos + ((row * g.inv_gp) >> 16) < 0 ? 0.f : NAN;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] *= inv;
     put8(rows + row * 80 + (warp >> 2) * 32, o);

@@ -320,7 +320,8 @@ chunkkv_status chunkkv_probe_ex2(float* sink, int32_t blocks, int32_t iters, chu
  *   out[i][hq] = sum over j <= i + Tk - Tq of softmax_j(scale * q[i][hq] . k[j][hq / G]) * v[j][hq / G]
  * per sequence (i, j local to it): the last query sits at the last key, so Tq < Tk
  * continues a sequence whose first Tk - Tq keys are cached, and Tq > Tk leaves the
- * first Tq - Tk queries without a key; their rows are zeros.  A key that a query
+ * first Tq - Tk queries without a key; their rows are zeros (logits that are all
+ * -inf give NaN, as the formula does).  A key that a query
  * does not see adds nothing to it, whatever k and v hold there (infinities and NaN
  * included).
  *   q, out [Tq_total, Hq, d], k, v [Tk_total, Hkv, d]: device memory, dtype's type

@@ -73,6 +73,22 @@ def test_prefill_references_far_from_zero(ckv, d, size, split):  # noqa: F811
     assert bool((err <= tol).all()), float((err / tol).max())
 
 
+@pytest.mark.parametrize("dtype,d,T", [(BF, 128, 300), (BF, 64, 5000), (F32, 64, 300), (BF, 256, 100)])
+def test_prefill_rows_of_minus_infinite_logits_alone(ckv, dtype, d, T):  # noqa: F811
+    # the softmax of logits that are all -inf is NaN; a row without a key gives zeros
+    rows = 40
+    q, k, v = make_qkv([rows + 3], [T], 2, 1, d, dtype, seed=29)
+    q = q.abs() + 0.01
+    k = k.clone()
+    k[:T - rows + 10, :, 0] = -float("inf")
+    out = ckv.prefill_attention(q[:rows], k, v, [0, rows], [0, T])
+    assert bool(out[:10].isnan().all()) and bool(torch.isfinite(out[10:]).all())
+    # three queries more than keys
+    k[:, :, 0] = -float("inf")
+    out = ckv.prefill_attention(q, k[:rows], v[:rows], [0, rows + 3], [0, rows])
+    assert bool((out[:3] == 0).all()) and bool(out[3:].isnan().all())
+
+
 # ------------------------------------------------------------------ decode attention
 
 @pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])
