@@ -23,11 +23,18 @@ def _bytes(t):
     return t.numel() * t.element_size()
 
 
-def _stream(t) -> int:
-    """The current stream of the tensor's device, as the integer that ctypes passes on."""
-    if not t.is_cuda:
+def _stream(t, *others) -> int:
+    """The current stream of the tensors' device, as the integer that ctypes passes on.  They lie on one GPU, and it
+    is the current one: the library asks the current device for its size and launches there."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("the tensors live in GPU memory")
-    return torch._C._cuda_getCurrentRawStream(t.device.index or 0)
+    for o in others:
+        if o.get_device() != dev:
+            raise ValueError("the tensors of a call lie on one GPU")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors lie on cuda:{dev}, which is not the current device (torch.cuda.device makes it so)")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 # ------------------------------------------------------------------ prefill attention
@@ -73,7 +80,7 @@ def chunkkv_prefill_path(p: PrefillParams) -> int:
 def chunkkv_prefill_attention(p: PrefillParams, q, k, v, out, ws) -> None:
     _check("chunkkv_prefill_attention",
            LIB.chunkkv_prefill_attention(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), ws.data_ptr(), _bytes(ws),
-                                         _stream(q)))
+                                         _stream(q, k, v, out, ws)))
 
 
 def prefill_attention(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, out=None, workspace=None):
@@ -118,6 +125,8 @@ class Q8Cache:
             raise ValueError("table [B * Hkv, max_pages], lens [B * Hkv], state [4]")
         if not len(self.k_pages) == len(self.v_pages) == len(self.scales):
             raise ValueError("k_pages, v_pages and scales of every layer")
+        if len({t.device for t in (*ints, *self.k_pages, *self.v_pages, *self.scales)}) != 1:
+            raise ValueError("the tensors of a cache lie on one device")
         for k, v, s in zip(self.k_pages, self.v_pages, self.scales):
             if (k.shape != (n_pages, d64 // 64, Q8_PAGE, 64) or v.shape != (n_pages, d64, Q8_PAGE)
                     or s.shape != (n_pages, 2) or k.dtype != torch.int8 or v.dtype != torch.int8
@@ -172,8 +181,9 @@ def chunkkv_q8_resize(cache: Q8Cache, new_lens, slots=None) -> None:
         if slots.dtype != torch.int64 or slots.dim() != 2 or slots.shape[0] != cache.rows or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
         n_cap = slots.shape[1]
+    stream = _stream(cache.lens, new_lens) if slots is None else _stream(cache.lens, new_lens, slots)
     _check("chunkkv_q8_resize", LIB.chunkkv_q8_resize(cache.layer(0), new_lens.data_ptr(), None if slots is None else slots.data_ptr(), n_cap,
-                                                      _stream(cache.lens)))
+                                                      stream))
 
 
 def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
@@ -188,7 +198,8 @@ def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
         raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
     _check("chunkkv_q8_append",
            LIB.chunkkv_q8_append(cache.layer(layer), dt, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2],
-                                 counts.data_ptr(), slots.data_ptr(), shape[2], _stream(cache.lens)))
+                                 counts.data_ptr(), slots.data_ptr(), shape[2],
+                                 _stream(cache.lens, k, v, counts, slots)))
 
 
 def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out) -> None:
@@ -200,7 +211,7 @@ def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out)
         raise ValueError("k_out, v_out [tokens, d] of one type and layout, the head dimension contiguous")
     _check("chunkkv_q8_load",
            LIB.chunkkv_q8_load(cache.layer(layer), _DT[k_out.dtype], start.data_ptr(), n_cap, k_out.data_ptr(), v_out.data_ptr(),
-                               k_out.stride(0), _stream(cache.lens)))
+                               k_out.stride(0), _stream(cache.lens, start, k_out, v_out)))
 
 
 def chunkkv_q8_workspace_size(cache: Q8Cache, G: int) -> int:
@@ -219,7 +230,8 @@ def chunkkv_q8_attention(cache: Q8Cache, layer: int, q, out, ws, scale: float | 
     _check("chunkkv_q8_attention",
            LIB.chunkkv_q8_attention(cache.layer(layer), dt, shape[1] // cache.Hkv,
                                     1.0 / math.sqrt(cache.d) if scale is None else scale, q.data_ptr(), qs[0], qs[1],
-                                    out.data_ptr(), os_[0], os_[1], ws.data_ptr(), _bytes(ws), _stream(cache.lens)))
+                                    out.data_ptr(), os_[0], os_[1], ws.data_ptr(), _bytes(ws),
+                                    _stream(cache.lens, q, out, ws)))
 
 
 def q8_attention(cache: Q8Cache, layer: int, q, *, scale: float | None = None, out=None, workspace=None):

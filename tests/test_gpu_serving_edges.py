@@ -153,3 +153,25 @@ def test_decode_value_scales_far_apart(ckv, dtype, d, G):  # noqa: F811
         tol = (2 * (d + 4) * 2.0 ** -22 * E + (n + 16) * 2.0 ** -22) * A + (2.0 ** -8 * ref.abs() if dtype == BF else 0)
         err = (out[i].double() - ref).abs()
         assert bool((err <= tol).all()), f"2^{int(r[i])}, row {i}: {float((err / tol).max())} of the tolerance"
+
+
+def test_calls_refuse_tensors_outside_the_gpu(ckv):  # noqa: F811
+    # one argument at a time in host memory: an error on the host, and nothing is launched
+    cache, _ = random_cache(ckv, 1, 2, 64, [70, 5], seed=91)
+    i32, i64 = torch.zeros(2, dtype=torch.int32, device=DEV), torch.zeros(2, 4, dtype=torch.int64, device=DEV)
+    k = torch.zeros(1, 2, 4, 64, device=DEV)
+    start, rows = torch.zeros(2, dtype=torch.int64, device=DEV), torch.zeros(100, 64, device=DEV)
+    q, ws = torch.zeros(1, 4, 64, device=DEV), torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    p, keep = ckv.prefill_params_for(rows[:, None], rows[:, None], [0, 100])
+    calls = [(lambda n, s: ckv.chunkkv_q8_resize(cache, n, s), (i32, i64)),
+             (lambda k, v, n, s: ckv.chunkkv_q8_append(cache, 0, k, v, n, s), (k, k, i32, i64)),
+             (lambda s, k, v: ckv.chunkkv_q8_load(cache, 0, s, 4, k, v), (start, rows, rows)),
+             (lambda q, o, w: ckv.chunkkv_q8_attention(cache, 0, q, o, w), (q, q.clone(), ws)),
+             (lambda *a: ckv.chunkkv_prefill_attention(p, *a), (rows[:, None],) * 4 + (ws,))]
+    torch.cuda.synchronize()
+    before = ckv.chunkkv_launch_count()
+    for call, args in calls:
+        for i in range(len(args)):
+            with pytest.raises(ValueError):
+                call(*args[:i], args[i].cpu(), *args[i + 1:])
+    assert ckv.chunkkv_launch_count() == before
