@@ -89,6 +89,7 @@ def _load():
         "chunkkv_q8_resize": [Q8, vp, vp, i32, vp],
         "chunkkv_q8_append": [Q8, i32, vp, vp, i64, i64, i64, vp, vp, i32, vp],
         "chunkkv_q8_load": [Q8, i32, vp, i32, vp, vp, i64, vp],
+        "chunkkv_q8_load_bounded": [Q8, i32, vp, i32, i64, vp, vp, i64, vp],
         "chunkkv_q8_workspace_size": [Q8, i32, ctypes.POINTER(sz)],
         "chunkkv_q8_attention": [Q8, i32, i32, ctypes.c_float, vp, i64, i64, vp, i64, i64, vp, sz, vp],
     }

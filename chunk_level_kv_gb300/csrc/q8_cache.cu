@@ -361,7 +361,7 @@ append_kernel(Q8Geom g, AppendArgs a, const int32_t* __restrict__ counts, const 
 struct LoadArgs {
   const int8_t* pages[2];
   void* out[2];
-  int64_t st_t;
+  int64_t st_t, n_rows;            // rows of the outputs: what lies past them is not written
   int32_t n_cap;
 };
 
@@ -376,11 +376,12 @@ load_kernel(Q8Geom g, LoadArgs a, const int32_t* __restrict__ table, const int32
   pdl_wait();
   const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, j = blockIdx.x;
   const int n = min(safe_len(lens[r], g.max_pages), a.n_cap);
-  const int nt = min(kPage, n - j * kPage);
+  int nt = min(kPage, n - j * kPage);
   const int64_t at = start[r];
   if (nt > 0 && at >= 0) {
     const int64_t page = safe_page(table[(int64_t)r * g.max_pages + j], g.n_pages);
     const float scale = scales[page * 2 + which];
+    nt = (int)min((int64_t)nt, max(a.n_rows - at - j * kPage, (int64_t)0));
     const int8_t* pg = (which ? a.pages[1] : a.pages[0]) + page * (int64_t)(g.d64 * kPage);
     T* out = (T*)(which ? a.out[1] : a.out[0]) + (at + j * kPage) * a.st_t;
     const int v8 = g.d / 8;
@@ -456,9 +457,9 @@ cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const vo
 }
 
 cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,
-                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, void* k_out,
-                           void* v_out, int64_t st_t, cudaStream_t s) {
-  LoadArgs a = {{k_pages, v_pages}, {k_out, v_out}, st_t, n_cap};
+                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, int64_t n_rows,
+                           void* k_out, void* v_out, int64_t st_t, cudaStream_t s) {
+  LoadArgs a = {{k_pages, v_pages}, {k_out, v_out}, st_t, n_rows, n_cap};
   const size_t smem = (size_t)g.d64 * (kPage + 4);
   const dim3 grid((n_cap + kPage - 1) / kPage, g.rows, 2);
   auto fn = bf16 ? load_kernel<__nv_bfloat16> : load_kernel<float>;

@@ -26,8 +26,8 @@ cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const vo
                              int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, int8_t* k_pages,
                              int8_t* v_pages, float* scales, cudaStream_t s);
 cudaError_t launch_q8_load(const Q8Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const int8_t* k_pages,
-                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, void* k_out,
-                           void* v_out, int64_t st_t, cudaStream_t s);
+                           const int8_t* v_pages, const float* scales, const int64_t* start, int n_cap, int64_t n_rows,
+                           void* k_out, void* v_out, int64_t st_t, cudaStream_t s);
 size_t q8_workspace_bytes(const Q8Geom& g, int G, int sms);                                   // q8_attention.cu
 cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, const void* q, int64_t q_sb,
                                 int64_t q_sh, void* out, int64_t o_sb, int64_t o_sh, const int8_t* k_pages,
@@ -285,17 +285,23 @@ chunkkv_status chunkkv_q8_append(const chunkkv_q8_cache* c, int32_t dtype, const
 
 chunkkv_status chunkkv_q8_load(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
                                void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream) {
+  return chunkkv_q8_load_bounded(c, dtype, start, n_cap, INT64_MAX, k_out, v_out, st_t, stream);
+}
+
+chunkkv_status chunkkv_q8_load_bounded(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                                       int64_t n_rows, void* k_out, void* v_out, int64_t st_t,
+                                       chunkkv_stream_t stream) {
   Q8Geom g;
   const chunkkv_status st = check_cache(c, true, &g);
   if (st != CHUNKKV_OK) return st;
-  if (!valid_dtype(dtype) || n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype) || n_cap < 0 || n_rows < 0) return CHUNKKV_ERR_INVALID_ARG;
   const int elt = elt_size(dtype);
   if ((g.d * elt) % 16 != 0 || !stride_ok(st_t, elt)) return CHUNKKV_ERR_INVALID_ARG;
   if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
-  if (g.rows == 0 || n_cap == 0) return CHUNKKV_OK;
+  if (g.rows == 0 || n_cap == 0 || n_rows == 0) return CHUNKKV_OK;
   if (!aligned(start, 8) || !aligned(k_out) || !aligned(v_out)) return CHUNKKV_ERR_INVALID_ARG;
   return cuda_result(launch_q8_load(g, dtype == CHUNKKV_BF16, c->table, c->lens, c->k_pages, c->v_pages, c->scales,
-                                    start, std::min(n_cap, c->max_pages * kPage), k_out, v_out, st_t,
+                                    start, std::min(n_cap, c->max_pages * kPage), n_rows, k_out, v_out, st_t,
                                     (cudaStream_t)stream));
 }
 

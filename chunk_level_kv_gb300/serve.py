@@ -203,15 +203,16 @@ def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
 
 
 def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out) -> None:
-    """Reads rows back into k_out, v_out [tokens, d]: token i of row r to start[r] + i (int64), i < min(lens, n_cap)."""
+    """Reads rows back into k_out, v_out [tokens, d]: token i of row r to start[r] + i (int64), i < min(lens, n_cap).
+    Tokens past the end of k_out are not written."""
     if start.dtype != torch.int64 or start.numel() != cache.rows or not start.is_contiguous():
         raise ValueError("start: one contiguous int64 per (sequence, KV head)")
     if (k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or k_out.stride() != v_out.stride()
             or k_out.dtype not in _DT or k_out.dim() != 2 or k_out.shape[1] != cache.d or k_out.stride(1) != 1):
         raise ValueError("k_out, v_out [tokens, d] of one type and layout, the head dimension contiguous")
     _check("chunkkv_q8_load",
-           LIB.chunkkv_q8_load(cache.layer(layer), _DT[k_out.dtype], start.data_ptr(), n_cap, k_out.data_ptr(), v_out.data_ptr(),
-                               k_out.stride(0), _stream(cache.lens, start, k_out, v_out)))
+           LIB.chunkkv_q8_load_bounded(cache.layer(layer), _DT[k_out.dtype], start.data_ptr(), n_cap, k_out.shape[0],
+                                       k_out.data_ptr(), v_out.data_ptr(), k_out.stride(0), _stream(cache.lens, start, k_out, v_out)))
 
 
 def chunkkv_q8_workspace_size(cache: Q8Cache, G: int) -> int:

@@ -417,10 +417,15 @@ chunkkv_status chunkkv_q8_append(const chunkkv_q8_cache* c, int32_t dtype, const
  * Reads rows back: token i < min(lens[r], n_cap) of row r goes to k_out and
  * v_out[(start[r] + i) * st_t + e] (device, dtype's type; start: device [B * Hkv]
  * int64, a negative entry skips the row), e.g. as the packed keys of a further
- * chunkkv_compress_layers or chunkkv_compress_tail call.
+ * chunkkv_compress_layers or chunkkv_compress_tail call.  Where they end is in device
+ * memory: chunkkv_q8_load trusts start, chunkkv_q8_load_bounded writes none of the rows
+ * at or past n_rows of k_out and v_out.
  */
 chunkkv_status chunkkv_q8_load(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
                                void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream);
+chunkkv_status chunkkv_q8_load_bounded(const chunkkv_q8_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                                       int64_t n_rows, void* k_out, void* v_out, int64_t st_t,
+                                       chunkkv_stream_t stream);
 
 /*
  * Single-token attention over one layer's cache, G query heads per KV head:

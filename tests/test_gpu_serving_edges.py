@@ -89,6 +89,29 @@ def test_prefill_rows_of_minus_infinite_logits_alone(ckv, dtype, d, T):  # noqa:
     assert bool((out[:3] == 0).all()) and bool(out[3:].isnan().all())
 
 
+# ------------------------------------------------------------------ 8-bit cache
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_load_stays_inside_its_outputs(ckv, dtype):  # noqa: F811
+    # rows that would end past the outputs, begin there, or begin nowhere near; the rows behind are left alone
+    lens = [130, 70, 64, 5, 300]
+    cache, _ = random_cache(ckv, 1, 5, 64, lens, seed=95)
+    rows = read(ckv, cache, dtype)
+    begin = [180, 0, 250, 1 << 40, 100]
+    wide = torch.full((2, 1000, 64), 5.0, dtype=dtype, device=DEV)
+    k, v = wide[0, 100:300], wide[1, 100:300]
+    for r in range(5):
+        wide.fill_(5.0)
+        start = torch.tensor([b if i == r else -1 for i, b in enumerate(begin)], dtype=torch.int64, device=DEV)
+        ckv.chunkkv_q8_load(cache, 0, start, 200, k, v)
+        n = max(0, min(lens[r], 200, 200 - begin[r]))
+        want = torch.full_like(wide, 5.0)
+        if n:
+            for i in range(2):
+                want[i, 100 + begin[r]:100 + begin[r] + n] = rows[r][i][:n]
+        assert torch.equal(wide, want), r
+
+
 # ------------------------------------------------------------------ decode attention
 
 @pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])

@@ -42,3 +42,19 @@ def test_a_cache_lies_on_one_device(ckv):
     with pytest.raises(ValueError):
         ckv.Q8Cache(B=2, Hkv=2, d=64, k_pages=c.k_pages, v_pages=c.v_pages, scales=c.scales, table=c.table, lens=far,
                     ring=c.ring, state=c.state)
+
+
+def test_load_bounded_arguments(ckv):
+    import ctypes
+
+    from chunk_level_kv_gb300._lib import LIB, Q8CacheStruct
+    OK, INVALID = 0, 1
+    before = ckv.chunkkv_launch_count()
+    c = Q8CacheStruct(B=2, Hkv=2, d=64, n_pages=10, max_pages=4, k_pages=0x10000, v_pages=0x20000, scales=0x30000,
+                      table=0x40000, lens=0x50000, ring=0x60000, state=0x70000)
+
+    def load(start=0x1000, n_cap=3, n_rows=10, k=0x1000, st=64):
+        return LIB.chunkkv_q8_load_bounded(ctypes.byref(c), 1, start, n_cap, n_rows, k, 0x2000, st, None)
+    assert load(start=None) == load(n_cap=-1) == load(n_rows=-1) == load(k=None) == load(st=9) == INVALID
+    assert load(n_rows=0, k=None) == OK                                      # nothing to write
+    assert ckv.chunkkv_launch_count() == before
