@@ -84,11 +84,14 @@ def chunkkv_prefill_attention(p: PrefillParams, q, k, v, out, ws) -> None:
 
 
 def prefill_attention(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, out=None, workspace=None):
-    """Causal attention over packed prompts on the current stream; allocates the output with torch unless given."""
+    """Causal attention over packed prompts on the current stream; allocates the output with torch unless given.
+    Rows of q behind cu_q's last offset belong to no sequence: zeros in an output allocated here, else left alone."""
     if v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
         raise ValueError("v must have k's shape, type and strides")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if len(cu_q) > 0 and 0 <= cu_q[-1] < q.shape[0]:
+            out[cu_q[-1]:].zero_()
     if out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
         raise ValueError("out must have q's shape and type, its head dimension contiguous")
     p, keep = prefill_params_for(q, k, cu_q, cu_k, scale=scale, o_strides=(out.stride(0), out.stride(1)))

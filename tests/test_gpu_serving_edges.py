@@ -112,6 +112,21 @@ def test_load_stays_inside_its_outputs(ckv, dtype):  # noqa: F811
         assert torch.equal(wide, want), r
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_rows_of_no_sequence(ckv, dtype):  # noqa: F811
+    # rows of q behind the last offset: zeros where the binding makes the output, whatever its memory held
+    q, k, v = make_qkv([60], [60], 4, 2, 64, dtype, seed=33)
+    for last in (40, 0):
+        dirt = [torch.full_like(q, float("nan")) for _ in range(8)]
+        del dirt
+        out = ckv.prefill_attention(q, k, v, [0, last])
+        check_prefill(out[:last], q[:last], k[:last], v[:last], [0, last], [0, last], 1 / 8, dtype == BF)
+        assert bool((out[last:] == 0).all())
+        mine = torch.full_like(q, 7.0)
+        ckv.prefill_attention(q, k, v, [0, last], out=mine)
+        assert torch.equal(mine[:last], out[:last]) and bool((mine[last:] == 7.0).all())
+
+
 # ------------------------------------------------------------------ decode attention
 
 @pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])
