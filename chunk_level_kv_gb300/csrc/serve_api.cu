@@ -258,6 +258,7 @@ chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_l
   const chunkkv_status st = check_cache(c, false, &g);
   if (st != CHUNKKV_OK) return st;
   if (n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
   if (g.rows == 0) return CHUNKKV_OK;
   if (!aligned(new_lens, 4) || !aligned(c->ring, 4) || !aligned(c->state, 4) || (slots && !aligned(slots, 8)) ||
       new_lens == c->lens)

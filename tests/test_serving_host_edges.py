@@ -58,3 +58,15 @@ def test_load_bounded_arguments(ckv):
     assert load(start=None) == load(n_cap=-1) == load(n_rows=-1) == load(k=None) == load(st=9) == INVALID
     assert load(n_rows=0, k=None) == OK                                      # nothing to write
     assert ckv.chunkkv_launch_count() == before
+
+
+def test_slot_maps_beyond_the_counters(ckv):
+    # as for the append: runs of a row are counted in 32 bits
+    import ctypes
+
+    from chunk_level_kv_gb300._lib import LIB, Q8CacheStruct
+    UNSUPPORTED = 2
+    c = Q8CacheStruct(B=2, Hkv=2, d=64, n_pages=10, max_pages=4, k_pages=0x10000, v_pages=0x20000, scales=0x30000,
+                      table=0x40000, lens=0x50000, ring=0x60000, state=0x70000)
+    for n_cap in (2147483647, 2147483647 - 255):
+        assert LIB.chunkkv_q8_resize(ctypes.byref(c), 0x1000, 0x2000, n_cap, None) == UNSUPPORTED
