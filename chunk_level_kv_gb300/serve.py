@@ -16,7 +16,10 @@ from .api import _check, _DT
 
 
 def _host_i32(xs):
-    return (ctypes.c_int32 * len(xs))(*[int(x) for x in xs])
+    xs = [int(x) for x in xs]
+    if xs and not -(1 << 31) <= min(xs) <= max(xs) < 1 << 31:
+        raise ValueError("offsets beyond 32 bits")           # ctypes would drop their upper bits
+    return (ctypes.c_int32 * len(xs))(*xs)
 
 
 def _bytes(t):

@@ -70,3 +70,14 @@ def test_slot_maps_beyond_the_counters(ckv):
                       table=0x40000, lens=0x50000, ring=0x60000, state=0x70000)
     for n_cap in (2147483647, 2147483647 - 255):
         assert LIB.chunkkv_q8_resize(ctypes.byref(c), 0x1000, 0x2000, n_cap, None) == UNSUPPORTED
+
+
+def test_offsets_that_pass_32_bits(ckv):
+    # an offset must not wrap into a small one on its way into the library
+    q = torch.zeros(10, 2, 64)
+    for cu in ([0, (1 << 32) + 3, 10], [0, -(1 << 32) + 3, 10]):
+        with pytest.raises(ValueError):
+            ckv.prefill_params_for(q, q, cu)
+        with pytest.raises(ValueError):
+            ckv.prefill_params_for(q, q, [0, 3, 10], cu)
+    ckv.prefill_params_for(q, q, [0, 3, 10])
