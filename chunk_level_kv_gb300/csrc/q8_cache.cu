@@ -63,13 +63,16 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& b, long lon
 // that it gives back go behind the ring's free part, and the slots of its new tokens
 // follow from both.  The entries read (free before the call) and those written (not
 // free before it) never meet, so the CTAs need no order among them; the last one to
-// finish writes the lengths and the ring's state, which all of them read before.
+// arrive writes the lengths and the ring's state.  A CTA arrives once it has read them
+// (its own rows' lengths go to shared memory), before it writes anything: a release
+// with nothing to wait for, behind which the writes run.
 // Latency bounds it (four dependent trips to L2): 6 us for 2048 rows with a 288-token
 // slot map (4.7 MB) and for 128 rows that gain 6.5 thousand tokens each (6.7 MB).
 __global__ void __launch_bounds__(kResizeThreads)
 resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restrict__ lens, int32_t* __restrict__ table,
               int32_t* __restrict__ ring, int32_t* state, int64_t* __restrict__ slots, int n_cap, int rows_per_cta) {
   extern __shared__ long long s_off[];                      // [2][rows_per_cta] pages gained / given before the row
+  int* s_len = (int*)(s_off + 2 * rows_per_cta);            // [2][rows_per_cta] its length, and the new one
   __shared__ bool s_last;
   pdl_wait();
   const int tid = threadIdx.x;
@@ -92,19 +95,27 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
   block_scan2(grow, give, grown, given);
   const bool ok = !bad && grown <= n_free && n_free - grown + given <= g.n_pages;
   for (int r = c0; r < c1; ++r) {
+    const int n = lens[r], m = new_lens[r];
     if (r >= r0 && r < r1) {
       s_off[r - r0] = grow;
       s_off[rows_per_cta + r - r0] = give;
+      s_len[r - r0] = n;
+      s_len[rows_per_cta + r - r0] = m;
     }
-    const int d = pages_of(new_lens[r]) - pages_of(lens[r]);
+    const int d = pages_of(m) - pages_of(n);
     grow += max(d, 0);
     give += max(-d, 0);
   }
   __syncthreads();
+  if (tid == 0) {
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(&state[kRingTicket]) : "memory");
+    s_last = before == (int)gridDim.x - 1;
+  }
   if (ok) {
     // table entries: a warp per row
     for (int r = r0 + (tid >> 5); r < r1; r += kResizeThreads / 32) {
-      const int have = pages_of(lens[r]), need = pages_of(new_lens[r]);
+      const int have = pages_of(s_len[r - r0]), need = pages_of(s_len[rows_per_cta + r - r0]);
       int32_t* row = table + (int64_t)r * g.max_pages;
       for (int j = have + (tid & 31); j < need; j += 32)
         row[j] = ring[wrap(head + s_off[r - r0] + (j - have), g.n_pages)];
@@ -120,7 +131,7 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
     const int runs = (n_cap + kSlotRun - 1) / kSlotRun, lane = tid & 31;
     for (int w = tid >> 5; w < (r1 - r0) * runs; w += kResizeThreads / 32) {
       const int r = r0 + w / runs, i0 = w % runs * kSlotRun, i1 = min(n_cap, i0 + kSlotRun);
-      const int n = lens[r], m = new_lens[r], have = pages_of(n);
+      const int n = s_len[r - r0], m = s_len[rows_per_cta + r - r0], have = pages_of(n);
       const int added = ok ? m - n : 0;
       int64_t* row_slots = slots + (int64_t)r * n_cap;
       int32_t page = -1;
@@ -134,11 +145,6 @@ resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restric
         if (i < i1) row_slots[i] = i < added ? (int64_t)p * kPage + pos % kPage : -1;
       }
     }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    // no fence: the last CTA changes what the others have read by now, and reads nothing that they wrote
-    s_last = atomicAdd(&state[kRingTicket], 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (s_last) {
@@ -445,7 +451,7 @@ cudaError_t launch_q8_resize(const Q8Geom& g, const int32_t* new_lens, int32_t* 
   const int grid = max(1, min(g.rows, sms));
   const int per = (g.rows + grid - 1) / grid;
   return launch_pdl(resize_kernel, dim3((g.rows + per - 1) / per), dim3(kResizeThreads),
-                    (size_t)per * 2 * sizeof(long long), s, g, new_lens, lens, table, ring, state, slots, n_cap, per);
+                    (size_t)per * 2 * (sizeof(long long) + sizeof(int)), s, g, new_lens, lens, table, ring, state, slots, n_cap, per);
 }
 
 cudaError_t launch_q8_append(const Q8Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
