@@ -127,6 +127,43 @@ def test_prefill_rows_of_no_sequence(ckv, dtype):  # noqa: F811
         assert torch.equal(mine[:last], out[:last]) and bool((mine[last:] == 7.0).all())
 
 
+@pytest.mark.parametrize("tq,T,Hq,Hkv,d", [(1, 9000, 8, 2, 128), (3, 5000, 4, 1, 64), (130, 6000, 2, 1, 128), (40, 700, 2, 2, 128)])
+def test_prefill_counts_every_key_once(ckv, tq, T, Hq, Hkv, d):  # noqa: F811
+    # equal weights, and a value of 1 in column c for key w + c: each of the last row's outputs is 1 / T
+    q = torch.zeros(tq, Hq, d, dtype=BF, device=DEV)
+    k = torch.zeros(T, Hkv, d, dtype=BF, device=DEV)
+    p, keep = ckv.prefill_params_for(q, k, [0, tq], [0, T])
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    sees = torch.arange(tq, device=DEV) + (T - tq + 1)                       # keys that a row sees
+    for w in range(0, T, d):
+        n = min(d, T - w)
+        v = torch.zeros(T, Hkv, d, dtype=BF, device=DEV)
+        v[w + torch.arange(n), :, torch.arange(n)] = 1
+        ckv.chunkkv_prefill_attention(p, q, k, v, out, ws)
+        want = ((w + torch.arange(d, device=DEV) < sees[:, None]) & (torch.arange(d, device=DEV) < n)) / sees[:, None].double()
+        # weights that are equal and exact in bf16, their sum in fp32, the output's rounding
+        assert bool(((out.double() - want[:, None]).abs() <= (2.0 ** -8 + (T + 16) * 2.0 ** -23) * want[:, None]).all()), w
+
+
+@pytest.mark.parametrize("tq,T", [(1, 9000), (70, 6000)])
+def test_prefill_one_key_of_a_split_row_takes_all(ckv, tq, T):  # noqa: F811
+    # the winner on both sides of every boundary of two blocks of keys, and so of two parts
+    q = torch.zeros(tq, 2, 128, dtype=BF, device=DEV)
+    q[:, :, 0] = 64.0
+    v = torch.randn(T, 1, 128, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV).to(BF)
+    k = torch.zeros(T, 1, 128, dtype=BF, device=DEV)
+    p, keep = ckv.prefill_params_for(q, k, [0, tq], [0, T], scale=1.0)
+    ws = torch.zeros(ckv.chunkkv_prefill_workspace_size(p), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 1 << 16
+    out = torch.empty_like(q)
+    for at in [x for b in range(0, T - tq, 128) for x in (b - 1, b) if x >= 0] + [T - tq]:
+        k[at, 0, 0] = 64.0
+        ckv.chunkkv_prefill_attention(p, q, k, v, out, ws)
+        assert torch.equal(out, v[at].expand(tq, 2, 128)), at
+        k[at, 0, 0] = 0.0
+
+
 # ------------------------------------------------------------------ decode attention
 
 @pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])
@@ -213,3 +250,50 @@ def test_calls_refuse_tensors_outside_the_gpu(ckv):  # noqa: F811
             with pytest.raises(ValueError):
                 call(*args[:i], args[i].cpu(), *args[i + 1:])
     assert ckv.chunkkv_launch_count() == before
+
+
+@pytest.mark.parametrize("lens", [[6582] * 8, [800, 900], [577, 64, 4000, 1, 1300], [3000] * 40])
+def test_decode_counts_every_token_once(ckv, lens):  # noqa: F811
+    # zero keys, so equal weights; a value code of 127 in column c for token w + c gives 127 / n there
+    d, rows = 128, len(lens)
+    cache, g = random_cache(ckv, rows, 1, d, lens, seed=71)
+    cache.k_pages[0].zero_()
+    cache.scales[0].fill_(1.0)
+    q = torch.randn(rows, 2, d, generator=g, device=DEV)
+    ws = torch.zeros(ckv.chunkkv_q8_workspace_size(cache, 2), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    n = torch.tensor(lens, device=DEV)[:, None, None]
+    for w in range(0, max(lens), d):
+        cache.v_pages[0].zero_()
+        for half in (0, 64):
+            j = (w + half) // 64
+            has = [r for r in range(rows) if lens[r] > w + half]
+            if has:
+                page = cache.table[has, j].long()
+                cache.v_pages[0][page[:, None], torch.arange(64, device=DEV) + half, torch.arange(64, device=DEV)] = 127
+        ckv.chunkkv_q8_attention(cache, 0, q, out, ws)
+        want = (w + torch.arange(d, device=DEV) < n) * (127.0 / n.double())
+        assert bool(((out.double() - want).abs() <= (n + 16) * 2.0 ** -22 * want).all()), w
+
+
+@pytest.mark.parametrize("rows,n", [(8, 6582), (2, 800), (3, 2500)])
+def test_decode_one_token_takes_all(ckv, rows, n):  # noqa: F811
+    # the dominant key at the first and the last token of every page, and so of every run of pages
+    d = 64
+    cache, g = random_cache(ckv, rows, 1, d, [n] * rows, seed=81)
+    cache.k_pages[0].zero_()
+    cache.scales[0].fill_(1.0)
+    q = torch.zeros(rows, 4, d, device=DEV)
+    q[:, :, 0] = 4.0
+    ws = torch.zeros(ckv.chunkkv_q8_workspace_size(cache, 4), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    spots = [x for j in range(-(-n // 64)) for x in (64 * j, min(64 * j + 63, n - 1))]
+    row = torch.arange(rows, device=DEV)
+    for i in range(len(spots)):
+        at = torch.tensor([spots[(i + r * 31) % len(spots)] for r in range(rows)], device=DEV)
+        page = cache.table[row, at // 64].long()
+        cache.k_pages[0][page, 0, at % 64, 0] = 100
+        ckv.chunkkv_q8_attention(cache, 0, q, out, ws, 1.0)
+        want = cache.v_pages[0][page, :, at % 64].double()                   # [rows, d]
+        assert bool(((out.double() - want[:, None]).abs() <= 2.0 ** -20 * want[:, None].abs()).all()), i
+        cache.k_pages[0][page, 0, at % 64, 0] = 0
