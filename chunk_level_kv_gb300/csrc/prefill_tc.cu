@@ -182,12 +182,14 @@ __device__ __forceinline__ float row_max(uint32_t tS) {
 // reach into (any of a row's finite logits would do), or over all where a row has none
 // there.
 __device__ __noinline__ float first_reference(uint32_t tS, int lo) {
-  if (lo < 0) return row_max(tS);
-  float s[32], m = -INFINITY;
-  tmem_ld32(tS + min(lo >> 5, 3) * 32, s);
-  tmem_wait(s);
+  float m = -INFINITY;
+  if (lo >= 0) {
+    float s[32];
+    tmem_ld32(tS + min(lo >> 5, 3) * 32, s);
+    tmem_wait(s);
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
+    for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
+  }
   return __any_sync(0xffffffffu, m == -INFINITY) ? row_max(tS) : m;
 }
 
@@ -225,30 +227,37 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, ui
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// The same, of (S - base) alpha + neg.
-__device__ __forceinline__ float row_exp_from(uint32_t tS, float base, float alpha, float neg, uint32_t (&p)[64]) {
+// The same of (S - base) alpha + neg, with P written: its 16 columns of 32 logits lie among the columns read by then.
+__device__ __forceinline__ float write_exp_from(uint32_t tS, float base, float alpha, float neg) {
   float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float s[32];
     tmem_ld32(tS + 32 * c, s);
     tmem_wait(s);
+    uint32_t p[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float a = ex2(fmaf(s[2 * i] - base, alpha, neg)), b = ex2(fmaf(s[2 * i + 1] - base, alpha, neg));
       sum += a + b;
       const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
-      p[16 * c + i] = *(const uint32_t*)&w;
+      p[i] = *(const uint32_t*)&w;
     }
+    tmem_st16(tS + 16 * c, p);
   }
   return sum;
 }
 
+// -m alpha, as row_exp takes it; NaN for a huge reference, so that the sums of its blocks are and block_again does them.
+__device__ __forceinline__ float offset_of(float m, float alpha) {
+  const float neg = -m * alpha;
+  return fabsf(neg) <= kHuge ? neg : NAN;
+}
 // What the rounding of -m alpha took from a row's reference: its terms are 2^(S alpha - (m alpha - residual)).  Terms
 // under two references are comparable only with it (near kHuge -m alpha is rounded to multiples of 1/4).
 __device__ __forceinline__ float residual(float m, float alpha) {
-  const float neg = -m * alpha;
-  return fabsf(neg) <= kHuge ? fmaf(m, alpha, neg) : 0.f;     // huge references: see block_again
+  const float neg = offset_of(m, alpha);
+  return neg == neg ? fmaf(m, alpha, neg) : 0.f;
 }
 
 // A block whose sum passed the bound, or whose reference is huge, done over: rows that are `over` move their
@@ -265,7 +274,7 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
     f = m == -INFINITY ? 0.f : ex2((m - mn) * alpha - residual(m, alpha) + residual(mn, alpha));
     m = mn;
   }
-  const float neg = m == -INFINITY ? 0.f : -m * alpha;
+  const float neg = m == -INFINITY ? 0.f : offset_of(m, alpha);
   if (tO != 0xFFFFFFFFu) {
     // the blocks before are done: their products were issued before this S
 #pragma unroll 1
@@ -278,11 +287,8 @@ __device__ __noinline__ float3 block_again(uint32_t tS, uint32_t tO, float alpha
       tmem_st32(tO + 32 * c, o);
     }
   }
-  uint32_t p[64];
-  const bool huge = !(fabsf(neg) <= kHuge);
-  const float sum = row_exp_from(tS, huge ? m : 0.f, alpha, huge ? 0.f : neg, p);
-  tmem_st32<0>(tS, p);
-  tmem_st32<32>(tS + 32, p);
+  const bool huge = neg != neg;
+  const float sum = write_exp_from(tS, huge ? m : 0.f, alpha, huge ? 0.f : neg);
   return make_float3(m, neg, l * f + sum);
 }
 
@@ -466,12 +472,12 @@ prefill_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
           const float bm = first_reference(tS, lo);
           if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
             m = bm;
-            neg = -m * g.alpha;
+            neg = offset_of(m, g.alpha);
           }
         }
         uint32_t p[64];
         const float sum = row_exp(tS, g.alpha, neg, p);
-        const bool over = live && !(l + sum <= kBig && fabsf(neg) <= kHuge);         // a NaN too
+        const bool over = live && !(l + sum <= kBig);         // a NaN too, as under a huge reference
         if (!__any_sync(0xffffffffu, over)) {
           l += sum;
           tmem_st32<0>(tS, p);

@@ -159,6 +159,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[M])
       "r"(r[N + 21]), "r"(r[N + 22]), "r"(r[N + 23]), "r"(r[N + 24]), "r"(r[N + 25]), "r"(r[N + 26]), "r"(r[N + 27]),
       "r"(r[N + 28]), "r"(r[N + 29]), "r"(r[N + 30]), "r"(r[N + 31]) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
