@@ -29,7 +29,10 @@ def _bytes(t):
 def _stream(t, *others) -> int:
     """The current stream of the tensors' device, as the integer that ctypes passes on.  They lie on one GPU, and it
     is the current one: the library asks the current device for its size and launches there."""
-    dev = t.get_device()
+    return _stream_of(t.get_device(), *others)
+
+
+def _stream_of(dev: int, *others) -> int:
     if dev < 0:
         raise ValueError("the tensors live in GPU memory")
     for o in others:
@@ -120,10 +123,15 @@ class Q8Cache:
     lens: torch.Tensor       # [B * Hkv] int32
     ring: torch.Tensor       # [n_pages] int32
     state: torch.Tensor      # [4] int32: head, free pages, status of the last resize, 0
+    rows: int = field(init=False, repr=False)
     _c: list = field(default_factory=list, repr=False)
+    _refs: list = field(init=False, repr=False)     # _c by reference, the tensors' device and the usual scale: made
+    _dev: int = field(init=False, repr=False)       # once, since a call's host time counts
+    _scale: float = field(init=False, repr=False)
 
     def __post_init__(self):
-        rows, n_pages, d64 = self.B * self.Hkv, self.ring.numel(), -(-self.d // 64) * 64
+        self.rows = self.B * self.Hkv
+        rows, n_pages, d64 = self.rows, self.ring.numel(), -(-self.d // 64) * 64
         ints = (self.table, self.lens, self.ring, self.state)
         if any(t.dtype != torch.int32 or not t.is_contiguous() for t in ints):
             raise ValueError("table, lens, ring and state are contiguous int32")
@@ -143,18 +151,16 @@ class Q8Cache:
             pages = [x[i].data_ptr() if x else None for x in (self.k_pages, self.v_pages, self.scales)]
             self._c.append(Q8CacheStruct(self.B, self.Hkv, self.d, n_pages, self.table.shape[1], *pages,
                                          *[t.data_ptr() for t in ints]))
+        self._refs = [ctypes.byref(c) for c in self._c]
+        self._dev, self._scale = self.lens.get_device(), 1.0 / math.sqrt(self.d)
 
     @property
     def device(self):
         return self.lens.device
 
-    @property
-    def rows(self) -> int:
-        return self.B * self.Hkv
-
     def layer(self, i: int):
         """The chunkkv_q8_cache of layer i, by reference (the tensors' addresses as they were at construction)."""
-        return ctypes.byref(self._c[i])
+        return self._refs[i]
 
 
 def q8_cache(B: int, Hkv: int, d: int, *, n_pages: int, max_pages: int, n_layers: int = 1, device="cuda") -> Q8Cache:
@@ -182,14 +188,16 @@ def _rows_i32(cache: Q8Cache, t, what: str):
 def chunkkv_q8_resize(cache: Q8Cache, new_lens, slots=None) -> None:
     """Sets every row's length (device int32, one per row); slots: None or int64 [rows, n_cap] for the slot map."""
     _rows_i32(cache, new_lens, "new_lens")
-    n_cap = 0
-    if slots is not None:
-        if slots.dtype != torch.int64 or slots.dim() != 2 or slots.shape[0] != cache.rows or not slots.is_contiguous():
+    if slots is None:
+        at, n_cap, stream = None, 0, _stream_of(cache._dev, new_lens)
+    else:
+        shape = slots.shape
+        if slots.dtype != torch.int64 or len(shape) != 2 or shape[0] != cache.rows or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
-        n_cap = slots.shape[1]
-    stream = _stream(cache.lens, new_lens) if slots is None else _stream(cache.lens, new_lens, slots)
-    _check("chunkkv_q8_resize", LIB.chunkkv_q8_resize(cache.layer(0), new_lens.data_ptr(), None if slots is None else slots.data_ptr(), n_cap,
-                                                      stream))
+        at, n_cap, stream = slots.data_ptr(), shape[1], _stream_of(cache._dev, new_lens, slots)
+    code = LIB.chunkkv_q8_resize(cache._refs[0], new_lens.data_ptr(), at, n_cap, stream)
+    if code:
+        _check("chunkkv_q8_resize", code)
 
 
 def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
@@ -197,15 +205,17 @@ def chunkkv_q8_append(cache: Q8Cache, layer: int, k, v, counts, slots) -> None:
     shape, st, dt = k.shape, k.stride(), _DT.get(k.dtype)
     if dt is None or v.shape != shape or v.stride() != st or v.dtype != k.dtype:
         raise ValueError("k and v of one shape, type (float32 or bfloat16) and strides")
-    if len(shape) != 4 or shape[0] != cache.B or shape[1] != cache.Hkv or shape[3] != cache.d or st[3] != 1:
+    n_cap = shape[2] if len(shape) == 4 else -1
+    if shape != (cache.B, cache.Hkv, n_cap, cache.d) or st[3] != 1:
         raise ValueError("k, v [B, Hkv, n_cap, d], the head dimension contiguous")
     _rows_i32(cache, counts, "counts")
-    if slots.dtype != torch.int64 or slots.shape != (cache.rows, shape[2]) or not slots.is_contiguous():
+    if slots.dtype != torch.int64 or slots.shape != (cache.rows, n_cap) or not slots.is_contiguous():
         raise ValueError("slots: contiguous int64 [B * Hkv, n_cap]")
-    _check("chunkkv_q8_append",
-           LIB.chunkkv_q8_append(cache.layer(layer), dt, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2],
-                                 counts.data_ptr(), slots.data_ptr(), shape[2],
-                                 _stream(cache.lens, k, v, counts, slots)))
+    code = LIB.chunkkv_q8_append(cache._refs[layer], dt, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2],
+                                 counts.data_ptr(), slots.data_ptr(), n_cap,
+                                 _stream_of(cache._dev, k, v, counts, slots))
+    if code:
+        _check("chunkkv_q8_append", code)
 
 
 def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out) -> None:
@@ -213,12 +223,14 @@ def chunkkv_q8_load(cache: Q8Cache, layer: int, start, n_cap: int, k_out, v_out)
     Tokens past the end of k_out are not written."""
     if start.dtype != torch.int64 or start.numel() != cache.rows or not start.is_contiguous():
         raise ValueError("start: one contiguous int64 per (sequence, KV head)")
-    if (k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or k_out.stride() != v_out.stride()
-            or k_out.dtype not in _DT or k_out.dim() != 2 or k_out.shape[1] != cache.d or k_out.stride(1) != 1):
+    shape, st, dt = k_out.shape, k_out.stride(), _DT.get(k_out.dtype)
+    if (dt is None or v_out.shape != shape or v_out.stride() != st or v_out.dtype != k_out.dtype
+            or len(shape) != 2 or shape[1] != cache.d or st[1] != 1):
         raise ValueError("k_out, v_out [tokens, d] of one type and layout, the head dimension contiguous")
-    _check("chunkkv_q8_load",
-           LIB.chunkkv_q8_load_bounded(cache.layer(layer), _DT[k_out.dtype], start.data_ptr(), n_cap, k_out.shape[0],
-                                       k_out.data_ptr(), v_out.data_ptr(), k_out.stride(0), _stream(cache.lens, start, k_out, v_out)))
+    code = LIB.chunkkv_q8_load_bounded(cache._refs[layer], dt, start.data_ptr(), n_cap, shape[0], k_out.data_ptr(),
+                                       v_out.data_ptr(), st[0], _stream_of(cache._dev, start, k_out, v_out))
+    if code:
+        _check("chunkkv_q8_load", code)
 
 
 def chunkkv_q8_workspace_size(cache: Q8Cache, G: int) -> int:
@@ -234,11 +246,11 @@ def chunkkv_q8_attention(cache: Q8Cache, layer: int, q, out, ws, scale: float | 
         raise ValueError("q and out [B, Hq, d] of one type, float32 or bfloat16")
     if shape[0] != cache.B or shape[2] != cache.d or shape[1] % cache.Hkv or qs[2] != 1 or os_[2] != 1:
         raise ValueError("q and out [B, Hkv * G, d], the head dimension contiguous")
-    _check("chunkkv_q8_attention",
-           LIB.chunkkv_q8_attention(cache.layer(layer), dt, shape[1] // cache.Hkv,
-                                    1.0 / math.sqrt(cache.d) if scale is None else scale, q.data_ptr(), qs[0], qs[1],
-                                    out.data_ptr(), os_[0], os_[1], ws.data_ptr(), _bytes(ws),
-                                    _stream(cache.lens, q, out, ws)))
+    code = LIB.chunkkv_q8_attention(cache._refs[layer], dt, shape[1] // cache.Hkv, cache._scale if scale is None else scale,
+                                    q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1], ws.data_ptr(), ws.nbytes,
+                                    _stream_of(cache._dev, q, out, ws))
+    if code:
+        _check("chunkkv_q8_attention", code)
 
 
 def q8_attention(cache: Q8Cache, layer: int, q, *, scale: float | None = None, out=None, workspace=None):
