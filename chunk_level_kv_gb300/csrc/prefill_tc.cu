@@ -23,11 +23,12 @@
 // is the chain of one tile: P ready, products (1024), S ready, softmax (950), with about
 // 200 cycles of barrier latency on each side, 2500 cycles a block pair for 2048 of products.
 //
-// Measured (one layer, 128 columns): 16384 tokens of 28 / 4 heads 1.03 ms, 1.87 PFLOP/s of
-// the visible pairs; 8192 tokens of 32 / 8 heads 0.31 ms, 1.76 PFLOP/s; 16 prompts of 100
-// to 2000 tokens packed 0.18 ms, 1.12 PFLOP/s (an item there has 6 block pairs, and its
-// begin and end cost as much as three more); 420 and 455 new tokens on 5.3 and 7.7
-// thousand cached ones 0.09 ms; 64 new tokens on 9000 26 us.
+// Measured (one layer, 128 columns; the power limit decides within the ranges): 16384
+// tokens of 28 / 4 heads 1.10 to 1.25 ms, 1.54 to 1.75 PFLOP/s of the visible pairs; 8192
+// tokens of 32 / 8 heads 0.31 to 0.35 ms, 1.57 to 1.76 PFLOP/s; 16 prompts of 100 to 2000
+// tokens packed 0.19 ms, 1.07 PFLOP/s (an item there has 6 block pairs, and its begin and
+// end cost as much as three more); 420 and 455 new tokens on 5.3 and 7.7 thousand cached
+// ones 0.09 ms; 64 new tokens on 9000 28 us.
 //
 // The reference m of a row is the maximum of some of its first logits and stays while
 // the row's sum is below 2^24: a common factor of P, O and the sum costs no precision
@@ -45,7 +46,8 @@
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA producer, 9 and 10 MMA
 // issuers of tile 0 and 1 (with one issuer for both, its waits for one tile kept the
-// other's products back: a block pair took 3250 cycles), 11 V check.
+// other's products back: a block pair took 3250 cycles), 11 V check, which holds every V
+// block until it has seen it there.
 // Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -66,8 +66,8 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& b, long lon
 // arrive writes the lengths and the ring's state.  A CTA arrives once it has read them
 // (its own rows' lengths go to shared memory), before it writes anything: a release
 // with nothing to wait for, behind which the writes run.
-// Latency bounds it (four dependent trips to L2): 6 us for 2048 rows with a 288-token
-// slot map (4.7 MB) and for 128 rows that gain 6.5 thousand tokens each (6.7 MB).
+// Latency bounds it (four dependent trips to L2): 6.5 us for 2048 rows with a 288-token
+// slot map (4.7 MB), 6.2 us for 128 rows that gain 6.5 thousand tokens each (6.7 MB).
 __global__ void __launch_bounds__(kResizeThreads)
 resize_kernel(Q8Geom g, const int32_t* __restrict__ new_lens, int32_t* __restrict__ lens, int32_t* __restrict__ table,
               int32_t* __restrict__ ring, int32_t* state, int64_t* __restrict__ slots, int n_cap, int rows_per_cta) {
@@ -246,8 +246,9 @@ struct AppendArgs {
 // vector; values go through shared memory as codes and leave in 16-token pieces of a
 // column, the bytes transposed 4 x 4 in registers.
 // HBM bounds it: 8 x 6582 bf16 tokens of 128 columns (40 MB) are written and then read
-// back (load_kernel, the same bytes the other way) in 16.4 us, 4.9 TB/s with both
-// launches; with the tokens in shared memory as fp32 it was 27 us.
+// back (load_kernel, the same bytes the other way) in 19.8 us, 3.8 TB/s with both
+// launches (16.7 us, 10.4 and 6.3, while the L2 holds them); with the tokens in shared
+// memory as fp32 it was 27 us there.
 template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 append_kernel(Q8Geom g, AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
