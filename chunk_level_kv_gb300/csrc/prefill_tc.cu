@@ -230,8 +230,9 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, ui
 }
 
 // The same of (S - base) alpha + neg, with P written: its 16 columns of 32 logits lie among the columns read by then.
+// The terms are added in row_exp's order: a row that is here only because another of its warp is keeps its bits.
 __device__ __forceinline__ float write_exp_from(uint32_t tS, float base, float alpha, float neg) {
-  float sum = 0.f;
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float s[32];
@@ -240,14 +241,14 @@ __device__ __forceinline__ float write_exp_from(uint32_t tS, float base, float a
     uint32_t p[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float a = ex2(fmaf(s[2 * i] - base, alpha, neg)), b = ex2(fmaf(s[2 * i + 1] - base, alpha, neg));
-      sum += a + b;
-      const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
-      p[i] = *(const uint32_t*)&w;
+      const float2 w = make_float2(ex2(fmaf(s[2 * i] - base, alpha, neg)), ex2(fmaf(s[2 * i + 1] - base, alpha, neg)));
+      sum[i & 1] = __fadd2_rn(sum[i & 1], w);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
+      p[i] = *(const uint32_t*)&b;
     }
     tmem_st16(tS + 16 * c, p);
   }
-  return sum;
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // -m alpha, as row_exp takes it; NaN for a huge reference, so that the sums of its blocks are and block_again does them.

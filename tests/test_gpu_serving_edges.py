@@ -164,6 +164,22 @@ def test_prefill_one_key_of_a_split_row_takes_all(ckv, tq, T):  # noqa: F811
         k[at, 0, 0] = 0.0
 
 
+@pytest.mark.parametrize("kind", ["large", "zero"])
+@pytest.mark.parametrize("dtype,d,tq,tk", [(BF, 128, 700, 700), (BF, 64, 300, 900), (BF, 128, 40, 6000), (F32, 64, 200, 300)])
+def test_prefill_rows_keep_their_bits_whatever_others_ask(ckv, dtype, d, tq, tk, kind):  # noqa: F811
+    # another query for some rows (one that moves its reference, or has no finite logit) changes those rows alone
+    q, k, v = make_qkv([tq], [tk], 4, 2, d, dtype, seed=43)
+    want = ckv.prefill_attention(q, k, v, [0, tq], [0, tk])
+    other = q.clone()
+    hit = torch.zeros(tq, 4, dtype=torch.bool, device=DEV)
+    hit[3::37, 1] = True
+    hit[11::53] = True
+    other[hit] = {"large": q[hit] * 60, "nan": torch.full_like(q[hit], float("nan")), "zero": q[hit] * 0}[kind]
+    out = ckv.prefill_attention(other, k, v, [0, tq], [0, tk])
+    assert torch.equal(out[~hit], want[~hit])
+    assert bool(out[hit].isnan().all()) == (kind == "nan") and not torch.equal(out[hit], want[hit])
+
+
 # ------------------------------------------------------------------ decode attention
 
 @pytest.mark.parametrize("between,heads", [("prompt", (4, 12, 20, 130)), ("scoring", (4, 8, 1))])
@@ -297,3 +313,15 @@ def test_decode_one_token_takes_all(ckv, rows, n):  # noqa: F811
         want = cache.v_pages[0][page, :, at % 64].double()                   # [rows, d]
         assert bool(((out.double() - want[:, None]).abs() <= 2.0 ** -20 * want[:, None].abs()).all()), i
         cache.k_pages[0][page, 0, at % 64, 0] = 0
+
+
+@pytest.mark.parametrize("kind", ["large", "nan"])
+def test_decode_heads_keep_their_bits_whatever_others_ask(ckv, kind):  # noqa: F811
+    cache, g = random_cache(ckv, 3, 2, 128, [3000, 70, 1, 900, 64, 2000], seed=97, spread=2.0)
+    q = torch.randn(3, 12, 128, generator=g, device=DEV)
+    want = ckv.q8_attention(cache, 0, q)
+    other = q.clone()
+    other[:, 2::6] = q[:, 2::6] * 60 if kind == "large" else float("nan")
+    out = ckv.q8_attention(cache, 0, other)
+    rest = [h for h in range(12) if h % 6 != 2]
+    assert torch.equal(out[:, rest], want[:, rest])
