@@ -192,7 +192,11 @@ __device__ __noinline__ float first_reference(uint32_t tS, int lo) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(s[i], s[i + 1]));
   }
-  return __any_sync(0xffffffffu, m == -INFINITY) ? row_max(tS) : m;
+  if (__any_sync(0xffffffffu, m == -INFINITY)) {
+    const float all = row_max(tS);
+    m = m == -INFINITY ? all : m;                             // a row's reference hangs on its own logits alone
+  }
+  return m;
 }
 
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum

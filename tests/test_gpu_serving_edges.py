@@ -164,7 +164,7 @@ def test_prefill_one_key_of_a_split_row_takes_all(ckv, tq, T):  # noqa: F811
         k[at, 0, 0] = 0.0
 
 
-@pytest.mark.parametrize("kind", ["large", "zero"])
+@pytest.mark.parametrize("kind", ["large", "nan", "zero"])
 @pytest.mark.parametrize("dtype,d,tq,tk", [(BF, 128, 700, 700), (BF, 64, 300, 900), (BF, 128, 40, 6000), (F32, 64, 200, 300)])
 def test_prefill_rows_keep_their_bits_whatever_others_ask(ckv, dtype, d, tq, tk, kind):  # noqa: F811
     # another query for some rows (one that moves its reference, or has no finite logit) changes those rows alone
