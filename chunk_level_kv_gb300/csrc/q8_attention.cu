@@ -13,8 +13,9 @@
 // a KV head as the 16-row operand's rows 0-7.  Rows 8-15 carry what f16 cut off: the
 // query is split into two f16 parts (22 bits) and so are the weights, so the products
 // are as good as fp32 ones (down to 2^-38 of the largest weight times value scale, where
-// f16 ends) and cost nothing more than the 16 rows that the instruction computes anyway.  mma.sync and not tcgen05: the operands come from
-// registers after the conversion, and an m128 tile would be 1/16 full.
+// f16 ends) and cost nothing more than the 16 rows that the instruction computes anyway.
+// mma.sync and not tcgen05: the operands come from registers after the conversion, and an
+// m128 tile would be 1/16 full.
 //
 // Work split: the pages of all rows in order are cut into one contiguous run per CTA
 // (one CTA per SM), whatever the rows' lengths, which only the device knows: every CTA
@@ -606,8 +607,9 @@ cudaError_t launch(const Q8Geom& g, const Q8AttnArgs& a, const int8_t* k_pages, 
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = raise_smem(q8_attention_kernel<ND, T>, (int)smem_bytes<ND>(), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, min(kMaxGroups, (a.G - a.g0 + kMaxG - 1) / kMaxG)), dim3(32 * warps_of<ND>()),
-                    smem_bytes<ND>(), s, g, a, k_pages, v_pages, (const float2*)scales, table, lens);
+  const int passes = min(kMaxGroups, (a.G - a.g0 + kMaxG - 1) / kMaxG);
+  return launch_pdl(q8_attention_kernel<ND, T>, dim3(grid, passes), dim3(32 * warps_of<ND>()), smem_bytes<ND>(), s, g,
+                    a, k_pages, v_pages, (const float2*)scales, table, lens);
 }
 
 template <typename T>
