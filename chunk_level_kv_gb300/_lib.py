@@ -56,6 +56,21 @@ class Q8CacheStruct(ctypes.Structure):
     ]
 
 
+class Q4CacheStruct(ctypes.Structure):
+    """chunkkv_q4_cache."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("ring", ctypes.c_void_p),
+        ("state", ctypes.c_void_p),
+    ]
+
+
+def q4_page_bytes(d: int) -> int:
+    """CHUNKKV_Q4_PAGE_BYTES."""
+    return 4608 * -(-d // 64)
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
@@ -65,7 +80,7 @@ def _load():
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     pp = ctypes.POINTER(ctypes.c_void_p)
     i64 = ctypes.c_int64
-    PP, Q8 = ctypes.POINTER(PrefillParams), ctypes.POINTER(Q8CacheStruct)
+    PP, Q8, Q4 = ctypes.POINTER(PrefillParams), ctypes.POINTER(Q8CacheStruct), ctypes.POINTER(Q4CacheStruct)
     sigs = {
         "chunkkv_out_capacity": [P, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "chunkkv_workspace_size": [P, i32, i32, ctypes.POINTER(sz)],
@@ -92,6 +107,12 @@ def _load():
         "chunkkv_q8_load_bounded": [Q8, i32, vp, i32, i64, vp, vp, i64, vp],
         "chunkkv_q8_workspace_size": [Q8, i32, ctypes.POINTER(sz)],
         "chunkkv_q8_attention": [Q8, i32, i32, ctypes.c_float, vp, i64, i64, vp, i64, i64, vp, sz, vp],
+        "chunkkv_q4_resize": [Q4, vp, vp, i32, vp],
+        "chunkkv_q4_append": [Q4, i32, vp, vp, i64, i64, i64, vp, vp, i32, vp],
+        "chunkkv_q4_load": [Q4, i32, vp, i32, i64, vp, vp, i64, vp],
+        "chunkkv_q4_workspace_size": [Q4, i32, i32, i32, ctypes.POINTER(sz)],
+        "chunkkv_q4_path": [Q4, i32, i32, i32],
+        "chunkkv_q4_attention": [Q4, i32, i32, i32, vp, ctypes.c_float, vp, i64, i64, i64, vp, i64, i64, i64, vp, sz, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)

@@ -1,0 +1,289 @@
+// The 4-bit paged cache: writing rows, reading rows back (its tables are the 8-bit cache's,
+// resize_kernel of q8_cache.cu).
+//
+// A token's groups of 64 columns are quantised by themselves, so a token is final when it is
+// written: nothing of a page changes when further tokens join it.  For a group whose values
+// lie in [lo, hi],
+//   m = lo rounded down to bf16,  s = (hi - m) / 15 rounded up to bf16,  c = round((x - m) / s)
+// and a code stands for s c + m.  Rounding outwards keeps every value within half a step of
+// a code; bf16 keeps fp32's range, and m is exact where the inputs are bf16.
+#include "q4.cuh"
+
+namespace chunkkv {
+namespace {
+
+constexpr int kIoThreads = 256;
+constexpr float kInv15 = 1.0f / 15.0f;
+constexpr float kSmallest = 7.888609052210118e-31f;          // 2^-100: a group that spans less has step 0
+
+// Smallest and largest, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight elements of a row.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *(const uint4*)p;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
+  *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *(const uint32_t*)&b;
+  }
+  *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------ writing
+
+struct Q4AppendArgs {
+  const void* x[2];                // keys, values [B, Hkv, n_cap, d]
+  int64_t st_b, st_h, st_t;
+  int32_t n_cap;
+};
+
+// One CTA writes the part of one page that a row's new tokens fill, of the keys
+// (blockIdx.z 0) or of the values (1).  Eight lanes hold a group of a token, eight columns
+// each, and find its smallest and largest value by shuffles.  A lane's eight codes are a word
+// of the keys' part; values go through shared memory, a byte a code, and leave as words of
+// eight tokens of a column, merged with the older tokens' codes where a word is shared.
+template <int ND, typename T>
+__global__ void __launch_bounds__(kIoThreads)
+q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
+                 uint8_t* __restrict__ pages) {
+  constexpr int kV8 = 8 * ND, kVecs = kPage * kV8 / kIoThreads;      // vectors of a token, and of a thread
+  constexpr int kPitch = 64 * ND + 4;                                // bytes of a token's codes in shared memory
+  __shared__ __align__(16) uint8_t s_code[kPage * kPitch];
+  pdl_wait();
+  const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
+  const int64_t* row_slots = slots + (int64_t)r * a.n_cap;
+  const int n = min(max(counts[r], 0), a.n_cap);
+  const int off0 = (int)(row_slots[0] & (kPage - 1));
+  const int i0 = max(0, (int)blockIdx.x * kPage - off0), i1 = min(n, ((int)blockIdx.x + 1) * kPage - off0);
+  if (i0 < i1) {                                                     // the same for the whole CTA
+    const int64_t slot = row_slots[i0];
+    const int64_t page = slot >> 6;
+    const int t0 = (int)(slot & (kPage - 1)), nt = min(i1 - i0, kPage - t0);
+    const T* x = (const T*)(which ? a.x[1] : a.x[0]) + (r / g.Hkv) * a.st_b + (r % g.Hkv) * a.st_h + i0 * a.st_t;
+    const bool inside = slot >= 0 && page < g.n_pages;
+    uint8_t* pg = pages + page * q4_page_bytes(ND);
+    uint32_t* k_words = (uint32_t*)pg;
+    uint32_t* ms_words = (uint32_t*)(pg + (which ? q4_v_ms(ND) : q4_k_ms(ND)));
+    if (inside) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int v = i * kIoThreads + tid, t = v / kV8, c = v % kV8 * 8;
+        if ((i * kIoThreads + (tid & ~31)) / kV8 >= nt) break;       // the whole warp is past the tokens
+        const bool live = t < nt && c < g.d;
+        float w[8], lo = INFINITY, hi = -INFINITY;
+        if (live) {
+          load8(x + t * a.st_t + c, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            lo = min_nan(lo, w[e]);
+            hi = max_nan(hi, w[e]);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        // m downwards, s upwards: towards larger magnitudes is up by 0xFFFF and cut off
+        const uint32_t lb = __float_as_uint(lo);
+        float m = __uint_as_float((lb + ((int)lb < 0 ? 0xFFFFu : 0u)) & 0xFFFF0000u);
+        const float span = hi - m;
+        float s = span >= kSmallest ? __uint_as_float((__float_as_uint(span * kInv15) + 0xFFFFu) & 0xFFFF0000u) : 0.f;
+        const bool bad = !(span <= 3.402823466e38f);                 // NaN, infinities, or further apart than fp32 holds
+        if (bad) {
+          m = __uint_as_float(0x7FC00000u);
+          s = 0.f;
+        }
+        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+        uint32_t code = 0;
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            code |= (uint32_t)max(0, min(15, bad ? 0 : __float2int_rn((w[e] - m) * inv))) << (4 * q4_nibble(e));
+        }
+        if (t < nt) {
+          if (which == 0) {
+            k_words[q4_k_word(ND, t0 + t, c)] = code;
+          } else {
+            uint32_t lo4 = 0, hi4 = 0;                               // a byte a code, in the columns' order
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              lo4 |= (code >> (4 * q4_nibble(e)) & 15u) << (8 * e);
+              hi4 |= (code >> (4 * q4_nibble(e + 4)) & 15u) << (8 * e);
+            }
+            uint32_t* dst = (uint32_t*)(s_code + (t0 + t) * kPitch + c);
+            dst[0] = lo4;
+            dst[1] = hi4;
+          }
+          if ((c & 63) == 0) ms_words[(c >> 6) * kPage + t0 + t] = (__float_as_uint(m) >> 16) | (__float_as_uint(s) & 0xFFFF0000u);
+        }
+      }
+    }
+    if (which == 1) {
+      __syncthreads();
+      uint32_t* v_words = (uint32_t*)(pg + q4_v(ND));
+      for (int i = tid; inside && i < 64 * ND * 8; i += kIoThreads) {
+        const int c = (i >> 7) * 16 + ((i >> 1) & 1) * 8 + ((i >> 4) & 7), t = ((i >> 2) & 3) * 16 + (i & 1) * 8;   // word i
+        if (t >= t0 + nt || t + 8 <= t0) continue;
+        uint32_t w = 0, keep = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (t + e >= t0 && t + e < t0 + nt) w |= (uint32_t)s_code[(t + e) * kPitch + c] << (4 * q4_nibble(e));
+          else keep |= 15u << (4 * q4_nibble(e));
+        }
+        v_words[i] = keep ? w | (v_words[i] & keep) : w;
+      }
+    }
+  }
+  pdl_trigger();
+}
+
+// ------------------------------------------------------------ reading back
+
+struct Q4LoadArgs {
+  void* out[2];
+  int64_t st_t, n_rows;            // rows of the outputs: what lies past them is not written
+  int32_t n_cap;
+};
+
+// One CTA reads one page of a row: s c + m, rounded once to the output's type.  The values'
+// codes come through shared memory (blocks of 16 columns 528 bytes apart: their words of
+// the same tokens lie in different banks).
+template <int ND, typename T>
+__global__ void __launch_bounds__(kIoThreads)
+q4_load_kernel(Q4Geom g, Q4LoadArgs a, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
+               const uint8_t* __restrict__ pages, const int64_t* __restrict__ start) {
+  constexpr int kV8 = 8 * ND, kBlock = 132;                   // words of 16 columns, padded
+  __shared__ __align__(16) uint32_t s_words[4 * ND * kBlock];
+  __shared__ uint32_t s_ms[ND * kPage];
+  pdl_wait();
+  const int r = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, j = blockIdx.x;
+  const int n = min(safe_len(lens[r], g.max_pages), a.n_cap);
+  int nt = min(kPage, n - j * kPage);
+  const int64_t at = start[r];
+  if (nt > 0 && at >= 0) {
+    const int64_t page = safe_page(table[(int64_t)r * g.max_pages + j], g.n_pages);
+    nt = (int)min((int64_t)nt, max(a.n_rows - at - j * kPage, (int64_t)0));
+    const uint8_t* pg = pages + page * q4_page_bytes(ND);
+    T* out = (T*)(which ? a.out[1] : a.out[0]) + (at + j * kPage) * a.st_t;
+    const uint32_t* ms = (const uint32_t*)(pg + (which ? q4_v_ms(ND) : q4_k_ms(ND)));
+    for (int i = tid; i < ND * kPage; i += kIoThreads) s_ms[i] = ms[i];
+    if (which) {
+      const uint4* src = (const uint4*)(pg + q4_v(ND));
+      for (int i = tid; i < 128 * ND; i += kIoThreads) *(uint4*)(s_words + (i >> 5) * kBlock + (i & 31) * 4) = src[i];
+    }
+    __syncthreads();
+    if (which == 0) {
+      const uint32_t* words = (const uint32_t*)pg;
+#pragma unroll 4
+      for (int i = tid; i < nt * kV8; i += kIoThreads) {
+        const int t = i / kV8, c = i % kV8 * 8;
+        if (c >= g.d) continue;
+        const uint32_t w = words[q4_k_word(ND, t, c)], p = s_ms[(c >> 6) * kPage + t];
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf((float)(w >> (4 * q4_nibble(e)) & 15u), q4_s(p), q4_m(p));
+        store8(out + t * a.st_t + c, x);
+      }
+    } else {
+      for (int i = tid; i < kV8 * 16; i += kIoThreads) {
+        const int c = i % kV8 * 8, t = i / kV8 * 4;           // 8 columns, 4 tokens
+        if (t >= nt || c >= g.d) continue;
+        const uint32_t* src = s_words + (c >> 4) * kBlock + (q4_v_word(c & 15, t) & 127);
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = src[16 * e] >> (t & 4 ? 8 : 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (t + k >= nt) break;
+          const uint32_t p = s_ms[(c >> 6) * kPage + t + k];
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf((float)(w[e] >> (4 * q4_nibble(k)) & 15u), q4_s(p), q4_m(p));
+          store8(out + (t + k) * a.st_t + c, x);
+        }
+      }
+    }
+  }
+  pdl_trigger();
+}
+
+template <int ND, typename T>
+cudaError_t append_nd(const Q4Geom& g, const Q4AppendArgs& a, const int32_t* counts, const int64_t* slots, uint8_t* pages,
+                      cudaStream_t s) {
+  // n_cap tokens that begin anywhere in a page touch this many pages
+  const dim3 grid((a.n_cap + 2 * (kPage - 1)) / kPage, g.rows, 2);
+  return launch_pdl(q4_append_kernel<ND, T>, grid, dim3(kIoThreads), 0, s, g, a, counts, slots, pages);
+}
+template <int ND, typename T>
+cudaError_t load_nd(const Q4Geom& g, const Q4LoadArgs& a, const int32_t* table, const int32_t* lens, const uint8_t* pages,
+                    const int64_t* start, cudaStream_t s) {
+  const dim3 grid((a.n_cap + kPage - 1) / kPage, g.rows, 2);
+  return launch_pdl(q4_load_kernel<ND, T>, grid, dim3(kIoThreads), 0, s, g, a, table, lens, pages, start);
+}
+
+template <typename T>
+cudaError_t append_t(const Q4Geom& g, const Q4AppendArgs& a, const int32_t* counts, const int64_t* slots, uint8_t* pages,
+                     cudaStream_t s) {
+  switch (g.d64 / 64) {
+    case 1: return append_nd<1, T>(g, a, counts, slots, pages, s);
+    case 2: return append_nd<2, T>(g, a, counts, slots, pages, s);
+    case 3: return append_nd<3, T>(g, a, counts, slots, pages, s);
+    default: return append_nd<4, T>(g, a, counts, slots, pages, s);
+  }
+}
+template <typename T>
+cudaError_t load_t(const Q4Geom& g, const Q4LoadArgs& a, const int32_t* table, const int32_t* lens, const uint8_t* pages,
+                   const int64_t* start, cudaStream_t s) {
+  switch (g.d64 / 64) {
+    case 1: return load_nd<1, T>(g, a, table, lens, pages, start, s);
+    case 2: return load_nd<2, T>(g, a, table, lens, pages, start, s);
+    case 3: return load_nd<3, T>(g, a, table, lens, pages, start, s);
+    default: return load_nd<4, T>(g, a, table, lens, pages, start, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_append(const Q4Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
+                             int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, uint8_t* pages,
+                             cudaStream_t s) {
+  const Q4AppendArgs a = {{k, v}, st_b, st_h, st_t, n_cap};
+  return bf16 ? append_t<__nv_bfloat16>(g, a, counts, slots, pages, s) : append_t<float>(g, a, counts, slots, pages, s);
+}
+
+cudaError_t launch_q4_load(const Q4Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const uint8_t* pages,
+                           const int64_t* start, int n_cap, int64_t n_rows, void* k_out, void* v_out, int64_t st_t,
+                           cudaStream_t s) {
+  const Q4LoadArgs a = {{k_out, v_out}, st_t, n_rows, n_cap};
+  return bf16 ? load_t<__nv_bfloat16>(g, a, table, lens, pages, start, s) : load_t<float>(g, a, table, lens, pages, start, s);
+}
+
+}  // namespace chunkkv

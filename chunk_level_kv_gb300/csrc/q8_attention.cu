@@ -30,12 +30,12 @@
 // 6.0 TB/s, 89 % of a copy's rate, and its DRAM reads are the pages' bytes; one sequence
 // of 8 KV heads x 6.5 thousand tokens 12.3 us, 16 sequences of 256 to 300 tokens 7.4 us
 // (latency: lengths, page index, page, products and join one after another).
-#include <cuda_fp16.h>
-
-#include "serve.cuh"
+#include "decode.cuh"
 
 namespace chunkkv {
 namespace {
+
+using namespace decode;
 
 constexpr int kMaxG = 8;                         // query heads per pass
 constexpr int kMaxGrid = 224;                    // CTAs of a pass (one per SM): a count for each in the header
@@ -59,15 +59,6 @@ struct Q8AttnArgs {
   float* part;                                   // [passes][2 CTAs][8][d64 + 4]: O, m, l, O's reference
 };
 
-// Rows of up to this many pages are not cut: a row in two pieces costs the CTAs that
-// share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's
-// share of the bandwidth, and the eight warps take eight pages at once.
-// A cut within kNearEnd pages of a long row's begin or end moves there, so that a CTA
-// seldom has a second row for a few pages.
-constexpr int kWholeRow = 8;
-constexpr int kNearEnd = 3;
-static_assert(kWholeRow > 2 * kNearEnd, "a row's two ends do not meet");
-
 template <int ND>
 constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
 template <int ND>
@@ -84,23 +75,6 @@ constexpr size_t smem_bytes() {
                                    (q_in_regs<ND>() ? 0 : ND * 4 * 32 * 16));
 }
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// D (16 x 8, fp32) += A (16 x 16, f16) B (16 x 8, f16)
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
 // Four int8 codes as two f16 pairs: a code plus 128 in the low byte of 0x64.. is
 // 1024 + 128 + code, exactly.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -111,102 +85,10 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   lo = *(const uint32_t*)&x;
   hi = *(const uint32_t*)&y;
 }
-__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *(const uint32_t*)&h;
-}
-// x = hi + lo in two f16 pairs (lo times up).
-__device__ __forceinline__ void split_half2(float x, float y, float up, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  hi = *(const uint32_t*)&h;
-  lo = pack_half2((x - f.x) * up, (y - f.y) * up);
-}
-
-__device__ __forceinline__ void load4f(const float* p, float (&x)[4]) {
-  const float4 v = *(const float4*)p;
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4f(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = *(const uint2*)p;
-  x[0] = __uint_as_float(v.x << 16);
-  x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(v.y << 16);
-  x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ void store4(float* p, float4 v) { *(float4*)p = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-  *(uint2*)p = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
-}
-
 // O over the sum, from O's reference to the sum's.
 __device__ __forceinline__ float4 finish(float4 o, float sum, float up) {
   return make_float4(o.x / sum * up, o.y / sum * up, o.z / sum * up, o.w / sum * up);
 }
-
-__device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
-
-// A bounded wait for one phase of a copy that this warp started.  Nothing but the
-// copy itself completes it, so the limit (seconds) is never met in a healthy run; a
-// warp that meets it records an error, waits no more and lets the kernel end.
-__device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity, bool& dead, int32_t* err) {
-  if (dead) return;
-  for (int i = 0; i < 4096; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
-    if (ok) return;
-  }
-  atomicCAS(err, 0, (int)kDevTimeoutTmaProducer);
-  dead = true;
-}
-__device__ __forceinline__ void copy_page(uint32_t dst, const int8_t* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"((uint64_t)src), "r"(bytes), "r"(bar) : "memory");
-}
-
-// Where global page x lies: rows are looked up 32 at a time, a lane each.
-struct Cursor {
-  int base;                 // row of lane 0
-  int64_t start;            // pages before it
-  int len;                  // this lane's row's length
-  int64_t end;              // pages up to and with this lane's row
-
-  __device__ void load(const Q8Geom& g, const int32_t* lens, int lane) {
-    const int r = base + lane;
-    len = r < g.rows ? safe_len(lens[r], g.max_pages) : 0;
-    int n = pages_of(len);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += y;
-    }
-    end = start + n;
-  }
-  // Row, page inside the row and length of the row of page x (below the total, not
-  // before an earlier call's).
-  __device__ void locate(const Q8Geom& g, const int32_t* lens, int lane, int64_t x, int& row, int& j, int& n) {
-    while (true) {
-      const uint32_t above = __ballot_sync(0xffffffffu, end > x);
-      if (above || base + 32 >= g.rows) {
-        const int at = above ? __ffs(above) - 1 : 31;
-        row = min(base + at, g.rows - 1);
-        n = __shfl_sync(0xffffffffu, len, at);
-        j = (int)(x - (__shfl_sync(0xffffffffu, end, at) - pages_of(n)));
-        return;
-      }
-      start = __shfl_sync(0xffffffffu, end, 31);
-      base += 32;
-      load(g, lens, lane);
-    }
-  }
-};
 
 template <int ND, typename T>
 __global__ void __launch_bounds__(32 * warps_of<ND>(), 1)
@@ -219,9 +101,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
   constexpr int NT = 8 * ND;                     // 8-column tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[2 * W];
-  __shared__ long long s_scan[W];
-  __shared__ int64_t s_cut[2], s_start[2];       // the run's ends, and the pages before the rows that they lie in
-  __shared__ int s_row[2], s_last;
+  __shared__ RunShared<W> run;
+  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
   uint8_t* sK = smem + warp * 2 * kBytes;
   uint8_t* sV = sK + kBytes;
@@ -236,47 +117,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
   pdl_wait();
 
   // ---- this CTA's run [x0, x1) of the pages of all rows, and the row in which it begins
-  const int chunk = (g.rows + kThreads - 1) / kThreads;
-  const int c0 = min(g.rows, tid * chunk), c1 = min(g.rows, c0 + chunk);
-  long long mine = 0;
-  for (int r = c0; r < c1; ++r) mine += pages_of(safe_len(lens[r], g.max_pages));
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (i == warp) before = total;
-    total += s_scan[i];
-  }
-  before += incl - mine;                         // pages before this thread's rows
-  // no more runs than pages: every CTA that shares a row has a part of it
-  const int64_t nc = total < gridDim.x ? total : gridDim.x;
-  const bool busy = blockIdx.x < nc;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t cut = busy ? total * (blockIdx.x + k) / nc : total;
-    if (cut == total) {
-      if (tid == 0) s_cut[k] = total;
-    } else if (cut >= before && cut < before + mine) {
-      int64_t x = before;
-      int r = c0, n = 0;
-      for (; r < c1; ++r) {
-        n = pages_of(safe_len(lens[r], g.max_pages));
-        if (x + n > cut) break;
-        x += n;
-      }
-      // short rows stay in one piece, and a long one's end is no place to cut either
-      s_cut[k] = n <= kWholeRow || cut - x <= kNearEnd ? x : x + n - cut <= kNearEnd ? x + n : cut;
-      s_row[k] = r;
-      s_start[k] = x;
-    }
-  }
+  const Run plan = plan_run<W>(g, lens, run);
+  const int64_t total = plan.total, nc = plan.nc;
   const int g0 = a.g0 + blockIdx.y * kMaxG, gn = min(kMaxG, a.G - g0);
   // rows without a token
   for (int r = blockIdx.x; r < g.rows; r += gridDim.x)
@@ -284,7 +126,7 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
       for (int i = tid; i < gn * g.d; i += kThreads)
         store1((T*)a.out + (r / g.Hkv) * a.o_sb + ((r % g.Hkv) * a.G + g0 + i / g.d) * a.o_sh + i % g.d, 0.f);
   __syncthreads();
-  const int64_t x0 = s_cut[0], x1 = s_cut[1];
+  const int64_t x0 = run.cut[0], x1 = run.cut[1];
   if (x0 >= x1) {
     pdl_trigger();
     return;
@@ -292,8 +134,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
 
   // ---- pages under way: [x] in the slots, [x + W] known by its index and scales, [x + 2 W] by its index
   Cursor cur;
-  cur.base = s_row[0];
-  cur.start = s_start[0];
+  cur.base = run.row[0];
+  cur.start = run.start[0];
   cur.load(g, lens, lane);
   int64_t x = x0 + warp;
   int j0 = 0, n0 = 0, j1 = 0, n1 = 0, row = 0;
@@ -315,8 +157,8 @@ q8_attention_kernel(Q8Geom g, Q8AttnArgs a, const int8_t* __restrict__ k_pages, 
     page1 = safe_page(table[(int64_t)row * g.max_pages + j1], g.n_pages);
   }
 
-  int r = s_row[0];                              // segment by segment: the CTA's part of row r
-  int64_t xr = s_start[0];
+  int r = run.row[0];                              // segment by segment: the CTA's part of row r
+  int64_t xr = run.start[0];
   while (true) {
     const int len = safe_len(lens[r], g.max_pages), np = pages_of(len);
     const int64_t sa = xr > x0 ? xr : x0, sb = xr + np < x1 ? xr + np : x1;

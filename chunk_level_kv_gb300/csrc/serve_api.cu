@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "serve.cuh"
+#include "q4.cuh"
 
 namespace chunkkv {
 
@@ -33,6 +33,17 @@ cudaError_t launch_q8_attention(const Q8Geom& g, bool bf16, int G, float alpha, 
                                 int64_t q_sh, void* out, int64_t o_sb, int64_t o_sh, const int8_t* k_pages,
                                 const int8_t* v_pages, const float* scales, const int32_t* table, const int32_t* lens,
                                 void* ws, int sms, cudaStream_t s);
+cudaError_t launch_q4_append(const Q4Geom& g, bool bf16, const void* k, const void* v, int64_t st_b, int64_t st_h,
+                             int64_t st_t, const int32_t* counts, const int64_t* slots, int n_cap, uint8_t* pages,
+                             cudaStream_t s);                                                 // q4_cache.cu
+cudaError_t launch_q4_load(const Q4Geom& g, bool bf16, const int32_t* table, const int32_t* lens, const uint8_t* pages,
+                           const int64_t* start, int n_cap, int64_t n_rows, void* k_out, void* v_out, int64_t st_t,
+                           cudaStream_t s);
+size_t q4_workspace_bytes(const Q4Geom& g, bool bf16, int G, int n_q, int sms);               // q4_attention.cu
+cudaError_t launch_q4_attention(const Q4Geom& g, bool bf16, int G, int n_q, float alpha, const int32_t* q_lens, const void* q,
+                                int64_t q_sb, int64_t q_st, int64_t q_sh, void* out, int64_t o_sb, int64_t o_st,
+                                int64_t o_sh, const uint8_t* pages, const int32_t* table, const int32_t* lens, void* ws,
+                                int sms, cudaStream_t s);
 
 namespace {
 
@@ -58,6 +69,8 @@ int sm_count() {
 bool valid_dtype(int dtype) { return dtype == CHUNKKV_F32 || dtype == CHUNKKV_BF16; }
 int elt_size(int dtype) { return dtype == CHUNKKV_BF16 ? 2 : 4; }
 bool stride_ok(int64_t s, int elt) { return s >= 0 && s < (INT64_MAX >> 32) && (s * elt) % 16 == 0; }
+// Query rows of a KV head are counted in 32 bits, with room for a pass of them more.
+bool rows_ok(int32_t G, int32_t n_q) { return (int64_t)G * n_q <= INT32_MAX / 2; }
 bool scale_ok(float s) { return s > 0.f && isfinite(s); }
 
 chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
@@ -194,15 +207,33 @@ chunkkv_status plan_prefill(const chunkkv_prefill_params* p, bool* tc, int* kb, 
 }
 
 // The part of a cache that every call uses; `pages`: the call reads or writes them.
-chunkkv_status check_cache(const chunkkv_q8_cache* c, bool pages, Q8Geom* g) {
+bool pages_ok(const chunkkv_q8_cache* c) { return aligned(c->k_pages) && aligned(c->v_pages) && aligned(c->scales, 8); }
+bool pages_ok(const chunkkv_q4_cache* c) { return aligned(c->pages); }
+template <typename Cache>
+chunkkv_status check_cache(const Cache* c, bool pages, Q8Geom* g) {
   if (c == nullptr || c->B < 0 || c->Hkv < 1 || c->d < 1 || c->n_pages < 1 || c->max_pages < 1)
     return CHUNKKV_ERR_INVALID_ARG;
   if ((int64_t)c->B * c->Hkv > CHUNKKV_Q8_MAX_ROWS || c->d > kMaxD || c->max_pages > INT32_MAX / kPage - 2)
     return CHUNKKV_ERR_UNSUPPORTED;
   if (c->d % 8 != 0 || !aligned(c->table, 4) || !aligned(c->lens, 4)) return CHUNKKV_ERR_INVALID_ARG;
-  if (pages && (!aligned(c->k_pages) || !aligned(c->v_pages) || !aligned(c->scales, 8))) return CHUNKKV_ERR_INVALID_ARG;
+  if (pages && !pages_ok(c)) return CHUNKKV_ERR_INVALID_ARG;
   *g = {c->B * c->Hkv, c->Hkv, c->d, (c->d + 63) / 64 * 64, c->n_pages, c->max_pages};
   return CHUNKKV_OK;
+}
+
+template <typename Cache>
+chunkkv_status resize(const Cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap, chunkkv_stream_t stream) {
+  Q8Geom g;
+  const chunkkv_status st = check_cache(c, false, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0) return CHUNKKV_OK;
+  if (!aligned(new_lens, 4) || !aligned(c->ring, 4) || !aligned(c->state, 4) || (slots && !aligned(slots, 8)) ||
+      new_lens == c->lens)
+    return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q8_resize(g, new_lens, c->lens, c->table, c->ring, c->state, slots, n_cap, sm_count(),
+                                      (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -254,17 +285,7 @@ chunkkv_status chunkkv_prefill_attention(const chunkkv_prefill_params* p, const 
 
 chunkkv_status chunkkv_q8_resize(const chunkkv_q8_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
                                  chunkkv_stream_t stream) {
-  Q8Geom g;
-  const chunkkv_status st = check_cache(c, false, &g);
-  if (st != CHUNKKV_OK) return st;
-  if (n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
-  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
-  if (g.rows == 0) return CHUNKKV_OK;
-  if (!aligned(new_lens, 4) || !aligned(c->ring, 4) || !aligned(c->state, 4) || (slots && !aligned(slots, 8)) ||
-      new_lens == c->lens)
-    return CHUNKKV_ERR_INVALID_ARG;
-  return cuda_result(launch_q8_resize(g, new_lens, c->lens, c->table, c->ring, c->state, slots, n_cap, sm_count(),
-                                      (cudaStream_t)stream));
+  return resize(c, new_lens, slots, n_cap, stream);
 }
 
 chunkkv_status chunkkv_q8_append(const chunkkv_q8_cache* c, int32_t dtype, const void* k, const void* v, int64_t st_b,
@@ -333,6 +354,80 @@ chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, in
   if (ws_bytes < q8_workspace_bytes(g, G, sm_count())) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
   return cuda_result(launch_q8_attention(g, dtype == CHUNKKV_BF16, G, (float)(scale * kLog2e), q, q_stride_b,
                                          q_stride_h, out, o_stride_b, o_stride_h, c->k_pages, c->v_pages, c->scales,
+                                         c->table, c->lens, ws, sm_count(), (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q4_resize(const chunkkv_q4_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
+                                 chunkkv_stream_t stream) {
+  return resize(c, new_lens, slots, n_cap, stream);
+}
+
+chunkkv_status chunkkv_q4_append(const chunkkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t st_b,
+                                 int64_t st_h, int64_t st_t, const int32_t* counts, const int64_t* slots,
+                                 int32_t n_cap, chunkkv_stream_t stream) {
+  Q4Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || n_cap < 0) return CHUNKKV_ERR_INVALID_ARG;
+  const int elt = elt_size(dtype);
+  if (!stride_ok(st_b, elt) || !stride_ok(st_h, elt) || !stride_ok(st_t, elt)) return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0 || n_cap == 0) return CHUNKKV_OK;
+  if (!aligned(k) || !aligned(v) || !aligned(counts, 4) || !aligned(slots, 8)) return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q4_append(g, dtype == CHUNKKV_BF16, k, v, st_b, st_h, st_t, counts, slots, n_cap, c->pages,
+                                      (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q4_load(const chunkkv_q4_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                               int64_t n_rows, void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream) {
+  Q4Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || n_cap < 0 || n_rows < 0) return CHUNKKV_ERR_INVALID_ARG;
+  if (!stride_ok(st_t, elt_size(dtype))) return CHUNKKV_ERR_INVALID_ARG;
+  if (n_cap > INT32_MAX - 4 * kPage) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0 || n_cap == 0 || n_rows == 0) return CHUNKKV_OK;
+  if (!aligned(start, 8) || !aligned(k_out) || !aligned(v_out)) return CHUNKKV_ERR_INVALID_ARG;
+  return cuda_result(launch_q4_load(g, dtype == CHUNKKV_BF16, c->table, c->lens, c->pages, start,
+                                    std::min(n_cap, c->max_pages * kPage), n_rows, k_out, v_out, st_t,
+                                    (cudaStream_t)stream));
+}
+
+chunkkv_status chunkkv_q4_workspace_size(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q, size_t* bytes) {
+  Q4Geom g;
+  const chunkkv_status st = check_cache(c, false, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (bytes == nullptr || !valid_dtype(dtype) || G < 1 || n_q < 1) return CHUNKKV_ERR_INVALID_ARG;
+  if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
+  *bytes = q4_workspace_bytes(g, dtype == CHUNKKV_BF16, G, n_q, sm_count());
+  return CHUNKKV_OK;
+}
+
+int32_t chunkkv_q4_path(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q) {
+  Q4Geom g;
+  if (check_cache(c, false, &g) != CHUNKKV_OK || !valid_dtype(dtype) || G < 1 || n_q < 1 || !rows_ok(G, n_q)) return -1;
+  return 0;
+}
+
+chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q,
+                                    const int32_t* q_lens, float scale, const void* q, int64_t q_stride_b,
+                                    int64_t q_stride_t, int64_t q_stride_h, void* out, int64_t o_stride_b,
+                                    int64_t o_stride_t, int64_t o_stride_h, void* ws, size_t ws_bytes,
+                                    chunkkv_stream_t stream) {
+  Q4Geom g;
+  const chunkkv_status st = check_cache(c, true, &g);
+  if (st != CHUNKKV_OK) return st;
+  if (!valid_dtype(dtype) || G < 1 || n_q < 1 || !scale_ok(scale)) return CHUNKKV_ERR_INVALID_ARG;
+  const int elt = elt_size(dtype);
+  const int64_t strides[6] = {q_stride_b, q_stride_t, q_stride_h, o_stride_b, o_stride_t, o_stride_h};
+  for (int64_t s : strides)
+    if (!stride_ok(s, elt)) return CHUNKKV_ERR_INVALID_ARG;
+  if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
+  if (g.rows == 0) return CHUNKKV_OK;
+  if (!aligned(q) || !aligned(out) || !aligned(ws) || (q_lens != nullptr && !aligned(q_lens, 4))) return CHUNKKV_ERR_INVALID_ARG;
+  if (ws_bytes < q4_workspace_bytes(g, dtype == CHUNKKV_BF16, G, n_q, sm_count())) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_result(launch_q4_attention(g, dtype == CHUNKKV_BF16, G, n_q, (float)(scale * kLog2e), q_lens, q, q_stride_b,
+                                         q_stride_t, q_stride_h, out, o_stride_b, o_stride_t, o_stride_h, c->pages,
                                          c->table, c->lens, ws, sm_count(), (cudaStream_t)stream));
 }
 

@@ -444,6 +444,80 @@ chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, in
                                     int64_t q_stride_b, int64_t q_stride_h, void* out, int64_t o_stride_b,
                                     int64_t o_stride_h, void* ws, size_t ws_bytes, chunkkv_stream_t stream);
 
+/*
+ * The compressed cache in 4 bits: rows, tables, lengths and the ring as in
+ * chunkkv_q8_cache, with one pool of pages a layer.  Every token's groups of 64
+ * columns (ND = ceil(d / 64) of them, the last one maybe shorter) are quantised by
+ * themselves, in fp32: for a group whose values lie in [lo, hi]
+ *   m = lo rounded down to bf16
+ *   s = (hi - m) * (1 / 15) rounded up to bf16; 0 if hi - m is below 2^-100
+ *   c = round((x - m) * (1 / s)) in 0 .. 15, ties to even; 0 where s is 0
+ * and a code stands for s * c + m.  A group with a NaN or an infinity, or whose values
+ * lie further apart than fp32 can say, has m = NaN and s = 0: it reads as NaN.
+ * A page holds CHUNKKV_Q8_PAGE (64) tokens of one row in CHUNKKV_Q4_PAGE_BYTES(d) bytes:
+ *   keys            [64 tokens][4][ND][8 bytes]     bytes (t, g) of a token: columns 64 g + 16 t .. + 15
+ *   their (m, s)    [ND][64 tokens][2] bf16
+ *   values          [4 ND][8][4][2][8 bytes]        bytes (p, c, t, h): tokens 16 t .. + 15 of column 16 p + 8 h + c
+ *   their (m, s)    [ND][64 tokens][2] bf16
+ * Of 16 codes in 8 bytes, code 8 w + 2 p + e (w, e: 0 .. 1, p: 0 .. 3) is nibble p + 4 e of the
+ * w-th 32-bit word (little endian, nibble 0 the lowest).
+ *   pages   [n_pages][CHUNKKV_Q4_PAGE_BYTES(d)], device, 16-byte aligned
+ * d is a multiple of 8, at most 256.
+ */
+#define CHUNKKV_Q4_PAGE_BYTES(d) (4608 * (((d) + 63) / 64))
+typedef struct chunkkv_q4_cache {
+  int32_t B, Hkv, d;
+  int32_t n_pages, max_pages;
+  uint8_t* pages;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* ring;
+  int32_t* state;
+} chunkkv_q4_cache;
+
+/* chunkkv_q8_resize for a 4-bit cache (pages may be NULL). */
+chunkkv_status chunkkv_q4_resize(const chunkkv_q4_cache* c, const int32_t* new_lens, int64_t* slots, int32_t n_cap,
+                                 chunkkv_stream_t stream);
+
+/*
+ * Writes new rows into one layer's pages; arguments as chunkkv_q8_append's.  A token is
+ * final when it is written: no other token's codes change.
+ */
+chunkkv_status chunkkv_q4_append(const chunkkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t st_b,
+                                 int64_t st_h, int64_t st_t, const int32_t* counts, const int64_t* slots,
+                                 int32_t n_cap, chunkkv_stream_t stream);
+
+/* Reads rows back, s * c + m rounded once to dtype's type; arguments as chunkkv_q8_load_bounded's. */
+chunkkv_status chunkkv_q4_load(const chunkkv_q4_cache* c, int32_t dtype, const int64_t* start, int32_t n_cap,
+                               int64_t n_rows, void* k_out, void* v_out, int64_t st_t, chunkkv_stream_t stream);
+
+/*
+ * Attention of n_q >= 1 query tokens a sequence over one layer's cache, G query heads per
+ * KV head.  The m = q_lens[b] query tokens of sequence b (q_lens: device [B] int32, values
+ * outside 0 .. n_q are taken as the nearer of the two; NULL: n_q each) are the last m of
+ * every row's tokens, whose keys and values the cache holds already:
+ *   out[b][i][h * G + g] = sum_j softmax_j(scale * q[b][i][h * G + g] . K_j) V_j
+ * over the tokens j < lens[r] - m + 1 + i of row r = b * Hkv + h, for i < m: with n_q = 1 the
+ * single-token attention over all of a row.  A query that sees no token gives zeros; logits
+ * that are all -inf give NaN.  What a query does not see adds nothing, whatever it holds.
+ * out[b][i] of i >= m is not written.
+ *   q, out: device [B, n_q, Hkv * G, d] with element strides (b, token, head), multiples of
+ *   16 bytes; out overlaps no input;
+ *   scale > 0 and finite; sums and softmax statistics in fp32.  For bf16 the weights are
+ *   rounded to f16 (2^-11 each) before they weigh the values;
+ *   ws: device workspace of chunkkv_q4_workspace_size bytes, under chunkkv_q8_attention's
+ *   terms: zero-filled before its first use, not shared by calls that can overlap; it may
+ *   serve any of the attention calls in turn.
+ */
+chunkkv_status chunkkv_q4_workspace_size(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q, size_t* bytes);
+/* Which kernel such a call takes: 0 = one for few query rows, 1 = one for many, -1 = invalid arguments. */
+int32_t chunkkv_q4_path(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q);
+chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q,
+                                    const int32_t* q_lens, float scale, const void* q, int64_t q_stride_b,
+                                    int64_t q_stride_t, int64_t q_stride_h, void* out, int64_t o_stride_b,
+                                    int64_t o_stride_t, int64_t o_stride_h, void* ws, size_t ws_bytes,
+                                    chunkkv_stream_t stream);
+
 /* Static description of a status code. */
 const char* chunkkv_status_string(chunkkv_status s);
 
