@@ -14,10 +14,18 @@
 // nibbles into f16 pairs, 5 instructions for 8 codes, and the other operand's elements that
 // meet the higher ones are divided by 16 beforehand.  The products are m16n8k16 in f16 with
 // fp32 sums; tcgen05 would want the codes expanded in shared memory, 4 times their bytes.
-//   bf16: the 16 operand rows are up to 16 query rows (8 where there are no more).  A query in
+//   S = Q K^T takes the query as the 16-row operand and gives a lane two tokens of one query
+//   row; that is how O^T = V^T P^T wants its 8-column operand, so the weights go from one to
+//   the other in registers, and V's codes fill all 16 rows (half the products and half the
+//   sums' registers of O = P V).
+//   bf16: up to 8 query rows, or 16 as two columns' worth of the second product.  A query in
 //         f16, scaled by a power of two, loses only what is below 2^-25 of its largest element;
 //         the weights p s are rounded to f16, 2^-11 each, where the output's rounding is 2^-8.
-//   fp32: 8 query rows, and rows 8-15 carry what f16 cut off (22 bits of each).
+//         Sums of products with subnormals are good to about 2^-17 of their largest term (the
+//         unit aligns them by the exponent that a subnormal is stored with).
+//   fp32: 8 query rows, and rows 8-15 carry what f16 cut off (22 bits of each); the weights in
+//         two products.  The codes are made whole numbers c - 8 (m becomes m + 8 s), 11 instructions
+//         for 8 codes; with subnormals the output was off by 60e-6.
 //
 // A weight p s is held as a multiple of the largest p s of its row so far (2^d times 2^max t), so
 // that f16 holds it however far apart the steps of a row lie.
@@ -41,7 +49,6 @@ constexpr int kCountByte = 32;                   // the counts of parts that hav
 static_assert(kCountByte + kMaxGrid * kMaxGroups <= (int)kServeHeader, "the counts lie in the serving header");
 constexpr float kWeightExp = 14.f;               // the largest weight is 2^14 (f16 ends at 2^16)
 constexpr int kQueryExp = 14;                    // the largest query element is in [2^14, 2^15)
-constexpr int kSlots = 2;                        // pages of a warp in shared memory
 
 struct Q4AttnArgs {
   const void* q;
@@ -54,21 +61,51 @@ struct Q4AttnArgs {
   float* part;                                   // [passes][2 CTAs][rows][64 ND + 4]: O, m, l
 };
 
-template <int ND>
-constexpr int warps_of() { return ND <= 2 ? 8 : 4; }
-// Rows of a pass.
-template <typename T, int RS>
-constexpr int pass_rows() { return 8 * RS; }
+// Warps of a CTA, a page each in shared memory.  Sixteen hide the products' latency best, and 8
+// query rows of up to 128 columns fit their 128 registers a thread.
+template <int ND, typename T, int RS>
+constexpr int warps_of() { return sizeof(T) == 2 && RS == 1 && ND <= 2 ? 16 : 8; }
 template <int ND>
 constexpr int pitch() { return 64 * ND + 4; }    // O, m, l: in 16-byte rows
 template <int ND>
 constexpr bool q_in_regs() { return ND <= 2; }   // wider heads keep their query fragments in shared memory
-template <int ND, int RS>
+template <int ND, typename T, int RS>
 constexpr size_t smem_bytes() {
-  return (size_t)warps_of<ND>() * (kSlots * q4_page_bytes(ND) + 8 * RS * pitch<ND>() * 4 + (q_in_regs<ND>() ? 0 : ND * 4 * 32 * 16));
+  return (size_t)warps_of<ND, T, RS>() * (q4_page_bytes(ND) + 8 * RS * pitch<ND>() * 4) + (q_in_regs<ND>() ? 0 : ND * 4 * 32 * 16);
 }
+// The halves of a page, each with its steps: two copies, and two barriers.
+constexpr int half_bytes(int nd) { return q4_v(nd); }
+static_assert(2 * half_bytes(1) == q4_page_bytes(1), "keys and values take the same room");
 
 __device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
+// Four codes of a word, of its items 4 h .. 4 h + 3, as two f16 pairs.
+template <bool kExact>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, int h, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kExact) {                        // c - 8: a code below 1024's last bits, less 1032
+    const uint32_t a = (w >> (8 * h) & 0x000F000Fu) | 0x64006400u, b = (w >> (8 * h + 4) & 0x000F000Fu) | 0x64006400u;
+    const __half2 k = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
+    const __half2 x = __hsub2(*(const __half2*)&a, k), y = __hsub2(*(const __half2*)&b, k);
+    lo = *(const uint32_t*)&x;
+    hi = *(const uint32_t*)&y;
+  } else {                                       // c 2^-24 and c 2^-20
+    w >>= 8 * h;
+    lo = w & 0x000F000Fu;
+    hi = w & 0x00F000F0u;
+  }
+}
+// What code 0 (or code 8, kExact) stands for, of two tokens.
+template <bool kExact>
+__device__ __forceinline__ float2 base_of(uint32_t a, uint32_t b, float2 s) {
+  const float2 m = f2(q4_m(a), q4_m(b));
+  return kExact ? __ffma2_rn(s, f2(8.f, 8.f), m) : m;
+}
+// D = A B (decode.cuh: D += A B).
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // The sequence's query tokens, kept inside what the query tensor holds.
@@ -77,26 +114,29 @@ __device__ __forceinline__ int queries_of(const Q4AttnArgs& a, int b) {
 }
 
 template <int ND, typename T, int RS>
-__global__ void __launch_bounds__(32 * warps_of<ND>(), 1)
+__global__ void __launch_bounds__(32 * warps_of<ND, T, RS>(), 1)
 q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, const int32_t* __restrict__ table,
                     const int32_t* __restrict__ lens) {
-  constexpr int W = warps_of<ND>(), kThreads = 32 * W, kBytes = q4_page_bytes(ND), kPitch = pitch<ND>();
-  constexpr int PR = pass_rows<T, RS>();
-  constexpr bool kSplit = sizeof(T) == 4;        // rows 8-15 carry the low parts of rows 0-7
+  constexpr int W = warps_of<ND, T, RS>(), kThreads = 32 * W, kBytes = q4_page_bytes(ND), kHalf = half_bytes(ND);
+  constexpr int kPitch = pitch<ND>(), PR = 8 * RS;
+  constexpr bool kSplit = sizeof(T) == 4;        // the query's rows 8-15 carry the low parts of rows 0-7
   static_assert(!kSplit || RS == 1, "an operand has 16 rows");
+  constexpr int kCodeExp = kSplit ? 0 : 24;      // a code is c 2^-kCodeExp, or c - 8
+  constexpr float kSecond = kSplit ? 1.f : 0.0625f;            // of what meets the second pair of codes
   constexpr int KS = 4 * ND;                     // k steps of a logit, 16 columns each
-  constexpr int NT = 8 * ND;                     // 8-column tiles of the output
+  constexpr int MT = 4 * ND;                     // 16-column tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[kSlots * W];
+  __shared__ uint64_t bars[2 * W];
   __shared__ RunShared<W> run;
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
-  uint8_t* slots = smem + warp * kSlots * kBytes;
-  float* sM = (float*)(smem + W * kSlots * kBytes);                    // [W][PR][kPitch]
-  uint4* sQ = (uint4*)(sM + W * PR * kPitch) + warp * KS * 32;
-  const uint32_t bar = smem_u32(&bars[kSlots * warp]);
+  uint8_t* pg = smem + warp * kBytes;
+  float* sM = (float*)(smem + W * kBytes);       // [W][PR][kPitch]
+  uint4* sQ = (uint4*)(sM + W * PR * kPitch);    // one for all warps: they work on one cache row at a time
+  const uint32_t kbar = smem_u32(&bars[2 * warp]), vbar = kbar + 8;
   if (lane == 0) {
-    for (int i = 0; i < kSlots; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8 * i) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(kbar) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(vbar) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
@@ -122,7 +162,7 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
     return;
   }
 
-  // ---- pages under way: this warp's are x0 + warp + W i, page i in slot i % kSlots
+  // ---- this warp's pages are x0 + warp + W i
   Cursor cur;
   cur.base = run.row[0];
   cur.start = run.start[0];
@@ -134,13 +174,14 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
   };
   int64_t x = x0 + warp;
   bool dead = false;
-  uint32_t slot = 0, phase = 0;                  // phase: a bit per slot
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i)
-    if (x + i * W < x1) {
-      const int64_t page = page_at(x + i * W);
-      if (lane == 0) copy_page(smem_u32(slots + i * kBytes), pages + page * kBytes, kBytes, bar + 8 * i);
+  uint32_t phase = 0;
+  if (x < x1) {
+    const uint8_t* src = pages + page_at(x) * kBytes;
+    if (lane == 0) {
+      copy_page(smem_u32(pg), src, kHalf, kbar);
+      copy_page(smem_u32(pg) + kHalf, src + kHalf, kHalf, vbar);
     }
+  }
 
   int r = run.row[0];                            // segment by segment: the CTA's part of cache row r
   int64_t xr = run.start[0];
@@ -149,9 +190,9 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
     const int64_t sa = xr > x0 ? xr : x0, sb = xr + np < x1 ? xr + np : x1;
     const int b = r / g.Hkv, h = r % g.Hkv, nq = queries_of(a, b);
     if (sa < sb) {
-      // the query's fragments: columns 64 p + 16 t + 4 kk .. + 3 meet the 16 bits from 8 (kk & 1) on of the words that
-      // lane t reads; their second pair meets codes that are 16 times as large
-      float ca[RS], cb[RS][ND];                  // t = ca 2^(24 - kQueryExp) sum_g s acc + sum_g cb m
+      // the query's fragments: columns 64 p + 16 t + 4 kk .. + 3 meet the items 4 (kk & 1) .. + 3 of the words that lane
+      // t reads
+      float ca[RS], cb[RS][ND];                  // t = ca 2^(kCodeExp - kQueryExp) sum_g s acc + sum_g cb base
       int seen[RS];                              // tokens that the row's query sees
       uint4 qf[q_in_regs<ND>() ? KS : 1];
       int seen_min = len;
@@ -189,9 +230,11 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
         ca[rs] = a.alpha * power_of_two(e2);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const float c0 = qv[s][0] * down, c1 = qv[s][1] * down, c2 = qv[s][2] * down * 0.0625f, c3 = qv[s][3] * down * 0.0625f;
+          const float c0 = qv[s][0] * down, c1 = qv[s][1] * down, c2 = qv[s][2] * down * kSecond, c3 = qv[s][3] * down * kSecond;
           uint4 f = make_uint4(0, 0, 0, 0);
-          if constexpr (q_in_regs<ND>()) f = rs > 0 ? qf[s] : f; else f = rs > 0 ? sQ[s * 32 + lane] : f;
+          if (rs > 0) {
+            if constexpr (q_in_regs<ND>()) f = qf[s]; else f = sQ[s * 32 + lane];
+          }
           if constexpr (kSplit) {
             split_half2(c0, c1, 1.f, f.x, f.y);
             split_half2(c2, c3, 1.f, f.z, f.w);
@@ -214,15 +257,18 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
 #pragma unroll
         for (int p = 0; p < ND; ++p) z[rs][p] = 0.f;
       }
-      float o[NT][4];
+      float o[RS][MT][4];                        // O^T: columns 16 i + gid (+ 8: elements 2, 3) of rows 2 t, 2 t + 1
 #pragma unroll
-      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[rs][i][0] = o[rs][i][1] = o[rs][i][2] = o[rs][i][3] = 0.f;
 
       while (x < sb) {
-        const bool more = x + kSlots * W < x1;
-        const int64_t next = more ? page_at(x + kSlots * W) : 0;
-        const uint8_t* pg = slots + slot * kBytes;
-        wait_copy(bar + 8 * slot, (phase >> slot) & 1, dead, a.err);
+        const int64_t nx = x + W;
+        const bool more = nx < x1;
+        // the page to come: mostly of this row
+        const int64_t next = nx < sb ? safe_page(table[(int64_t)r * g.max_pages + (nx - xr)], g.n_pages) : more ? page_at(nx) : 0;
+        wait_copy(kbar, phase, dead, a.err);
         // ---- t.  Column 2 t + e of tile i is token 16 t + 2 i + e of the page: the tokens that lane t's pieces of V hold
         float2 t[RS][8];
 #pragma unroll
@@ -254,15 +300,16 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
             float2 sum[RS], off[RS];
 #pragma unroll
             for (int p = 0; p < ND; ++p) {
-              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              float acc[4];
 #pragma unroll
               for (int s = 0; s < 4; ++s) {
-                const uint32_t w = kw[2 * p + (s >> 1)] >> (8 * (s & 1));
+                uint32_t b0, b1;
+                codes_to_f16<kSplit>(kw[2 * p + (s >> 1)], s & 1, b0, b1);
                 uint4 f;
                 if constexpr (q_in_regs<ND>()) f = qf[4 * p + s]; else f = sQ[(4 * p + s) * 32 + lane];
-                mma16816(acc, f, w & 0x000F000Fu, w & 0x00F000F0u);
+                if (s == 0) mma16816_first(acc, f, b0, b1); else mma16816(acc, f, b0, b1);
               }
-              const float2 s2 = f2(q4_s(ms[p][2 * y]), q4_s(ms[p][2 * y + 1])), m2 = f2(q4_m(ms[p][2 * y]), q4_m(ms[p][2 * y + 1]));
+              const float2 s2 = f2(q4_s(ms[p][2 * y]), q4_s(ms[p][2 * y + 1])), m2 = base_of<kSplit>(ms[p][2 * y], ms[p][2 * y + 1], s2);
 #pragma unroll
               for (int rs = 0; rs < RS; ++rs) {
                 const float2 v = kSplit ? f2(acc[0] + acc[2], acc[1] + acc[3]) : f2(acc[2 * rs], acc[2 * rs + 1]);
@@ -273,13 +320,16 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
             }
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
-              constexpr float kUp = 1 << (24 - kQueryExp);
+              constexpr float kUp = kSplit ? 1.f / (1 << kQueryExp) : 1 << (24 - kQueryExp);
               t[rs][i] = __ffma2_rn(__fmul2_rn(sum[rs], f2(kUp, kUp)), f2(ca[rs], ca[rs]), off[rs]);
             }
           }
         }
-        // ---- weights p s and their largest, the reference, O's unit; A fragments of the second product
-        uint4 pf[ND][4];
+        __syncwarp();                            // every lane has read the keys
+        if (more && lane == 0 && !dead) copy_page(smem_u32(pg), pages + next * kBytes, kHalf, kbar);
+        wait_copy(vbar, phase, dead, a.err);
+        // ---- weights p s and their largest, the reference, O's unit; the second product's operands
+        uint32_t pb[RS * (kSplit ? 2 : 1)][ND][4][2];
         auto weigh = [&](auto masked_c) {
           constexpr bool kMasked = decltype(masked_c)::value;
           const int at = (int)(x - xr) * kPage + 16 * t4;     // the row's token that this lane holds first
@@ -326,8 +376,9 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const float2 pr = t[rs][2 * x4 + y];
-                  w[p][2 * x4 + y] = __fmul2_rn(pr, f2(q4_s(ms[2 * y]), q4_s(ms[2 * y + 1])));
-                  off[p] = __ffma2_rn(pr, f2(q4_m(ms[2 * y]), q4_m(ms[2 * y + 1])), off[p]);
+                  const float2 s2 = f2(q4_s(ms[2 * y]), q4_s(ms[2 * y + 1]));
+                  w[p][2 * x4 + y] = __fmul2_rn(pr, s2);
+                  off[p] = __ffma2_rn(pr, base_of<kSplit>(ms[2 * y], ms[2 * y + 1], s2), off[p]);
                   u = fmaxf(u, fmaxf(w[p][2 * x4 + y].x, w[p][2 * x4 + y].y));
                 }
               }
@@ -339,57 +390,52 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
             const float had = dl[rs] - drop, need = u > 0.f ? fmaxf(lg2(u), -112.f) : -INFINITY, now = fmaxf(had, need);
             if (__any_sync(0xffffffffu, now != had)) {
               const float fo = had == -INFINITY ? 0.f : ex2(had - now);
+              const float fa = __shfl_sync(0xffffffffu, fo, 8 * t4), fb = __shfl_sync(0xffffffffu, fo, 8 * t4 + 4);
 #pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                o[i][2 * rs] *= fo;
-                o[i][2 * rs + 1] *= fo;
-                if (kSplit) {
-                  o[i][2] *= fo;
-                  o[i][3] *= fo;
-                }
+              for (int i = 0; i < MT; ++i) {
+                o[rs][i][0] *= fa;
+                o[rs][i][1] *= fb;
+                o[rs][i][2] *= fa;
+                o[rs][i][3] *= fb;
               }
             }
             dl[rs] = now;
-            const float f = ex2(fminf(kWeightExp - now, 126.f)), f16th = f * 0.0625f;
+            const float f = ex2(fminf(kWeightExp - now, 126.f)), fs = f * kSecond;
 #pragma unroll
             for (int p = 0; p < ND; ++p)
 #pragma unroll
               for (int s = 0; s < 4; ++s) {
-                const float2 a0 = __fmul2_rn(w[p][2 * s], f2(f, f)), a1 = __fmul2_rn(w[p][2 * s + 1], f2(f16th, f16th));
+                const float2 a0 = __fmul2_rn(w[p][2 * s], f2(f, f)), a1 = __fmul2_rn(w[p][2 * s + 1], f2(fs, fs));
                 if constexpr (kSplit) {
-                  split_half2(a0.x, a0.y, 1.f, pf[p][s].x, pf[p][s].y);
-                  split_half2(a1.x, a1.y, 1.f, pf[p][s].z, pf[p][s].w);
-                } else if (rs == 0) {
-                  pf[p][s].x = pack_half2(a0.x, a0.y);
-                  pf[p][s].z = pack_half2(a1.x, a1.y);
-                  if (RS == 1) pf[p][s].y = pf[p][s].w = 0;
+                  split_half2(a0.x, a0.y, 1.f, pb[0][p][s][0], pb[1][p][s][0]);
+                  split_half2(a1.x, a1.y, 1.f, pb[0][p][s][1], pb[1][p][s][1]);
                 } else {
-                  pf[p][s].y = pack_half2(a0.x, a0.y);
-                  pf[p][s].w = pack_half2(a1.x, a1.y);
+                  pb[rs][p][s][0] = pack_half2(a0.x, a0.y);
+                  pb[rs][p][s][1] = pack_half2(a1.x, a1.y);
                 }
               }
           }
         };
         if ((int)(x - xr) * kPage + kPage > seen_min) weigh(std::true_type{}); else weigh(std::false_type{});
-        // ---- O += (p s) c
+        // ---- O^T += c^T (p s)^T
 #pragma unroll
-        for (int p2 = 0; p2 < NT / 2; ++p2) {
-          const uint4 w = *(const uint4*)(pg + q4_v(ND) + p2 * 512 + gid * 64 + t4 * 16);
+        for (int i = 0; i < MT; ++i) {
+          const uint4 w = *(const uint4*)(pg + q4_v(ND) + i * 512 + gid * 64 + t4 * 16);
           const uint32_t vw[2][2] = {{w.x, w.y}, {w.z, w.w}};
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int s = 0; s < 4; ++s) {
+            uint4 c;
+            codes_to_f16<kSplit>(vw[0][s >> 1], s & 1, c.x, c.z);
+            codes_to_f16<kSplit>(vw[1][s >> 1], s & 1, c.y, c.w);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const uint32_t c = vw[e][s >> 1] >> (8 * (s & 1));
-              mma16816(o[2 * p2 + e], pf[p2 / 4][s], c & 0x000F000Fu, c & 0x00F000F0u);
-            }
+            for (int k = 0; k < RS * (kSplit ? 2 : 1); ++k)
+              mma16816(o[kSplit ? 0 : k][i], c, pb[k][i / 4][s][0], pb[k][i / 4][s][1]);
+          }
         }
-        __syncwarp();                            // every lane has read the slot
-        if (more && lane == 0 && !dead)
-          copy_page(smem_u32(slots + slot * kBytes), pages + next * kBytes, kBytes, bar + 8 * slot);
-        phase ^= 1u << slot;
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
-        x += W;
+        __syncwarp();                            // every lane has read the values
+        if (more && lane == 0 && !dead) copy_page(smem_u32(pg) + kHalf, pages + next * kBytes + kHalf, kHalf, vbar);
+        phase ^= 1;
+        x = nx;
       }
 
       // ---- the warps' parts of the segment together, in the reference's unit
@@ -397,21 +443,27 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
       for (int rs = 0; rs < RS; ++rs) {
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
-        float* mw = sM + (warp * PR + gid + 8 * rs) * kPitch;
-        const float up = dl[rs] == -INFINITY ? 0.f : ex2(dl[rs] * 0.5f + 0.5f * (24.f - kWeightExp));   // squared: 2^dl alone may be subnormal
+        float* mw = sM + (warp * PR + 8 * rs) * kPitch;
+        // squared: 2^dl alone may be subnormal
+        const float up = dl[rs] == -INFINITY ? 0.f : ex2(dl[rs] * 0.5f + 0.5f * (kCodeExp - kWeightExp));
+        const float ua = __shfl_sync(0xffffffffu, up, 8 * t4), ub = __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
 #pragma unroll
         for (int p = 0; p < ND; ++p) {
           z[rs][p] += __shfl_xor_sync(0xffffffffu, z[rs][p], 1);
           z[rs][p] += __shfl_xor_sync(0xffffffffu, z[rs][p], 2);
+          const float za = __shfl_sync(0xffffffffu, z[rs][p], 8 * t4), zb = __shfl_sync(0xffffffffu, z[rs][p], 8 * t4 + 4);
 #pragma unroll
-          for (int i = 8 * p; i < 8 * p + 8; ++i) {
-            const float c0 = kSplit ? o[i][0] + o[i][2] : o[i][2 * rs], c1 = kSplit ? o[i][1] + o[i][3] : o[i][2 * rs + 1];
-            *(float2*)(mw + 8 * i + 2 * t4) = f2(fmaf(c0 * up, up, z[rs][p]), fmaf(c1 * up, up, z[rs][p]));
+          for (int i = 4 * p; i < 4 * p + 4; ++i) {
+            float* dst = mw + 2 * t4 * kPitch + 16 * i + gid;
+            dst[0] = fmaf(o[rs][i][0] * ua, ua, za);
+            dst[8] = fmaf(o[rs][i][2] * ua, ua, za);
+            dst[kPitch] = fmaf(o[rs][i][1] * ub, ub, zb);
+            dst[kPitch + 8] = fmaf(o[rs][i][3] * ub, ub, zb);
           }
         }
         if (t4 == 0) {
-          mw[64 * ND] = m[rs];
-          mw[64 * ND + 1] = l[rs];
+          mw[gid * kPitch + 64 * ND] = m[rs];
+          mw[gid * kPitch + 64 * ND + 1] = l[rs];
         }
       }
       __syncthreads();
@@ -528,7 +580,8 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
   }
   if (dead) {                                    // copies still under way land before the CTA's memory is released
     bool gave_up = false;
-    for (int i = 0; i < kSlots; ++i) wait_copy(bar + 8 * i, (phase >> i) & 1, gave_up, a.err);
+    wait_copy(kbar, phase, gave_up, a.err);
+    wait_copy(vbar, phase, gave_up, a.err);
   }
   pdl_trigger();
 }
@@ -537,10 +590,10 @@ template <int ND, typename T, int RS>
 cudaError_t launch(const Q4Geom& g, const Q4AttnArgs& a, const uint8_t* pages, const int32_t* table, const int32_t* lens,
                    int grid, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = raise_smem(q4_attention_kernel<ND, T, RS>, (int)smem_bytes<ND, RS>(), done);
+  const cudaError_t e = raise_smem(q4_attention_kernel<ND, T, RS>, (int)smem_bytes<ND, T, RS>(), done);
   if (e != cudaSuccess) return e;
   const int passes = min((int64_t)kMaxGroups, ((int64_t)a.n_q * a.G - a.p0 + 8 * RS - 1) / (8 * RS));
-  return launch_pdl(q4_attention_kernel<ND, T, RS>, dim3(grid, passes), dim3(32 * warps_of<ND>()), smem_bytes<ND, RS>(), s,
+  return launch_pdl(q4_attention_kernel<ND, T, RS>, dim3(grid, passes), dim3(32 * warps_of<ND, T, RS>()), smem_bytes<ND, T, RS>(), s,
                     g, a, pages, table, lens);
 }
 
