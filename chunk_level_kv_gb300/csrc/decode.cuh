@@ -118,8 +118,8 @@ struct Cursor {
   }
 };
 
-// The pages of all rows in order are cut into one contiguous run [x0, x1) per CTA, whatever
-// the rows' lengths, which only the device knows: every CTA finds its run by a scan over the
+// The pages of all rows in order (or what else work is counted in: size(i) of item i) are cut
+// into one contiguous run [x0, x1) per CTA, whatever the rows' lengths, which only the device knows: every CTA finds its run by a scan over the
 // lengths.  Rows of up to kWholeRow pages are not cut: a row in two pieces costs the CTAs that
 // share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's share of
 // the bandwidth, and the eight warps take eight pages at once.  A cut within kNearEnd pages
@@ -139,14 +139,14 @@ struct Run {
   int64_t total, nc;                             // pages of all rows, and CTAs that have a run
 };
 // Ends in shared memory; to be read after a __syncthreads.
-template <int W>
-__device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restrict__ lens, RunShared<W>& sh) {
+template <int W, typename F>
+__device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh) {
   constexpr int kThreads = 32 * W;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int chunk = (g.rows + kThreads - 1) / kThreads;
-  const int c0 = min(g.rows, tid * chunk), c1 = min(g.rows, c0 + chunk);
+  const int chunk = (count + kThreads - 1) / kThreads;
+  const int c0 = min(count, tid * chunk), c1 = min(count, c0 + chunk);
   long long mine = 0;
-  for (int r = c0; r < c1; ++r) mine += pages_of(safe_len(lens[r], g.max_pages));
+  for (int r = c0; r < c1; ++r) mine += size(r);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -174,7 +174,7 @@ __device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restri
       int64_t x = before;
       int r = c0, n = 0;
       for (; r < c1; ++r) {
-        n = pages_of(safe_len(lens[r], g.max_pages));
+        n = size(r);
         if (x + n > cut) break;
         x += n;
       }
@@ -185,6 +185,16 @@ __device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restri
     }
   }
   return {total, nc};
+}
+template <int W>
+__device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restrict__ lens, RunShared<W>& sh) {
+  return plan_run<W>(g.rows, [&](int r) { return pages_of(safe_len(lens[r], g.max_pages)); }, sh);
+}
+// The CTAs that share an item whose n units begin at unit x and that is cut: from the last one whose cut is at its
+// begin or moves there, to the last one whose cut does not move to its end.
+__device__ __forceinline__ int first_of(const Run& run, int64_t x) { return (int)(((x + kNearEnd + 1) * run.nc - 1) / run.total); }
+__device__ __forceinline__ int last_of(const Run& run, int64_t x, int n) {
+  return (int)(((x + n - kNearEnd) * run.nc - 1) / run.total);
 }
 
 }  // namespace decode

@@ -143,7 +143,7 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
   pdl_wait();
 
   const Run plan = plan_run<W>(g, lens, run);
-  const int64_t total = plan.total, nc = plan.nc;
+  const int64_t nc = plan.nc;
   const int p0 = a.p0 + blockIdx.y * PR, gn = min(PR, a.n_q * a.G - p0);
   auto out_at = [&](int b, int h, int row) {     // where row `row` of the pass is written
     const int i = (p0 + row) / a.G;
@@ -468,9 +468,7 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
       }
       __syncthreads();
       const bool whole = sa == xr && sb == xr + np;
-      // the CTAs of a row that is cut: from the last one whose cut is at its begin or moves there, to the last
-      // one whose cut does not move to its end
-      const int64_t first = ((xr + kNearEnd + 1) * nc - 1) / total, last = ((xr + np - kNearEnd) * nc - 1) / total;
+      const int64_t first = first_of(plan, xr), last = last_of(plan, xr, np);
       float* part = a.part + (int64_t)blockIdx.y * 2 * nc * PR * kPitch;
       // a row that sees no token is zeros; logits that are all -inf give 0 / 0
       auto sees_none = [&](int q) { return len - nq + 1 + (p0 + q) / a.G <= 0; };

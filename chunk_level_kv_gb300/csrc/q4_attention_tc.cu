@@ -1,0 +1,829 @@
+// Attention of many query rows over the 4-bit paged cache on the tensor cores (tcgen05 + TMA +
+// TMEM): bf16, head dimension up to 128.
+//
+//   O_i = sum_{j < n - m + 1 + i} softmax_j(scale q_i . k_j) v_j,   k_j and v_j = s c + m, rounded to bf16
+//
+// for the m query tokens at the end of a cache row of n tokens.  The products, the tiles and the
+// softmax are those of the attention over packed prompts (prefill_tc.cu): two tiles of 128 query
+// rows (the gp query heads of a KV head at 128 / gp consecutive positions) against blocks of 128
+// keys, S and O in TMEM, one thread per row.  What differs:
+//
+// - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
+//   four converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
+//   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
+//   consecutive bytes of a K-major operand: V is stored as V^T, and both products take both
+//   operands K-major.  128 + c is a bf16 number with c as its last bits; less 128 it is c, and
+//   one packed FMA makes s c + m of it, rounded once: 16 instructions for 8 codes.  At 128 columns
+//   these are 550 instructions a block and warp, next to 2048 cycles of products for two tiles.
+// - The lengths are in device memory.  Work is counted in (two tiles, block) pairs; every CTA
+//   takes an equal run of them (plan_run of decode.cuh), so that few rows against many keys
+//   keep every SM busy.  Of query tiles whose keys are cut, the CTAs write parts (m, l, O), and a
+//   second launch joins them in order, 32 columns of 128 rows per CTA.
+// - What a row must not see: S is set to -inf as for prompts.  A value can only be non-finite
+//   as a group's m = NaN; where some row of the item does not see it, the converting warps
+//   replace it by zero and note the first such token of each group of columns, and a row that
+//   sees that token gets NaN there.
+//
+// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
+// 12-15 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "decode.cuh"
+#include "q4.cuh"
+#include "tc_softmax.cuh"
+
+namespace chunkkv {
+
+int prefill_tc_heads(int G);                      // prefill_tc.cu
+
+namespace {
+
+using namespace tcgen;
+using decode::Run;
+
+constexpr int kStages = 3;                        // expanded K and V blocks
+constexpr int kPacked = 5;                        // halves (K or V) of blocks as codes
+constexpr int kItemRing = 2;
+constexpr int kThreads = 512;                     // 16 warps, four warpgroups
+constexpr int kSoftmaxRegs = 192, kIssueRegs = 48, kConvertRegs = 80;
+static_assert(kIssueRegs < 128 && kConvertRegs < 128, "of the launch's 128 a thread");
+static_assert(256 * kSoftmaxRegs + 128 * (kIssueRegs + kConvertRegs) <= kThreads * 128, "register shares within the launch's");
+constexpr int kNever = 0x7FFFFFFF;
+
+template <int ND> constexpr int block_bytes() { return kTile * 64 * ND * 2; }
+template <int ND> constexpr int packed_bytes() { return 2 * q4_v(ND); }           // the halves of two pages
+static_assert(q4_page_bytes(1) == 2 * q4_v(1), "keys and values take the same room");
+constexpr int kStageOut = 32 * 64;                // a softmax warp's 32 rows x 32 output columns
+constexpr int kControl = 1024;
+template <int ND> constexpr int smem_bytes() {
+  return (2 + kStages) * block_bytes<ND>() + kPacked * packed_bytes<ND>() + 8 * kStageOut + kControl;
+}
+// A tile's part: O as [4 warps][D columns][32 lanes], then the rows' m and l.
+template <int D> constexpr int part_floats() { return kTile * (D + 2); }
+template <int N> constexpr uint32_t idesc() {     // fp32 D, bf16 A and B, M = 128
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+struct Q4TcGeom {
+  Q4Geom c;
+  int32_t G, n_q;
+  int32_t gp, inv_gp, pos;                        // query heads and positions of a tile; ceil(65536 / gp)
+  int32_t per_kv;                                 // head groups of gp per KV head
+  int32_t upr, units;                             // units (two tiles) of a row's head group, and of the call
+  float alpha;
+  int64_t o_sb;
+  int32_t o_st, o_sh;
+  long long timeout;
+  const int32_t* q_lens;
+  const uint8_t* pages;
+  const int32_t* table;
+  const int32_t* lens;
+  __nv_bfloat16* out;
+  int2* cut;                                      // [CTAs]: the unit that is cut and begins in the CTA's run (-1: none), its last CTA
+  float* part;                                    // [2 CTAs][2 tiles][part_floats]
+};
+
+// A unit: two tiles of query rows of one head group of a cache row.
+struct Unit {
+  int b, hk, h, row;                              // sequence, KV head, first query head, cache row
+  int q0, rows;                                   // first position, and how many exist
+  int limit;                                      // last key that the first position sees (may be negative)
+  int nb0, nb1, nb;                               // key blocks of the two tiles, and of both
+  int tk;                                         // keys
+};
+__device__ __forceinline__ Unit unit_of(const Q4TcGeom& g, int i) {
+  Unit u;
+  const int hg = i / g.upr;
+  u.row = hg / g.per_kv;
+  u.b = u.row / g.c.Hkv;
+  u.hk = u.row - u.b * g.c.Hkv;
+  u.h = u.hk * g.G + (hg - u.row * g.per_kv) * g.gp;
+  u.tk = safe_len(g.lens[u.row], g.c.max_pages);
+  const int nq = g.q_lens ? min(max(g.q_lens[u.b], 0), g.n_q) : g.n_q;
+  u.q0 = (i - hg * g.upr) * 2 * g.pos;
+  u.rows = min(2 * g.pos, nq - u.q0);             // none or fewer: nothing to do
+  u.limit = u.q0 + u.tk - nq;
+  const int last0 = u.limit + min(u.rows, g.pos) - 1, last1 = u.limit + u.rows - 1;
+  u.nb0 = u.rows <= 0 || last0 < 0 ? 0 : last0 / kTile + 1;
+  u.nb1 = u.rows <= g.pos || last1 < 0 ? 0 : last1 / kTile + 1;
+  u.nb = max(u.nb0, u.nb1);
+  return u;
+}
+
+// A unit's part in one CTA, its keys counted from the part's first; the copying thread hands it to the other roles.
+struct Item {
+  int unit;                                       // -1: no more
+  int b, h, q0, rows, limit, tk;
+  int nb0, nb1, nb;
+  int low;                                        // blocks low .. nb - 1 hold keys hidden to some row
+  int part;                                       // where its part goes; -1: it is whole
+};
+
+__device__ __forceinline__ void put_row(const Q4TcGeom& g, __nv_bfloat16* out, int pos, int head, int c, uint4 w) {
+  *(uint4*)(out + pos * g.o_st + head * g.o_sh + c) = w;
+}
+
+// A warp's rows of the output, 32 columns at a time through the warp's own staging rows: 16-byte piece k of row r lies at
+// k ^ (r >> 1 & 3).  out: the tile's first position and head; left: positions of it that exist; tO: 0xFFFFFFFF for rows
+// without any key; nan: a bit per group of 64 columns that is NaN.
+template <int D>
+__device__ __noinline__ void write_rows(const Q4TcGeom& g, __nv_bfloat16* out, int left, uint32_t tO, float inv, uint8_t* stage,
+                                        int row, uint32_t nan) {
+  const int lane = row & 31, d = g.c.d;
+  uint8_t* mine = stage + lane * 64;
+  // of the rows that this lane writes pieces of, -1: none (a tile's rows lie within 2^31 elements)
+  int where[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int tr = row - lane + 8 * i + (lane >> 2), pos = (tr * g.inv_gp) >> 16;
+    where[i] = pos < left ? pos * g.o_st + (tr - pos * g.gp) * g.o_sh + (lane & 3) * 8 : -1;
+  }
+#pragma unroll 1
+  for (int c = 0; c < D && c < d; c += 32) {
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      float o[16];
+      if (tO != 0xFFFFFFFFu) tmem_get16(tO + c + 16 * k, o);
+      const bool bad = nan >> (c >> 6) & 1;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = bad ? NAN : tO != 0xFFFFFFFFu ? o[i] * inv : 0.f;
+      put8(mine + ((2 * k) ^ (lane >> 1 & 3)) * 16, o);
+      put8(mine + ((2 * k + 1) ^ (lane >> 1 & 3)) * 16, o + 8);
+    }
+    __syncwarp();
+    const bool inside = c + (lane & 3) * 8 < d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 w = *(const uint4*)(stage + r * 64 + ((lane & 3) ^ (r >> 1 & 3)) * 16);
+      if (inside && where[i] >= 0) *(uint4*)(out + where[i] + c) = w;
+    }
+    __syncwarp();
+  }
+}
+
+// A warp's rows of a tile's part to the workspace, a lane per row: whole lines per column.  tO: 0xFFFFFFFF where the part
+// holds no key of the tile (m = -inf and l = 0 say so).
+template <int D>
+__device__ __noinline__ void store_part(float* part, uint32_t tO, float m, float l, int row, uint32_t nan) {
+  float* po = part + (row >> 5) * (D * 32) + (row & 31);
+  if (tO != 0xFFFFFFFFu) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      float o[16];
+      tmem_get16(tO + c, o);
+      const bool bad = nan >> (c >> 6) & 1;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) __stcg(po + (c + i) * 32, bad ? NAN : o[i]);
+    }
+  }
+  __stcg(part + kTile * D + row, m);
+  __stcg(part + kTile * D + kTile + row, l);
+}
+
+// Eight codes of a word (items 0 .. 7 in order) to eight bf16, s c + m each; s and m of items 2 k, 2 k + 1 in pairs.
+__device__ __forceinline__ uint4 expand(uint32_t w, const uint32_t (&s)[4], const uint32_t (&m)[4]) {
+  const __nv_bfloat162 big = __halves2bfloat162(__ushort_as_bfloat16(0x4300), __ushort_as_bfloat16(0x4300));
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = (w >> (4 * k) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hfma2(__hsub2(*(const __nv_bfloat162*)&a, big), *(const __nv_bfloat162*)&s[k], *(const __nv_bfloat162*)&m[k]);
+    o[k] = *(const uint32_t*)&x;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Keys of one page, a warp's half of its tokens, into rows of 64 columns (128 bytes, 16-byte pieces swizzled).
+template <int ND>
+__device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, int lane) {
+#pragma unroll 2
+  for (int i = 0; i < 4; ++i) {
+    const int token = first + 8 * i + (lane >> 2), t4 = lane & 3, row = page_row + token;
+    const uint8_t* src = page + (token * 4 + t4) * (8 * ND);
+#pragma unroll
+    for (int p = 0; p < ND; ++p) {
+      const uint2 w = *(const uint2*)(src + 8 * p);
+      const uint32_t ms = *(const uint32_t*)(page + q4_k_ms(ND) + (p * kPage + token) * 4);
+      const uint32_t s1 = __byte_perm(ms, ms, 0x3232), m1 = __byte_perm(ms, ms, 0x1010);
+      const uint32_t s[4] = {s1, s1, s1, s1}, m[4] = {m1, m1, m1, m1};
+      uint8_t* dst = tile + p * (kTile * 128) + row * 128;
+      *(uint4*)(dst + ((2 * t4) ^ (row & 7)) * 16) = expand(w.x, s, m);
+      *(uint4*)(dst + ((2 * t4 + 1) ^ (row & 7)) * 16) = expand(w.y, s, m);
+    }
+  }
+}
+
+// Values of one page, 2 ND tiles of 16 columns from `first` on (all of one group), into rows of 64 tokens.
+// MASKED: tokens from `left` on are zeros, and a NaN is replaced by zero; returns the first token that had one.
+template <int ND, bool MASKED>
+__device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile, int first, int left, int lane) {
+  const int t4 = lane & 3, gid = lane >> 2, group = first >> 2;
+  uint32_t s[2][4], m[2][4];
+  int bad = kNever;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint4 v = *(const uint4*)(half + 2048 * ND + (group * kPage + 16 * t4 + 4 * x) * 4);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (MASKED) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int token = 16 * t4 + 4 * x + e;
+        if (token >= left) {
+          w[e] = 0;
+        } else if ((w[e] & 0x7F80u) == 0x7F80u) {
+          w[e] = 0;
+          bad = min(bad, token);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int k = 2 * (x & 1) + y;
+      m[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x5410);
+      s[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x7632);
+    }
+  }
+#pragma unroll 2
+  for (int i = 0; i < 2 * ND; ++i) {
+    const uint4 w = *(const uint4*)(half + (first + i) * 512 + gid * 64 + t4 * 16);
+    uint8_t* dst = tile + (16 * (first + i) + gid) * 128;     // columns 16 i + gid and 8 further: gid is the row in the swizzle
+    const int a = ((2 * t4) ^ gid) * 16, b = ((2 * t4 + 1) ^ gid) * 16;
+    *(uint4*)(dst + a) = expand(w.x, s[0], m[0]);
+    *(uint4*)(dst + b) = expand(w.y, s[1], m[1]);
+    *(uint4*)(dst + 1024 + a) = expand(w.z, s[0], m[0]);
+    *(uint4*)(dst + 1024 + b) = expand(w.w, s[1], m[1]);
+  }
+  return bad;
+}
+
+template <int ND>
+__global__ void __launch_bounds__(kThreads, 1)
+q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Q4TcGeom g, int32_t* __restrict__ err) {
+  constexpr int D = 64 * ND;
+  constexpr int kBlock = block_bytes<ND>(), kPackedBytes = packed_bytes<ND>(), kHalf = q4_v(ND);
+  constexpr int kKPanel = kTile * 128, kVPanel = D * 128;     // 64 columns of 128 keys; 64 keys of D columns
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ decode::RunShared<16> run;
+  if (smem_u32(smem) & 1023u) {                   // the swizzle pattern needs 1024-byte alignment
+    if (threadIdx.x == 0) atomicCAS(err, 0, (int)kDevMisalignedSmem);
+    return;
+  }
+  uint8_t* sQ = smem;                             // two tiles
+  uint8_t* sKV = smem + 2 * kBlock;               // kStages blocks: K, V, K, V ... of descending blocks
+  uint8_t* sP = sKV + kStages * kBlock;           // kPacked halves of blocks
+  uint8_t* sOut = sP + kPacked * kPackedBytes;    // [8][kStageOut]
+  uint64_t* bars = (uint64_t*)(sOut + 8 * kStageOut);
+  const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;      // drained: [2]
+  const uint32_t turn = q_full + 32, s_full = q_full + 48, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
+  const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages;
+  const uint32_t packed_full = kv_empty + 8 * kStages, packed_empty = packed_full + 8 * kPacked;
+  const uint32_t item_full = packed_empty + 8 * kPacked, item_empty = item_full + 8 * kItemRing;
+  constexpr int kBars = 6 + 6 + 2 * kStages + 2 * kPacked + 2 * kItemRing;
+  uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile Item* s_items = (volatile Item*)(abort_flag + 1);                               // [kItemRing]
+  volatile int* s_bad = (volatile int*)(s_items + kItemRing);      // [kItemRing][4 converting warps]: first NaN token of its group
+  static_assert(8 * kBars + 8 + (sizeof(Item) + 16) * kItemRing <= kControl, "control block");
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
+    mbar_init(turn, 1); mbar_init(turn + 8, 1);
+    for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 4); mbar_init(kv_empty + 8 * i, 2); }
+    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, 4); }
+    // an item's slot is released by the MMA issuers, the converting and the softmax warps
+    for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 14); }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&qmap) : "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  const Run plan = decode::plan_run<16>(g.units, [&](int i) { return unit_of(g, i).nb; }, run);
+  // units whose rows see no key: zeros
+  for (int i = blockIdx.x; i < g.units; i += gridDim.x) {
+    const Unit u = unit_of(g, i);
+    if (u.nb > 0) continue;
+    const int pieces = g.c.d / 8;
+    __nv_bfloat16* out = g.out + u.b * g.o_sb + (int64_t)u.q0 * g.o_st + (int64_t)u.h * g.o_sh;
+    for (int x = threadIdx.x; x < u.rows * g.gp * pieces; x += kThreads) {
+      const int row = x / pieces;
+      put_row(g, out, row / g.gp, row % g.gp, x % pieces * 8, make_uint4(0, 0, 0, 0));
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const Ctl ctl{err, abort_flag, g.timeout};
+  const int64_t x0 = run.cut[0], x1 = run.cut[1];
+  uint32_t loaded = 0, q_loaded = 0;              // copies that the copying thread armed (for the teardown)
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------ softmax: one query row per thread
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    // positions of this row and of the warp's first row
+    const int my_pos = (row * g.inv_gp) >> 16, pos_lo = ((row - lane) * g.inv_gp) >> 16;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = lanes + t * kTile, tO = lanes + 256 + t * kTile;
+    uint32_t sc = 0, oc = 0;                      // phases of s_full and o_full
+    for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
+      const int slot = n % kItemRing;
+      if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+      const volatile Item& it = s_items[slot];                // read where it is used: registers are short
+      if (it.unit < 0) break;
+      const int nb = t ? it.nb1 : it.nb0;
+      const int limit = it.limit + t * g.pos + my_pos;        // last key that this row sees
+      const bool live = my_pos < g.pos && t * g.pos + my_pos < it.rows;
+      // the row's reference, -m alpha, and its sum; rows of the tile that do not exist never look for one
+      float m = live ? -INFINITY : 0.f, neg = 0.f, l = 0.f;
+      bool ok = true;
+      for (int j = nb - 1; j >= 0; --j) {
+        if (!wait_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
+        ++sc;
+        fence_after();
+        const int seen = limit - j * kTile, lo = seen - (my_pos - pos_lo);       // columns 0 .. seen; the warp's first row's
+        if (kTile - 1 > lo) hide(tS, seen, lo);               // a hidden key in the warp
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+          const float bm = first_reference(tS, lo);
+          if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
+            m = bm;
+            neg = offset_of(m, g.alpha);
+          }
+        }
+        uint32_t p[64];
+        const float sum = row_exp(tS, g.alpha, neg, p);
+        const bool over = live && !(l + sum <= kBig);         // a NaN too, as under a huge reference
+        if (!__any_sync(0xffffffffu, over)) {
+          l += sum;
+          tmem_st32<0>(tS, p);
+          tmem_st32<32>(tS + 32, p);
+        } else {
+          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, over);
+          m = r.x;
+          neg = r.y;
+          l = r.z;
+        }
+        tmem_st_wait();
+        fence_before();
+        mbar_arrive(p_full + 8 * t);
+      }
+      if (!ok) break;
+      // ---- the item's rows
+      if (nb > 0) {
+        if (!wait_warp(ctl, o_full + 8 * t, oc & 1, kDevTimeoutEpilogue)) break;
+        ++oc;
+        fence_after();
+      }
+      uint32_t nan = 0;                                       // groups of columns whose NaN was taken out of the products
+      if (nb > 0 && live)
+        for (int i = 0; i < 4; ++i)
+          if (s_bad[4 * slot + i] <= limit) nan |= 1u << (ND == 2 ? i >> 1 : 0);
+      const uint32_t src = nb > 0 ? tO : 0xFFFFFFFFu;
+      if (pos_lo < g.pos && t * g.pos + pos_lo < it.rows) {   // a row of the warp exists
+        if (it.part >= 0) {
+          store_part<D>(g.part + ((int64_t)it.part * 2 + t) * part_floats<D>(), src, nb > 0 ? m : -INFINITY, l, row, nan);
+        } else {
+          // no visible key: zeros; logits that are all -inf: NaN (else l is 1 or more, from its reference)
+          const float inv = l != 0.f ? __fdividef(1.f, l) : limit < 0 ? 0.f : NAN;
+          write_rows<D>(g, g.out + it.b * g.o_sb + (int64_t)(it.q0 + t * g.pos) * g.o_st + (int64_t)it.h * g.o_sh,
+                        min(g.pos, it.rows - t * g.pos), src, inv, sOut + warp * kStageOut, row, nan);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 8 && lane == 0) {
+      // ------------------------------------------------ copies: pages of codes, queries
+      bool ok = true;
+      int2 cut = make_int2(-1, 0);
+      int i = run.row[0];
+      int64_t xr = x0 < x1 ? run.start[0] : x1;
+      uint32_t n = 0;
+      for (; ok && !*abort_flag; ++n) {
+        const int slot = n % kItemRing;
+        if (!wait_bar(ctl, item_empty + 8 * slot, ((n / kItemRing) & 1) ^ 1, kDevTimeoutTmaProducer)) break;
+        Unit u;
+        int64_t sa = 0, sb = 0;
+        while (xr < x1) {                         // the next unit with work in this run
+          u = unit_of(g, i);
+          sa = xr > x0 ? xr : x0;
+          sb = xr + u.nb < x1 ? xr + u.nb : x1;
+          if (sa < sb) break;
+          xr += u.nb;
+          ++i;
+        }
+        if (xr >= x1) {
+          s_items[slot].unit = -1;
+          mbar_arrive(item_full + 8 * slot);
+          break;
+        }
+        const int b0 = (int)(sa - xr), nb = (int)(sb - sa);
+        const bool whole = nb == u.nb;
+        Item it;
+        it.unit = i;
+        it.b = u.b;
+        it.h = u.h;
+        it.q0 = u.q0;
+        it.rows = u.rows;
+        it.limit = u.limit - b0 * kTile;
+        it.tk = u.tk - b0 * kTile;
+        it.nb0 = min(max(u.nb0 - b0, 0), nb);
+        it.nb1 = min(max(u.nb1 - b0, 0), nb);
+        it.nb = nb;
+        it.low = max(it.limit + 1, 0) / kTile;
+        it.part = whole ? -1 : 2 * (int)blockIdx.x + (b0 > 0 ? 0 : 1);
+        if (!whole && b0 == 0) cut = make_int2(i, decode::last_of(plan, xr, u.nb));
+        const int* from = (const int*)&it;
+        volatile int* to = (volatile int*)&s_items[slot];
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(Item) / 4); ++k) to[k] = from[k];
+        mbar_arrive(item_full + 8 * slot);
+        auto load_q = [&]() {
+          const int tiles = it.rows > g.pos ? 2 : 1;
+          mbar_expect_tx(q_full, tiles * ND * g.gp * g.pos * 128);
+          for (int x = 0; x < tiles * ND; ++x)
+            tma_load_4d(smem_u32(sQ) + x * kKPanel, &qmap, q_full, 64 * (x % ND), it.h, it.q0 + x / ND * g.pos, it.b);
+          ++q_loaded;
+        };
+        const int pages_held = decode::pages_of(u.tk);
+        const int32_t* row_table = g.table + (int64_t)u.row * g.c.max_pages;
+        int64_t page[2] = {0, 0};
+        int pages = 0;
+        for (int b = 0; b < 2 * nb && ok; ++b) {
+          if (b == 2) {
+            // the queries after the first K and V blocks: the last item's products still read the old ones
+            ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
+            if (!ok) break;
+            load_q();
+          }
+          if ((b & 1) == 0) {
+            const int j = 2 * (b0 + nb - 1 - (b >> 1));       // the block's first page in the row
+            pages = min(2, pages_held - j);
+            for (int k = 0; k < pages; ++k) page[k] = safe_page(row_table[j + k], g.c.n_pages);
+          }
+          const int st = loaded % kPacked;
+          ok = wait_bar(ctl, packed_empty + 8 * st, ((loaded / kPacked) & 1) ^ 1, kDevTimeoutTmaProducer);
+          if (!ok) break;
+          const uint32_t bar = packed_full + 8 * st;
+          mbar_expect_tx(bar, pages * kHalf);
+          for (int k = 0; k < pages; ++k)
+            bulk_load(smem_u32(sP) + st * kPackedBytes + k * kHalf, g.pages + page[k] * q4_page_bytes(ND) + (b & 1) * kHalf, kHalf, bar);
+          ++loaded;
+        }
+        if (ok && nb == 1) {                      // an item of one block: its queries come last
+          ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
+          if (!ok) break;
+          load_q();
+        }
+        xr += u.nb;
+        ++i;
+      }
+      g.cut[blockIdx.x] = cut;
+    } else if (warp == 9 || warp == 10) {
+      // ------------------------------------------------ MMA issuer of one tile (the whole warp, one elected lane at an issue)
+      const int t = warp - 9;
+      uint32_t qc = 0, pc = 0, tc = 0;            // query loads, P tiles, turns
+      int st = 0;                                 // stage in turn and its parity
+      uint32_t ph = 0;
+      const uint32_t tS = tmem + t * kTile, tO = tmem + 256 + t * kTile;
+      const uint64_t qdesc = sw128_desc(smem_u32(sQ) + t * kBlock, 16, 1024);
+      const uint64_t kvdesc = sw128_desc(smem_u32(sKV), 16, 1024);
+      // S = Q K^T for the K block in stage sk, O += P V for the V block in stage sv; the stages are released
+      // with the products that read them
+      auto scores = [&](int sk, bool pass) {
+        const uint64_t kd = kvdesc + sk * (kBlock >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kKPanel + (kk & 3) * 32) >> 4;
+          mma_ss(tS, qdesc + off, kd + off, idesc<kTile>(), kk > 0);
+          if (kk == D / 16 - 3 && pass) mbar_arrive(turn + 8 * (t ^ 1));
+        }
+        commit(s_full + 8 * t);
+        commit(kv_empty + 8 * sk);
+      };
+      auto values = [&](int sv, bool add) {
+        const uint64_t vd = kvdesc + sv * (kBlock >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tO, tS + 8 * kk, vd + (((kk >> 2) * kVPanel + (kk & 3) * 32) >> 4), idesc<D>(), add || kk > 0);
+        commit(kv_empty + 8 * sv);
+      };
+      // a block that this tile does not need: released only once it is there, so that the
+      // release counts for this use of the stage
+      auto skip = [&](int sx) { if (lane == 0) mbar_arrive(kv_empty + 8 * sx); };
+      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1; } };
+      for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
+        const int slot = n % kItemRing;
+        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
+        struct { int unit, nb, nb0, nb1; } it;
+        it.unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
+        it.nb = __shfl_sync(0xffffffffu, s_items[slot].nb, 0);
+        it.nb0 = __shfl_sync(0xffffffffu, s_items[slot].nb0, 0);
+        it.nb1 = __shfl_sync(0xffffffffu, s_items[slot].nb1, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+        if (it.unit < 0) break;
+        const int nb = t ? it.nb1 : it.nb0;
+        bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma);
+        if (!ok) break;
+        ++qc;
+        fence_after();
+        if (it.nb - 1 < nb) {
+          if (elect_one()) {
+            scores(st, false);
+            if (it.nb == 1) commit(q_empty);
+          }
+        } else {
+          skip(st);
+        }
+        __syncwarp();
+        next();
+        for (int j = it.nb - 1; j >= 0; --j) {
+          // V of this block and K of the one below it, and then P: nothing is waited for between the products
+          const int sv = st;
+          ok = wait_warp(ctl, kv_full + 8 * sv, ph, kDevTimeoutMma);
+          next();
+          const int sk = st;
+          if (ok && j >= 1) {
+            ok = wait_warp(ctl, kv_full + 8 * sk, ph, kDevTimeoutMma);
+            next();
+          }
+          if (!ok) break;
+          if (j < nb) {
+            // the two tiles take turns, tile 0 first
+            const bool both = j < min(it.nb0, it.nb1);
+            if (both) {
+              ok = wait_warp(ctl, turn + 8 * t, (tc & 1) ^ (t ^ 1), kDevTimeoutMma);
+              ++tc;
+            }
+            ok = ok && wait_warp(ctl, p_full + 8 * t, pc & 1, kDevTimeoutMma);
+            if (!ok) break;
+            ++pc;
+            fence_after();
+            if (elect_one()) {
+              values(sv, j < nb - 1);
+              if (j >= 1) {
+                scores(sk, both);
+              } else {
+                if (both) mbar_arrive(turn + 8 * (t ^ 1));
+                commit(o_full + 8 * t);
+              }
+              if (j == 1) commit(q_empty);        // the queries have been read
+            }
+          } else {
+            skip(sv);
+            if (j >= 1 && j - 1 < nb) {
+              fence_after();
+              if (elect_one()) {
+                scores(sk, false);
+                if (j == 1) commit(q_empty);
+              }
+            } else if (j >= 1) {
+              skip(sk);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (nb == 0 && lane == 0) mbar_arrive(q_empty);
+        __syncwarp();
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    // ------------------------------------------------ conversion: warp w takes page w & 1 of a block, and half of its tokens
+    // (keys) or of its columns (values)
+    const int w = warp - 12, page = w & 1, part = w >> 1;
+    uint32_t pc = 0;                              // halves of blocks so far
+    int st = 0;
+    uint32_t ph = 0;
+    for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
+      const int slot = n % kItemRing;
+      if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+      const int unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
+      if (unit < 0) break;
+      const int nb = s_items[slot].nb, low = s_items[slot].low, tk = s_items[slot].tk;
+      int bad = kNever;
+      bool ok = true;
+      for (int b = 0; b < 2 * nb && ok; ++b) {
+        const int j = nb - 1 - (b >> 1), ps = pc % kPacked;
+        ok = wait_warp(ctl, packed_full + 8 * ps, (pc / kPacked) & 1, kDevTimeoutEpilogue) &&
+             wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
+        if (!ok) break;
+        const uint8_t* src = sP + ps * kPackedBytes + page * kHalf;
+        uint8_t* dst = sKV + st * kBlock;
+        if ((b & 1) == 0) {
+          expand_keys<ND>(src, dst, page * kPage, 32 * part, lane);
+        } else if (j < low) {
+          expand_values<ND, false>(src, dst + page * kVPanel, 2 * ND * part, 0, lane);
+        } else {
+          // a later block's tokens come first: the smallest is kept
+          const int at = j * kTile + page * kPage;
+          const int x = expand_values<ND, true>(src, dst + page * kVPanel, 2 * ND * part, tk - at, lane);
+          if (x != kNever) bad = min(bad, at + x);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");          // the products read it next
+        if (b == 2 * nb - 1) {
+          bad = __reduce_min_sync(0xffffffffu, bad);
+          if (lane == 0) s_bad[4 * slot + w] = bad;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv_full + 8 * st);
+          mbar_arrive(packed_empty + 8 * ps);
+        }
+        ++pc;
+        if (++st == kStages) { st = 0; ph ^= 1; }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+    }
+  }
+
+  // ------------------------------------------------ teardown
+  __syncwarp();
+  pdl_trigger();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (*abort_flag) {
+    bool landed = true;
+    if (warp == 8 && lane == 0) {
+      for (uint32_t i = loaded > kPacked ? loaded - kPacked : 0; i < loaded; ++i)
+        landed &= drain_phase(packed_full + 8 * (i % kPacked), (i / kPacked) & 1);
+      if (q_loaded > 0) landed &= drain_phase(q_full, (q_loaded - 1) & 1);
+    }
+    if (warp == 9 || warp == 10) {
+      const uint32_t bar = drained + 8 * (warp - 9);
+      if (elect_one()) commit(bar);
+      __syncwarp();
+      landed &= drain_phase(bar, 0);
+    }
+    if (!landed) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < kDrainCycles) {
+      }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// The parts of a cut unit's tile together: 32 columns of its 128 rows per CTA, two warps for 32 rows
+// (16 columns each), a lane per row; the parts are added in order.
+template <int ND>
+__global__ void __launch_bounds__(256)
+q4_join_kernel(const __grid_constant__ Q4TcGeom g) {
+  constexpr int D = 64 * ND;
+  __shared__ __align__(16) uint8_t rows[kTile * 80];          // 64 bytes a row, 80 apart
+  pdl_wait();
+  const int2 cut = g.cut[blockIdx.x];
+  const int t = blockIdx.y & 1, c0 = (blockIdx.y >> 1) * 32;
+  if (cut.x >= 0 && c0 < g.c.d) {
+    const Unit u = unit_of(g, cut.x);
+    const int left = min(g.pos, u.rows - t * g.pos);          // positions of the tile that exist
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, c = c0 + (warp >> 2) * 16;
+    const int pos_lo = (((warp & 3) * 32) * g.inv_gp) >> 16;
+    if (left > 0 && pos_lo < left) {                          // the warp has a row that exists
+      auto part = [&](int k) { return g.part + ((int64_t)(2 * k + (k == (int)blockIdx.x)) * 2 + t) * part_floats<D>(); };
+      float M = -INFINITY, L = 0.f, o[16];
+#pragma unroll 8
+      for (int k = blockIdx.x; k <= cut.y; ++k) M = fmaxf(M, __ldcg(part(k) + kTile * D + row));
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
+      for (int k = blockIdx.x; k <= cut.y; ++k) {
+        const float* p = part(k);
+        const float m = __ldcg(p + kTile * D + row), l = __ldcg(p + kTile * D + kTile + row);
+        if (m == -INFINITY && l == 0.f) continue;             // no key of the row: its O may not be there
+        const float f = ex2((m - ref) * g.alpha - residual(m, g.alpha));
+        p += (warp & 3) * (D * 32) + c * 32 + lane;
+        L = fmaf(l, f, L);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i), f, o[i]);
+      }
+      // no visible key: zeros; logits that are all -inf: NaN
+      const float inv = L != 0.f ? 1.f / L : u.limit + t * g.pos + ((row * g.inv_gp) >> 16) < 0 ? 0.f : NAN;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] *= inv;
+      put8(rows + row * 80 + (warp >> 2) * 32, o);
+      put8(rows + row * 80 + (warp >> 2) * 32 + 16, o + 8);
+    }
+    __syncthreads();
+    __nv_bfloat16* out = g.out + u.b * g.o_sb + (int64_t)(u.q0 + t * g.pos) * g.o_st + (int64_t)u.h * g.o_sh;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 64 + (threadIdx.x >> 2), k = threadIdx.x & 3, pos = (r * g.inv_gp) >> 16;
+      if (pos < left && c0 + k * 8 < g.c.d) put_row(g, out, pos, r - pos * g.gp, c0 + k * 8, *(const uint4*)(rows + r * 80 + k * 16));
+    }
+  }
+  pdl_trigger();
+}
+
+// ---------------------------------------------------------------- host side
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = (EncodeFn)p;
+  });
+  return fn;
+}
+
+template <int ND>
+cudaError_t launch(const CUtensorMap& map, const Q4TcGeom& g, int32_t* err, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(q4_attention_tc_kernel<ND>, smem_bytes<ND>(), done);
+  if (e != cudaSuccess) return e;
+  const cudaError_t run = launch_pdl(q4_attention_tc_kernel<ND>, dim3(sms), dim3(kThreads), (size_t)smem_bytes<ND>(), s, map, g, err);
+  if (run != cudaSuccess) return run;
+  return launch_pdl(q4_join_kernel<ND>, dim3(sms, 4 * ND), dim3(256), 0, s, g);
+}
+
+constexpr size_t kCutBytes = 4096;                // [CTAs] int2
+constexpr int kMaxCtas = kCutBytes / sizeof(int2);
+
+}  // namespace
+
+// Units of a call.
+int64_t q4_tc_units(const Q4Geom& g, int G, int n_q) {
+  const int gp = prefill_tc_heads(G), positions = 2 * (kTile / gp);
+  return (int64_t)g.rows * (G / gp) * (((int64_t)n_q + positions - 1) / positions);
+}
+
+// [serving header | cut units | parts].
+size_t q4_tc_workspace_bytes(const Q4Geom& g, int sms) {
+  sms = std::min(sms, kMaxCtas);
+  return kServeHeader + kCutBytes + (size_t)sms * 4 * (g.d64 == 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
+}
+
+cudaError_t launch_q4_attention_tc(const Q4Geom& c, int G, int n_q, float alpha, const int32_t* q_lens, const void* q,
+                                   int64_t q_sb, int64_t q_st, int64_t q_sh, void* out, int64_t o_sb, int64_t o_st,
+                                   int64_t o_sh, const uint8_t* pages, const int32_t* table, const int32_t* lens, void* ws,
+                                   int sms, cudaStream_t s) {
+  const EncodeFn enc = encode_fn();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const int gp = prefill_tc_heads(G), B = c.rows / c.Hkv, pos = kTile / gp;
+  // [B][n_q][Hq][d] in boxes of 64 columns of a tile's heads and positions; columns past d and positions past the end
+  // read as zeros.  The stride of an axis of extent 1 is unused.
+  CUtensorMap map;
+  cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.Hkv * G, (cuuint64_t)n_q, (cuuint64_t)B};
+  cuuint64_t strides[3] = {c.Hkv * G == 1 ? 16 : (cuuint64_t)q_sh * 2, n_q == 1 ? 16 : (cuuint64_t)q_st * 2, B == 1 ? 16 : (cuuint64_t)q_sb * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)gp, (cuuint32_t)pos, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  char* w = (char*)ws;
+  Q4TcGeom g = {};
+  g.c = c;
+  g.G = G;
+  g.n_q = n_q;
+  g.gp = gp;
+  g.inv_gp = (65536 + gp - 1) / gp;
+  g.pos = pos;
+  g.per_kv = G / gp;
+  g.upr = (n_q + 2 * pos - 1) / (2 * pos);
+  g.units = (int32_t)q4_tc_units(c, G, n_q);
+  g.alpha = alpha;
+  g.o_sb = o_sb;
+  g.o_st = (int32_t)o_st;
+  g.o_sh = (int32_t)o_sh;
+  g.timeout = 4000000000LL;
+  g.q_lens = q_lens;
+  g.pages = pages;
+  g.table = table;
+  g.lens = lens;
+  g.out = (__nv_bfloat16*)out;
+  g.cut = (int2*)(w + kServeHeader);
+  g.part = (float*)(w + kServeHeader + kCutBytes);
+  sms = std::min(sms, kMaxCtas);
+  return c.d64 == 64 ? launch<1>(map, g, (int32_t*)w, sms, s) : launch<2>(map, g, (int32_t*)w, sms, s);
+}
+
+}  // namespace chunkkv

@@ -44,6 +44,12 @@ cudaError_t launch_q4_attention(const Q4Geom& g, bool bf16, int G, int n_q, floa
                                 int64_t q_sb, int64_t q_st, int64_t q_sh, void* out, int64_t o_sb, int64_t o_st,
                                 int64_t o_sh, const uint8_t* pages, const int32_t* table, const int32_t* lens, void* ws,
                                 int sms, cudaStream_t s);
+int64_t q4_tc_units(const Q4Geom& g, int G, int n_q);                                         // q4_attention_tc.cu
+size_t q4_tc_workspace_bytes(const Q4Geom& g, int sms);
+cudaError_t launch_q4_attention_tc(const Q4Geom& c, int G, int n_q, float alpha, const int32_t* q_lens, const void* q,
+                                   int64_t q_sb, int64_t q_st, int64_t q_sh, void* out, int64_t o_sb, int64_t o_st,
+                                   int64_t o_sh, const uint8_t* pages, const int32_t* table, const int32_t* lens, void* ws,
+                                   int sms, cudaStream_t s);
 
 namespace {
 
@@ -157,12 +163,13 @@ void plan_items(const chunkkv_prefill_params* p, int sms, int* kb, int64_t* n_it
   }
 }
 
+// An axis that a tensor map can address.
+bool axis(int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < (int64_t)1 << 39); }
+
 // The tensor-core kernel: bf16 rows of up to 128 columns that tensor maps can address (no axis
 // longer than 1 with stride 0, strides below 2^40 bytes), a tile of the output within 2^31 elements,
 // and a key to attend to.
 bool prefill_on_tc(const chunkkv_prefill_params* p) {
-  const int64_t most = (int64_t)1 << 39;
-  auto axis = [most](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < most); };
   return p->dtype == CHUNKKV_BF16 && p->d <= 128 && p->B > 0 && p->cu_k[p->B] > 0 &&
          axis(p->q_stride_t, p->cu_q[p->B]) && axis(p->q_stride_h, p->Hq) && axis(p->kv_stride_t, p->cu_k[p->B]) &&
          axis(p->kv_stride_h, p->Hkv) && p->o_stride_t < (1 << 22) && p->o_stride_h < (1 << 22);
@@ -176,6 +183,18 @@ bool device_pointer(const void* p) {
     return false;
   }
   return a.type == cudaMemoryTypeDevice;
+}
+
+// Query rows of a KV head up to which the 4-bit cache's attention takes the kernel for few rows: a pass of it.
+constexpr int64_t kFewRows = 16;
+
+// The 4-bit cache's attention on the tensor cores' own path: bf16, up to 128 columns, more rows than a pass of the other.
+bool q4_many_rows(const Q4Geom& g, int dtype, int32_t G, int32_t n_q) {
+  return dtype == CHUNKKV_BF16 && g.d <= 128 && (int64_t)G * n_q > kFewRows && q4_tc_units(g, G, n_q) <= INT32_MAX / 2;
+}
+size_t q4_workspace(const Q4Geom& g, int dtype, int32_t G, int32_t n_q) {
+  const size_t few = q4_workspace_bytes(g, dtype == CHUNKKV_BF16, G, n_q, sm_count());
+  return q4_many_rows(g, dtype, G, n_q) ? std::max(few, q4_tc_workspace_bytes(g, sm_count())) : few;
 }
 
 template <int MAXB>
@@ -399,14 +418,14 @@ chunkkv_status chunkkv_q4_workspace_size(const chunkkv_q4_cache* c, int32_t dtyp
   if (st != CHUNKKV_OK) return st;
   if (bytes == nullptr || !valid_dtype(dtype) || G < 1 || n_q < 1) return CHUNKKV_ERR_INVALID_ARG;
   if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
-  *bytes = q4_workspace_bytes(g, dtype == CHUNKKV_BF16, G, n_q, sm_count());
+  *bytes = q4_workspace(g, dtype, G, n_q);
   return CHUNKKV_OK;
 }
 
 int32_t chunkkv_q4_path(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q) {
   Q4Geom g;
   if (check_cache(c, false, &g) != CHUNKKV_OK || !valid_dtype(dtype) || G < 1 || n_q < 1 || !rows_ok(G, n_q)) return -1;
-  return 0;
+  return q4_many_rows(g, dtype, G, n_q) ? 1 : 0;
 }
 
 chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q,
@@ -425,10 +444,17 @@ chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, in
   if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
   if (g.rows == 0) return CHUNKKV_OK;
   if (!aligned(q) || !aligned(out) || !aligned(ws) || (q_lens != nullptr && !aligned(q_lens, 4))) return CHUNKKV_ERR_INVALID_ARG;
-  if (ws_bytes < q4_workspace_bytes(g, dtype == CHUNKKV_BF16, G, n_q, sm_count())) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
-  return cuda_result(launch_q4_attention(g, dtype == CHUNKKV_BF16, G, n_q, (float)(scale * kLog2e), q_lens, q, q_stride_b,
-                                         q_stride_t, q_stride_h, out, o_stride_b, o_stride_t, o_stride_h, c->pages,
-                                         c->table, c->lens, ws, sm_count(), (cudaStream_t)stream));
+  if (ws_bytes < q4_workspace(g, dtype, G, n_q)) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;
+  const float alpha = (float)(scale * kLog2e);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  // rows that no tensor map can address take the other kernel
+  if (q4_many_rows(g, dtype, G, n_q) && axis(q_stride_b, c->B) && axis(q_stride_t, n_q) && axis(q_stride_h, c->Hkv * (int64_t)G) &&
+      o_stride_t < (1 << 22) && o_stride_h < (1 << 22) && device_pointer(q))
+    return cuda_result(launch_q4_attention_tc(g, G, n_q, alpha, q_lens, q, q_stride_b, q_stride_t, q_stride_h, out, o_stride_b,
+                                              o_stride_t, o_stride_h, c->pages, c->table, c->lens, ws, sm_count(), cs));
+  return cuda_result(launch_q4_attention(g, dtype == CHUNKKV_BF16, G, n_q, alpha, q_lens, q, q_stride_b, q_stride_t,
+                                         q_stride_h, out, o_stride_b, o_stride_t, o_stride_h, c->pages, c->table, c->lens, ws,
+                                         sm_count(), cs));
 }
 
 }  // extern "C"
