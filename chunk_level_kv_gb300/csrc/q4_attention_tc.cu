@@ -1,31 +1,42 @@
 // Attention of many query rows over the 4-bit paged cache on the tensor cores (tcgen05 + TMA +
 // TMEM): bf16, head dimension up to 128.
 //
-//   O_i = sum_{j < n - m + 1 + i} softmax_j(scale q_i . k_j) v_j,   k_j and v_j = s c + m, rounded to bf16
+//   O_i = sum_{j < n - m + 1 + i} softmax_j(scale q_i . k_j) v_j,   k_j and v_j = s c + m
 //
 // for the m query tokens at the end of a cache row of n tokens.  The products, the tiles and the
-// softmax are those of the attention over packed prompts (prefill_tc.cu): two tiles of 128 query
-// rows (the gp query heads of a KV head at 128 / gp consecutive positions) against blocks of 128
-// keys, S and O in TMEM, one thread per row.  What differs:
+// order of work are those of the attention over packed prompts (prefill_tc.cu): two tiles of 128
+// query rows (the gp query heads of a KV head at 128 / gp consecutive positions) against blocks of
+// 128 keys from the last one down, S and O in TMEM, one thread per row.  What differs:
 //
+// - Operands are f16 (11 bits; in bf16 the rounding of the keys, the values and the weights made
+//   the output's error 3 times that of its own rounding).  f16's range is kept by powers of two: a
+//   query row is scaled by its largest element, a block's keys and its values by theirs (2^EK
+//   and 2^EV; one warp looks them up in the pages' steps), so what a block holds below 2^-29 of its
+//   largest value loses bits, and below 2^-40 is lost.  The scales leave again through the
+//   exponent: a weight is P = 2^(S alpha 2^EK + EV - Z) with the row's reference Z, so O gathers
+//   2^-Z V with every block's V at its own scale, and a block whose values are huge under
+//   negligible weights costs the others nothing.
 // - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
 //   four converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
 //   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
 //   consecutive bytes of a K-major operand: V is stored as V^T, and both products take both
-//   operands K-major.  128 + c is a bf16 number with c as its last bits; less 128 it is c, and
-//   one packed FMA makes s c + m of it, rounded once: 16 instructions for 8 codes.  At 128 columns
-//   these are 550 instructions a block and warp, next to 2048 cycles of products for two tiles.
+//   operands K-major.  1024 + c is an f16 number with c as its last bits; less 1024 it is c, and
+//   one packed FMA makes s c + m of it, rounded once: 16 instructions for 8 codes.
 // - The lengths are in device memory.  Work is counted in (two tiles, block) pairs; every CTA
 //   takes an equal run of them (plan_run of decode.cuh), so that few rows against many keys
-//   keep every SM busy.  Of query tiles whose keys are cut, the CTAs write parts (m, l, O), and a
+//   keep every SM busy.  Of query tiles whose keys are cut, the CTAs write parts (Z, l, O), and a
 //   second launch joins them in order, 32 columns of 128 rows per CTA.
 // - What a row must not see: S is set to -inf as for prompts.  A value can only be non-finite
 //   as a group's m = NaN; where some row of the item does not see it, the converting warps
 //   replace it by zero and note the first such token of each group of columns, and a row that
 //   sees that token gets NaN there.
 //
+// A row's reference Z is a whole number near its first logits (plus EV, less kLift) and stays while
+// a block's sum of weights is below kMost, which f16 holds; a block that passes it is done over
+// from its own maximum.  The lift keeps weights down to 2^-18 of the reference's at full precision.
+//
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
-// 12-15 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+// 11 scales, 12-15 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,6 +64,13 @@ constexpr int kSoftmaxRegs = 192, kIssueRegs = 48, kConvertRegs = 80;
 static_assert(kIssueRegs < 128 && kConvertRegs < 128, "of the launch's 128 a thread");
 static_assert(256 * kSoftmaxRegs + 128 * (kIssueRegs + kConvertRegs) <= kThreads * 128, "register shares within the launch's");
 constexpr int kNever = 0x7FFFFFFF;
+constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
+constexpr int kScaledRing = 4;                    // of them, those that the conversion may still wait for
+constexpr float kMost = 65000.f;                  // bound of a block's sum of weights: f16 ends at 65504
+constexpr float kLift = 4.f;                      // a row's first weight is about 2^4
+constexpr int kTopExp = 14;                       // the largest element of an operand is in [2^14, 2^15)
+constexpr float kBack = 262144.f;                 // 2^(kSumExp - kTopExp): O over l back to its size
+constexpr int kSumExp = 32;                       // l gathers 2^(kSumExp - Z) times the weights: far from both ends of fp32
 
 template <int ND> constexpr int block_bytes() { return kTile * 64 * ND * 2; }
 template <int ND> constexpr int packed_bytes() { return 2 * q4_v(ND); }           // the halves of two pages
@@ -62,10 +80,10 @@ constexpr int kControl = 1024;
 template <int ND> constexpr int smem_bytes() {
   return (2 + kStages) * block_bytes<ND>() + kPacked * packed_bytes<ND>() + 8 * kStageOut + kControl;
 }
-// A tile's part: O as [4 warps][D columns][32 lanes], then the rows' m and l.
+// A tile's part: O as [4 warps][D columns][32 lanes], then the rows' Z and l.
 template <int D> constexpr int part_floats() { return kTile * (D + 2); }
-template <int N> constexpr uint32_t idesc() {     // fp32 D, bf16 A and B, M = 128
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+template <int N> constexpr uint32_t idesc() {     // fp32 D, f16 A and B, M = 128
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
 struct Q4TcGeom {
@@ -167,9 +185,9 @@ __device__ __noinline__ void write_rows(const Q4TcGeom& g, __nv_bfloat16* out, i
 }
 
 // A warp's rows of a tile's part to the workspace, a lane per row: whole lines per column.  tO: 0xFFFFFFFF where the part
-// holds no key of the tile (m = -inf and l = 0 say so).
+// holds no key of the tile (Z = -inf and l = 0 say so).
 template <int D>
-__device__ __noinline__ void store_part(float* part, uint32_t tO, float m, float l, int row, uint32_t nan) {
+__device__ __noinline__ void store_part(float* part, uint32_t tO, float Z, float l, int row, uint32_t nan) {
   float* po = part + (row >> 5) * (D * 32) + (row & 31);
   if (tO != 0xFFFFFFFFu) {
 #pragma unroll 1
@@ -181,39 +199,146 @@ __device__ __noinline__ void store_part(float* part, uint32_t tO, float m, float
       for (int i = 0; i < 16; ++i) __stcg(po + (c + i) * 32, bad ? NAN : o[i]);
     }
   }
-  __stcg(part + kTile * D + row, m);
+  __stcg(part + kTile * D + row, Z);
   __stcg(part + kTile * D + kTile + row, l);
 }
 
-// Eight codes of a word (items 0 .. 7 in order) to eight bf16, s c + m each; s and m of items 2 k, 2 k + 1 in pairs.
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *(const uint32_t*)&h;
+}
+// A group's m and s (two bf16 in a word), scaled, as two f16.
+__device__ __forceinline__ uint32_t scaled(uint32_t w, float by) { return pack_half2(q4_m(w) * by, q4_s(w) * by); }
+
+// Eight codes of a word (items 0 .. 7 in order) to eight f16, s c + m each; s and m of items 2 k, 2 k + 1 in pairs (of odd
+// k, s / 16: those codes are taken 4 bits higher).
 __device__ __forceinline__ uint4 expand(uint32_t w, const uint32_t (&s)[4], const uint32_t (&m)[4]) {
-  const __nv_bfloat162 big = __halves2bfloat162(__ushort_as_bfloat16(0x4300), __ushort_as_bfloat16(0x4300));
+  const __half2 big = __halves2half2(__ushort_as_half(0x6400), __ushort_as_half(0x6400));
+  const uint32_t u = w >> 8;
+  const uint32_t a[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, (u & 0x000F000Fu) | 0x64006400u,
+                         (u & 0x00F000F0u) | 0x64006400u};
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t a = (w >> (4 * k) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 x = __hfma2(__hsub2(*(const __nv_bfloat162*)&a, big), *(const __nv_bfloat162*)&s[k], *(const __nv_bfloat162*)&m[k]);
+    const __half2 x = __hfma2(__hsub2(*(const __half2*)&a[k], big), *(const __half2*)&s[k], *(const __half2*)&m[k]);
     o[k] = *(const uint32_t*)&x;
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+__device__ __forceinline__ uint32_t sixteenth(uint32_t s) {
+  const __half2 x = __hmul2(*(const __half2*)&s, __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00)));
+  return *(const uint32_t*)&x;
+}
+
+// The largest magnitude that codes of a group can stand for (NaN: the other argument).
+__device__ __forceinline__ float reach(uint32_t w, float most) {
+  const float m = q4_m(w);
+  return fmaxf(most, fmaxf(fabsf(m), fabsf(fmaf(15.f, q4_s(w), m))));
+}
+// Of the halves of two pages: a lane's share, over tokens below `left`.
+template <int ND>
+__device__ __forceinline__ float reach_of(const uint8_t* half2, int left, int lane) {
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < ND; ++i) {
+    const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;    // words [ND][64] of each page
+    const uint4 w = *(const uint4*)(half2 + page * q4_v(ND) + 2048 * ND + at * 4);
+    const int token = page * kPage + (at & (kPage - 1));
+    if (token + 3 < left) {
+      most = reach(w.x, reach(w.y, reach(w.z, reach(w.w, most))));
+    } else {
+      if (token < left) most = reach(w.x, most);
+      if (token + 1 < left) most = reach(w.y, most);
+      if (token + 2 < left) most = reach(w.z, most);
+    }
+  }
+  return most;
+}
+// A block's scales: what the keys and the values were multiplied by, and what takes it back.
+struct Scales {
+  float k_down, v_down;                           // 2^(kTopExp - E)
+  float k_up;                                     // 2^(EK - kTopExp)
+  float ev, sum_up;                               // EV, and 2^(kSumExp - EV)
+};
+
+// A query row in shared memory (ND panels of 64 columns, 16-byte pieces swizzled) from bf16 to f16, its largest element in
+// [2^kTopExp, 2^(kTopExp + 1)); returns the exponent that takes it back.
+template <int ND>
+__device__ __noinline__ int narrow_row(uint8_t* tile, int row) {
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int i = 0; i < 8 * ND; ++i) {
+    const uint4 w = *(const uint4*)(tile + (i >> 3) * (kTile * 128) + row * 128 + ((i ^ row) & 7) * 16);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(x[e] << 16 & 0x7FFF0000u, x[e] & 0x7FFF0000u));
+  }
+  const int e2 = min(127, max(-110, (int)(top >> 23) - 127));
+  const float down = power_of_two(kTopExp - e2);
+#pragma unroll 4
+  for (int i = 0; i < 8 * ND; ++i) {
+    uint4* p = (uint4*)(tile + (i >> 3) * (kTile * 128) + row * 128 + ((i ^ row) & 7) * 16);
+    const uint4 w = *p;
+    *p = make_uint4(scaled(w.x, down), scaled(w.y, down), scaled(w.z, down), scaled(w.w, down));
+  }
+  return e2 - kTopExp;
+}
+
+// The exponentials of a block's sum that passed kMost done over: rows that are `over` move Z to the block's maximum, and
+// what O (at tO, unless it is still empty) and l hold goes with it.  Their differences to the maximum are taken before
+// they are scaled: under a huge Z one rounding of S alpha + EV - Z is off by more than an exponential bears.  The other
+// rows' weights are what they were, and are added in row_exp's order.  Returns (Z, l).
+template <int D>
+__device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha, float ev, float sum_up, float Z, float l, bool over) {
+  const float top = row_max(tS);
+  float base = 0.f, neg = ev - (Z == -INFINITY ? ev : Z), f = 1.f;
+  if (over) {
+    const float zn = rintf(fmaf(top, alpha, ev)) - kLift;
+    f = Z == -INFINITY ? 0.f : ex2(Z - zn);
+    Z = zn;
+    base = top;
+    // top's own exponent, kLift and what Z was rounded by: a later block's terms stand beside these under one Z
+    neg = fminf(fmaxf(fmaf(top, alpha, ev - zn), kLift - 1.f), kLift + 1.f);
+  }
+  if (tO != 0xFFFFFFFFu) {
+    // the blocks before are done: their products were issued before this S
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      tmem_ld32(tO + 32 * c, o);
+      tmem_wait(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] *= f;
+      tmem_st32(tO + 32 * c, o);
+    }
+  }
+  return make_float2(Z, fmaf(write_exp_from<true>(tS, base, alpha, neg), sum_up, l * f));
+}
 
 // Keys of one page, a warp's half of its tokens, into rows of 64 columns (128 bytes, 16-byte pieces swizzled).
 template <int ND>
-__device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, int lane) {
-#pragma unroll 2
+__device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, float by, int lane) {
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int token = first + 8 * i + (lane >> 2), t4 = lane & 3, row = page_row + token;
-    const uint8_t* src = page + (token * 4 + t4) * (8 * ND);
+    uint32_t w[2 * ND];
+    if constexpr (ND == 2) {
+      const uint4 v = *(const uint4*)(page + (token * 4 + t4) * 16);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      const uint2 v = *(const uint2*)(page + (token * 4 + t4) * 8);
+      w[0] = v.x; w[1] = v.y;
+    }
+    uint8_t* dst = tile + row * 128;
+    const int a = ((2 * t4) ^ (row & 7)) * 16, b = ((2 * t4 + 1) ^ (row & 7)) * 16;
 #pragma unroll
     for (int p = 0; p < ND; ++p) {
-      const uint2 w = *(const uint2*)(src + 8 * p);
-      const uint32_t ms = *(const uint32_t*)(page + q4_k_ms(ND) + (p * kPage + token) * 4);
-      const uint32_t s1 = __byte_perm(ms, ms, 0x3232), m1 = __byte_perm(ms, ms, 0x1010);
-      const uint32_t s[4] = {s1, s1, s1, s1}, m[4] = {m1, m1, m1, m1};
-      uint8_t* dst = tile + p * (kTile * 128) + row * 128;
-      *(uint4*)(dst + ((2 * t4) ^ (row & 7)) * 16) = expand(w.x, s, m);
-      *(uint4*)(dst + ((2 * t4 + 1) ^ (row & 7)) * 16) = expand(w.y, s, m);
+      const uint32_t ms = scaled(*(const uint32_t*)(page + q4_k_ms(ND) + (p * kPage + token) * 4), by);
+      const uint32_t s1 = __byte_perm(ms, ms, 0x3232), m1 = __byte_perm(ms, ms, 0x1010), s16 = sixteenth(s1);
+      const uint32_t s[4] = {s1, s16, s1, s16}, m[4] = {m1, m1, m1, m1};
+      *(uint4*)(dst + p * (kTile * 128) + a) = expand(w[2 * p], s, m);
+      *(uint4*)(dst + p * (kTile * 128) + b) = expand(w[2 * p + 1], s, m);
     }
   }
 }
@@ -221,7 +346,7 @@ __device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, 
 // Values of one page, 2 ND tiles of 16 columns from `first` on (all of one group), into rows of 64 tokens.
 // MASKED: tokens from `left` on are zeros, and a NaN is replaced by zero; returns the first token that had one.
 template <int ND, bool MASKED>
-__device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile, int first, int left, int lane) {
+__device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile, int first, int left, float by, int lane) {
   const int t4 = lane & 3, gid = lane >> 2, group = first >> 2;
   uint32_t s[2][4], m[2][4];
   int bad = kNever;
@@ -242,13 +367,16 @@ __device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile,
       }
     }
 #pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = scaled(w[e], by);
+#pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int k = 2 * (x & 1) + y;
       m[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x5410);
       s[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x7632);
+      if (y) s[x >> 1][k] = sixteenth(s[x >> 1][k]);
     }
   }
-#pragma unroll 2
+#pragma unroll 1
   for (int i = 0; i < 2 * ND; ++i) {
     const uint4 w = *(const uint4*)(half + (first + i) * 512 + gid * 64 + t4 * 16);
     uint8_t* dst = tile + (16 * (first + i) + gid) * 128;     // columns 16 i + gid and 8 further: gid is the row in the swizzle
@@ -283,12 +411,14 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages;
   const uint32_t packed_full = kv_empty + 8 * kStages, packed_empty = packed_full + 8 * kPacked;
   const uint32_t item_full = packed_empty + 8 * kPacked, item_empty = item_full + 8 * kItemRing;
-  constexpr int kBars = 6 + 6 + 2 * kStages + 2 * kPacked + 2 * kItemRing;
+  const uint32_t q_ready = item_empty + 8 * kItemRing, scaled_full = q_ready + 16;         // [2], [kScaledRing]
+  constexpr int kBars = 6 + 6 + 2 * kStages + 2 * kPacked + 2 * kItemRing + 2 + kScaledRing;
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile Item* s_items = (volatile Item*)(abort_flag + 1);                               // [kItemRing]
   volatile int* s_bad = (volatile int*)(s_items + kItemRing);      // [kItemRing][4 converting warps]: first NaN token of its group
-  static_assert(8 * kBars + 8 + (sizeof(Item) + 16) * kItemRing <= kControl, "control block");
+  volatile Scales* s_scales = (volatile Scales*)(s_bad + 4 * kItemRing);                  // [kScaleRing]
+  static_assert(8 * kBars + 8 + (sizeof(Item) + 16) * kItemRing + sizeof(Scales) * kScaleRing <= kControl, "control block");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -296,9 +426,11 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
     for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 4); mbar_init(kv_empty + 8 * i, 2); }
-    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, 4); }
-    // an item's slot is released by the MMA issuers, the converting and the softmax warps
-    for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 14); }
+    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, 5); }
+    // an item's slot is released by the MMA issuers, the scaling, the converting and the softmax warps
+    for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 15); }
+    for (int t = 0; t < 2; ++t) mbar_init(q_ready + 8 * t, 128);
+    for (int i = 0; i < kScaledRing; ++i) mbar_init(scaled_full + 8 * i, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&qmap) : "memory");
@@ -337,7 +469,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     const int my_pos = (row * g.inv_gp) >> 16, pos_lo = ((row - lane) * g.inv_gp) >> 16;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = lanes + t * kTile, tO = lanes + 256 + t * kTile;
-    uint32_t sc = 0, oc = 0;                      // phases of s_full and o_full
+    uint32_t sc = 0, oc = 0, qc = 0;              // phases of s_full, o_full and q_full
+    uint32_t before = 0;                          // blocks of the items before
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
       if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
@@ -346,34 +479,42 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       const int nb = t ? it.nb1 : it.nb0;
       const int limit = it.limit + t * g.pos + my_pos;        // last key that this row sees
       const bool live = my_pos < g.pos && t * g.pos + my_pos < it.rows;
-      // the row's reference, -m alpha, and its sum; rows of the tile that do not exist never look for one
-      float m = live ? -INFINITY : 0.f, neg = 0.f, l = 0.f;
+      // ---- the queries as f16
+      if (!wait_warp(ctl, q_full, qc & 1, kDevTimeoutEpilogue)) break;
+      ++qc;
+      float row_alpha = 0.f;
+      if (nb > 0) row_alpha = g.alpha * power_of_two(max(-126, narrow_row<ND>(sQ + t * kBlock, row)));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(q_ready + 8 * t);
+      // the row's reference and its sum; rows of the tile that do not exist never look for one
+      float Z = live ? -INFINITY : 0.f, l = 0.f;
       bool ok = true;
+      const uint32_t first = before + it.nb - 1;              // of block 0
+      before += it.nb;
       for (int j = nb - 1; j >= 0; --j) {
         if (!wait_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
         ++sc;
         fence_after();
+        const volatile Scales& scales = s_scales[(first - j) % kScaleRing];
+        // never 0 (0 x -inf) nor infinite
+        const float alpha = fminf(fmaxf(row_alpha * scales.k_up, 1.2e-38f), 3.4e38f), ev = scales.ev;
         const int seen = limit - j * kTile, lo = seen - (my_pos - pos_lo);       // columns 0 .. seen; the warp's first row's
         if (kTile - 1 > lo) hide(tS, seen, lo);               // a hidden key in the warp
-        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+        if (__any_sync(0xffffffffu, Z == -INFINITY)) {
           const float bm = first_reference(tS, lo);
-          if (m == -INFINITY && bm != -INFINITY) {            // P and O of the row are zero so far
-            m = bm;
-            neg = offset_of(m, g.alpha);
-          }
+          if (Z == -INFINITY && bm != -INFINITY) Z = rintf(fmaf(bm, alpha, ev)) - kLift;     // P and O of the row are zero so far
         }
         uint32_t p[64];
-        const float sum = row_exp(tS, g.alpha, neg, p);
-        const bool over = live && !(l + sum <= kBig);         // a NaN too, as under a huge reference
+        const float sum = row_exp<true>(tS, alpha, Z == -INFINITY ? 0.f : ev - Z, p);
+        const bool over = live && !(sum <= kMost);            // a NaN too
         if (!__any_sync(0xffffffffu, over)) {
-          l += sum;
+          l = fmaf(sum, scales.sum_up, l);
           tmem_st32<0>(tS, p);
           tmem_st32<32>(tS + 32, p);
         } else {
-          const float3 r = block_again<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, g.alpha, m, l, over);
-          m = r.x;
-          neg = r.y;
-          l = r.z;
+          const float2 r = block_over<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, alpha, ev, scales.sum_up, Z, l, over);
+          Z = r.x;
+          l = r.y;
         }
         tmem_st_wait();
         fence_before();
@@ -393,10 +534,10 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       const uint32_t src = nb > 0 ? tO : 0xFFFFFFFFu;
       if (pos_lo < g.pos && t * g.pos + pos_lo < it.rows) {   // a row of the warp exists
         if (it.part >= 0) {
-          store_part<D>(g.part + ((int64_t)it.part * 2 + t) * part_floats<D>(), src, nb > 0 ? m : -INFINITY, l, row, nan);
+          store_part<D>(g.part + ((int64_t)it.part * 2 + t) * part_floats<D>(), src, nb > 0 ? Z : -INFINITY, l, row, nan);
         } else {
-          // no visible key: zeros; logits that are all -inf: NaN (else l is 1 or more, from its reference)
-          const float inv = l != 0.f ? __fdividef(1.f, l) : limit < 0 ? 0.f : NAN;
+          // no visible key: zeros; logits that are all -inf: NaN
+          const float inv = l != 0.f ? kBack / l : limit < 0 ? 0.f : NAN;
           write_rows<D>(g, g.out + it.b * g.o_sb + (int64_t)(it.q0 + t * g.pos) * g.o_st + (int64_t)it.h * g.o_sh,
                         min(g.pos, it.rows - t * g.pos), src, inv, sOut + warp * kStageOut, row, nan);
         }
@@ -539,7 +680,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         if (lane == 0) mbar_arrive(item_empty + 8 * slot);
         if (it.unit < 0) break;
         const int nb = t ? it.nb1 : it.nb0;
-        bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_full, qc & 1, kDevTimeoutMma);
+        bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_ready + 8 * t, qc & 1, kDevTimeoutMma);
         if (!ok) break;
         ++qc;
         fence_after();
@@ -603,6 +744,41 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         if (nb == 0 && lane == 0) mbar_arrive(q_empty);
         __syncwarp();
       }
+    } else if (warp == 11) {
+      // ------------------------------------------------ a block's scales, from the steps and smallest values of its groups
+      uint32_t bc = 0;                            // blocks so far
+      for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
+        const int slot = n % kItemRing;
+        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+        const int unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
+        if (unit < 0) break;
+        const int nb = s_items[slot].nb, tk = s_items[slot].tk;
+        bool ok = true;
+        for (int j = nb - 1; j >= 0 && ok; --j, ++bc) {
+          const uint32_t kp = 2 * bc % kPacked, vp = (2 * bc + 1) % kPacked;
+          ok = wait_warp(ctl, packed_full + 8 * kp, (2 * bc / kPacked) & 1, kDevTimeoutEpilogue) &&
+               wait_warp(ctl, packed_full + 8 * vp, ((2 * bc + 1) / kPacked) & 1, kDevTimeoutEpilogue);
+          if (!ok) break;
+          const int left = tk - j * kTile;        // stale tokens past the row's end have no say
+          const uint32_t kt = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_of<ND>(sP + kp * kPackedBytes, left, lane)));
+          const uint32_t vt = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_of<ND>(sP + vp * kPackedBytes, left, lane)));
+          if (lane == 0) {
+            const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
+            volatile Scales& out = s_scales[bc % kScaleRing];
+            out.k_down = power_of_two(kTopExp - ek);
+            out.v_down = power_of_two(kTopExp - ev);
+            out.k_up = power_of_two(ek - kTopExp);
+            out.ev = (float)ev;
+            out.sum_up = power_of_two(kSumExp - ev);
+            mbar_arrive(scaled_full + 8 * (bc % kScaledRing));
+            mbar_arrive(packed_empty + 8 * kp);
+            mbar_arrive(packed_empty + 8 * vp);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(item_empty + 8 * slot);
+      }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
@@ -622,19 +798,22 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       bool ok = true;
       for (int b = 0; b < 2 * nb && ok; ++b) {
         const int j = nb - 1 - (b >> 1), ps = pc % kPacked;
+        const uint32_t bc = pc >> 1;
         ok = wait_warp(ctl, packed_full + 8 * ps, (pc / kPacked) & 1, kDevTimeoutEpilogue) &&
+             wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue) &&
              wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
         if (!ok) break;
+        const volatile Scales& scales = s_scales[bc % kScaleRing];
         const uint8_t* src = sP + ps * kPackedBytes + page * kHalf;
         uint8_t* dst = sKV + st * kBlock;
         if ((b & 1) == 0) {
-          expand_keys<ND>(src, dst, page * kPage, 32 * part, lane);
+          expand_keys<ND>(src, dst, page * kPage, 32 * part, scales.k_down, lane);
         } else if (j < low) {
-          expand_values<ND, false>(src, dst + page * kVPanel, 2 * ND * part, 0, lane);
+          expand_values<ND, false>(src, dst + page * kVPanel, 2 * ND * part, 0, scales.v_down, lane);
         } else {
           // a later block's tokens come first: the smallest is kept
           const int at = j * kTile + page * kPage;
-          const int x = expand_values<ND, true>(src, dst + page * kVPanel, 2 * ND * part, tk - at, lane);
+          const int x = expand_values<ND, true>(src, dst + page * kVPanel, 2 * ND * part, tk - at, scales.v_down, lane);
           if (x != kNever) bad = min(bad, at + x);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");          // the products read it next
@@ -714,16 +893,16 @@ q4_join_kernel(const __grid_constant__ Q4TcGeom g) {
 #pragma unroll 2
       for (int k = blockIdx.x; k <= cut.y; ++k) {
         const float* p = part(k);
-        const float m = __ldcg(p + kTile * D + row), l = __ldcg(p + kTile * D + kTile + row);
-        if (m == -INFINITY && l == 0.f) continue;             // no key of the row: its O may not be there
-        const float f = ex2((m - ref) * g.alpha - residual(m, g.alpha));
+        const float Z = __ldcg(p + kTile * D + row), l = __ldcg(p + kTile * D + kTile + row);
+        if (Z == -INFINITY && l == 0.f) continue;             // no key of the row: its O may not be there
+        const float f = ex2(Z - ref);
         p += (warp & 3) * (D * 32) + c * 32 + lane;
         L = fmaf(l, f, L);
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i), f, o[i]);
       }
       // no visible key: zeros; logits that are all -inf: NaN
-      const float inv = L != 0.f ? 1.f / L : u.limit + t * g.pos + ((row * g.inv_gp) >> 16) < 0 ? 0.f : NAN;
+      const float inv = L != 0.f ? kBack / L : u.limit + t * g.pos + ((row * g.inv_gp) >> 16) < 0 ? 0.f : NAN;
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] *= inv;
       put8(rows + row * 80 + (warp >> 2) * 32, o);

@@ -9,6 +9,8 @@
 // only after that test.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "tcgen.cuh"
 
 namespace chunkkv {
@@ -68,21 +70,33 @@ static __device__ __noinline__ float first_reference(uint32_t tS, int lo) {
   return m;
 }
 
+// A pair of probabilities as it is written: bf16, or f16 (HALF).
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack_p(float2 w) {
+  if constexpr (HALF) {
+    const __half2 h = __floats2half2_rn(w.x, w.y);
+    return *(const uint32_t*)&h;
+  } else {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
+    return *(const uint32_t*)&b;
+  }
+}
+
 // 32 columns of P from 32 of S: pairs by one packed FMA, two exponentials, a packed sum
 // and a packed conversion.
-template <int C>
+template <int C, bool HALF>
 __device__ __forceinline__ void chunk_exp(const float (&s)[32], float2 a2, float2 n2, float2 (&sum)[2], uint32_t (&p)[64]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), a2, n2);
     const float2 w = make_float2(ex2(e.x), ex2(e.y));
     sum[i & 1] = __fadd2_rn(sum[i & 1], w);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
-    p[16 * C + i] = *(const uint32_t*)&b;
+    p[16 * C + i] = pack_p<HALF>(w);
   }
 }
 // A row's P under the reference -neg, and its sum.  Straight-line code: a branch per
 // chunk cost 400 cycles of a block's 1000.
+template <bool HALF = false>
 __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, uint32_t (&p)[64]) {
   float ra[32], rb[32];
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -90,20 +104,21 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float alpha, float neg, ui
   tmem_ld32(tS, ra);
   tmem_wait(ra);
   tmem_ld32(tS + 32, rb);
-  chunk_exp<0>(ra, a2, n2, sum, p);
+  chunk_exp<0, HALF>(ra, a2, n2, sum, p);
   tmem_wait(rb);
   tmem_ld32(tS + 64, ra);
-  chunk_exp<1>(rb, a2, n2, sum, p);
+  chunk_exp<1, HALF>(rb, a2, n2, sum, p);
   tmem_wait(ra);
   tmem_ld32(tS + 96, rb);
-  chunk_exp<2>(ra, a2, n2, sum, p);
+  chunk_exp<2, HALF>(ra, a2, n2, sum, p);
   tmem_wait(rb);
-  chunk_exp<3>(rb, a2, n2, sum, p);
+  chunk_exp<3, HALF>(rb, a2, n2, sum, p);
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // The same of (S - base) alpha + neg, with P written: its 16 columns of 32 logits lie among the columns read by then.
 // The terms are added in row_exp's order: a row that is here only because another of its warp is keeps its bits.
+template <bool HALF = false>
 __device__ __forceinline__ float write_exp_from(uint32_t tS, float base, float alpha, float neg) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -116,8 +131,7 @@ __device__ __forceinline__ float write_exp_from(uint32_t tS, float base, float a
     for (int i = 0; i < 16; ++i) {
       const float2 w = make_float2(ex2(fmaf(s[2 * i] - base, alpha, neg)), ex2(fmaf(s[2 * i + 1] - base, alpha, neg)));
       sum[i & 1] = __fadd2_rn(sum[i & 1], w);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(w.x, w.y);
-      p[i] = *(const uint32_t*)&b;
+      p[i] = pack_p<HALF>(w);
     }
     tmem_st16(tS + 16 * c, p);
   }
