@@ -17,7 +17,7 @@
 //   2^-Z V with every block's V at its own scale, and a block whose values are huge under
 //   negligible weights costs the others nothing.
 // - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
-//   four converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
+//   eight converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
 //   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
 //   consecutive bytes of a K-major operand: V is stored as V^T, and both products take both
 //   operands K-major.  1024 + c is an f16 number with c as its last bits; less 1024 it is c, and
@@ -36,7 +36,7 @@
 // from its own maximum.  The lift keeps weights down to 2^-18 of the reference's at full precision.
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
-// 11 scales, 12-15 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
+// 11 scales, 12-19 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -59,10 +59,10 @@ using decode::Run;
 constexpr int kStages = 3;                        // expanded K and V blocks
 constexpr int kPacked = 5;                        // halves (K or V) of blocks as codes
 constexpr int kItemRing = 2;
-constexpr int kThreads = 512;                     // 16 warps, four warpgroups
-constexpr int kSoftmaxRegs = 192, kIssueRegs = 48, kConvertRegs = 80;
-static_assert(kIssueRegs < 128 && kConvertRegs < 128, "of the launch's 128 a thread");
-static_assert(256 * kSoftmaxRegs + 128 * (kIssueRegs + kConvertRegs) <= kThreads * 128, "register shares within the launch's");
+constexpr int kConvert = 8;                       // converting warps
+constexpr int kThreads = 384 + 32 * kConvert;     // five warpgroups
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 168, kOtherRegs = 48;
+static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "register shares within the launch's");
 constexpr int kNever = 0x7FFFFFFF;
 constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
 constexpr int kScaledRing = 4;                    // of them, those that the conversion may still wait for
@@ -236,28 +236,41 @@ __device__ __forceinline__ float reach(uint32_t w, float most) {
   const float m = q4_m(w);
   return fmaxf(most, fmaxf(fabsf(m), fabsf(fmaf(15.f, q4_s(w), m))));
 }
-// Of the halves of two pages: a lane's share, over tokens below `left`.
+// The steps and smallest values of the halves of two pages, a lane's share; and the largest reach, over tokens below `left`.
 template <int ND>
-__device__ __forceinline__ float reach_of(const uint8_t* half2, int left, int lane) {
+__device__ __forceinline__ uint4* steps_at(uint8_t* half2, int i, int lane, int& token) {
+  const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;    // words [ND][64] of each page
+  token = page * kPage + (at & (kPage - 1));
+  return (uint4*)(half2 + page * q4_v(ND) + 2048 * ND + at * 4);
+}
+template <int ND>
+__device__ __forceinline__ uint32_t reach_of(uint8_t* half2, int left, int lane, uint4 (&w)[ND]) {
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
-    const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;    // words [ND][64] of each page
-    const uint4 w = *(const uint4*)(half2 + page * q4_v(ND) + 2048 * ND + at * 4);
-    const int token = page * kPage + (at & (kPage - 1));
+    int token;
+    w[i] = *steps_at<ND>(half2, i, lane, token);
     if (token + 3 < left) {
-      most = reach(w.x, reach(w.y, reach(w.z, reach(w.w, most))));
+      most = reach(w[i].x, reach(w[i].y, reach(w[i].z, reach(w[i].w, most))));
     } else {
-      if (token < left) most = reach(w.x, most);
-      if (token + 1 < left) most = reach(w.y, most);
-      if (token + 2 < left) most = reach(w.z, most);
+      if (token < left) most = reach(w[i].x, most);
+      if (token + 1 < left) most = reach(w[i].y, most);
+      if (token + 2 < left) most = reach(w[i].z, most);
     }
   }
-  return most;
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(most));
 }
-// A block's scales: what the keys and the values were multiplied by, and what takes it back.
+// In place: scaled, as two f16.
+template <int ND>
+__device__ __forceinline__ void scale_steps(uint8_t* half2, float by, int lane, const uint4 (&w)[ND]) {
+#pragma unroll
+  for (int i = 0; i < ND; ++i) {
+    int token;
+    *steps_at<ND>(half2, i, lane, token) = make_uint4(scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by));
+  }
+}
+// A block's scales: what takes back that its keys and values were multiplied by 2^(kTopExp - EK), 2^(kTopExp - EV).
 struct Scales {
-  float k_down, v_down;                           // 2^(kTopExp - E)
   float k_up;                                     // 2^(EK - kTopExp)
   float ev, sum_up;                               // EV, and 2^(kSumExp - EV)
 };
@@ -316,11 +329,16 @@ __device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha,
   return make_float2(Z, fmaf(write_exp_from<true>(tS, base, alpha, neg), sum_up, l * f));
 }
 
-// Keys of one page, a warp's half of its tokens, into rows of 64 columns (128 bytes, 16-byte pieces swizzled).
+// A page's tokens or columns are dealt to kParts warps.
+constexpr int kParts = kConvert / 2;
+template <int ND> constexpr int kTiles = 4 * ND / kParts;
+template <int ND> __device__ __forceinline__ int group_of(int w) { return (w >> 1) * kTiles<ND> / 4; }
+
+// Keys of one page, a warp's share of its tokens (from `first` on; their steps already scaled f16), into rows of 64 columns (128 bytes, 16-byte pieces swizzled).
 template <int ND>
-__device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, float by, int lane) {
+__device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, int lane) {
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPage / kParts / 8; ++i) {
     const int token = first + 8 * i + (lane >> 2), t4 = lane & 3, row = page_row + token;
     uint32_t w[2 * ND];
     if constexpr (ND == 2) {
@@ -334,7 +352,7 @@ __device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, 
     const int a = ((2 * t4) ^ (row & 7)) * 16, b = ((2 * t4 + 1) ^ (row & 7)) * 16;
 #pragma unroll
     for (int p = 0; p < ND; ++p) {
-      const uint32_t ms = scaled(*(const uint32_t*)(page + q4_k_ms(ND) + (p * kPage + token) * 4), by);
+      const uint32_t ms = *(const uint32_t*)(page + q4_k_ms(ND) + (p * kPage + token) * 4);
       const uint32_t s1 = __byte_perm(ms, ms, 0x3232), m1 = __byte_perm(ms, ms, 0x1010), s16 = sixteenth(s1);
       const uint32_t s[4] = {s1, s16, s1, s16}, m[4] = {m1, m1, m1, m1};
       *(uint4*)(dst + p * (kTile * 128) + a) = expand(w[2 * p], s, m);
@@ -343,10 +361,10 @@ __device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, 
   }
 }
 
-// Values of one page, 2 ND tiles of 16 columns from `first` on (all of one group), into rows of 64 tokens.
+// Values of one page, kTiles tiles of 16 columns from `first` on (all of one group), into rows of 64 tokens.
 // MASKED: tokens from `left` on are zeros, and a NaN is replaced by zero; returns the first token that had one.
 template <int ND, bool MASKED>
-__device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile, int first, int left, float by, int lane) {
+__device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile, int first, int left, int lane) {
   const int t4 = lane & 3, gid = lane >> 2, group = first >> 2;
   uint32_t s[2][4], m[2][4];
   int bad = kNever;
@@ -360,14 +378,12 @@ __device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile,
         const int token = 16 * t4 + 4 * x + e;
         if (token >= left) {
           w[e] = 0;
-        } else if ((w[e] & 0x7F80u) == 0x7F80u) {
+        } else if ((w[e] & 0x7C00u) == 0x7C00u) {
           w[e] = 0;
           bad = min(bad, token);
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = scaled(w[e], by);
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int k = 2 * (x & 1) + y;
@@ -377,7 +393,7 @@ __device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile,
     }
   }
 #pragma unroll 1
-  for (int i = 0; i < 2 * ND; ++i) {
+  for (int i = 0; i < kTiles<ND>; ++i) {
     const uint4 w = *(const uint4*)(half + (first + i) * 512 + gid * 64 + t4 * 16);
     uint8_t* dst = tile + (16 * (first + i) + gid) * 128;     // columns 16 i + gid and 8 further: gid is the row in the swizzle
     const int a = ((2 * t4) ^ gid) * 16, b = ((2 * t4 + 1) ^ gid) * 16;
@@ -396,7 +412,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   constexpr int kBlock = block_bytes<ND>(), kPackedBytes = packed_bytes<ND>(), kHalf = q4_v(ND);
   constexpr int kKPanel = kTile * 128, kVPanel = D * 128;     // 64 columns of 128 keys; 64 keys of D columns
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ decode::RunShared<16> run;
+  __shared__ decode::RunShared<kThreads / 32> run;
   if (smem_u32(smem) & 1023u) {                   // the swizzle pattern needs 1024-byte alignment
     if (threadIdx.x == 0) atomicCAS(err, 0, (int)kDevMisalignedSmem);
     return;
@@ -416,19 +432,19 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   uint32_t* tmem_slot = (uint32_t*)(bars + kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile Item* s_items = (volatile Item*)(abort_flag + 1);                               // [kItemRing]
-  volatile int* s_bad = (volatile int*)(s_items + kItemRing);      // [kItemRing][4 converting warps]: first NaN token of its group
-  volatile Scales* s_scales = (volatile Scales*)(s_bad + 4 * kItemRing);                  // [kScaleRing]
-  static_assert(8 * kBars + 8 + (sizeof(Item) + 16) * kItemRing + sizeof(Scales) * kScaleRing <= kControl, "control block");
+  volatile int* s_bad = (volatile int*)(s_items + kItemRing);      // [kItemRing][kConvert]: first NaN token of a warp's group
+  volatile Scales* s_scales = (volatile Scales*)(s_bad + kConvert * kItemRing);                  // [kScaleRing]
+  static_assert(8 * kBars + 8 + (sizeof(Item) + 4 * kConvert) * kItemRing + sizeof(Scales) * kScaleRing <= kControl, "control block");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 2); mbar_init(drained, 1); mbar_init(drained + 8, 1);
     mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
-    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, 4); mbar_init(kv_empty + 8 * i, 2); }
-    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, 5); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, kConvert); mbar_init(kv_empty + 8 * i, 2); }
+    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, kConvert + 1); }
     // an item's slot is released by the MMA issuers, the scaling, the converting and the softmax warps
-    for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 15); }
+    for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11 + kConvert); }
     for (int t = 0; t < 2; ++t) mbar_init(q_ready + 8 * t, 128);
     for (int i = 0; i < kScaledRing; ++i) mbar_init(scaled_full + 8 * i, 1);
     *abort_flag = 0;
@@ -441,7 +457,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  const Run plan = decode::plan_run<16>(g.units, [&](int i) { return unit_of(g, i).nb; }, run);
+  const Run plan = decode::plan_run<kThreads / 32>(g.units, [&](int i) { return unit_of(g, i).nb; }, run);
   // units whose rows see no key: zeros
   for (int i = blockIdx.x; i < g.units; i += gridDim.x) {
     const Unit u = unit_of(g, i);
@@ -529,8 +545,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       }
       uint32_t nan = 0;                                       // groups of columns whose NaN was taken out of the products
       if (nb > 0 && live)
-        for (int i = 0; i < 4; ++i)
-          if (s_bad[4 * slot + i] <= limit) nan |= 1u << (ND == 2 ? i >> 1 : 0);
+        for (int i = 0; i < kConvert; ++i)
+          if (s_bad[kConvert * slot + i] <= limit) nan |= 1u << group_of<ND>(i);
       const uint32_t src = nb > 0 ? tO : 0xFFFFFFFFu;
       if (pos_lo < g.pos && t * g.pos + pos_lo < it.rows) {   // a row of the warp exists
         if (it.part >= 0) {
@@ -547,7 +563,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       if (lane == 0) mbar_arrive(item_empty + 8 * slot);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------ copies: pages of codes, queries
       bool ok = true;
@@ -760,13 +776,16 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                wait_warp(ctl, packed_full + 8 * vp, ((2 * bc + 1) / kPacked) & 1, kDevTimeoutEpilogue);
           if (!ok) break;
           const int left = tk - j * kTile;        // stale tokens past the row's end have no say
-          const uint32_t kt = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_of<ND>(sP + kp * kPackedBytes, left, lane)));
-          const uint32_t vt = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_of<ND>(sP + vp * kPackedBytes, left, lane)));
+          uint4 kw[ND], vw[ND];
+          const uint32_t kt = reach_of<ND>(sP + kp * kPackedBytes, left, lane, kw);
+          const uint32_t vt = reach_of<ND>(sP + vp * kPackedBytes, left, lane, vw);
+          const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
+          scale_steps<ND>(sP + kp * kPackedBytes, power_of_two(kTopExp - ek), lane, kw);
+          scale_steps<ND>(sP + vp * kPackedBytes, power_of_two(kTopExp - ev), lane, vw);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");        // the next copy writes here
+          __syncwarp();
           if (lane == 0) {
-            const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
             volatile Scales& out = s_scales[bc % kScaleRing];
-            out.k_down = power_of_two(kTopExp - ek);
-            out.v_down = power_of_two(kTopExp - ev);
             out.k_up = power_of_two(ek - kTopExp);
             out.ev = (float)ev;
             out.sum_up = power_of_two(kSumExp - ev);
@@ -781,9 +800,9 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
-    // ------------------------------------------------ conversion: warp w takes page w & 1 of a block, and half of its tokens
-    // (keys) or of its columns (values)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // ------------------------------------------------ conversion: warp w takes page w & 1 of a block, and a quarter of its
+    // tokens (keys) or of its columns (values)
     const int w = warp - 12, page = w & 1, part = w >> 1;
     uint32_t pc = 0;                              // halves of blocks so far
     int st = 0;
@@ -803,23 +822,22 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
              wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue) &&
              wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
         if (!ok) break;
-        const volatile Scales& scales = s_scales[bc % kScaleRing];
         const uint8_t* src = sP + ps * kPackedBytes + page * kHalf;
         uint8_t* dst = sKV + st * kBlock;
         if ((b & 1) == 0) {
-          expand_keys<ND>(src, dst, page * kPage, 32 * part, scales.k_down, lane);
+          expand_keys<ND>(src, dst, page * kPage, kPage / kParts * part, lane);
         } else if (j < low) {
-          expand_values<ND, false>(src, dst + page * kVPanel, 2 * ND * part, 0, scales.v_down, lane);
+          expand_values<ND, false>(src, dst + page * kVPanel, kTiles<ND> * part, 0, lane);
         } else {
           // a later block's tokens come first: the smallest is kept
           const int at = j * kTile + page * kPage;
-          const int x = expand_values<ND, true>(src, dst + page * kVPanel, 2 * ND * part, tk - at, scales.v_down, lane);
+          const int x = expand_values<ND, true>(src, dst + page * kVPanel, kTiles<ND> * part, tk - at, lane);
           if (x != kNever) bad = min(bad, at + x);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");          // the products read it next
         if (b == 2 * nb - 1) {
           bad = __reduce_min_sync(0xffffffffu, bad);
-          if (lane == 0) s_bad[4 * slot + w] = bad;
+          if (lane == 0) s_bad[kConvert * slot + w] = bad;
         }
         __syncwarp();
         if (lane == 0) {
