@@ -61,7 +61,7 @@ constexpr int kPacked = 5;                        // halves (K or V) of blocks a
 constexpr int kItemRing = 2;
 constexpr int kConvert = 8;                       // converting warps
 constexpr int kThreads = 384 + 32 * kConvert;     // five warpgroups
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 168, kOtherRegs = 48;
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 176, kOtherRegs = 40;
 static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "register shares within the launch's");
 constexpr int kNever = 0x7FFFFFFF;
 constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
