@@ -56,8 +56,8 @@ namespace {
 using namespace tcgen;
 using decode::Run;
 
-constexpr int kStages = 3;                        // expanded K and V blocks
-constexpr int kPacked = 5;                        // halves (K or V) of blocks as codes
+constexpr int kStages = 4;                        // expanded K and V blocks (with three, the keys' conversion held the products up)
+constexpr int kPacked = 7;                        // pages of codes, keys or values: what the rest leaves room for
 constexpr int kItemRing = 2;
 constexpr int kConvert = 8;                       // converting warps
 constexpr int kThreads = 384 + 32 * kConvert;     // five warpgroups
@@ -73,12 +73,10 @@ constexpr float kBack = 262144.f;                 // 2^(kSumExp - kTopExp): O ov
 constexpr int kSumExp = 32;                       // l gathers 2^(kSumExp - Z) times the weights: far from both ends of fp32
 
 template <int ND> constexpr int block_bytes() { return kTile * 64 * ND * 2; }
-template <int ND> constexpr int packed_bytes() { return 2 * q4_v(ND); }           // the halves of two pages
 static_assert(q4_page_bytes(1) == 2 * q4_v(1), "keys and values take the same room");
-constexpr int kStageOut = 32 * 64;                // a softmax warp's 32 rows x 32 output columns
 constexpr int kControl = 1024;
 template <int ND> constexpr int smem_bytes() {
-  return (2 + kStages) * block_bytes<ND>() + kPacked * packed_bytes<ND>() + 8 * kStageOut + kControl;
+  return (2 + kStages) * block_bytes<ND>() + kPacked * q4_v(ND) + kControl;
 }
 // A tile's part: O as [4 warps][D columns][32 lanes], then the rows' Z and l.
 template <int D> constexpr int part_floats() { return kTile * (D + 2); }
@@ -145,42 +143,21 @@ __device__ __forceinline__ void put_row(const Q4TcGeom& g, __nv_bfloat16* out, i
   *(uint4*)(out + pos * g.o_st + head * g.o_sh + c) = w;
 }
 
-// A warp's rows of the output, 32 columns at a time through the warp's own staging rows: 16-byte piece k of row r lies at
-// k ^ (r >> 1 & 3).  out: the tile's first position and head; left: positions of it that exist; tO: 0xFFFFFFFF for rows
-// without any key; nan: a bit per group of 64 columns that is NaN.
+// A row of the output, by its thread.  tO: 0xFFFFFFFF for rows without any key; nan: a bit per group of 64 columns that is
+// NaN.
 template <int D>
-__device__ __noinline__ void write_rows(const Q4TcGeom& g, __nv_bfloat16* out, int left, uint32_t tO, float inv, uint8_t* stage,
-                                        int row, uint32_t nan) {
-  const int lane = row & 31, d = g.c.d;
-  uint8_t* mine = stage + lane * 64;
-  // of the rows that this lane writes pieces of, -1: none (a tile's rows lie within 2^31 elements)
-  int where[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tr = row - lane + 8 * i + (lane >> 2), pos = (tr * g.inv_gp) >> 16;
-    where[i] = pos < left ? pos * g.o_st + (tr - pos * g.gp) * g.o_sh + (lane & 3) * 8 : -1;
-  }
+__device__ __noinline__ void write_row(__nv_bfloat16* out, bool mine, int d, uint32_t tO, float inv, uint32_t nan) {
 #pragma unroll 1
-  for (int c = 0; c < D && c < d; c += 32) {
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      float o[16];
-      if (tO != 0xFFFFFFFFu) tmem_get16(tO + c + 16 * k, o);
-      const bool bad = nan >> (c >> 6) & 1;
+  for (int c = 0; c < D && c < d; c += 16) {
+    float o[16];
+    if (tO != 0xFFFFFFFFu) tmem_get16(tO + c, o);
+    const bool bad = nan >> (c >> 6) & 1;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = bad ? NAN : tO != 0xFFFFFFFFu ? o[i] * inv : 0.f;
-      put8(mine + ((2 * k) ^ (lane >> 1 & 3)) * 16, o);
-      put8(mine + ((2 * k + 1) ^ (lane >> 1 & 3)) * 16, o + 8);
+    for (int i = 0; i < 16; ++i) o[i] = bad ? NAN : tO != 0xFFFFFFFFu ? o[i] * inv : 0.f;
+    if (mine) {
+      put8((uint8_t*)(out + c), o);
+      if (c + 8 < d) put8((uint8_t*)(out + c + 8), o + 8);
     }
-    __syncwarp();
-    const bool inside = c + (lane & 3) * 8 < d;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      const uint4 w = *(const uint4*)(stage + r * 64 + ((lane & 3) ^ (r >> 1 & 3)) * 16);
-      if (inside && where[i] >= 0) *(uint4*)(out + where[i] + c) = w;
-    }
-    __syncwarp();
   }
 }
 
@@ -238,18 +215,18 @@ __device__ __forceinline__ float reach(uint32_t w, float most) {
 }
 // The steps and smallest values of the halves of two pages, a lane's share; and the largest reach, over tokens below `left`.
 template <int ND>
-__device__ __forceinline__ uint4* steps_at(uint8_t* half2, int i, int lane, int& token) {
+__device__ __forceinline__ uint4* steps_at(uint8_t* const (&half)[2], int i, int lane, int& token) {
   const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;    // words [ND][64] of each page
   token = page * kPage + (at & (kPage - 1));
-  return (uint4*)(half2 + page * q4_v(ND) + 2048 * ND + at * 4);
+  return (uint4*)((page ? half[1] : half[0]) + 2048 * ND + at * 4);
 }
 template <int ND>
-__device__ __forceinline__ uint32_t reach_of(uint8_t* half2, int left, int lane, uint4 (&w)[ND]) {
+__device__ __forceinline__ uint32_t reach_of(uint8_t* const (&half)[2], int left, int lane, uint4 (&w)[ND]) {
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     int token;
-    w[i] = *steps_at<ND>(half2, i, lane, token);
+    w[i] = *steps_at<ND>(half, i, lane, token);
     if (token + 3 < left) {
       most = reach(w[i].x, reach(w[i].y, reach(w[i].z, reach(w[i].w, most))));
     } else {
@@ -262,11 +239,11 @@ __device__ __forceinline__ uint32_t reach_of(uint8_t* half2, int left, int lane,
 }
 // In place: scaled, as two f16.
 template <int ND>
-__device__ __forceinline__ void scale_steps(uint8_t* half2, float by, int lane, const uint4 (&w)[ND]) {
+__device__ __forceinline__ void scale_steps(uint8_t* const (&half)[2], float by, int lane, const uint4 (&w)[ND]) {
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     int token;
-    *steps_at<ND>(half2, i, lane, token) = make_uint4(scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by));
+    *steps_at<ND>(half, i, lane, token) = make_uint4(scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by));
   }
 }
 // A block's scales: what takes back that its keys and values were multiplied by 2^(kTopExp - EK), 2^(kTopExp - EV).
@@ -409,19 +386,17 @@ template <int ND>
 __global__ void __launch_bounds__(kThreads, 1)
 q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Q4TcGeom g, int32_t* __restrict__ err) {
   constexpr int D = 64 * ND;
-  constexpr int kBlock = block_bytes<ND>(), kPackedBytes = packed_bytes<ND>(), kHalf = q4_v(ND);
+  constexpr int kBlock = block_bytes<ND>(), kHalf = q4_v(ND);
   constexpr int kKPanel = kTile * 128, kVPanel = D * 128;     // 64 columns of 128 keys; 64 keys of D columns
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ decode::RunShared<kThreads / 32> run;
   if (smem_u32(smem) & 1023u) {                   // the swizzle pattern needs 1024-byte alignment
     if (threadIdx.x == 0) atomicCAS(err, 0, (int)kDevMisalignedSmem);
     return;
   }
   uint8_t* sQ = smem;                             // two tiles
   uint8_t* sKV = smem + 2 * kBlock;               // kStages blocks: K, V, K, V ... of descending blocks
-  uint8_t* sP = sKV + kStages * kBlock;           // kPacked halves of blocks
-  uint8_t* sOut = sP + kPacked * kPackedBytes;    // [8][kStageOut]
-  uint64_t* bars = (uint64_t*)(sOut + 8 * kStageOut);
+  uint8_t* sP = sKV + kStages * kBlock;           // kPacked pages: of a block, the keys' two and then the values'
+  uint64_t* bars = (uint64_t*)(sP + kPacked * kHalf);
   const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, drained = q_full + 16;      // drained: [2]
   const uint32_t turn = q_full + 32, s_full = q_full + 48, p_full = s_full + 16, o_full = p_full + 16;        // [2] each
   const uint32_t kv_full = o_full + 16, kv_empty = kv_full + 8 * kStages;
@@ -434,7 +409,10 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   volatile Item* s_items = (volatile Item*)(abort_flag + 1);                               // [kItemRing]
   volatile int* s_bad = (volatile int*)(s_items + kItemRing);      // [kItemRing][kConvert]: first NaN token of a warp's group
   volatile Scales* s_scales = (volatile Scales*)(s_bad + kConvert * kItemRing);                  // [kScaleRing]
-  static_assert(8 * kBars + 8 + (sizeof(Item) + 4 * kConvert) * kItemRing + sizeof(Scales) * kScaleRing <= kControl, "control block");
+  using RunOf = decode::RunShared<kThreads / 32>;
+  RunOf& run = *(RunOf*)((uint8_t*)bars + kControl - sizeof(RunOf));
+  static_assert(8 * kBars + 8 + (sizeof(Item) + 4 * kConvert) * kItemRing + sizeof(Scales) * kScaleRing + sizeof(RunOf) <= kControl &&
+                    sizeof(RunOf) % 8 == 0, "control block");
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -442,7 +420,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     mbar_init(turn, 1); mbar_init(turn + 8, 1);
     for (int t = 0; t < 2; ++t) { mbar_init(s_full + 8 * t, 1); mbar_init(p_full + 8 * t, 128); mbar_init(o_full + 8 * t, 1); }
     for (int i = 0; i < kStages; ++i) { mbar_init(kv_full + 8 * i, kConvert); mbar_init(kv_empty + 8 * i, 2); }
-    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, kConvert + 1); }
+    for (int i = 0; i < kPacked; ++i) { mbar_init(packed_full + 8 * i, 1); mbar_init(packed_empty + 8 * i, kConvert / 2 + 1); }
     // an item's slot is released by the MMA issuers, the scaling, the converting and the softmax warps
     for (int i = 0; i < kItemRing; ++i) { mbar_init(item_full + 8 * i, 1); mbar_init(item_empty + 8 * i, 11 + kConvert); }
     for (int t = 0; t < 2; ++t) mbar_init(q_ready + 8 * t, 128);
@@ -554,8 +532,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         } else {
           // no visible key: zeros; logits that are all -inf: NaN
           const float inv = l != 0.f ? kBack / l : limit < 0 ? 0.f : NAN;
-          write_rows<D>(g, g.out + it.b * g.o_sb + (int64_t)(it.q0 + t * g.pos) * g.o_st + (int64_t)it.h * g.o_sh,
-                        min(g.pos, it.rows - t * g.pos), src, inv, sOut + warp * kStageOut, row, nan);
+          write_row<D>(g.out + it.b * g.o_sb + (int64_t)(it.q0 + t * g.pos + my_pos) * g.o_st + (int64_t)(it.h + row - my_pos * g.gp) * g.o_sh,
+                       live, g.c.d, src, inv, nan);
         }
       }
       fence_before();
@@ -633,14 +611,18 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
             pages = min(2, pages_held - j);
             for (int k = 0; k < pages; ++k) page[k] = safe_page(row_table[j + k], g.c.n_pages);
           }
-          const int st = loaded % kPacked;
-          ok = wait_bar(ctl, packed_empty + 8 * st, ((loaded / kPacked) & 1) ^ 1, kDevTimeoutTmaProducer);
-          if (!ok) break;
-          const uint32_t bar = packed_full + 8 * st;
-          mbar_expect_tx(bar, pages * kHalf);
-          for (int k = 0; k < pages; ++k)
-            bulk_load(smem_u32(sP) + st * kPackedBytes + k * kHalf, g.pages + page[k] * q4_page_bytes(ND) + (b & 1) * kHalf, kHalf, bar);
-          ++loaded;
+          for (int k = 0; k < 2 && ok; ++k) {
+            const int st = loaded % kPacked;
+            ok = wait_bar(ctl, packed_empty + 8 * st, ((loaded / kPacked) & 1) ^ 1, kDevTimeoutTmaProducer);
+            if (!ok) break;
+            if (k < pages) {
+              mbar_expect_tx(packed_full + 8 * st, kHalf);
+              bulk_load(smem_u32(sP) + st * kHalf, g.pages + page[k] * q4_page_bytes(ND) + (b & 1) * kHalf, kHalf, packed_full + 8 * st);
+            } else {
+              mbar_arrive(packed_full + 8 * st);  // a row's last block may be of one page
+            }
+            ++loaded;
+          }
         }
         if (ok && nb == 1) {                      // an item of one block: its queries come last
           ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
@@ -771,17 +753,21 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         const int nb = s_items[slot].nb, tk = s_items[slot].tk;
         bool ok = true;
         for (int j = nb - 1; j >= 0 && ok; --j, ++bc) {
-          const uint32_t kp = 2 * bc % kPacked, vp = (2 * bc + 1) % kPacked;
-          ok = wait_warp(ctl, packed_full + 8 * kp, (2 * bc / kPacked) & 1, kDevTimeoutEpilogue) &&
-               wait_warp(ctl, packed_full + 8 * vp, ((2 * bc + 1) / kPacked) & 1, kDevTimeoutEpilogue);
+          uint8_t* half[2][2];
+#pragma unroll
+          for (int i = 0; i < 4 && ok; ++i) {
+            const uint32_t u = 4 * bc + i;
+            half[i >> 1][i & 1] = sP + u % kPacked * kHalf;
+            ok = wait_warp(ctl, packed_full + 8 * (u % kPacked), (u / kPacked) & 1, kDevTimeoutEpilogue);
+          }
           if (!ok) break;
           const int left = tk - j * kTile;        // stale tokens past the row's end have no say
           uint4 kw[ND], vw[ND];
-          const uint32_t kt = reach_of<ND>(sP + kp * kPackedBytes, left, lane, kw);
-          const uint32_t vt = reach_of<ND>(sP + vp * kPackedBytes, left, lane, vw);
+          const uint32_t kt = reach_of<ND>(half[0], left, lane, kw);
+          const uint32_t vt = reach_of<ND>(half[1], left, lane, vw);
           const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
-          scale_steps<ND>(sP + kp * kPackedBytes, power_of_two(kTopExp - ek), lane, kw);
-          scale_steps<ND>(sP + vp * kPackedBytes, power_of_two(kTopExp - ev), lane, vw);
+          scale_steps<ND>(half[0], power_of_two(kTopExp - ek), lane, kw);
+          scale_steps<ND>(half[1], power_of_two(kTopExp - ev), lane, vw);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");        // the next copy writes here
           __syncwarp();
           if (lane == 0) {
@@ -790,8 +776,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
             out.ev = (float)ev;
             out.sum_up = power_of_two(kSumExp - ev);
             mbar_arrive(scaled_full + 8 * (bc % kScaledRing));
-            mbar_arrive(packed_empty + 8 * kp);
-            mbar_arrive(packed_empty + 8 * vp);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mbar_arrive(packed_empty + 8 * ((4 * bc + i) % kPacked));
           }
           __syncwarp();
         }
@@ -816,13 +802,13 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       int bad = kNever;
       bool ok = true;
       for (int b = 0; b < 2 * nb && ok; ++b) {
-        const int j = nb - 1 - (b >> 1), ps = pc % kPacked;
-        const uint32_t bc = pc >> 1;
-        ok = wait_warp(ctl, packed_full + 8 * ps, (pc / kPacked) & 1, kDevTimeoutEpilogue) &&
-             wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue) &&
+        const int j = nb - 1 - (b >> 1);
+        const uint32_t bc = pc >> 1, ps = (2 * pc + page) % kPacked;
+        // the copies have landed once the scales are there
+        ok = wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue) &&
              wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
         if (!ok) break;
-        const uint8_t* src = sP + ps * kPackedBytes + page * kHalf;
+        const uint8_t* src = sP + ps * kHalf;
         uint8_t* dst = sKV + st * kBlock;
         if ((b & 1) == 0) {
           expand_keys<ND>(src, dst, page * kPage, kPage / kParts * part, lane);
@@ -862,7 +848,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   if (*abort_flag) {
     bool landed = true;
     if (warp == 8 && lane == 0) {
-      for (uint32_t i = loaded > kPacked ? loaded - kPacked : 0; i < loaded; ++i)
+      for (uint32_t i = loaded > (uint32_t)kPacked ? loaded - kPacked : 0; i < loaded; ++i)
         landed &= drain_phase(packed_full + 8 * (i % kPacked), (i / kPacked) & 1);
       if (q_loaded > 0) landed &= drain_phase(q_full, (q_loaded - 1) & 1);
     }
