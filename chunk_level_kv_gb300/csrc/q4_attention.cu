@@ -14,18 +14,19 @@
 // nibbles into f16 pairs, 5 instructions for 8 codes, and the other operand's elements that
 // meet the higher ones are divided by 16 beforehand.  The products are m16n8k16 in f16 with
 // fp32 sums; tcgen05 would want the codes expanded in shared memory, 4 times their bytes.
-//   S = Q K^T takes the query as the 16-row operand and gives a lane two tokens of one query
-//   row; that is how O^T = V^T P^T wants its 8-column operand, so the weights go from one to
-//   the other in registers, and V's codes fill all 16 rows (half the products and half the
-//   sums' registers of O = P V).
-//   bf16: up to 8 query rows, or 16 as two columns' worth of the second product.  A query in
-//         f16, scaled by a power of two, loses only what is below 2^-25 of its largest element;
-//         the weights p s are rounded to f16, 2^-11 each, where the output's rounding is 2^-8.
-//         Sums of products with subnormals are good to about 2^-17 of their largest term (the
-//         unit aligns them by the exponent that a subnormal is stored with).
-//   fp32: 8 query rows, and rows 8-15 carry what f16 cut off (22 bits of each); the weights in
-//         two products.  The codes are made whole numbers c - 8 (m becomes m + 8 s), 11 instructions
-//         for 8 codes; with subnormals the output was off by 60e-6.
+//   S^T = K Q^T and O^T = V^T P^T: the codes are the operand of 16 rows both times, 8 query rows
+//   the one of 8 columns, so no product is spent on rows that do not exist.  A lane's logits are
+//   2 query rows of 8 tokens; the weights p s change lanes for the second product as 8 x 8 f16
+//   matrices transposed by the warp.  (With the query as the operand of 16 rows, half of them
+//   zeros, the first product and its registers cost 300 of 1200 instructions a page.)
+//   bf16: 8 query rows, or 16 as two sets of columns.  A query in f16, scaled by a power of two,
+//         loses only what is below 2^-25 of its largest element; the weights p s are rounded to
+//         f16, 2^-11 each, where the output's rounding is 2^-8.  Sums of products with subnormals
+//         are good to about 2^-17 of their largest term (the unit aligns them by the exponent that
+//         a subnormal is stored with).
+//   fp32: 8 query rows; queries and weights as two f16 each (22 bits), in two products.  The codes
+//         are made whole numbers c - 8 (m becomes m + 8 s), 11 instructions for 8 codes; with
+//         subnormals the output was off by 60e-6.
 //
 // A weight p s is held as a multiple of the largest p s of its row so far (2^d times 2^max t), so
 // that f16 holds it however far apart the steps of a row lie.
@@ -47,7 +48,7 @@ constexpr int kMaxGrid = 224;                    // CTAs of a pass (one per SM):
 constexpr int kMaxGroups = 16;                   // passes in one launch
 constexpr int kCountByte = 32;                   // the counts of parts that have arrived, as decode attention's (q8_attention.cu)
 static_assert(kCountByte + kMaxGrid * kMaxGroups <= (int)kServeHeader, "the counts lie in the serving header");
-constexpr float kWeightExp = 14.f;               // the largest weight is 2^14 (f16 ends at 2^16)
+constexpr float kWeightExp = 12.f, kSlack = 3.f;  // the largest weight is 2^12 when O's unit is set, and 2^15 at most (f16 ends at 2^16)
 constexpr int kQueryExp = 14;                    // the largest query element is in [2^14, 2^15)
 
 struct Q4AttnArgs {
@@ -64,20 +65,19 @@ struct Q4AttnArgs {
 // Warps of a CTA, a page each in shared memory.  Sixteen hide the products' latency best, and 8
 // query rows of up to 128 columns fit their 128 registers a thread.
 template <int ND, typename T, int RS>
-constexpr int warps_of() { return sizeof(T) == 2 && RS == 1 && ND <= 2 ? 16 : 8; }
+constexpr int warps_of() { return sizeof(T) == 2 && RS == 1 && ND <= 2 ? 12 : 8; }
 template <int ND>
 constexpr int pitch() { return 64 * ND + 4; }    // O, m, l: in 16-byte rows
 template <int ND>
 constexpr bool q_in_regs() { return ND <= 2; }   // wider heads keep their query fragments in shared memory
 template <int ND, typename T, int RS>
 constexpr size_t smem_bytes() {
-  return (size_t)warps_of<ND, T, RS>() * (q4_page_bytes(ND) + 8 * RS * pitch<ND>() * 4) + (q_in_regs<ND>() ? 0 : ND * 4 * 32 * 16);
+  return (size_t)warps_of<ND, T, RS>() * (q4_page_bytes(ND) + 8 * RS * pitch<ND>() * 4) + (q_in_regs<ND>() ? 0 : 2 * ND * 4 * 32 * 8);
 }
 // The halves of a page, each with its steps: two copies, and two barriers.
 constexpr int half_bytes(int nd) { return q4_v(nd); }
 static_assert(2 * half_bytes(1) == q4_page_bytes(1), "keys and values take the same room");
 
-__device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
 // Four codes of a word, of its items 4 h .. 4 h + 3, as two f16 pairs.
 template <bool kExact>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, int h, uint32_t& lo, uint32_t& hi) {
@@ -93,11 +93,16 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, int h, uint32_t& lo, ui
     hi = w & 0x00F000F0u;
   }
 }
-// What code 0 (or code 8, kExact) stands for, of two tokens.
+// What code 0 (or code 8, kExact) stands for.
 template <bool kExact>
-__device__ __forceinline__ float2 base_of(uint32_t a, uint32_t b, float2 s) {
-  const float2 m = f2(q4_m(a), q4_m(b));
-  return kExact ? __ffma2_rn(s, f2(8.f, 8.f), m) : m;
+__device__ __forceinline__ float base_of(uint32_t ms) {
+  return kExact ? fmaf(q4_s(ms), 8.f, q4_m(ms)) : q4_m(ms);
+}
+// An 8 x 8 matrix of f16 transposed: lane (gid, t) held row gid, columns 2 t and 2 t + 1, and gets column gid, rows 2 t, 2 t + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 // D = A B (decode.cuh: D += A B).
 __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -119,8 +124,9 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
                     const int32_t* __restrict__ lens) {
   constexpr int W = warps_of<ND, T, RS>(), kThreads = 32 * W, kBytes = q4_page_bytes(ND), kHalf = half_bytes(ND);
   constexpr int kPitch = pitch<ND>(), PR = 8 * RS;
-  constexpr bool kSplit = sizeof(T) == 4;        // the query's rows 8-15 carry the low parts of rows 0-7
-  static_assert(!kSplit || RS == 1, "an operand has 16 rows");
+  constexpr bool kSplit = sizeof(T) == 4;        // queries and weights in two parts
+  static_assert(!kSplit || RS == 1, "two parts take the place of two sets of rows");
+  constexpr int NB = kSplit ? 2 : RS;            // operands of 8 columns
   constexpr int kCodeExp = kSplit ? 0 : 24;      // a code is c 2^-kCodeExp, or c - 8
   constexpr float kSecond = kSplit ? 1.f : 0.0625f;            // of what meets the second pair of codes
   constexpr int KS = 4 * ND;                     // k steps of a logit, 16 columns each
@@ -130,9 +136,10 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
   __shared__ RunShared<W> run;
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+  const int my_token = 16 * (gid >> 1) + (gid & 1);
   uint8_t* pg = smem + warp * kBytes;
   float* sM = (float*)(smem + W * kBytes);       // [W][PR][kPitch]
-  uint4* sQ = (uint4*)(sM + W * PR * kPitch);    // one for all warps: they work on one cache row at a time
+  uint2* sQ = (uint2*)(sM + W * PR * kPitch);    // [NB][KS][32], one for all warps: they work on one cache row at a time
   const uint32_t kbar = smem_u32(&bars[2 * warp]), vbar = kbar + 8;
   if (lane == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(kbar) : "memory");
@@ -192,16 +199,17 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
     if (sa < sb) {
       // the query's fragments: columns 64 p + 16 t + 4 kk .. + 3 meet the items 4 (kk & 1) .. + 3 of the words that lane
       // t reads
-      float ca[RS], cb[RS][ND];                  // t = ca 2^(kCodeExp - kQueryExp) sum_g s acc + sum_g cb base
-      int seen[RS];                              // tokens that the row's query sees
-      uint4 qf[q_in_regs<ND>() ? KS : 1];
+      // its rows are gid (+ 8); what the logits need of them goes to the lanes that hold rows 2 t, 2 t + 1
+      float ca[RS][2], cb[RS][2][ND];            // t = ca sum_g s acc + sum_g cb base
+      int seen[RS][2];                           // tokens that the row's query sees
+      uint2 qf[NB][q_in_regs<ND>() ? KS : 1];
       int seen_min = len;
 #pragma unroll
       for (int rs = 0; rs < RS; ++rs) {
         const int row = gid + 8 * rs, i = (p0 + row) / a.G;
         const bool live = row < gn && i < nq;
-        seen[rs] = live ? len - nq + 1 + i : len;
-        seen_min = min(seen_min, seen[rs]);
+        const int sees = live ? len - nq + 1 + i : len;
+        seen_min = min(seen_min, sees);
         const T* q = (const T*)a.q + b * a.q_sb + i * a.q_st + (int64_t)(h * a.G + p0 + row - i * a.G) * a.q_sh;
         float qv[KS][4];
         uint32_t top = 0;
@@ -213,6 +221,18 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(qv[s][e]) & 0x7FFFFFFFu);
         }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // scaled by a power of two into f16's range, whatever the query's size
+        const int e2 = min(127, max(-110, (int)(top >> 23) - 127));
+        const float down = power_of_two(kQueryExp - e2);
+        constexpr float kUp = kSplit ? 1.f / (1 << kQueryExp) : 1 << (24 - kQueryExp);
+        const float c0 = fminf(a.alpha * power_of_two(e2) * kUp, 3.4e38f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ca[rs][e] = __shfl_sync(0xffffffffu, c0, 8 * t4 + 4 * e);
+          seen[rs][e] = __shfl_sync(0xffffffffu, sees, 8 * t4 + 4 * e);
+        }
 #pragma unroll
         for (int p = 0; p < ND; ++p) {
           float sum = 0.f;
@@ -220,43 +240,39 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
           for (int s = 4 * p; s < 4 * p + 4; ++s) sum += (qv[s][0] + qv[s][1]) + (qv[s][2] + qv[s][3]);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          cb[rs][p] = sum * a.alpha;
+          sum *= a.alpha;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) cb[rs][e][p] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4 * e);
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // scaled by a power of two into f16's range, whatever the query's size
-        const int e2 = min(127, max(-110, (int)(top >> 23) - 127));
-        const float down = power_of_two(kQueryExp - e2);
-        ca[rs] = a.alpha * power_of_two(e2);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const float c0 = qv[s][0] * down, c1 = qv[s][1] * down, c2 = qv[s][2] * down * kSecond, c3 = qv[s][3] * down * kSecond;
-          uint4 f = make_uint4(0, 0, 0, 0);
-          if (rs > 0) {
-            if constexpr (q_in_regs<ND>()) f = qf[s]; else f = sQ[s * 32 + lane];
-          }
+          const float x0 = qv[s][0] * down, x1 = qv[s][1] * down, x2 = qv[s][2] * down * kSecond, x3 = qv[s][3] * down * kSecond;
+          uint2 f[2];
           if constexpr (kSplit) {
-            split_half2(c0, c1, 1.f, f.x, f.y);
-            split_half2(c2, c3, 1.f, f.z, f.w);
-          } else if (rs == 0) {
-            f.x = pack_half2(c0, c1);
-            f.z = pack_half2(c2, c3);
+            split_half2(x0, x1, 1.f, f[0].x, f[1].x);
+            split_half2(x2, x3, 1.f, f[0].y, f[1].y);
           } else {
-            f.y = pack_half2(c0, c1);
-            f.w = pack_half2(c2, c3);
+            f[0] = make_uint2(pack_half2(x0, x1), pack_half2(x2, x3));
           }
-          if constexpr (q_in_regs<ND>()) qf[s] = f; else sQ[s * 32 + lane] = f;
+#pragma unroll
+          for (int k = 0; k < (kSplit ? 2 : 1); ++k) {
+            if constexpr (q_in_regs<ND>()) qf[rs + k][s] = f[k]; else sQ[((rs + k) * KS + s) * 32 + lane] = f[k];
+          }
         }
       }
+      __syncwarp();
       seen_min = __reduce_min_sync(0xffffffffu, seen_min);
-      float m[RS], l[RS], dl[RS], z[RS][ND];     // reference, sum, O's unit as an exponent of 2 above the reference, sum of p m
+      // of rows 2 t, 2 t + 1: reference, sum, O's unit as an exponent of 2 above the reference, sum of p base (sums: this lane's)
+      float m[RS][2], l[RS][2], dl[RS][2], z[RS][2][ND];
 #pragma unroll
-      for (int rs = 0; rs < RS; ++rs) {
-        m[rs] = dl[rs] = -INFINITY;
-        l[rs] = 0.f;
+      for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-        for (int p = 0; p < ND; ++p) z[rs][p] = 0.f;
-      }
+        for (int e = 0; e < 2; ++e) {
+          m[rs][e] = dl[rs][e] = -INFINITY;
+          l[rs][e] = 0.f;
+#pragma unroll
+          for (int p = 0; p < ND; ++p) z[rs][e][p] = 0.f;
+        }
       float o[RS][MT][4];                        // O^T: columns 16 i + gid (+ 8: elements 2, 3) of rows 2 t, 2 t + 1
 #pragma unroll
       for (int rs = 0; rs < RS; ++rs)
@@ -269,128 +285,135 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
         // the page to come: mostly of this row
         const int64_t next = nx < sb ? safe_page(table[(int64_t)r * g.max_pages + (nx - xr)], g.n_pages) : more ? page_at(nx) : 0;
         wait_copy(kbar, phase, dead, a.err);
-        // ---- t.  Column 2 t + e of tile i is token 16 t + 2 i + e of the page: the tokens that lane t's pieces of V hold
-        float2 t[RS][8];
+        // ---- t.  Rows gid and gid + 8 of tile i are tokens 4 i + 16 (gid / 2) + gid % 2 and the second after it: transposed
+        // by eights, lane t then holds tokens 16 t + 2 j + e, as its pieces of V
+        float t[RS][8][2];
 #pragma unroll
-        for (int x4 = 0; x4 < 4; ++x4) {
-          uint32_t ms[ND][4];
-#pragma unroll
-          for (int p = 0; p < ND; ++p) {
-            const uint4 w = *(const uint4*)(pg + q4_k_ms(ND) + (p * kPage + 16 * t4 + 4 * x4) * 4);
-            ms[p][0] = w.x; ms[p][1] = w.y; ms[p][2] = w.z; ms[p][3] = w.w;
-          }
+        for (int i = 0; i < 4; ++i) {
+          float acc[NB][ND][4];
+          uint32_t kw[2][2 * ND];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int i = 2 * x4 + y, token = 16 * (gid >> 1) + 2 * i + (gid & 1);
-            const uint8_t* src = pg + token * (32 * ND) + t4 * (8 * ND);
-            uint32_t kw[2 * ND];
+            const uint8_t* src = pg + (my_token + 4 * i + 2 * y) * (32 * ND) + t4 * (8 * ND);
             if constexpr (ND % 2 == 0) {
 #pragma unroll
               for (int p = 0; p < ND / 2; ++p) {
                 const uint4 w = *(const uint4*)(src + 16 * p);
-                kw[4 * p] = w.x; kw[4 * p + 1] = w.y; kw[4 * p + 2] = w.z; kw[4 * p + 3] = w.w;
+                kw[y][4 * p] = w.x; kw[y][4 * p + 1] = w.y; kw[y][4 * p + 2] = w.z; kw[y][4 * p + 3] = w.w;
               }
             } else {
 #pragma unroll
               for (int p = 0; p < ND; ++p) {
                 const uint2 w = *(const uint2*)(src + 8 * p);
-                kw[2 * p] = w.x; kw[2 * p + 1] = w.y;
+                kw[y][2 * p] = w.x; kw[y][2 * p + 1] = w.y;
               }
             }
-            float2 sum[RS], off[RS];
+          }
+#pragma unroll
+          for (int p = 0; p < ND; ++p)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              uint4 c;
+              codes_to_f16<kSplit>(kw[0][2 * p + (s >> 1)], s & 1, c.x, c.z);
+              codes_to_f16<kSplit>(kw[1][2 * p + (s >> 1)], s & 1, c.y, c.w);
+#pragma unroll
+              for (int k = 0; k < NB; ++k) {
+                uint2 f;
+                if constexpr (q_in_regs<ND>()) f = qf[k][4 * p + s]; else f = sQ[(k * KS + 4 * p + s) * 32 + lane];
+                float (&d)[4] = acc[kSplit ? 0 : k][p];
+                if (s == 0 && (!kSplit || k == 0)) mma16816_first(d, c, f.x, f.y); else mma16816(d, c, f.x, f.y);
+              }
+            }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float sum[RS][2], off[RS][2];
 #pragma unroll
             for (int p = 0; p < ND; ++p) {
-              float acc[4];
+              const uint32_t ms = *(const uint32_t*)(pg + q4_k_ms(ND) + (p * kPage + my_token + 4 * i + 2 * y) * 4);
+              const float st = q4_s(ms), base = base_of<kSplit>(ms);
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                uint32_t b0, b1;
-                codes_to_f16<kSplit>(kw[2 * p + (s >> 1)], s & 1, b0, b1);
-                uint4 f;
-                if constexpr (q_in_regs<ND>()) f = qf[4 * p + s]; else f = sQ[(4 * p + s) * 32 + lane];
-                if (s == 0) mma16816_first(acc, f, b0, b1); else mma16816(acc, f, b0, b1);
-              }
-              const float2 s2 = f2(q4_s(ms[p][2 * y]), q4_s(ms[p][2 * y + 1])), m2 = base_of<kSplit>(ms[p][2 * y], ms[p][2 * y + 1], s2);
+              for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-              for (int rs = 0; rs < RS; ++rs) {
-                const float2 v = kSplit ? f2(acc[0] + acc[2], acc[1] + acc[3]) : f2(acc[2 * rs], acc[2 * rs + 1]);
-                const float2 c2 = f2(cb[rs][p], cb[rs][p]);
-                sum[rs] = p == 0 ? __fmul2_rn(v, s2) : __ffma2_rn(v, s2, sum[rs]);
-                off[rs] = p == 0 ? __fmul2_rn(c2, m2) : __ffma2_rn(c2, m2, off[rs]);
-              }
+                for (int e = 0; e < 2; ++e) {
+                  sum[rs][e] = p == 0 ? acc[rs][p][2 * y + e] * st : fmaf(acc[rs][p][2 * y + e], st, sum[rs][e]);
+                  off[rs][e] = p == 0 ? cb[rs][e][p] * base : fmaf(cb[rs][e][p], base, off[rs][e]);
+                }
             }
 #pragma unroll
-            for (int rs = 0; rs < RS; ++rs) {
-              constexpr float kUp = kSplit ? 1.f / (1 << kQueryExp) : 1 << (24 - kQueryExp);
-              t[rs][i] = __ffma2_rn(__fmul2_rn(sum[rs], f2(kUp, kUp)), f2(ca[rs], ca[rs]), off[rs]);
-            }
+            for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) t[rs][2 * i + y][e] = fmaf(sum[rs][e], ca[rs][e], off[rs][e]);
           }
         }
         __syncwarp();                            // every lane has read the keys
         if (more && lane == 0 && !dead) copy_page(smem_u32(pg), pages + next * kBytes, kHalf, kbar);
         wait_copy(vbar, phase, dead, a.err);
         // ---- weights p s and their largest, the reference, O's unit; the second product's operands
-        uint32_t pb[RS * (kSplit ? 2 : 1)][ND][4][2];
+        uint32_t pb[NB][ND][8];
         auto weigh = [&](auto masked_c) {
           constexpr bool kMasked = decltype(masked_c)::value;
-          const int at = (int)(x - xr) * kPage + 16 * t4;     // the row's token that this lane holds first
+          const int at = (int)(x - xr) * kPage + my_token;    // the row's token that this lane holds first
+          uint32_t vms[ND][8];
+#pragma unroll
+          for (int p = 0; p < ND; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) vms[p][j] = *(const uint32_t*)(pg + q4_v_ms(ND) + (p * kPage + my_token + 2 * j) * 4);
 #pragma unroll
           for (int rs = 0; rs < RS; ++rs) {
-            const int left = seen[rs] - at;
-            float top = -INFINITY;
+            float f[2], u[2] = {0.f, 0.f}, had[2], fl[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (kMasked) {
-                if (2 * i >= left) t[rs][i].x = -INFINITY;
-                if (2 * i + 1 >= left) t[rs][i].y = -INFINITY;
-              }
-              top = fmaxf(top, fmaxf(t[rs][i].x, t[rs][i].y));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float mn = fmaxf(m[rs], top), ref = mn == -INFINITY ? 0.f : mn;
-            const float drop = m[rs] == -INFINITY ? 0.f : mn - m[rs], fl = ex2(-drop);
-            m[rs] = mn;
-            float2 sum = f2(0.f, 0.f), off[ND];
+            for (int e = 0; e < 2; ++e) {
+              const int left = seen[rs][e] - at;
+              float top = -INFINITY;
 #pragma unroll
-            for (int p = 0; p < ND; ++p) off[p] = f2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              t[rs][i] = f2(ex2(t[rs][i].x - ref), ex2(t[rs][i].y - ref));
-              sum = __fadd2_rn(sum, t[rs][i]);
-            }
-            l[rs] = fmaf(l[rs], fl, sum.x + sum.y);
-            // p s, of which hidden tokens have none whatever their steps are
-            float u = 0.f;
-            float2 w[ND][8];
-#pragma unroll
-            for (int p = 0; p < ND; ++p)
-#pragma unroll
-              for (int x4 = 0; x4 < 4; ++x4) {
-                const uint4 v = *(const uint4*)(pg + q4_v_ms(ND) + (p * kPage + 16 * t4 + 4 * x4) * 4);
-                uint32_t ms[4] = {v.x, v.y, v.z, v.w};
-                if (kMasked) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (4 * x4 + e >= left) ms[e] = 0;
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const float2 pr = t[rs][2 * x4 + y];
-                  const float2 s2 = f2(q4_s(ms[2 * y]), q4_s(ms[2 * y + 1]));
-                  w[p][2 * x4 + y] = __fmul2_rn(pr, s2);
-                  off[p] = __ffma2_rn(pr, base_of<kSplit>(ms[2 * y], ms[2 * y + 1], s2), off[p]);
-                  u = fmaxf(u, fmaxf(w[p][2 * x4 + y].x, w[p][2 * x4 + y].y));
-                }
+              for (int j = 0; j < 8; ++j) {
+                if (kMasked && 2 * j >= left) t[rs][j][e] = -INFINITY;
+                top = fmaxf(top, t[rs][j][e]);
               }
 #pragma unroll
-            for (int p = 0; p < ND; ++p) z[rs][p] = fmaf(z[rs][p], fl, off[p].x + off[p].y);
-            u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 1));
-            u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 2));
-            // O's unit, 2^dl of the reference's: as large as the largest weight asks, and never smaller than it was
-            const float had = dl[rs] - drop, need = u > 0.f ? fmaxf(lg2(u), -112.f) : -INFINITY, now = fmaxf(had, need);
-            if (__any_sync(0xffffffffu, now != had)) {
-              const float fo = had == -INFINITY ? 0.f : ex2(had - now);
-              const float fa = __shfl_sync(0xffffffffu, fo, 8 * t4), fb = __shfl_sync(0xffffffffu, fo, 8 * t4 + 4);
+              for (int x4 = 4; x4 < 32; x4 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x4));
+              const float mn = fmaxf(m[rs][e], top), ref = mn == -INFINITY ? 0.f : mn;
+              const float drop = m[rs][e] == -INFINITY ? 0.f : mn - m[rs][e];
+              fl[e] = ex2(-drop);
+              had[e] = dl[rs][e] - drop;
+              m[rs][e] = mn;
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                t[rs][j][e] = ex2(t[rs][j][e] - ref);
+                sum += t[rs][j][e];
+              }
+              l[rs][e] = fmaf(l[rs][e], fl[e], sum);
+              // p s, of which hidden tokens have none whatever their steps are
+#pragma unroll
+              for (int p = 0; p < ND; ++p) {
+                float off = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const bool hidden = kMasked && 2 * j >= left;
+                  u[e] = fmaxf(u[e], hidden ? 0.f : t[rs][j][e] * q4_s(vms[p][j]));
+                  off = fmaf(t[rs][j][e], hidden ? 0.f : base_of<kSplit>(vms[p][j]), off);
+                }
+                z[rs][e][p] = fmaf(z[rs][e][p], fl[e], off);
+              }
+            }
+#pragma unroll
+            for (int x4 = 4; x4 < 32; x4 <<= 1) {
+              u[0] = fmaxf(u[0], __shfl_xor_sync(0xffffffffu, u[0], x4));
+              u[1] = fmaxf(u[1], __shfl_xor_sync(0xffffffffu, u[1], x4));
+            }
+            // O's unit, 2^dl of the reference's: never smaller than it was, and set anew once the largest weight asks for
+            // more than kSlack above it
+            bool moved = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float need = u[e] > 0.f ? fmaxf(lg2(u[e]), -112.f) : -INFINITY;
+              dl[rs][e] = need > had[e] + kSlack ? need : had[e];
+              moved |= dl[rs][e] != had[e];
+              f[e] = ex2(fminf(kWeightExp - dl[rs][e], 126.f));
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+              const float fa = had[0] == -INFINITY ? 0.f : ex2(had[0] - dl[rs][0]), fb = had[1] == -INFINITY ? 0.f : ex2(had[1] - dl[rs][1]);
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 o[rs][i][0] *= fa;
@@ -399,21 +422,26 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
                 o[rs][i][3] *= fb;
               }
             }
-            dl[rs] = now;
-            const float f = ex2(fminf(kWeightExp - now, 126.f)), fs = f * kSecond;
 #pragma unroll
-            for (int p = 0; p < ND; ++p)
+            for (int j = 0; j < 8; ++j) {
+              const float second = j & 1 ? kSecond : 1.f;
+              const float pa = t[rs][j][0] * (f[0] * second), pc = t[rs][j][1] * (f[1] * second);
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                const float2 a0 = __fmul2_rn(w[p][2 * s], f2(f, f)), a1 = __fmul2_rn(w[p][2 * s + 1], f2(fs, fs));
+              for (int p = 0; p < ND; ++p) {
+                const float st = q4_s(vms[p][j]);
+                float wa = pa * st, wb = pc * st;
+                if (kMasked && 2 * j >= seen[rs][0] - at) wa = 0.f;
+                if (kMasked && 2 * j >= seen[rs][1] - at) wb = 0.f;
                 if constexpr (kSplit) {
-                  split_half2(a0.x, a0.y, 1.f, pb[0][p][s][0], pb[1][p][s][0]);
-                  split_half2(a1.x, a1.y, 1.f, pb[0][p][s][1], pb[1][p][s][1]);
+                  uint32_t hi, lo;
+                  split_half2(wa, wb, 1.f, hi, lo);
+                  pb[0][p][j] = transpose8(hi);
+                  pb[1][p][j] = transpose8(lo);
                 } else {
-                  pb[rs][p][s][0] = pack_half2(a0.x, a0.y);
-                  pb[rs][p][s][1] = pack_half2(a1.x, a1.y);
+                  pb[rs][p][j] = transpose8(pack_half2(wa, wb));
                 }
               }
+            }
           }
         };
         if ((int)(x - xr) * kPage + kPage > seen_min) weigh(std::true_type{}); else weigh(std::false_type{});
@@ -428,8 +456,7 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
             codes_to_f16<kSplit>(vw[0][s >> 1], s & 1, c.x, c.z);
             codes_to_f16<kSplit>(vw[1][s >> 1], s & 1, c.y, c.w);
 #pragma unroll
-            for (int k = 0; k < RS * (kSplit ? 2 : 1); ++k)
-              mma16816(o[kSplit ? 0 : k][i], c, pb[k][i / 4][s][0], pb[k][i / 4][s][1]);
+            for (int k = 0; k < NB; ++k) mma16816(o[kSplit ? 0 : k][i], c, pb[k][i / 4][2 * s], pb[k][i / 4][2 * s + 1]);
           }
         }
         __syncwarp();                            // every lane has read the values
@@ -440,32 +467,31 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
 
       // ---- the warps' parts of the segment together, in the reference's unit
 #pragma unroll
-      for (int rs = 0; rs < RS; ++rs) {
-        l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
-        l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
-        float* mw = sM + (warp * PR + 8 * rs) * kPitch;
-        // squared: 2^dl alone may be subnormal
-        const float up = dl[rs] == -INFINITY ? 0.f : ex2(dl[rs] * 0.5f + 0.5f * (kCodeExp - kWeightExp));
-        const float ua = __shfl_sync(0xffffffffu, up, 8 * t4), ub = __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+      for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-        for (int p = 0; p < ND; ++p) {
-          z[rs][p] += __shfl_xor_sync(0xffffffffu, z[rs][p], 1);
-          z[rs][p] += __shfl_xor_sync(0xffffffffu, z[rs][p], 2);
-          const float za = __shfl_sync(0xffffffffu, z[rs][p], 8 * t4), zb = __shfl_sync(0xffffffffu, z[rs][p], 8 * t4 + 4);
+        for (int e = 0; e < 2; ++e) {
+          float* mw = sM + (warp * PR + 8 * rs + 2 * t4 + e) * kPitch;
+          // squared: 2^dl alone may be subnormal
+          const float up = dl[rs][e] == -INFINITY ? 0.f : ex2(dl[rs][e] * 0.5f + 0.5f * (kCodeExp - kWeightExp));
 #pragma unroll
-          for (int i = 4 * p; i < 4 * p + 4; ++i) {
-            float* dst = mw + 2 * t4 * kPitch + 16 * i + gid;
-            dst[0] = fmaf(o[rs][i][0] * ua, ua, za);
-            dst[8] = fmaf(o[rs][i][2] * ua, ua, za);
-            dst[kPitch] = fmaf(o[rs][i][1] * ub, ub, zb);
-            dst[kPitch + 8] = fmaf(o[rs][i][3] * ub, ub, zb);
+          for (int p = 0; p < ND; ++p) {
+            float zp = z[rs][e][p];
+#pragma unroll
+            for (int x4 = 4; x4 < 32; x4 <<= 1) zp += __shfl_xor_sync(0xffffffffu, zp, x4);
+#pragma unroll
+            for (int i = 4 * p; i < 4 * p + 4; ++i) {
+              mw[16 * i + gid] = fmaf(o[rs][i][e] * up, up, zp);
+              mw[16 * i + 8 + gid] = fmaf(o[rs][i][2 + e] * up, up, zp);
+            }
+          }
+          float sum = l[rs][e];
+#pragma unroll
+          for (int x4 = 4; x4 < 32; x4 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x4);
+          if (gid == 0) {
+            mw[64 * ND] = m[rs][e];
+            mw[64 * ND + 1] = sum;
           }
         }
-        if (t4 == 0) {
-          mw[gid * kPitch + 64 * ND] = m[rs];
-          mw[gid * kPitch + 64 * ND + 1] = l[rs];
-        }
-      }
       __syncthreads();
       const bool whole = sa == xr && sb == xr + np;
       const int64_t first = first_of(plan, xr), last = last_of(plan, xr, np);
