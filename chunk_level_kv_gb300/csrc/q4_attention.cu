@@ -384,16 +384,19 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
                 sum += t[rs][j][e];
               }
               l[rs][e] = fmaf(l[rs][e], fl[e], sum);
-              // p s, of which hidden tokens have none whatever their steps are
+              // the largest p s, of which hidden tokens have none whatever their steps are
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float st = q4_s(vms[0][j]);
+#pragma unroll
+                for (int p = 1; p < ND; ++p) st = fmaxf(st, q4_s(vms[p][j]));
+                u[e] = fmaxf(u[e], kMasked && 2 * j >= left ? 0.f : t[rs][j][e] * st);
+              }
 #pragma unroll
               for (int p = 0; p < ND; ++p) {
                 float off = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const bool hidden = kMasked && 2 * j >= left;
-                  u[e] = fmaxf(u[e], hidden ? 0.f : t[rs][j][e] * q4_s(vms[p][j]));
-                  off = fmaf(t[rs][j][e], hidden ? 0.f : base_of<kSplit>(vms[p][j]), off);
-                }
+                for (int j = 0; j < 8; ++j) off = fmaf(t[rs][j][e], kMasked && 2 * j >= left ? 0.f : base_of<kSplit>(vms[p][j]), off);
                 z[rs][e][p] = fmaf(z[rs][e][p], fl[e], off);
               }
             }
