@@ -28,20 +28,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Eight elements of a row.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *(const uint4*)p;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight elements of a row as they lie in memory, and as fp32.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) { a = ((const float4*)p)[0]; b = ((const float4*)p)[1]; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
-}
+};
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *(const uint4*)p; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
   *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -56,6 +66,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The 4 x 4 bytes of four words transposed: byte b of word i goes to byte i of word b.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, b, 0x5410);
+  w[1] = __byte_perm(a, b, 0x7632);
+  w[2] = __byte_perm(c, d, 0x5410);
+  w[3] = __byte_perm(c, d, 0x7632);
+}
+
 // ------------------------------------------------------------ writing
 
 struct Q4AppendArgs {
@@ -68,7 +88,8 @@ struct Q4AppendArgs {
 // (blockIdx.z 0) or of the values (1).  Eight lanes hold a group of a token, eight columns
 // each, and find its smallest and largest value by shuffles.  A lane's eight codes are a word
 // of the keys' part; values go through shared memory, a byte a code, and leave as words of
-// eight tokens of a column, merged with the older tokens' codes where a word is shared.
+// eight tokens of a column (bytes paired into nibbles and transposed 4 x 4 in registers),
+// merged with the older tokens' codes where a word is shared.
 template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
@@ -92,6 +113,12 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
     uint32_t* k_words = (uint32_t*)pg;
     uint32_t* ms_words = (uint32_t*)(pg + (which ? q4_v_ms(ND) : q4_k_ms(ND)));
     if (inside) {
+      Vec8<T> raw[kVecs];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {                              // every load is under way before the first is used
+        const int v = i * kIoThreads + tid, t = v / kV8, c = v % kV8 * 8;
+        if (t < nt && c < g.d) raw[i].load(x + t * a.st_t + c);
+      }
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
         const int v = i * kIoThreads + tid, t = v / kV8, c = v % kV8 * 8;
@@ -99,7 +126,7 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
         const bool live = t < nt && c < g.d;
         float w[8], lo = INFINITY, hi = -INFINITY;
         if (live) {
-          load8(x + t * a.st_t + c, w);
+          raw[i].get(w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             lo = min_nan(lo, w[e]);
@@ -149,16 +176,25 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
     if (which == 1) {
       __syncthreads();
       uint32_t* v_words = (uint32_t*)(pg + q4_v(ND));
-      for (int i = tid; inside && i < 64 * ND * 8; i += kIoThreads) {
-        const int c = (i >> 7) * 16 + ((i >> 1) & 1) * 8 + ((i >> 4) & 7), t = ((i >> 2) & 3) * 16 + (i & 1) * 8;   // word i
+      for (int i = tid; inside && i < 64 * ND * 2; i += kIoThreads) {
+        // columns c .. c + 3, tokens t .. t + 7; the words of a warp lie in runs of 16
+        const int c = (i >> 5) * 16 + ((i >> 1) & 1) * 8 + ((i >> 4) & 1) * 4, t = ((i >> 2) & 3) * 16 + (i & 1) * 8;
         if (t >= t0 + nt || t + 8 <= t0) continue;
-        uint32_t w = 0, keep = 0;
+        uint32_t b[8], keep = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (t + e >= t0 && t + e < t0 + nt) w |= (uint32_t)s_code[(t + e) * kPitch + c] << (4 * q4_nibble(e));
-          else keep |= 15u << (4 * q4_nibble(e));
+          const bool fresh = t + e >= t0 && t + e < t0 + nt;
+          b[e] = fresh ? *(const uint32_t*)(s_code + (t + e) * kPitch + c) : 0;
+          if (!fresh) keep |= 15u << (4 * q4_nibble(e));
         }
-        v_words[i] = keep ? w | (v_words[i] & keep) : w;
+        // byte k of a column's word holds nibbles 2 k and 2 k + 1: items 0 and 2, 4 and 6, 1 and 3, 5 and 7
+        uint32_t w[4] = {b[0] | b[2] << 4, b[4] | b[6] << 4, b[1] | b[3] << 4, b[5] | b[7] << 4};
+        transpose4(w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t* p = v_words + q4_v_word(c + j, t);
+          *p = keep ? w[j] | (*p & keep) : w[j];
+        }
       }
     }
   }
