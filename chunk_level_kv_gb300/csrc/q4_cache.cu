@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kIoThreads = 256;
 constexpr float kInv15 = 1.0f / 15.0f;
+constexpr float kRound = 12582912.f;                         // 1.5 2^23
 constexpr float kSmallest = 7.888609052210118e-31f;          // 2^-100: a group that spans less has step 0
 
 // Smallest and largest, NaN if either is.
@@ -38,6 +39,13 @@ struct Vec8<float> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
+  // smallest and largest element (NaN if one is)
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    float x[8];
+    get(x);
+    lo = min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
+    hi = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
+  }
 };
 template <>
 struct Vec8<__nv_bfloat16> {
@@ -50,6 +58,14 @@ struct Vec8<__nv_bfloat16> {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+  }
+  // in pairs: bf16 comparisons are exact
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    const __nv_bfloat162* x = (const __nv_bfloat162*)&v;
+    const __nv_bfloat162 l = __hmin2_nan(__hmin2_nan(x[0], x[1]), __hmin2_nan(x[2], x[3]));
+    const __nv_bfloat162 h = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+    lo = min_nan(__low2float(l), __high2float(l));
+    hi = max_nan(__low2float(h), __high2float(h));
   }
 };
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
@@ -85,16 +101,17 @@ struct Q4AppendArgs {
 };
 
 // One CTA writes the part of one page that a row's new tokens fill, of the keys
-// (blockIdx.z 0) or of the values (1).  Eight lanes hold a group of a token, eight columns
-// each, and find its smallest and largest value by shuffles.  A lane's eight codes are a word
-// of the keys' part; values go through shared memory, a byte a code, and leave as words of
+// (blockIdx.z 0) or of the values (1).  Four lanes hold a group of a token, 16 columns
+// each, and find its smallest and largest value by shuffles (with eight lanes, what a group
+// costs once was two thirds of the instructions).  A lane's codes are two words of the keys' part; values go through shared memory, a byte a code, and leave as words of
 // eight tokens of a column (bytes paired into nibbles and transposed 4 x 4 in registers),
 // merged with the older tokens' codes where a word is shared.
 template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
                  uint8_t* __restrict__ pages) {
-  constexpr int kV8 = 8 * ND, kVecs = kPage * kV8 / kIoThreads;      // vectors of a token, and of a thread
+  constexpr int kV16 = 4 * ND, kVecs = ND;                           // 16-column pieces of a token, and of a thread
+  static_assert(kPage * kV16 == kVecs * kIoThreads, "a page's pieces");
   constexpr int kPitch = 64 * ND + 4;                                // bytes of a token's codes in shared memory
   __shared__ __align__(16) uint8_t s_code[kPage * kPitch];
   pdl_wait();
@@ -113,28 +130,29 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
     uint32_t* k_words = (uint32_t*)pg;
     uint32_t* ms_words = (uint32_t*)(pg + (which ? q4_v_ms(ND) : q4_k_ms(ND)));
     if (inside) {
-      Vec8<T> raw[kVecs];
+      Vec8<T> raw[kVecs][2];
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {                              // every load is under way before the first is used
-        const int v = i * kIoThreads + tid, t = v / kV8, c = v % kV8 * 8;
-        if (t < nt && c < g.d) raw[i].load(x + t * a.st_t + c);
+        const int v = i * kIoThreads + tid, t = v / kV16, c = v % kV16 * 16;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (t < nt && c + 8 * k < g.d) raw[i][k].load(x + t * a.st_t + c + 8 * k);
       }
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        const int v = i * kIoThreads + tid, t = v / kV8, c = v % kV8 * 8;
-        if ((i * kIoThreads + (tid & ~31)) / kV8 >= nt) break;       // the whole warp is past the tokens
-        const bool live = t < nt && c < g.d;
-        float w[8], lo = INFINITY, hi = -INFINITY;
-        if (live) {
-          raw[i].get(w);
+        const int v = i * kIoThreads + tid, t = v / kV16, c = v % kV16 * 16;
+        if ((i * kIoThreads + (tid & ~31)) / kV16 >= nt) break;      // the whole warp is past the tokens
+        float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            lo = min_nan(lo, w[e]);
-            hi = max_nan(hi, w[e]);
+        for (int k = 0; k < 2; ++k)
+          if (t < nt && c + 8 * k < g.d) {
+            float l, h;
+            raw[i][k].range(l, h);
+            lo = min_nan(lo, l);
+            hi = max_nan(hi, h);
           }
-        }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
+        for (int o = 1; o < 4; o <<= 1) {
           lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
           hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
@@ -149,25 +167,31 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
           s = 0.f;
         }
         const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-        uint32_t code = 0;
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            code |= (uint32_t)max(0, min(15, bad ? 0 : __float2int_rn((w[e] - m) * inv))) << (4 * q4_nibble(e));
-        }
         if (t < nt) {
-          if (which == 0) {
-            k_words[q4_k_word(ND, t0 + t, c)] = code;
-          } else {
-            uint32_t lo4 = 0, hi4 = 0;                               // a byte a code, in the columns' order
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              lo4 |= (code >> (4 * q4_nibble(e)) & 15u) << (8 * e);
-              hi4 |= (code >> (4 * q4_nibble(e + 4)) & 15u) << (8 * e);
+          for (int k = 0; k < 2; ++k) {
+            // The codes as whole numbers in fp32, 0 to 15: 15 s is not below hi - m, so (x - m) / s rounds to 15 at most.
+            // Adding and taking off 1.5 2^23 rounds to the nearest, ties to even.
+            const bool zero = bad || c + 8 * k >= g.d;               // codes of no value, or of columns past the end
+            float w[8];
+            raw[i][k].get(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __fadd_rn(__fmul_rn(w[e] - m, inv), kRound) - kRound;
+            if (which == 0) {
+              // nibbles 0 .. 3 are items 0, 2, 4, 6: four codes are a whole number below 2^16
+              const float even = fmaf(fmaf(fmaf(w[6], 16.f, w[4]), 16.f, w[2]), 16.f, w[0]);
+              const float odd = fmaf(fmaf(fmaf(w[7], 16.f, w[5]), 16.f, w[3]), 16.f, w[1]);
+              const uint32_t word = __byte_perm(__float_as_uint(even + kRound), __float_as_uint(odd + kRound), 0x5410);
+              k_words[q4_k_word(ND, t0 + t, c + 8 * k)] = zero ? 0 : word;
+            } else {
+              uint32_t* dst = (uint32_t*)(s_code + (t0 + t) * kPitch + c + 8 * k);       // a byte a code, in the columns' order
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t four = __byte_perm(__float_as_uint(fmaf(w[4 * e + 1], 256.f, w[4 * e]) + kRound),
+                                                  __float_as_uint(fmaf(w[4 * e + 3], 256.f, w[4 * e + 2]) + kRound), 0x5410);
+                dst[e] = zero ? 0 : four;
+              }
             }
-            uint32_t* dst = (uint32_t*)(s_code + (t0 + t) * kPitch + c);
-            dst[0] = lo4;
-            dst[1] = hi4;
           }
           if ((c & 63) == 0) ms_words[(c >> 6) * kPage + t0 + t] = (__float_as_uint(m) >> 16) | (__float_as_uint(s) & 0xFFFF0000u);
         }
