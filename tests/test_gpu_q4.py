@@ -593,3 +593,19 @@ def test_calls_refuse_tensors_outside_the_gpu(ckv):
             with pytest.raises(ValueError):
                 call(*args[:i], args[i].cpu(), *args[i + 1:])
     assert ckv.chunkkv_launch_count() == before
+
+
+# ------------------------------------------------------------------ together
+
+def test_the_example_serves_a_layer_in_4_bits(ckv):
+    # a next turn, decoding and a second compression over the cache: each output within what the rounding of keys and
+    # values to 4 bits does (half a step of 1/15 of a group's range, 5 for normal data: 0.1 relative to a value)
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import serve_layer
+    result = serve_layer.serve(bits=4)
+    assert len(result["errors"]) == 40 and max(result["errors"]) < 0.3 and result["turn_error"] < 0.3
+    assert result["lengths"][2] != result["lengths"][1] and result["free_pages"] > 0
+    again = serve_layer.serve(bits=4)
+    assert again["errors"] == result["errors"]        # the same run gives the same bits
