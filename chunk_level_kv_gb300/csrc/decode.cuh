@@ -120,7 +120,7 @@ struct Cursor {
 
 // The pages of all rows in order (or what else work is counted in: size(i) of item i) are cut
 // into one contiguous run [x0, x1) per CTA, whatever the rows' lengths, which only the device knows: every CTA finds its run by a scan over the
-// lengths.  Rows of up to kWholeRow pages are not cut: a row in two pieces costs the CTAs that
+// lengths.  Rows of up to kWholeRow pages are not cut (each kernel has its own number): a row in two pieces costs the CTAs that
 // share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's share of
 // the bandwidth, and the eight warps take eight pages at once.  A cut within kNearEnd pages
 // of a long row's begin or end moves there, so that a CTA seldom has a second row for a few
@@ -139,8 +139,9 @@ struct Run {
   int64_t total, nc;                             // pages of all rows, and CTAs that have a run
 };
 // Ends in shared memory; to be read after a __syncthreads.
+// whole: items of up to this size are not cut.
 template <int W, typename F>
-__device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh) {
+__device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh, int whole = kWholeRow) {
   constexpr int kThreads = 32 * W;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = (count + kThreads - 1) / kThreads;
@@ -179,7 +180,7 @@ __device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh) {
         x += n;
       }
       // short rows stay in one piece, and a long one's end is no place to cut either
-      sh.cut[k] = n <= kWholeRow || cut - x <= kNearEnd ? x : x + n - cut <= kNearEnd ? x + n : cut;
+      sh.cut[k] = n <= whole || cut - x <= kNearEnd ? x : x + n - cut <= kNearEnd ? x + n : cut;
       sh.row[k] = r;
       sh.start[k] = x;
     }
@@ -187,8 +188,8 @@ __device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh) {
   return {total, nc};
 }
 template <int W>
-__device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restrict__ lens, RunShared<W>& sh) {
-  return plan_run<W>(g.rows, [&](int r) { return pages_of(safe_len(lens[r], g.max_pages)); }, sh);
+__device__ __forceinline__ Run plan_run(const Q8Geom& g, const int32_t* __restrict__ lens, RunShared<W>& sh, int whole = kWholeRow) {
+  return plan_run<W>(g.rows, [&](int r) { return pages_of(safe_len(lens[r], g.max_pages)); }, sh, whole);
 }
 // The CTAs that share an item whose n units begin at unit x and that is cut: from the last one whose cut is at its
 // begin or moves there, to the last one whose cut does not move to its end.

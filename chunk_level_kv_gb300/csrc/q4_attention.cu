@@ -49,6 +49,10 @@ constexpr int kMaxGroups = 16;                   // passes in one launch
 constexpr int kCountByte = 32;                   // the counts of parts that have arrived, as decode attention's (q8_attention.cu)
 static_assert(kCountByte + kMaxGrid * kMaxGroups <= (int)kServeHeader, "the counts lie in the serving header");
 constexpr float kWeightExp = 12.f, kSlack = 3.f;  // the largest weight is 2^12 when O's unit is set, and 2^15 at most (f16 ends at 2^16)
+// Rows that take the warps up to this many rounds are not cut: joining parts costs a call about 4 us, a round 1.
+// (128 rows of 12 pages 10.6 us, cut from 8 pages on 20 us; 512 rows of 24 to 30 pages 47 and 52 us.)
+constexpr int kWholeRounds = 3;
+static_assert(kWholeRounds * 8 > 2 * kNearEnd, "a row's two ends do not meet");
 constexpr int kQueryExp = 14;                    // the largest query element is in [2^14, 2^15)
 
 struct Q4AttnArgs {
@@ -149,7 +153,7 @@ q4_attention_kernel(Q4Geom g, Q4AttnArgs a, const uint8_t* __restrict__ pages, c
   __syncwarp();
   pdl_wait();
 
-  const Run plan = plan_run<W>(g, lens, run);
+  const Run plan = plan_run<W>(g, lens, run, kWholeRounds * W);
   const int64_t nc = plan.nc;
   const int p0 = a.p0 + blockIdx.y * PR, gn = min(PR, a.n_q * a.G - p0);
   auto out_at = [&](int b, int h, int row) {     // where row `row` of the pass is written
