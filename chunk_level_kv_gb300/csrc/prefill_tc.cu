@@ -49,13 +49,10 @@
 // other's products back: a block pair took 3250 cycles), 11 V check, which holds every V
 // block until it has seen it there.
 // Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
-#include <mutex>
 
 #include "tc_softmax.cuh"
+#include "tensor_map.cuh"
 
 namespace chunkkv {
 namespace {
@@ -696,20 +693,6 @@ join_kernel(const __grid_constant__ TcGeom g, const __grid_constant__ PrefillTab
 }
 
 // ---------------------------------------------------------------- host side
-using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
-EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = (EncodeFn)p;
-  });
-  return fn;
-}
-
 // [rows][heads][d] bf16 in boxes of 64 columns of some heads and rows; columns past d
 // and rows past the end read as zeros.  The stride of an axis of extent 1 is unused.
 bool encode(EncodeFn enc, CUtensorMap* map, const void* base, int d, int heads, int rows, int64_t st, int64_t sh,

@@ -37,15 +37,12 @@
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
 // 11 scales, 12-19 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
-#include <mutex>
 
 #include "decode.cuh"
 #include "q4.cuh"
 #include "tc_softmax.cuh"
+#include "tensor_map.cuh"
 
 namespace chunkkv {
 
@@ -390,7 +387,10 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   constexpr int kKPanel = kTile * 128, kVPanel = D * 128;     // 64 columns of 128 keys; 64 keys of D columns
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {                   // the swizzle pattern needs 1024-byte alignment
-    if (threadIdx.x == 0) atomicCAS(err, 0, (int)kDevMisalignedSmem);
+    if (threadIdx.x == 0) {
+      atomicCAS(err, 0, (int)kDevMisalignedSmem);
+      g.cut[blockIdx.x] = make_int2(-1, 0);
+    }
     return;
   }
   uint8_t* sQ = smem;                             // two tiles
@@ -924,20 +924,6 @@ q4_join_kernel(const __grid_constant__ Q4TcGeom g) {
 }
 
 // ---------------------------------------------------------------- host side
-using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
-EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = (EncodeFn)p;
-  });
-  return fn;
-}
-
 template <int ND>
 cudaError_t launch(const CUtensorMap& map, const Q4TcGeom& g, int32_t* err, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
@@ -976,7 +962,7 @@ cudaError_t launch_q4_attention_tc(const Q4Geom& c, int G, int n_q, float alpha,
   // read as zeros.  The stride of an axis of extent 1 is unused.
   CUtensorMap map;
   cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.Hkv * G, (cuuint64_t)n_q, (cuuint64_t)B};
-  cuuint64_t strides[3] = {c.Hkv * G == 1 ? 16 : (cuuint64_t)q_sh * 2, n_q == 1 ? 16 : (cuuint64_t)q_st * 2, B == 1 ? 16 : (cuuint64_t)q_sb * 2};
+  cuuint64_t strides[3] = {(int64_t)c.Hkv * G == 1 ? 16 : (cuuint64_t)q_sh * 2, n_q == 1 ? 16 : (cuuint64_t)q_st * 2, B == 1 ? 16 : (cuuint64_t)q_sb * 2};
   cuuint32_t box[4] = {64, (cuuint32_t)gp, (cuuint32_t)pos, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -75,8 +75,8 @@ int sm_count() {
 bool valid_dtype(int dtype) { return dtype == CHUNKKV_F32 || dtype == CHUNKKV_BF16; }
 int elt_size(int dtype) { return dtype == CHUNKKV_BF16 ? 2 : 4; }
 bool stride_ok(int64_t s, int elt) { return s >= 0 && s < (INT64_MAX >> 32) && (s * elt) % 16 == 0; }
-// Query rows of a KV head are counted in 32 bits, with room for a pass of them more.
-bool rows_ok(int32_t G, int32_t n_q) { return (int64_t)G * n_q <= INT32_MAX / 2; }
+// Query rows of a KV head, and query heads, are counted in 32 bits, with room for a pass of them more.
+bool rows_ok(int32_t Hkv, int32_t G, int32_t n_q) { return (int64_t)G * n_q <= INT32_MAX / 2 && (int64_t)Hkv * G <= INT32_MAX / 2; }
 bool scale_ok(float s) { return s > 0.f && isfinite(s); }
 
 chunkkv_status check_prefill(const chunkkv_prefill_params* p) {
@@ -417,14 +417,14 @@ chunkkv_status chunkkv_q4_workspace_size(const chunkkv_q4_cache* c, int32_t dtyp
   const chunkkv_status st = check_cache(c, false, &g);
   if (st != CHUNKKV_OK) return st;
   if (bytes == nullptr || !valid_dtype(dtype) || G < 1 || n_q < 1) return CHUNKKV_ERR_INVALID_ARG;
-  if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
+  if (!rows_ok(g.Hkv, G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
   *bytes = q4_workspace(g, dtype, G, n_q);
   return CHUNKKV_OK;
 }
 
 int32_t chunkkv_q4_path(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q) {
   Q4Geom g;
-  if (check_cache(c, false, &g) != CHUNKKV_OK || !valid_dtype(dtype) || G < 1 || n_q < 1 || !rows_ok(G, n_q)) return -1;
+  if (check_cache(c, false, &g) != CHUNKKV_OK || !valid_dtype(dtype) || G < 1 || n_q < 1 || !rows_ok(g.Hkv, G, n_q)) return -1;
   return q4_many_rows(g, dtype, G, n_q) ? 1 : 0;
 }
 
@@ -441,7 +441,7 @@ chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, in
   const int64_t strides[6] = {q_stride_b, q_stride_t, q_stride_h, o_stride_b, o_stride_t, o_stride_h};
   for (int64_t s : strides)
     if (!stride_ok(s, elt)) return CHUNKKV_ERR_INVALID_ARG;
-  if (!rows_ok(G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
+  if (!rows_ok(g.Hkv, G, n_q)) return CHUNKKV_ERR_UNSUPPORTED;
   if (g.rows == 0) return CHUNKKV_OK;
   if (!aligned(q) || !aligned(out) || !aligned(ws) || (q_lens != nullptr && !aligned(q_lens, 4))) return CHUNKKV_ERR_INVALID_ARG;
   if (ws_bytes < q4_workspace(g, dtype, G, n_q)) return CHUNKKV_ERR_WORKSPACE_TOO_SMALL;

@@ -55,6 +55,7 @@ def test_call_arguments(ckv):
         return LIB.chunkkv_q4_workspace_size(c, dtype, G, n_q, to)
     assert size(G=0) == size(n_q=0) == size(dtype=2) == size(to=None) == INVALID
     assert size(G=1 << 16, n_q=1 << 15) == UNSUPPORTED
+    assert size(G=1 << 30) == UNSUPPORTED                                          # 2^31 query heads
     assert size() == OK and n.value >= 256
     assert LIB.chunkkv_q4_path(c, 1, 2, 1) in (0, 1) and LIB.chunkkv_q4_path(c, 1, 2, 0) == LIB.chunkkv_q4_path(c, 3, 2, 1) == -1
     # resize
