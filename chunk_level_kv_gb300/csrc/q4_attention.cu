@@ -31,8 +31,13 @@
 // A weight p s is held as a multiple of the largest p s of its row so far (2^d times 2^max t), so
 // that f16 holds it however far apart the steps of a row lie.
 //
-// Work split, join of a row's parts and pages under way: as for the 8-bit cache (decode.cuh,
-// q8_attention.cu); a page with its steps is one copy.
+// Work split and join of a row's parts: as for the 8-bit cache (decode.cuh, q8_attention.cu).  A
+// warp holds one page, whose keys and values are copied again as soon as each has been read.
+//
+// Measured: 64 sequences x 4 KV heads of 12 to 13 thousand tokens, 7 heads each (0.47 GB) 96 us,
+// 4.9 TB/s, 72 % of a copy's rate (1050 instructions a page; issue slots 57 %, integer pipe 56 %,
+// tensor pipe 26 %); one sequence of 8 KV heads x 6.5 thousand tokens 12.6 us, 16 sequences of 256
+// to 300 tokens 8.1 us (latency); 16 query rows on 64 rows of 6.5 thousand tokens 48 us, cold.
 #include <algorithm>
 #include <type_traits>
 
