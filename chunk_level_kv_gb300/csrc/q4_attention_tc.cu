@@ -39,7 +39,7 @@
 // to the exponentials of 256 rows the converting warps issue 3 thousand instructions for its 32768
 // codes, and a tile's softmax, 950 cycles alone, takes 1.9 thousand beside them (without the
 // conversion, timing only, 597 us of 726).  Measured at 128 columns: 4001 queries on 16 to 17 thousand
-// tokens of 28 / 4 heads 0.69 ms, 1.2 PFLOP/s of the visible pairs; 300 to 700 queries of two sequences
+// tokens of 28 / 4 heads 0.68 ms, 1.2 PFLOP/s of the visible pairs; 300 to 700 queries of two sequences
 // on 4.9 to 9.7 thousand tokens of 32 / 8 heads 102 us; 5 queries of eight sequences on 6.5 thousand 66 us.
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
@@ -245,13 +245,17 @@ __device__ __forceinline__ uint32_t reach_of(uint8_t* const (&half)[2], int left
   }
   return __reduce_max_sync(0xffffffffu, __float_as_uint(most));
 }
-// In place: scaled, as two f16.
-template <int ND>
+// In place: scaled, as two f16.  PAIRS: the m of two tokens, and then their s (of odd pairs s / 16, see expand).
+template <int ND, bool PAIRS>
 __device__ __forceinline__ void scale_steps(uint8_t* const (&half)[2], float by, int lane, const uint4 (&w)[ND]) {
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     int token;
-    *steps_at<ND>(half, i, lane, token) = make_uint4(scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by));
+    uint4* to = steps_at<ND>(half, i, lane, token);
+    const uint32_t x[4] = {scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by)};
+    *to = PAIRS ? make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x5410),
+                             sixteenth(__byte_perm(x[2], x[3], 0x7632)))
+                : make_uint4(x[0], x[1], x[2], x[3]);
   }
 }
 // A block's scales: what takes back that its keys and values were multiplied by 2^(kTopExp - EK), 2^(kTopExp - EV).
@@ -356,25 +360,23 @@ __device__ __forceinline__ int expand_values(const uint8_t* half, uint8_t* tile,
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const uint4 v = *(const uint4*)(half + 2048 * ND + (group * kPage + 16 * t4 + 4 * x) * 4);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};         // m, s, m, s of two tokens each
     if (MASKED) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int token = 16 * t4 + 4 * x + e;
-        if (token >= left) {
-          w[e] = 0;
-        } else if ((w[e] & 0x7C00u) == 0x7C00u) {
-          w[e] = 0;
-          bad = min(bad, token);
+        const int token = 16 * t4 + 4 * x + e, shift = 16 * (e & 1);
+        const bool gone = token >= left, nan = (w[e & 2] >> shift & 0x7C00u) == 0x7C00u;
+        if (!gone && nan) bad = min(bad, token);
+        if (gone || nan) {
+          w[e & 2] &= 0xFFFF0000u >> shift;
+          w[(e & 2) + 1] &= 0xFFFF0000u >> shift;
         }
       }
     }
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const int k = 2 * (x & 1) + y;
-      m[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x5410);
-      s[x >> 1][k] = __byte_perm(w[2 * y], w[2 * y + 1], 0x7632);
-      if (y) s[x >> 1][k] = sixteenth(s[x >> 1][k]);
+      m[x >> 1][2 * (x & 1) + y] = w[2 * y];
+      s[x >> 1][2 * (x & 1) + y] = w[2 * y + 1];
     }
   }
 #pragma unroll 1
@@ -777,8 +779,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           const uint32_t kt = reach_of<ND>(half[0], left, lane, kw);
           const uint32_t vt = reach_of<ND>(half[1], left, lane, vw);
           const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
-          scale_steps<ND>(half[0], power_of_two(kTopExp - ek), lane, kw);
-          scale_steps<ND>(half[1], power_of_two(kTopExp - ev), lane, vw);
+          scale_steps<ND, false>(half[0], power_of_two(kTopExp - ek), lane, kw);
+          scale_steps<ND, true>(half[1], power_of_two(kTopExp - ev), lane, vw);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");        // the next copy writes here
           __syncwarp();
           if (lane == 0) {
@@ -802,7 +804,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     // tokens (keys) or of its columns (values)
     const int w = warp - 12, page = w & 1, part = w >> 1;
     uint32_t pc = 0;                              // halves of blocks so far
-    int st = 0;
+    int st = 0, ps = page;                        // stage and page of codes in turn
     uint32_t ph = 0;
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
@@ -814,9 +816,9 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       bool ok = true;
       for (int b = 0; b < 2 * nb && ok; ++b) {
         const int j = nb - 1 - (b >> 1);
-        const uint32_t bc = pc >> 1, ps = (2 * pc + page) % kPacked;
+        const uint32_t bc = pc >> 1;
         // the copies have landed once the scales are there
-        ok = wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue) &&
+        ok = ((b & 1) != 0 || wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue)) &&
              wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
         if (!ok) break;
         const uint8_t* src = sP + ps * kHalf;
@@ -842,6 +844,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           mbar_arrive(packed_empty + 8 * ps);
         }
         ++pc;
+        ps = ps + 2 >= kPacked ? ps + 2 - kPacked : ps + 2;
         if (++st == kStages) { st = 0; ph ^= 1; }
       }
       if (!ok) break;

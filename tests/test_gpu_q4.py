@@ -338,6 +338,25 @@ def test_several_query_tokens(ckv, dtype, d, B, Hkv, G, n_q, lens):
         assert torch.equal(torch.where(out == 7.0, 0.0, out.float()), torch.where(out == 7.0, 0.0, again.float()))
 
 
+@pytest.mark.parametrize("n_q,G,d,extra", [(1100, 4, 128, 0), (600, 7, 128, 3), (333, 1, 64, 129), (257, 128, 64, 0), (40, 300, 8, 2)])
+def test_a_whole_prompt_over_its_own_cache(ckv, n_q, G, d, extra):
+    # every token a query, each sees itself and those before it; many units, and heads that make several groups
+    cache, g = random_cache(ckv, 1, 2, d, [n_q + extra, n_q], seed=n_q, offset=0.3)
+    q = torch.randn(1, n_q, 2 * G, d, generator=g, device=DEV).to(BF)
+    check(ckv, cache, q, ckv.q4_attention(cache, 0, q), 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("dtype,n_q", [(BF, 4), (BF, 33), (F32, 3)])
+def test_axes_that_are_repeated(ckv, dtype, n_q):
+    # one query for all heads, or for all sequences (strides of zero): no tensor map can address it
+    cache, g = random_cache(ckv, 2, 2, 64, [200, 70, 64, 130], seed=23)
+    for shape in ((2, n_q, 1, 64), (1, n_q, 8, 64), (2, 1, 8, 64)):
+        q = torch.randn(*shape, generator=g, device=DEV).to(dtype).expand(2, n_q, 8, 64)
+        out = torch.full((2, n_q, 8, 64), float("nan"), dtype=dtype, device=DEV)
+        ckv.q4_attention(cache, 0, q, out=out)
+        check(ckv, cache, q, out, 1 / 8)
+
+
 def test_many_rows(ckv):
     lens = [int(x) for x in torch.randint(0, 200, (1200,), generator=torch.Generator().manual_seed(1))]
     cache, g = random_cache(ckv, 300, 4, 64, lens, seed=6)
