@@ -139,9 +139,9 @@ struct Run {
   int64_t total, nc;                             // pages of all rows, and CTAs that have a run
 };
 // Ends in shared memory; to be read after a __syncthreads.
-// whole: items of up to this size are not cut.
+// whole: items of up to this size are not cut; least: a CTA's run is not shorter (but for the last ones).
 template <int W, typename F>
-__device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh, int whole = kWholeRow) {
+__device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh, int whole = kWholeRow, int least = 1) {
   constexpr int kThreads = 32 * W;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = (count + kThreads - 1) / kThreads;
@@ -164,7 +164,7 @@ __device__ __forceinline__ Run plan_run(int count, F size, RunShared<W>& sh, int
   }
   before += incl - mine;                         // pages before this thread's rows
   // no more runs than pages: every CTA that shares a row has a part of it
-  const int64_t nc = total < gridDim.x ? total : gridDim.x;
+  const int64_t most = (total + least - 1) / least, nc = most < gridDim.x ? most : gridDim.x;
   const bool busy = blockIdx.x < nc;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -40,7 +40,7 @@
 // codes, and a tile's softmax, 950 cycles alone, takes 1.9 thousand beside them (without the
 // conversion, timing only, 597 us of 726).  Measured at 128 columns: 4001 queries on 16 to 17 thousand
 // tokens of 28 / 4 heads 0.68 ms, 1.2 PFLOP/s of the visible pairs; 300 to 700 queries of two sequences
-// on 4.9 to 9.7 thousand tokens of 32 / 8 heads 102 us; 5 queries of eight sequences on 6.5 thousand 66 us.
+// on 4.9 to 9.7 thousand tokens of 32 / 8 heads 0.10 ms; 5 queries of eight sequences on 6.5 thousand 65 us.
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
 // 11 scales, 12-19 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
@@ -71,6 +71,8 @@ constexpr int kThreads = 384 + 32 * kConvert;     // five warpgroups
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 176, kOtherRegs = 40;
 static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "register shares within the launch's");
 constexpr int kNever = 0x7FFFFFFF;
+// Blocks of a CTA's run at least: a block takes 2 us, a part half a microsecond of its unit's join.
+constexpr int kLeastRun = 4;
 constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
 constexpr int kScaledRing = 4;                    // of them, those that the conversion may still wait for
 constexpr float kMost = 65000.f;                  // bound of a block's sum of weights: f16 ends at 65504
@@ -448,7 +450,6 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  const Run plan = decode::plan_run<kThreads / 32>(g.units, [&](int i) { return unit_of(g, i).nb; }, run);
   // units whose rows see no key: zeros
   for (int i = blockIdx.x; i < g.units; i += gridDim.x) {
     const Unit u = unit_of(g, i);
@@ -460,6 +461,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       put_row(g, out, row / g.gp, row % g.gp, x % pieces * 8, make_uint4(0, 0, 0, 0));
     }
   }
+  const Run plan = decode::plan_run<kThreads / 32>(g.units, [&](int i) { return unit_of(g, i).nb; }, run, decode::kWholeRow, kLeastRun);
   fence_before();
   __syncthreads();
   fence_after();
@@ -908,7 +910,7 @@ q4_join_kernel(const __grid_constant__ Q4TcGeom g) {
       const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 2
+#pragma unroll 1                                              // it runs once, and its instructions' fetches count
       for (int k = blockIdx.x; k <= cut.y; ++k) {
         const float* p = part(k);
         const float Z = __ldcg(p + kTile * D + row), l = __ldcg(p + kTile * D + kTile + row);
