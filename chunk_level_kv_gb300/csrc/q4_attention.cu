@@ -71,8 +71,9 @@ struct Q4AttnArgs {
   float* part;                                   // [passes][2 CTAs][rows][64 ND + 4]: O, m, l
 };
 
-// Warps of a CTA, a page each in shared memory.  Sixteen hide the products' latency best, and 8
-// query rows of up to 128 columns fit their 128 registers a thread.
+// Warps of a CTA, a page each in shared memory.  For 8 query rows of up to 128 columns twelve, of 168 registers a thread
+// (256 rows of 12.8 thousand tokens, cold: 107 us; sixteen of 128 spill, 121 us; eight 119 us); more rows or columns take
+// the registers of eight.
 template <int ND, typename T, int RS>
 constexpr int warps_of() { return sizeof(T) == 2 && RS == 1 && ND <= 2 ? 12 : 8; }
 template <int ND>

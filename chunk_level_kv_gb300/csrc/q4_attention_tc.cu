@@ -21,7 +21,7 @@
 //   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
 //   consecutive bytes of a K-major operand: V is stored as V^T, and both products take both
 //   operands K-major.  1024 + c is an f16 number with c as its last bits; less 1024 it is c, and
-//   one packed FMA makes s c + m of it, rounded once: 16 instructions for 8 codes.
+//   one packed FMA makes s c + m of it, rounded once: 13 instructions for 8 codes.
 // - The lengths are in device memory.  Work is counted in (two tiles, block) pairs; every CTA
 //   takes an equal run of them (plan_run of decode.cuh), so that few rows against many keys
 //   keep every SM busy.  Of query tiles whose keys are cut, the CTAs write parts (Z, l, O), and a

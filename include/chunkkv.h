@@ -504,7 +504,8 @@ chunkkv_status chunkkv_q4_load(const chunkkv_q4_cache* c, int32_t dtype, const i
  *   q, out: device [B, n_q, Hkv * G, d] with element strides (b, token, head), multiples of
  *   16 bytes; out overlaps no input;
  *   scale > 0 and finite; sums and softmax statistics in fp32.  For bf16 the weights are
- *   rounded to f16 (2^-11 each) before they weigh the values; with many query rows
+ *   rounded to f16 (2^-11 each) before they weigh the values, and q . c is good to about
+ *   2^-17 of its largest term; with many query rows
  *   (chunkkv_q4_path 1) the keys and values are too, as multiples of the largest of their
  *   block of 128 tokens: what lies below 2^-29 of it loses bits, below 2^-40 it is lost;
  *   ws: device workspace of chunkkv_q4_workspace_size bytes, under chunkkv_q8_attention's
