@@ -76,6 +76,7 @@ constexpr int kLeastRun = 4;
 constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
 constexpr int kScaledRing = 4;                    // of them, those that the conversion may still wait for
 constexpr float kMost = 65000.f;                  // bound of a block's sum of weights: f16 ends at 65504
+constexpr float kStay = 8.f;                      // largest weight of a block under a huge Z that stays, as an exponent (kMost: 2^9)
 constexpr float kLift = 4.f;                      // a row's first weight is about 2^4
 constexpr int kTopExp = 14;                       // the largest element of an operand is in [2^14, 2^15)
 constexpr float kBack = 262144.f;                 // 2^(kSumExp - kTopExp): O over l back to its size
@@ -289,21 +290,27 @@ __device__ __noinline__ int narrow_row(uint8_t* tile, int row) {
   return e2 - kTopExp;
 }
 
-// The exponentials of a block's sum that passed kMost done over: rows that are `over` move Z to the block's maximum, and
-// what O (at tO, unless it is still empty) and l hold goes with it.  Their differences to the maximum are taken before
-// they are scaled: under a huge Z one rounding of S alpha + EV - Z is off by more than an exponential bears.  The other
-// rows' weights are what they were, and are added in row_exp's order.  Returns (Z, l).
+// The exponentials of a block whose sum passed kMost, or whose Z is huge, done over: rows that are `over` move Z to the
+// block's maximum, and what O (at tO, unless it is still empty) and l hold goes with it; a huge Z that is not passed stays.
+// Their differences to the maximum are taken before they are scaled: under a huge Z one rounding of S alpha + EV - Z is off
+// by more than an exponential bears (Z itself is: from 2^25 on no float lies within 1 of a row's first exponent).  The
+// other rows' weights are what they were, and are added in row_exp's order.  Returns (Z, l).
 template <int D>
 __device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha, float ev, float sum_up, float Z, float l, bool over) {
   const float top = row_max(tS);
   float base = 0.f, neg = ev - (Z == -INFINITY ? ev : Z), f = 1.f;
   if (over) {
-    const float zn = rintf(fmaf(top, alpha, ev)) - kLift;
-    f = Z == -INFINITY ? 0.f : ex2(Z - zn);
-    Z = zn;
+    neg = fmaf(top, alpha, ev - Z);               // top's weight as an exponent
     base = top;
-    // top's own exponent, kLift and what Z was rounded by: a later block's terms stand beside these under one Z
-    neg = fminf(fmaxf(fmaf(top, alpha, ev - zn), kLift - 1.f), kLift + 1.f);
+    if (top == -INFINITY) {
+      base = neg = 0.f;                           // no logit but -inf (and NaN)
+    } else if (Z == -INFINITY || l == 0.f || !(neg <= kStay)) {
+      const float zn = rintf(fmaf(top, alpha, ev)) - kLift;
+      if (l != 0.f) f = ex2(fminf(Z - zn, 0.f));              // else O is zero too, and Z this block's own first reference
+      Z = zn;
+      // top's own exponent, kLift and what Z was rounded by: a later block's terms stand beside these under one Z
+      neg = fminf(fmaxf(fmaf(top, alpha, ev - zn), kLift - 1.f), kLift + 1.f);
+    }
   }
   if (tO != 0xFFFFFFFFu) {
     // the blocks before are done: their products were issued before this S
@@ -514,7 +521,9 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           if (Z == -INFINITY && bm != -INFINITY) Z = rintf(fmaf(bm, alpha, ev)) - kLift;     // P and O of the row are zero so far
         }
         uint32_t p[64];
-        const float sum = row_exp<true>(tS, alpha, Z == -INFINITY ? 0.f : ev - Z, p);
+        // exact up to kHuge; NaN for a larger Z, so that block_over does its blocks
+        const float neg = fabsf(Z) <= kHuge ? ev - Z : Z == -INFINITY ? 0.f : NAN;
+        const float sum = row_exp<true>(tS, alpha, neg, p);
         const bool over = live && !(sum <= kMost);            // a NaN too
         if (!__any_sync(0xffffffffu, over)) {
           l = fmaf(sum, scales.sum_up, l);
