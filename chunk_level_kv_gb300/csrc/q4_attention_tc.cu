@@ -16,6 +16,9 @@
 //   exponent: a weight is P = 2^(S alpha 2^EK + EV - Z) with the row's reference Z, so O gathers
 //   2^-Z V with every block's V at its own scale, and a block whose values are huge under
 //   negligible weights costs the others nothing.
+// - A block whose tokens' largest values lie more than 2^8 apart gets an exponent for each token, or
+//   a large token that a row does not see, or weighs by nothing, would take the others' bits.  The row's
+//   threads then weigh it column by column, in code of its own (block_apart: twice the time of a block).
 // - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
 //   eight converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
 //   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
@@ -75,6 +78,10 @@ constexpr int kNever = 0x7FFFFFFF;
 constexpr int kLeastRun = 4;
 constexpr int kScaleRing = 8;                     // blocks whose scales are known: the warps are at most 5 blocks apart
 constexpr int kScaledRing = 4;                    // of them, those that the conversion may still wait for
+// Exponents of 2 by which the largest values of a block's tokens may differ under one scale: more, and every token has its own.
+constexpr int kNear = 8;
+constexpr int kApartMost = 9;                     // block_apart's largest weight is 2^kApartMost: 128 of them stay in f16
+constexpr int kKeyFloor = -100, kValueFloor = -60;        // scales' least exponents: l has room for 2^(kSumExp + 60)
 constexpr float kMost = 65000.f;                  // bound of a block's sum of weights: f16 ends at 65504
 constexpr float kStay = 8.f;                      // largest weight of a block under a huge Z that stays, as an exponent (kMost: 2^9)
 constexpr float kLift = 4.f;                      // a row's first weight is about 2^4
@@ -85,14 +92,30 @@ constexpr int kSumExp = 32;                       // l gathers 2^(kSumExp - Z) t
 template <int ND> constexpr int block_bytes() { return kTile * 64 * ND * 2; }
 static_assert(q4_page_bytes(1) == 2 * q4_v(1), "keys and values take the same room");
 constexpr int kControl = 1024;
+constexpr int kTokenExps = kScaleRing * 2 * kTile;        // bytes: the exponents of a block's keys, and of its values
 template <int ND, int QT> constexpr int smem_bytes() {
-  return (QT + kStages) * block_bytes<ND>() + packed_pages<QT>() * q4_v(ND) + kControl;
+  return (QT + kStages) * block_bytes<ND>() + packed_pages<QT>() * q4_v(ND) + kControl + kTokenExps;
 }
 static_assert(smem_bytes<2, 1>() <= 227 * 1024 && smem_bytes<2, 2>() <= 227 * 1024, "an SM's shared memory");
 // A tile's part: O as [4 warps][D columns][32 lanes], then the rows' Z and l.
 template <int D> constexpr int part_floats() { return kTile * (D + 2); }
 template <int N> constexpr uint32_t idesc() {     // fp32 D, f16 A and B, M = 128
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// tcgen's waits, with what follows a first try that fails out of the way: twelve roles' loops share the instruction caches,
+// and with the waits' own loops among them a block took 15 % longer.
+__device__ __forceinline__ bool wait_long(int32_t* err, volatile int* abort, long long timeout, uint32_t bar, uint32_t parity, int code) {
+  const Ctl ctl{err, abort, timeout};
+  return wait_bar(ctl, bar, parity, code);
+}
+__device__ __forceinline__ bool await(const Ctl& ctl, uint32_t bar, uint32_t parity, int code) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  return wait_long(ctl.err, ctl.abort, ctl.timeout, bar, parity, code);
+}
+__device__ __forceinline__ bool await_warp(const Ctl& ctl, uint32_t bar, uint32_t parity, int code) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
+  return __all_sync(0xffffffffu, wait_long(ctl.err, ctl.abort, ctl.timeout, bar, parity, code));
 }
 
 struct Q4TcGeom {
@@ -219,51 +242,77 @@ __device__ __forceinline__ uint32_t sixteenth(uint32_t s) {
   return *(const uint32_t*)&x;
 }
 
-// The largest magnitude that codes of a group can stand for (NaN: the other argument).
-__device__ __forceinline__ float reach(uint32_t w, float most) {
+// The largest magnitude that codes of a group can stand for (NaN: 0).
+__device__ __forceinline__ float reach(uint32_t w) {
   const float m = q4_m(w);
-  return fmaxf(most, fmaxf(fabsf(m), fabsf(fmaf(15.f, q4_s(w), m))));
+  return fmaxf(0.f, fmaxf(fabsf(m), fabsf(fmaf(15.f, q4_s(w), m))));
 }
-// The steps and smallest values of the halves of two pages, a lane's share; and the largest reach, over tokens below `left`.
+__device__ __forceinline__ int exponent_of(uint32_t reach, int floor) { return min(127, max(floor, (int)(reach >> 23) - 127)); }
+// Of the steps and smallest values (words [ND][64] of two pages) a lane's i-th share: where it lies, and its first token.
 template <int ND>
-__device__ __forceinline__ uint4* steps_at(uint8_t* const (&half)[2], int i, int lane, int& token) {
-  const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;    // words [ND][64] of each page
+__device__ __forceinline__ uint4* steps_at(uint8_t* half0, uint8_t* half1, int i, int lane, int& token) {
+  const int v = i * 32 + lane, page = v / (16 * ND), at = v % (16 * ND) * 4;
   token = page * kPage + (at & (kPage - 1));
-  return (uint4*)((page ? half[1] : half[0]) + 2048 * ND + at * 4);
+  return (uint4*)((page ? half1 : half0) + 2048 * ND + at * 4);
 }
+// What four tokens of a group reach, those from `left` on nothing.
+__device__ __forceinline__ uint4 reach_four(const uint4& w, int token, int left) {
+  auto of = [&](uint32_t x, int e) { return token + e < left ? __float_as_uint(reach(x)) : 0u; };
+  return make_uint4(of(w.x, 0), of(w.y, 1), of(w.z, 2), of(w.w, 3));
+}
+// Scaled, as two f16.  pairs: the m of two tokens, and then their s (of odd pairs s / 16, see expand).
+__device__ __forceinline__ uint4 scale_four(const uint4& w, const float4& by, bool pairs) {
+  const uint4 x = make_uint4(scaled(w.x, by.x), scaled(w.y, by.y), scaled(w.z, by.z), scaled(w.w, by.w));
+  return pairs ? make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
+                            sixteenth(__byte_perm(x.z, x.w, 0x7632)))
+               : x;
+}
+// The keys' or the values' two pages of a block scaled in place, by one exponent, or token by token where their largest
+// values lie too far apart; the tokens' exponents go to exps[token].  Returns the largest.
 template <int ND>
-__device__ __forceinline__ uint32_t reach_of(uint8_t* const (&half)[2], int left, int lane, uint4 (&w)[ND]) {
-  float most = 0.f;
-#pragma unroll
+__device__ __forceinline__ int scale_half(uint8_t* half0, uint8_t* half1, int left, int floor, bool pairs, int lane, int8_t* exps,
+                                          bool& apart) {
+  int token;
+  uint32_t most = 0, least = 0xFFFFFFFFu;         // least: less one, so that zeros have no say
+#pragma unroll 1
   for (int i = 0; i < ND; ++i) {
-    int token;
-    w[i] = *steps_at<ND>(half, i, lane, token);
-    if (token + 3 < left) {
-      most = reach(w[i].x, reach(w[i].y, reach(w[i].z, reach(w[i].w, most))));
-    } else {
-      if (token < left) most = reach(w[i].x, most);
-      if (token + 1 < left) most = reach(w[i].y, most);
-      if (token + 2 < left) most = reach(w[i].z, most);
+    const uint4 r = reach_four(*steps_at<ND>(half0, half1, i, lane, token), token, left);
+    most = max(max(most, max(r.x, r.y)), max(r.z, r.w));
+    least = min(min(least, min(r.x - 1, r.y - 1)), min(r.z - 1, r.w - 1));
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  const int top = exponent_of(most, floor);
+  // by groups, which may lie further apart than tokens: exponents of their own are right for any tokens
+  const bool own = most != 0 && top - exponent_of(least + 1, floor) > kNear;
+  apart |= own;
+  const float all = power_of_two(kTopExp - top);
+  *(uint32_t*)(exps + 4 * lane) = 0x01010101u * (uint8_t)top;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < ND; ++i) {
+    uint4* to = steps_at<ND>(half0, half1, i, lane, token);
+    const uint4 w = *to;
+    float4 by = make_float4(all, all, all, all);
+    if (__builtin_expect(own, 0)) {
+      uint4 r = reach_four(w, token, left);
+      if (ND == 2) {                              // the token's other group
+        r.x = max(r.x, __shfl_xor_sync(0xffffffffu, r.x, 16));
+        r.y = max(r.y, __shfl_xor_sync(0xffffffffu, r.y, 16));
+        r.z = max(r.z, __shfl_xor_sync(0xffffffffu, r.z, 16));
+        r.w = max(r.w, __shfl_xor_sync(0xffffffffu, r.w, 16));
+      }
+      const int4 e = make_int4(exponent_of(r.x, floor), exponent_of(r.y, floor), exponent_of(r.z, floor), exponent_of(r.w, floor));
+      by = make_float4(power_of_two(kTopExp - e.x), power_of_two(kTopExp - e.y), power_of_two(kTopExp - e.z), power_of_two(kTopExp - e.w));
+      *(char4*)(exps + token) = make_char4(e.x, e.y, e.z, e.w);
     }
+    *to = scale_four(w, by, pairs);
   }
-  return __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-}
-// In place: scaled, as two f16.  PAIRS: the m of two tokens, and then their s (of odd pairs s / 16, see expand).
-template <int ND, bool PAIRS>
-__device__ __forceinline__ void scale_steps(uint8_t* const (&half)[2], float by, int lane, const uint4 (&w)[ND]) {
-#pragma unroll
-  for (int i = 0; i < ND; ++i) {
-    int token;
-    uint4* to = steps_at<ND>(half, i, lane, token);
-    const uint32_t x[4] = {scaled(w[i].x, by), scaled(w[i].y, by), scaled(w[i].z, by), scaled(w[i].w, by)};
-    *to = PAIRS ? make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x5410),
-                             sixteenth(__byte_perm(x[2], x[3], 0x7632)))
-                : make_uint4(x[0], x[1], x[2], x[3]);
-  }
+  return top;
 }
 // A block's scales: what takes back that its keys and values were multiplied by 2^(kTopExp - EK), 2^(kTopExp - EV).
 struct Scales {
-  float k_up;                                     // 2^(EK - kTopExp)
+  float k_up;                                     // 2^(EK - kTopExp); negative: the block is block_apart's
   float ev, sum_up;                               // EV, and 2^(kSumExp - EV)
 };
 
@@ -290,6 +339,20 @@ __device__ __noinline__ int narrow_row(uint8_t* tile, int row) {
   return e2 - kTopExp;
 }
 
+// A row of O times f; a whole warp's rows.  The blocks before are done: their products were issued before this S.
+template <int D>
+__device__ __forceinline__ void scale_row(uint32_t tO, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(tO + 32 * c, o);
+    tmem_wait(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= f;
+    tmem_st32(tO + 32 * c, o);
+  }
+}
+
 // The exponentials of a block whose sum passed kMost, or whose Z is huge, done over: rows that are `over` move Z to the
 // block's maximum, and what O (at tO, unless it is still empty) and l hold goes with it; a huge Z that is not passed stays.
 // Their differences to the maximum are taken before they are scaled: under a huge Z one rounding of S alpha + EV - Z is off
@@ -312,19 +375,59 @@ __device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha,
       neg = fminf(fmaxf(fmaf(top, alpha, ev - zn), kLift - 1.f), kLift + 1.f);
     }
   }
-  if (tO != 0xFFFFFFFFu) {
-    // the blocks before are done: their products were issued before this S
-#pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      tmem_ld32(tO + 32 * c, o);
-      tmem_wait(o);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] *= f;
-      tmem_st32(tO + 32 * c, o);
-    }
-  }
+  if (tO != 0xFFFFFFFFu) scale_row<D>(tO, f);
   return make_float2(Z, fmaf(write_exp_from<true>(tS, base, alpha, neg), sum_up, l * f));
+}
+
+// A block whose tokens have exponents of their own: keys in exps[0 .. 127], values in exps[128 .. 255].  A row's weight of
+// token c is 2^(S 2^EK_c alpha + EV_c - Z) as ever, but Z goes by the tokens that the row sees, and l takes each weight at
+// its own scale.  Two passes over S: the largest exponent, then P, in write_exp_from's places.  Returns (Z, l).
+template <int D>
+__device__ __noinline__ float2 block_apart(uint32_t tS, uint32_t tO, float row_alpha, const volatile int8_t* exps, float Z, float l) {
+  auto alpha_of = [&](int c) { return fminf(fmaxf(row_alpha * power_of_two((int)exps[c] - kTopExp), 1.2e-38f), 3.4e38f); };
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 32) {
+    float s[32];
+    tmem_ld32(tS + c, s);
+    tmem_wait(s);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, fmaf(s[i], alpha_of(c + i), (float)exps[kTile + c + i]));
+  }
+  float f = 1.f;
+  float largest = top - Z;                        // the largest weight's exponent
+  if (top != -INFINITY && !(largest <= (float)kApartMost)) {
+    const float zn = rintf(top) - kLift;
+    f = Z == -INFINITY ? 0.f : ex2(Z - zn);
+    Z = zn;
+    largest = kLift;
+  }
+  l *= f;
+  if (tO != 0xFFFFFFFFu) scale_row<D>(tO, f);
+  const float ref = Z == -INFINITY ? 0.f : Z;
+  const bool huge = fabsf(ref) > kHuge && top != -INFINITY;   // as in block_over: differences first
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float s[32];
+    tmem_ld32(tS + 32 * c, s);
+    tmem_wait(s);
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float2 w;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = 32 * c + 2 * i + k;
+        const float ev = (float)exps[kTile + at], u = fmaf(s[2 * i + k], alpha_of(at), huge ? ev : ev - ref);
+        const float e = huge ? u - top + largest : u;
+        (k ? w.y : w.x) = ex2(e);
+        l += ex2(e - ev + (float)kSumExp);
+      }
+      p[i] = pack_p<true>(w);
+    }
+    tmem_st16(tS + 16 * c, p);
+  }
+  return make_float2(Z, l);
 }
 
 // A page's tokens or columns are dealt to kParts warps.
@@ -433,6 +536,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
   volatile Scales* s_scales = (volatile Scales*)(s_bad + kConvert * kItemRing);                  // [kScaleRing]
   using RunOf = decode::RunShared<kThreads / 32>;
   RunOf& run = *(RunOf*)((uint8_t*)bars + kControl - sizeof(RunOf));
+  int8_t* s_exps = (int8_t*)bars + kControl;                  // [kScaleRing][keys, values][kTile]
   static_assert(8 * kBars + 8 + (sizeof(Item) + 4 * kConvert) * kItemRing + sizeof(Scales) * kScaleRing + sizeof(RunOf) <= kControl &&
                     sizeof(RunOf) % 8 == 0, "control block");
 
@@ -489,14 +593,14 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     uint32_t before = 0;                          // blocks of the items before
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
-      if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+      if (!await_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
       const volatile Item& it = s_items[slot];                // read where it is used: registers are short
       if (it.unit < 0) break;
       const int nb = t ? it.nb1 : it.nb0;
       const int limit = it.limit + t * g.pos + my_pos;        // last key that this row sees
       const bool live = my_pos < g.pos && t * g.pos + my_pos < it.rows;
       // ---- the queries as f16
-      if (!wait_warp(ctl, q_full, qc & 1, kDevTimeoutEpilogue)) break;
+      if (!await_warp(ctl, q_full, qc & 1, kDevTimeoutEpilogue)) break;
       ++qc;
       float row_alpha = 0.f;
       if (nb > 0) row_alpha = g.alpha * power_of_two(max(-126, narrow_row<ND>(sQ + t * kBlock, row)));
@@ -508,15 +612,26 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       const uint32_t first = before + it.nb - 1;              // of block 0
       before += it.nb;
       for (int j = nb - 1; j >= 0; --j) {
-        if (!wait_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
+        if (!await_warp(ctl, s_full + 8 * t, sc & 1, kDevTimeoutEpilogue)) { ok = false; break; }
         ++sc;
         fence_after();
         const volatile Scales& scales = s_scales[(first - j) % kScaleRing];
         // never 0 (0 x -inf) nor infinite
-        const float alpha = fminf(fmaxf(row_alpha * scales.k_up, 1.2e-38f), 3.4e38f), ev = scales.ev;
         const int seen = limit - j * kTile, lo = seen - (my_pos - pos_lo);       // columns 0 .. seen; the warp's first row's
-        if (kTile - 1 > lo) hide(tS, seen, lo);               // a hidden key in the warp
-        if (__any_sync(0xffffffffu, Z == -INFINITY)) {
+        if (__builtin_expect(kTile - 1 > lo, 0)) hide(tS, seen, lo);          // a hidden key in the warp
+        const float k_up = scales.k_up;
+        if (__builtin_expect(k_up < 0.f, 0)) {
+          const float2 r = block_apart<D>(tS, j < nb - 1 ? tO : 0xFFFFFFFFu, row_alpha,
+                                          s_exps + (first - j) % kScaleRing * (2 * kTile), Z, l);
+          Z = r.x;
+          l = r.y;
+          tmem_st_wait();
+          fence_before();
+          mbar_arrive(p_full + 8 * t);
+          continue;
+        }
+        const float alpha = fminf(fmaxf(row_alpha * k_up, 1.2e-38f), 3.4e38f), ev = scales.ev;
+        if (__builtin_expect(__any_sync(0xffffffffu, Z == -INFINITY), 0)) {
           const float bm = first_reference(tS, lo);
           if (Z == -INFINITY && bm != -INFINITY) Z = rintf(fmaf(bm, alpha, ev)) - kLift;     // P and O of the row are zero so far
         }
@@ -525,7 +640,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         const float neg = fabsf(Z) <= kHuge ? ev - Z : Z == -INFINITY ? 0.f : NAN;
         const float sum = row_exp<true>(tS, alpha, neg, p);
         const bool over = live && !(sum <= kMost);            // a NaN too
-        if (!__any_sync(0xffffffffu, over)) {
+        if (__builtin_expect(!__any_sync(0xffffffffu, over), 1)) {
           l = fmaf(sum, scales.sum_up, l);
           tmem_st32<0>(tS, p);
           tmem_st32<32>(tS + 32, p);
@@ -541,7 +656,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       if (!ok) break;
       // ---- the item's rows
       if (nb > 0) {
-        if (!wait_warp(ctl, o_full + 8 * t, oc & 1, kDevTimeoutEpilogue)) break;
+        if (!await_warp(ctl, o_full + 8 * t, oc & 1, kDevTimeoutEpilogue)) break;
         ++oc;
         fence_after();
       }
@@ -575,7 +690,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       uint32_t n = 0;
       for (; ok && !*abort_flag; ++n) {
         const int slot = n % kItemRing;
-        if (!wait_bar(ctl, item_empty + 8 * slot, ((n / kItemRing) & 1) ^ 1, kDevTimeoutTmaProducer)) break;
+        if (!await(ctl, item_empty + 8 * slot, ((n / kItemRing) & 1) ^ 1, kDevTimeoutTmaProducer)) break;
         Unit u;
         int64_t sa = 0, sb = 0;
         while (xr < x1) {                         // the next unit with work in this run
@@ -626,7 +741,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         for (int b = 0; b < 2 * nb && ok; ++b) {
           if (b == 2) {
             // the queries after the first K and V blocks: the last item's products still read the old ones
-            ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
+            ok = await(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
             if (!ok) break;
             load_q();
           }
@@ -637,7 +752,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           }
           for (int k = 0; k < 2 && ok; ++k) {
             const int st = loaded % kPacked;
-            ok = wait_bar(ctl, packed_empty + 8 * st, ((loaded / kPacked) & 1) ^ 1, kDevTimeoutTmaProducer);
+            ok = await(ctl, packed_empty + 8 * st, ((loaded / kPacked) & 1) ^ 1, kDevTimeoutTmaProducer);
             if (!ok) break;
             if (k < pages) {
               mbar_expect_tx(packed_full + 8 * st, kHalf);
@@ -649,7 +764,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           }
         }
         if (ok && nb == 1) {                      // an item of one block: its queries come last
-          ok = wait_bar(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
+          ok = await(ctl, q_empty, (q_loaded & 1) ^ 1, kDevTimeoutTmaProducer);
           if (!ok) break;
           load_q();
         }
@@ -692,7 +807,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
       auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1; } };
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
-        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
+        if (!await_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutMma)) break;
         struct { int unit, nb, nb0, nb1; } it;
         it.unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
         it.nb = __shfl_sync(0xffffffffu, s_items[slot].nb, 0);
@@ -702,7 +817,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         if (lane == 0) mbar_arrive(item_empty + 8 * slot);
         if (it.unit < 0) break;
         const int nb = t ? it.nb1 : it.nb0;
-        bool ok = wait_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && wait_warp(ctl, q_ready + 8 * t, qc & 1, kDevTimeoutMma);
+        bool ok = await_warp(ctl, kv_full + 8 * st, ph, kDevTimeoutMma) && await_warp(ctl, q_ready + 8 * t, qc & 1, kDevTimeoutMma);
         if (!ok) break;
         ++qc;
         fence_after();
@@ -719,11 +834,11 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         for (int j = it.nb - 1; j >= 0; --j) {
           // V of this block and K of the one below it, and then P: nothing is waited for between the products
           const int sv = st;
-          ok = wait_warp(ctl, kv_full + 8 * sv, ph, kDevTimeoutMma);
+          ok = await_warp(ctl, kv_full + 8 * sv, ph, kDevTimeoutMma);
           next();
           const int sk = st;
           if (ok && j >= 1) {
-            ok = wait_warp(ctl, kv_full + 8 * sk, ph, kDevTimeoutMma);
+            ok = await_warp(ctl, kv_full + 8 * sk, ph, kDevTimeoutMma);
             next();
           }
           if (!ok) break;
@@ -731,10 +846,10 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
             // the two tiles take turns, tile 0 first
             const bool both = j < min(it.nb0, it.nb1);
             if (both) {
-              ok = wait_warp(ctl, turn + 8 * t, (tc & 1) ^ (t ^ 1), kDevTimeoutMma);
+              ok = await_warp(ctl, turn + 8 * t, (tc & 1) ^ (t ^ 1), kDevTimeoutMma);
               ++tc;
             }
-            ok = ok && wait_warp(ctl, p_full + 8 * t, pc & 1, kDevTimeoutMma);
+            ok = ok && await_warp(ctl, p_full + 8 * t, pc & 1, kDevTimeoutMma);
             if (!ok) break;
             ++pc;
             fence_after();
@@ -769,39 +884,49 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     } else if (warp == 11) {
       // ------------------------------------------------ a block's scales, from the steps and smallest values of its groups
       uint32_t bc = 0;                            // blocks so far
+      int st = 0;                                 // page of codes in turn and its parity
+      uint32_t ph = 0;
       for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
         const int slot = n % kItemRing;
-        if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+        if (!await_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
         const int unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
         if (unit < 0) break;
         const int nb = s_items[slot].nb, tk = s_items[slot].tk;
         bool ok = true;
         for (int j = nb - 1; j >= 0 && ok; --j, ++bc) {
-          uint8_t* half[2][2];
-#pragma unroll
-          for (int i = 0; i < 4 && ok; ++i) {
-            const uint32_t u = 4 * bc + i;
-            half[i >> 1][i & 1] = sP + u % kPacked * kHalf;
-            ok = wait_warp(ctl, packed_full + 8 * (u % kPacked), (u / kPacked) & 1, kDevTimeoutEpilogue);
+          int8_t* exps = s_exps + bc % kScaleRing * (2 * kTile);
+          bool apart = false;
+          int ek = 0, ev = 0;
+          // in loops: what runs once a block costs most by its instructions' fetches
+#pragma unroll 1
+          for (int which = 0; which < 2 && ok; ++which) {
+            int at[2];
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              ok = ok && await_warp(ctl, packed_full + 8 * st, ph, kDevTimeoutEpilogue);
+              at[0] = i ? at[0] : st;
+              at[1] = st;
+              if (++st == kPacked) { st = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            ek = ev;
+            // stale tokens past the row's end have no say
+            ev = scale_half<ND>(sP + at[0] * kHalf, sP + at[1] * kHalf, tk - j * kTile, which ? kValueFloor : kKeyFloor, which, lane,
+                                exps + which * kTile, apart);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");      // the next copy writes here
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(packed_empty + 8 * at[0]);
+              mbar_arrive(packed_empty + 8 * at[1]);
+            }
           }
           if (!ok) break;
-          const int left = tk - j * kTile;        // stale tokens past the row's end have no say
-          uint4 kw[ND], vw[ND];
-          const uint32_t kt = reach_of<ND>(half[0], left, lane, kw);
-          const uint32_t vt = reach_of<ND>(half[1], left, lane, vw);
-          const int ek = min(127, max(-100, (int)(kt >> 23) - 127)), ev = min(127, max(-60, (int)(vt >> 23) - 127));
-          scale_steps<ND, false>(half[0], power_of_two(kTopExp - ek), lane, kw);
-          scale_steps<ND, true>(half[1], power_of_two(kTopExp - ev), lane, vw);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");        // the next copy writes here
-          __syncwarp();
           if (lane == 0) {
             volatile Scales& out = s_scales[bc % kScaleRing];
-            out.k_up = power_of_two(ek - kTopExp);
+            out.k_up = apart ? -1.f : power_of_two(ek - kTopExp);
             out.ev = (float)ev;
             out.sum_up = power_of_two(kSumExp - ev);
             mbar_arrive(scaled_full + 8 * (bc % kScaledRing));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mbar_arrive(packed_empty + 8 * ((4 * bc + i) % kPacked));
           }
           __syncwarp();
         }
@@ -819,7 +944,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     uint32_t ph = 0;
     for (uint32_t n = 0; __all_sync(0xffffffffu, !*abort_flag); ++n) {
       const int slot = n % kItemRing;
-      if (!wait_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
+      if (!await_warp(ctl, item_full + 8 * slot, (n / kItemRing) & 1, kDevTimeoutEpilogue)) break;
       const int unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
       if (unit < 0) break;
       const int nb = s_items[slot].nb, low = s_items[slot].low, tk = s_items[slot].tk;
@@ -829,8 +954,8 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         const int j = nb - 1 - (b >> 1);
         const uint32_t bc = pc >> 1;
         // the copies have landed once the scales are there
-        ok = ((b & 1) != 0 || wait_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue)) &&
-             wait_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
+        ok = ((b & 1) != 0 || await_warp(ctl, scaled_full + 8 * (bc % kScaledRing), (bc / kScaledRing) & 1, kDevTimeoutEpilogue)) &&
+             await_warp(ctl, kv_empty + 8 * st, ph ^ 1, kDevTimeoutEpilogue);
         if (!ok) break;
         const uint8_t* src = sP + ps * kHalf;
         uint8_t* dst = sKV + st * kBlock;

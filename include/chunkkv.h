@@ -507,7 +507,8 @@ chunkkv_status chunkkv_q4_load(const chunkkv_q4_cache* c, int32_t dtype, const i
  *   rounded to f16 (2^-11 each) before they weigh the values, and q . c is good to about
  *   2^-17 of its largest term; with many query rows
  *   (chunkkv_q4_path 1) the keys and values are too, as multiples of the largest of their
- *   block of 128 tokens: what lies below 2^-29 of it loses bits, below 2^-40 it is lost;
+ *   token: what lies below 2^-20 of it loses bits, below 2^-31 it is lost (tokens whose
+ *   largest are within 2^8 of each other may share one multiple);
  *   ws: device workspace of chunkkv_q4_workspace_size bytes, under chunkkv_q8_attention's
  *   terms: zero-filled before its first use, not shared by calls that can overlap; it may
  *   serve any of the attention calls in turn.

@@ -12,6 +12,105 @@ from test_gpu_q4 import BF, DEV, F32, ckv, fill, held  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
+def check_query(ckv, cache, r, q, out, n, scale, path, spread=0, count=None):  # noqa: F811
+    """One query token's heads q, out [G, d] against 64 bits over the first n tokens of cache row r.
+
+    spread: in the kernel for many query rows, what shares a block of 128 tokens with the seen ones may raise its
+    powers of two by this many bits (2^8 of the largest seen value, and one for where in an octave the two lie), so an
+    element's error below f16's normal numbers is 2^(spread - 39) of the largest, a weight's 2^(spread - 28).
+    count: of the n tokens, those whose weight counts (None: all).
+    """
+    (ks, km), (vs, vm) = held(cache, r, 0), held(cache, r, 1)
+    ks, km, vs, vm = ks[:n], km[:n], vs[:n], vm[:n]
+    qr, d = q.double(), q.shape[-1]
+    p = torch.softmax(qr @ (ks + km).T * scale, -1)
+    ref, A = p @ (vs + vm), p @ (vs + vm.abs())
+    at = slice(None) if count is None else count
+    E = (qr.abs() @ (ks + km.abs())[at].T * scale).amax(1, keepdim=True)
+    tol = (2 * (d + 8) * 2.0 ** -22 * E + (n + 16) * 2.0 ** -22) * A + 1e-30
+    if q.dtype == BF:
+        tol = tol + 2.0 ** -8 * ref.abs() + (2.0 ** -11 + n * 2.0 ** -35) * A
+    if path:
+        kmax, vmax = (ks + km.abs())[at].max(), (vs + vm.abs())[at].max()
+        small = 2.0 ** (spread - 39) * scale * qr.abs().sum(1, keepdim=True) * kmax
+        tol = tol + (2 * (2.0 ** -11 * E + small) + 2.0 ** -11) * A + n * 2.0 ** (spread - 28) * vmax
+    err = (out.double() - ref).abs()
+    assert bool(torch.isfinite(out).all()) and bool((err <= tol).all()), \
+        f"row {r}, {n} tokens: {float((err / tol).max())} of the tolerance"
+
+
+# ------------------------------------------------------------------ what a query does not see
+
+@pytest.mark.parametrize("power", [6, 20, 35, 60, 100])
+@pytest.mark.parametrize("dtype,n_q,d,G", [(BF, 3, 128, 4), (BF, 5, 128, 4), (BF, 60, 128, 4), (BF, 90, 64, 2), (BF, 17, 80, 1), (F32, 5, 64, 2)])
+def test_hidden_tokens_of_any_size_cost_the_others_nothing(ckv, dtype, n_q, d, G, power):  # noqa: F811
+    lens = [300, n_q, 130, n_q + 1]
+    at = n_q // 2                                     # the query token from which the large one is seen
+    g = torch.Generator(device=DEV).manual_seed(n_q + d)
+    q = torch.randn(2, n_q, 2 * G, d, generator=g, device=DEV).to(dtype)
+    for which in (0, 1, 2):
+        kv = [torch.randn(2, 2, 300, d, generator=g, device=DEV) for _ in range(2)]
+        for r, n in enumerate(lens):
+            for i in range(2):
+                if which in (i, 2):
+                    kv[i][r // 2, r % 2, n - n_q + at] *= 2.0 ** power
+        cache = ckv.q4_cache(2, 2, d, n_pages=20, max_pages=6)
+        fill(ckv, cache, lens, kv[0].to(dtype), kv[1].to(dtype))
+        out = ckv.q4_attention(cache, 0, q)
+        assert bool(torch.isfinite(out).all())
+        path = ckv.chunkkv_q4_path(cache, G, n_q, dtype)
+        for r, n in enumerate(lens):
+            b, h = divmod(r, 2)
+            for i in range(at):
+                if n - n_q + 1 + i > 0:
+                    heads = slice(h * G, (h + 1) * G)
+                    check_query(ckv, cache, r, q[b, i, heads], out[b, i, heads], n - n_q + 1 + i, 1 / math.sqrt(d), path, spread=9)
+
+
+@pytest.mark.parametrize("dtype,n_q,G", [(BF, 4, 4), (BF, 5, 4), (BF, 40, 7), (F32, 5, 2)])
+def test_every_query_sees_a_larger_value_than_the_one_before(ckv, dtype, n_q, G):  # noqa: F811
+    d, n = 128, 200
+    g = torch.Generator(device=DEV).manual_seed(n_q)
+    k, v = (torch.randn(1, 2, n, d, generator=g, device=DEV) for _ in range(2))
+    v[:, :, n - n_q:] *= 2.0 ** (3.0 * torch.arange(n_q, device=DEV))[:, None]
+    cache = ckv.q4_cache(1, 2, d, n_pages=10, max_pages=4)
+    fill(ckv, cache, [n, n], k.to(dtype), v.to(dtype))
+    q = torch.randn(1, n_q, 2 * G, d, generator=g, device=DEV).to(dtype)
+    out = ckv.q4_attention(cache, 0, q)
+    for h in range(2):
+        for i in range(n_q):
+            heads = slice(h * G, (h + 1) * G)
+            check_query(ckv, cache, h, q[0, i, heads], out[0, i, heads], n - n_q + 1 + i, 1 / math.sqrt(d),
+                        ckv.chunkkv_q4_path(cache, G, n_q, dtype), spread=9)
+
+
+@pytest.mark.parametrize("dtype,G,n_q", [(BF, 4, 1), (F32, 4, 1), (BF, 4, 3), (BF, 4, 20), (BF, 4, 200)])
+@pytest.mark.parametrize("cut", [384 + 37, 70, 600])
+def test_value_steps_far_apart_inside_a_block(ckv, dtype, G, n_q, cut):  # noqa: F811
+    # tokens up to `cut` (or from there on) hold values 2^r times the others' under weights below 2^-150 of theirs: one
+    # block of 128 tokens holds both kinds
+    d, n, powers = 64, 1000, [0, 20, 40, 60, 80]
+    rows = 2 * len(powers)
+    g = torch.Generator(device=DEV).manual_seed(62)
+    cache = ckv.q4_cache(rows, 1, d, n_pages=rows * 16, max_pages=16)
+    k = 0.1 * torch.randn(rows, 1, n, d, generator=g, device=DEV)
+    v = torch.randn(rows, 1, n, d, generator=g, device=DEV)
+    far = (torch.arange(n, device=DEV)[None] < cut) ^ (torch.arange(rows, device=DEV) % 2 == 1)[:, None]
+    k[:, 0, :, 0] = torch.where(far, -150.0, 1.0)
+    k[:, 0, :, 1] = torch.where(far, 150.0, 1.0)
+    v *= torch.where(far, 2.0 ** torch.tensor(powers, device=DEV).repeat_interleave(2)[:, None], 1.0)[:, None, :, None]
+    fill(ckv, cache, [n] * rows, k, v)
+    q = torch.zeros(rows, n_q, G, d, device=DEV)
+    q[..., 0] = 1 + torch.arange(G, device=DEV) / 16
+    q = q.to(dtype)
+    out = ckv.q4_attention(cache, 0, q, scale=1.0)
+    for r in range(rows):
+        for i in range(n_q):
+            seen = n - n_q + 1 + i
+            check_query(ckv, cache, r, q[r, i], out[r, i], seen, 1.0, ckv.chunkkv_q4_path(cache, G, n_q, dtype),
+                        spread=9, count=~far[r, :seen])
+
+
 # ------------------------------------------------------------------ weights and sums at far apart scales
 
 @pytest.mark.parametrize("dtype,G,n_q", [(BF, 4, 1), (F32, 2, 1), (BF, 4, 3), (BF, 4, 20), (BF, 4, 150)])
