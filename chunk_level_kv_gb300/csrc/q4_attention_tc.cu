@@ -18,7 +18,8 @@
 //   negligible weights costs the others nothing.
 // - A block whose tokens' largest values lie more than 2^8 apart gets an exponent for each token, or
 //   a large token that a row does not see, or weighs by nothing, would take the others' bits.  The row's
-//   threads then weigh it column by column, in code of its own (block_apart: twice the time of a block).
+//   threads then weigh it column by column, in code of its own (block_apart: twice the time of a block).  So they do where EV
+//   falls far below an earlier block's: weights that vanish beside Z still count in l.
 // - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
 //   eight converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
 //   consecutive columns of a key, or 8 consecutive tokens of a value's column, which are 16
@@ -81,6 +82,9 @@ constexpr int kScaledRing = 4;                    // of them, those that the con
 // Exponents of 2 by which the largest values of a block's tokens may differ under one scale: more, and every token has its own.
 constexpr int kNear = 8;
 constexpr int kApartMost = 9;                     // block_apart's largest weight is 2^kApartMost: 128 of them stay in f16
+// A block whose values' exponent is this much below an earlier one's of the item is weighed by block_apart: its weights may
+// be 2^-126 and less beside the reference, and yet count in the row's sum.
+constexpr int kFar = 80;
 constexpr int kKeyFloor = -100, kValueFloor = -60;        // scales' least exponents: l has room for 2^(kSumExp + 60)
 constexpr float kMost = 65000.f;                  // bound of a block's sum of weights: f16 ends at 65504
 constexpr float kStay = 8.f;                      // largest weight of a block under a huge Z that stays, as an exponent (kMost: 2^9)
@@ -339,16 +343,27 @@ __device__ __noinline__ int narrow_row(uint8_t* tile, int row) {
   return e2 - kTopExp;
 }
 
+// 2^d, d <= 0, in two factors: Z holds EV, so from one block to the next it may move by more than ex2's 2^-126, while what l
+// has gathered still counts.
+struct Fall {
+  float a, b;
+  __device__ __forceinline__ explicit Fall(float d) {
+    const float first = fmaxf(d, -120.f);
+    a = ex2(first);
+    b = ex2(fmaxf(d - first, -120.f));
+  }
+  __device__ __forceinline__ float of(float x) const { return x * a * b; }
+};
 // A row of O times f; a whole warp's rows.  The blocks before are done: their products were issued before this S.
 template <int D>
-__device__ __forceinline__ void scale_row(uint32_t tO, float f) {
+__device__ __forceinline__ void scale_row(uint32_t tO, const Fall& f) {
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     float o[32];
     tmem_ld32(tO + 32 * c, o);
     tmem_wait(o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] *= f;
+    for (int i = 0; i < 32; ++i) o[i] = f.of(o[i]);
     tmem_st32(tO + 32 * c, o);
   }
 }
@@ -361,7 +376,8 @@ __device__ __forceinline__ void scale_row(uint32_t tO, float f) {
 template <int D>
 __device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha, float ev, float sum_up, float Z, float l, bool over) {
   const float top = row_max(tS);
-  float base = 0.f, neg = ev - (Z == -INFINITY ? ev : Z), f = 1.f;
+  float base = 0.f, neg = ev - (Z == -INFINITY ? ev : Z);
+  Fall f(0.f);
   if (over) {
     neg = fmaf(top, alpha, ev - Z);               // top's weight as an exponent
     base = top;
@@ -369,14 +385,14 @@ __device__ __noinline__ float2 block_over(uint32_t tS, uint32_t tO, float alpha,
       base = neg = 0.f;                           // no logit but -inf (and NaN)
     } else if (Z == -INFINITY || l == 0.f || !(neg <= kStay)) {
       const float zn = rintf(fmaf(top, alpha, ev)) - kLift;
-      if (l != 0.f) f = ex2(fminf(Z - zn, 0.f));              // else O is zero too, and Z this block's own first reference
+      if (l != 0.f) f = Fall(fminf(Z - zn, 0.f));             // else O is zero too, and Z this block's own first reference
       Z = zn;
       // top's own exponent, kLift and what Z was rounded by: a later block's terms stand beside these under one Z
       neg = fminf(fmaxf(fmaf(top, alpha, ev - zn), kLift - 1.f), kLift + 1.f);
     }
   }
   if (tO != 0xFFFFFFFFu) scale_row<D>(tO, f);
-  return make_float2(Z, fmaf(write_exp_from<true>(tS, base, alpha, neg), sum_up, l * f));
+  return make_float2(Z, fmaf(write_exp_from<true>(tS, base, alpha, neg), sum_up, f.of(l)));
 }
 
 // A block whose tokens have exponents of their own: keys in exps[0 .. 127], values in exps[128 .. 255].  A row's weight of
@@ -394,15 +410,15 @@ __device__ __noinline__ float2 block_apart(uint32_t tS, uint32_t tO, float row_a
 #pragma unroll
     for (int i = 0; i < 32; ++i) top = fmaxf(top, fmaf(s[i], alpha_of(c + i), (float)exps[kTile + c + i]));
   }
-  float f = 1.f;
+  Fall f(0.f);
   float largest = top - Z;                        // the largest weight's exponent
   if (top != -INFINITY && !(largest <= (float)kApartMost)) {
     const float zn = rintf(top) - kLift;
-    f = Z == -INFINITY ? 0.f : ex2(Z - zn);
+    f = Fall(Z - zn);
     Z = zn;
     largest = kLift;
   }
-  l *= f;
+  l = f.of(l);
   if (tO != 0xFFFFFFFFu) scale_row<D>(tO, f);
   const float ref = Z == -INFINITY ? 0.f : Z;
   const bool huge = fabsf(ref) > kHuge && top != -INFINITY;   // as in block_over: differences first
@@ -892,6 +908,7 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         const int unit = __shfl_sync(0xffffffffu, s_items[slot].unit, 0);
         if (unit < 0) break;
         const int nb = s_items[slot].nb, tk = s_items[slot].tk;
+        int ev_top = kValueFloor;                 // of the item's blocks so far
         bool ok = true;
         for (int j = nb - 1; j >= 0 && ok; --j, ++bc) {
           int8_t* exps = s_exps + bc % kScaleRing * (2 * kTile);
@@ -923,11 +940,12 @@ q4_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
           if (!ok) break;
           if (lane == 0) {
             volatile Scales& out = s_scales[bc % kScaleRing];
-            out.k_up = apart ? -1.f : power_of_two(ek - kTopExp);
+            out.k_up = apart || ev_top - ev > kFar ? -1.f : power_of_two(ek - kTopExp);
             out.ev = (float)ev;
             out.sum_up = power_of_two(kSumExp - ev);
             mbar_arrive(scaled_full + 8 * (bc % kScaledRing));
           }
+          ev_top = max(ev_top, ev);
           __syncwarp();
         }
         if (!ok) break;
@@ -1049,11 +1067,11 @@ q4_join_kernel(const __grid_constant__ Q4TcGeom g) {
         const float* p = part(k);
         const float Z = __ldcg(p + kTile * D + row), l = __ldcg(p + kTile * D + kTile + row);
         if (Z == -INFINITY && l == 0.f) continue;             // no key of the row: its O may not be there
-        const float f = ex2(Z - ref);
+        const Fall f(Z - ref);
         p += (warp & 3) * (D * 32) + c * 32 + lane;
-        L = fmaf(l, f, L);
+        L = fmaf(l * f.a, f.b, L);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i), f, o[i]);
+        for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + 32 * i) * f.a, f.b, o[i]);
       }
       // no visible key: zeros; logits that are all -inf: NaN
       const float inv = L != 0.f ? kBack / L : u.limit + t * g.pos + ((row * g.inv_gp) >> 16) < 0 ? 0.f : NAN;

@@ -113,6 +113,32 @@ def test_value_steps_far_apart_inside_a_block(ckv, dtype, G, n_q, cut):  # noqa:
 
 # ------------------------------------------------------------------ weights and sums at far apart scales
 
+@pytest.mark.parametrize("dtype,G,n_q", [(BF, 4, 1), (F32, 2, 1), (BF, 4, 3), (BF, 4, 20), (BF, 7, 60)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_equal_weights_of_values_far_apart(ckv, dtype, G, n_q, rows):  # noqa: F811
+    # keys of zero, so equal weights: tokens up to `cut` (or from there on) hold 0 or small values and the others values of
+    # 2^power; the former add nothing to the sum, and as much weight as the latter.  One row is cut into parts
+    d, n = 128, 5120 if rows == 1 else 900
+    for power in (0, 60, 66, 67, 70, 90, 100):
+        for cut, low in ((n // 2 // 128 * 128, 0.0), (n // 2 // 128 * 128, 1.0), (200, 0.0), (n - 300, 2.0 ** -70)):
+            for swap in (False, True):
+                g = torch.Generator(device=DEV).manual_seed(power)
+                cache = ckv.q4_cache(rows, 1, d, n_pages=rows * -(-n // 64), max_pages=-(-n // 64))
+                v = 1.0 + torch.rand(1, 1, n, d, generator=g, device=DEV)
+                small = (torch.arange(n, device=DEV) < cut) ^ swap
+                v = (v * torch.where(small, low, 2.0 ** power)[:, None]).expand(rows, 1, n, d).contiguous().to(dtype)
+                fill(ckv, cache, [n] * rows, torch.zeros_like(v), v)
+                q = torch.randn(rows, n_q, G, d, generator=g, device=DEV).to(dtype)
+                out = ckv.q4_attention(cache, 0, q).double()
+                vs, vm = held(cache, 0, 1)
+                total = (vs + vm).cumsum(0)
+                seen = torch.arange(n - n_q, n, device=DEV)
+                want = (total[seen] / (seen + 1)[:, None])[None, :, None]
+                # weights and values in f16 (2^-11 each), the output's rounding (2^-8), n terms in fp32
+                tol = ((n + 16) * 2.0 ** -22 + (2.0 ** -8 + 2.0 ** -10 if dtype == BF else 0)) * want
+                assert bool(((out - want).abs() <= tol).all()), (power, cut, low, swap, float(((out - want).abs() / want).max()))
+
+
 @pytest.mark.parametrize("dtype,G,n_q", [(BF, 4, 1), (F32, 2, 1), (BF, 4, 3), (BF, 4, 20), (BF, 4, 150)])
 def test_the_largest_of_huge_logits_wins(ckv, dtype, G, n_q):  # noqa: F811
     # logits of about 2^power (as exponents of 2) at one token a row and a half of it and less at the others: its value is the
