@@ -6,7 +6,8 @@
 // lie in [lo, hi],
 //   m = lo rounded down to bf16,  s = (hi - m) / 15 rounded up to bf16,  c = round((x - m) / s)
 // and a code stands for s c + m.  Rounding outwards keeps every value within half a step of
-// a code; bf16 keeps fp32's range, and m is exact where the inputs are bf16.
+// a code; bf16 keeps fp32's range, and m is exact where the inputs are bf16.  Only where
+// 15 s + m would be infinite is s the next lower bf16: values still are within half a step.
 #include "q4.cuh"
 
 namespace chunkkv {
@@ -27,6 +28,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// The step of a group near the end of the range: s, rounded up, is lowered to the next bf16 as long as 15 s + m would be
+// infinite, in bf16 if hi itself is finite there.  Twice at most: 15 s + m then is below hi by more than roundings raise it.
+constexpr float kHighEnd = 1.7e38f;                          // 2^127: 15 s + m passes hi by 2^-7 of it at most
+constexpr float kBf16End = 339617752923046005526922703901628039168.f;      // (2 - 2^-8) 2^127, which rounds to infinity in bf16
+__device__ __noinline__ float s_below_end(float m, float s, float hi) {
+  const float end = hi < kBf16End ? kBf16End : INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i)
+    if (s > 0.f && !(fmaf(15.f, s, m) < end)) s = __uint_as_float(__float_as_uint(s) - 0x10000u);
+  return s;
 }
 
 // Eight elements of a row as they lie in memory, and as fp32.
@@ -167,11 +180,13 @@ q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, c
           m = __uint_as_float(0x7FC00000u);
           s = 0.f;
         }
+        if (hi > kHighEnd) s = s_below_end(m, s, hi);
         const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
         if (t < nt) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            // The codes as whole numbers in fp32, 0 to 15: 15 s is not below hi - m, so (x - m) / s rounds to 15 at most.
+            // The codes as whole numbers in fp32, 0 to 15: 15 s is not below hi - m (by a fiftieth, if s was lowered), so
+            // (x - m) / s rounds to 15 at most.
             // Adding and taking off 1.5 2^23 rounds to the nearest, ties to even.
             const bool zero = bad || c + 8 * k >= g.d;               // codes of no value, or of columns past the end
             float w[8];

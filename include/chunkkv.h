@@ -451,9 +451,12 @@ chunkkv_status chunkkv_q8_attention(const chunkkv_q8_cache* c, int32_t dtype, in
  * themselves, in fp32: for a group whose values lie in [lo, hi]
  *   m = lo rounded down to bf16
  *   s = (hi - m) * (1 / 15) rounded up to bf16; 0 if hi - m is below 2^-100
+ *       (lowered to the next bf16, twice at most, while 15 s + m is infinite in fp32, or in
+ *       bf16 where hi is finite in bf16: then 15 s may be below hi - m, by 2 % at most)
  *   c = round((x - m) * (1 / s)) in 0 .. 15, ties to even; 0 where s is 0
- * and a code stands for s * c + m.  A group with a NaN or an infinity, or whose values
- * lie further apart than fp32 can say, has m = NaN and s = 0: it reads as NaN.
+ * and a code stands for s * c + m, within half a step of x.  A group with a NaN or an infinity, or
+ * whose m or hi - m is infinite (values below bf16's lowest, or further apart than fp32 can say),
+ * has m = NaN and s = 0: it reads as NaN.
  * A page holds CHUNKKV_Q8_PAGE (64) tokens of one row in CHUNKKV_Q4_PAGE_BYTES(d) bytes:
  *   keys            [64 tokens][4][ND][8 bytes]     bytes (t, g) of a token: columns 64 g + 16 t .. + 15
  *   their (m, s)    [ND][64 tokens][2] bf16

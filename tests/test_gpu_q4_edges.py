@@ -164,3 +164,55 @@ def test_the_largest_of_huge_logits_wins(ckv, dtype, G, n_q):  # noqa: F811
         tol = ((2.0 ** -8 + 2.0 ** -10 if dtype == BF else 0) + 2.0 ** -18) * (vs + vm.abs())[at[i % len(at)]]
         err = (out[i] - want).abs()
         assert bool((err <= tol).all()), (powers[i // len(at)], at[i % len(at)], float((err / tol).max()))
+
+
+# ------------------------------------------------------------------ writing near the ends of the types
+
+def step_of(lo, hi):
+    """(m, s) of a group with these ends, by the definition: s is lowered where 15 s + m would be infinite."""
+    m = lo.to(BF)
+    m = torch.where(m.float() > lo, torch.nextafter(m, torch.full_like(m, -math.inf)), m).float()
+    want = (hi - m) * torch.tensor(1.0 / 15.0, dtype=F32, device=lo.device)
+    s = want.to(BF)
+    s = torch.where(s.float() < want, torch.nextafter(s, torch.full_like(s, math.inf)), s)
+    end = torch.tensor((2.0 - 2.0 ** -8) * 2.0 ** 127, dtype=torch.float64, device=lo.device)      # rounds to infinity in bf16
+    limit = torch.where(hi.double() < end, end, end.new_tensor(2.0 ** 128 - 2.0 ** 103))           # and in fp32
+    for _ in range(2):
+        over = 15 * s.double() + m.double() >= limit
+        s = torch.where(over, torch.nextafter(s, torch.zeros_like(s)), s)
+    return m, s.float()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_finite_groups_read_back_finite(ckv, dtype):  # noqa: F811
+    # values up to the type's largest: 15 s + m must not pass it
+    d, n = 64, 512
+    top = torch.finfo(dtype).max
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.rand(n, d, generator=g, device=DEV, dtype=torch.float64)
+    scale = top * (1 - torch.rand(n, 1, generator=g, device=DEV, dtype=torch.float64) * 2.0 ** -8 * (torch.arange(n, device=DEV) % 3)[:, None])
+    shift = torch.rand(n, 1, generator=g, device=DEV, dtype=torch.float64) * (torch.arange(n, device=DEV) % 4 > 1)[:, None]
+    x = (shift + x * (1 - shift)) * scale             # from shift * scale up
+    x[:, 7] = scale[:, 0]                             # the largest
+    x[:64, 9] = 0.0
+    x[64:80, 9] = -1.0
+    x[80:96, 9] = -1e30
+    x = x.to(dtype)
+    k = x.float()[None, None]
+    cache = ckv.q4_cache(1, 1, d, n_pages=8, max_pages=8)
+    fill(ckv, cache, [n], k.to(dtype), -k.to(dtype))
+    m, s = step_of(x.float().min(1).values, x.float().max(1).values)
+    sc, km = held(cache, 0, 0)
+    assert torch.equal(km[:, 0], m.double())
+    codes = torch.round((x.float() - m[:, None]) * (1.0 / s[:, None]))
+    assert float(codes.max()) <= 15 and torch.equal(sc, codes.double() * s[:, None].double())
+    # half a step, and the rounding of x - m and of its product with 1 / s
+    assert bool(((sc + km - x.double()).abs() <= s[:, None].double() * (0.5 + 16 * 2.0 ** -22)).all())
+    outs = [torch.empty(n, d, dtype=dtype, device=DEV) for _ in range(2)]
+    ckv.chunkkv_q4_load(cache, 0, torch.zeros(1, dtype=torch.int64, device=DEV), n, *outs)
+    assert bool(torch.isfinite(outs[0]).all())
+    # the other sign: a group whose smallest value is below bf16's lowest has an infinite m (-2^128 < x < -(2 - 2^-7) 2^127
+    # rounds down to -inf), and so reads as NaN by the definition; all others are finite
+    below = torch.isinf(step_of(-x.float().max(1).values, -x.float().min(1).values)[0])
+    assert bool(outs[1][below].isnan().all()) and bool(torch.isfinite(outs[1][~below]).all())
+    assert bool(below.any()) == (dtype == F32) and not bool(below.all())
