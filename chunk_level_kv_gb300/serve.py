@@ -380,6 +380,8 @@ def chunkkv_q4_workspace_size(cache: Q4Cache, G: int, n_q: int = 1, dtype=torch.
 
 
 def chunkkv_q4_path(cache: Q4Cache, G: int, n_q: int = 1, dtype=torch.bfloat16) -> int:
+    """0 or 1: the kernel for few or for many query rows (-1: invalid), for contiguous q and out.  Repeated axes (strides
+    of 0) and strides of out of 2^22 elements and more take the one for few whatever this says."""
     return int(LIB.chunkkv_q4_path(cache.layer(0), _DT.get(dtype, -1), G, n_q))
 
 

@@ -506,18 +506,26 @@ chunkkv_status chunkkv_q4_load(const chunkkv_q4_cache* c, int32_t dtype, const i
  * out[b][i] of i >= m is not written.
  *   q, out: device [B, n_q, Hkv * G, d] with element strides (b, token, head), multiples of
  *   16 bytes; out overlaps no input;
- *   scale > 0 and finite; sums and softmax statistics in fp32.  For bf16 the weights are
- *   rounded to f16 (2^-11 each) before they weigh the values, and q . c is good to about
- *   2^-17 of its largest term; with many query rows
- *   (chunkkv_q4_path 1) the keys and values are too, as multiples of the largest of their
- *   token: what lies below 2^-20 of it loses bits, below 2^-31 it is lost (tokens whose
- *   largest are within 2^8 of each other may share one multiple);
+ *   scale > 0 and finite, scale * |q| below 2^116;
+ *   sums and softmax statistics in fp32 (a row's tokens times its largest value must stay within it).
+ *   For bf16 the weights are rounded to f16 (2^-11 each) before they weigh the values, as
+ *   multiples of the row's largest product of a weight and its token's step (many query rows: its
+ *   token's largest value): what lies below 2^-18 of it loses bits, below 2^-29 it is lost.
+ *   q . c is good to about 2^-17 of its largest term.  With many query rows (chunkkv_q4_path 1)
+ *   keys and values are rounded to f16 too, as multiples of the largest of their token, or of 2^-100
+ *   (keys) and 2^-60 (values) if that is less: what lies below 2^-20 of it loses bits, below 2^-31
+ *   it is lost (tokens whose largest are within 2^8 of each other may share one multiple);
  *   ws: device workspace of chunkkv_q4_workspace_size bytes, under chunkkv_q8_attention's
  *   terms: zero-filled before its first use, not shared by calls that can overlap; it may
  *   serve any of the attention calls in turn.
  */
 chunkkv_status chunkkv_q4_workspace_size(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q, size_t* bytes);
-/* Which kernel such a call takes: 0 = one for few query rows, 1 = one for many, -1 = invalid arguments. */
+/*
+ * Which kernel such a call takes: 0 = one for few query rows, 1 = one for many, -1 = invalid
+ * arguments.  A call that gets 1 takes 0 all the same where no tensor map can address q (an axis of
+ * more than one element with a stride of 0, or q outside device memory) or where out's token or
+ * head stride is 2^22 elements or more.
+ */
 int32_t chunkkv_q4_path(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q);
 chunkkv_status chunkkv_q4_attention(const chunkkv_q4_cache* c, int32_t dtype, int32_t G, int32_t n_q,
                                     const int32_t* q_lens, float scale, const void* q, int64_t q_stride_b,

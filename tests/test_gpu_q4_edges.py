@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_q4 import BF, DEV, F32, ckv, fill, held  # noqa: F401
+from test_gpu_q4 import BF, DEV, F32, ckv, fill, held, random_cache  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,21 @@ def test_finite_groups_read_back_finite(ckv, dtype):  # noqa: F811
     below = torch.isinf(step_of(-x.float().max(1).values, -x.float().min(1).values)[0])
     assert bool(outs[1][below].isnan().all()) and bool(torch.isfinite(outs[1][~below]).all())
     assert bool(below.any()) == (dtype == F32) and not bool(below.all())
+
+
+# ------------------------------------------------------------------ which kernel a call takes
+
+@pytest.mark.parametrize("n_q", [5, 33])
+def test_repeated_axes_take_the_kernel_for_few_rows(ckv, n_q):  # noqa: F811
+    # no tensor map can address a stride of zero: the other kernel's tolerance holds, whatever chunkkv_q4_path says of
+    # strides that one can
+    cache, g = random_cache(ckv, 2, 2, 64, [200, 70, 64, 130], seed=24)
+    for shape in ((2, n_q, 1, 64), (1, n_q, 8, 64), (2, 1, 8, 64)):
+        q = torch.randn(*shape, generator=g, device=DEV).to(BF).expand(2, n_q, 8, 64)
+        out = ckv.q4_attention(cache, 0, q, out=torch.empty(2, n_q, 8, 64, dtype=BF, device=DEV))
+        for r in range(4):
+            b, h = divmod(r, 2)
+            for i in range(n_q):
+                n = int(cache.lens[r]) - n_q + 1 + i
+                heads = slice(4 * h, 4 * h + 4)
+                check_query(ckv, cache, r, q[b, i, heads], out[b, i, heads], n, 1 / 8, 0)
