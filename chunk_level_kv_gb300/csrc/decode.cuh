@@ -119,10 +119,11 @@ struct Cursor {
 };
 
 // The pages of all rows in order (or what else work is counted in: size(i) of item i) are cut
-// into one contiguous run [x0, x1) per CTA, whatever the rows' lengths, which only the device knows: every CTA finds its run by a scan over the
-// lengths.  Rows of up to kWholeRow pages are not cut (each kernel has its own number): a row in two pieces costs the CTAs that
-// share it about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's share of
-// the bandwidth, and the eight warps take eight pages at once.  A cut within kNearEnd pages
+// into one contiguous run [x0, x1) per CTA, whatever the rows' lengths, which only the device
+// knows: every CTA finds its run by a scan over the lengths.  Rows of up to kWholeRow pages are
+// not cut (each kernel has its own number): a row in two pieces costs the CTAs that share it
+// about 4 us (partials, a counter, the join), a page about 0.4 us of a CTA's share of the
+// bandwidth, and the eight warps take eight pages at once.  A cut within kNearEnd pages
 // of a long row's begin or end moves there, so that a CTA seldom has a second row for a few
 // pages.
 constexpr int kWholeRow = 8;

@@ -36,8 +36,10 @@
 //
 // Measured: 64 sequences x 4 KV heads of 12 to 13 thousand tokens, 7 heads each (0.47 GB) 96 us,
 // 4.9 TB/s, 72 % of a copy's rate (1050 instructions a page; issue slots 57 %, integer pipe 56 %,
-// tensor pipe 26 %); one sequence of 8 KV heads x 6.5 thousand tokens 12.6 us, 16 sequences of 256
-// to 300 tokens 8.1 us (latency); 16 query rows on 64 rows of 6.5 thousand tokens 48 us, cold.
+// tensor pipe 26 %: with three warps a scheduler, latency); one sequence of 8 KV heads x 6.5 thousand
+// tokens 12.6 us, 16 sequences of 256 to 300 tokens 8.1 us (latency).  Cold: 64 rows of 6.5 thousand
+// tokens 35 us for 8 query rows, 48 us for 16; 256 rows of 6.5 thousand, 7 heads, 95 us at 192 columns
+// (3.8 TB/s), 117 us at 256 (4.1), 103 us in fp32 at 128 (2.3).
 #include <algorithm>
 #include <type_traits>
 
@@ -71,9 +73,9 @@ struct Q4AttnArgs {
   float* part;                                   // [passes][2 CTAs][rows][64 ND + 4]: O, m, l
 };
 
-// Warps of a CTA, a page each in shared memory.  For 8 query rows of up to 128 columns twelve, of 168 registers a thread
-// (256 rows of 12.8 thousand tokens, cold: 107 us; sixteen of 128 spill, 121 us; eight 119 us); more rows or columns take
-// the registers of eight.
+// Warps of a CTA, a page each in shared memory.  For 8 query rows of up to 128 columns twelve, of 168 registers a thread and
+// 40 bytes spilled (256 rows of 12.8 thousand tokens, cold: 107 us; sixteen of 128 spill more, 121 us; eight 119 us); more
+// rows or columns take the registers of eight (16 rows of 128 columns spill 60 bytes there, 256 columns 36, in fp32 28).
 template <int ND, typename T, int RS>
 constexpr int warps_of() { return sizeof(T) == 2 && RS == 1 && ND <= 2 ? 12 : 8; }
 template <int ND>

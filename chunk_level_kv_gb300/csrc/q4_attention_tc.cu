@@ -18,7 +18,7 @@
 //   negligible weights costs the others nothing.
 // - A block whose tokens' largest values lie more than 2^8 apart gets an exponent for each token, or
 //   a large token that a row does not see, or weighs by nothing, would take the others' bits.  The row's
-//   threads then weigh it column by column, in code of its own (block_apart: twice the time of a block).  So they do where EV
+//   threads then weigh it column by column, in code of its own (block_apart: three times the time of a block).  So they do where EV
 //   falls far below an earlier block's: weights that vanish beside Z still count in l.
 // - A block's keys and values arrive as pages of codes (18 KB for 128 columns, bulk copies) and
 //   eight converting warps expand them into the tensor cores' operands.  A word of 8 codes is 8
@@ -39,12 +39,13 @@
 // a block's sum of weights is below kMost, which f16 holds; a block that passes it is done over
 // from its own maximum.  The lift keeps weights down to 2^-18 of the reference's at full precision.
 //
-// What bounds it: issue slots.  A block pair takes 2048 cycles of products, and 3.7 thousand in all: next
-// to the exponentials of 256 rows the converting warps issue 3 thousand instructions for its 32768
-// codes, and a tile's softmax, 950 cycles alone, takes 1.9 thousand beside them (without the
-// conversion, timing only, 597 us of 726).  Measured at 128 columns: 4001 queries on 16 to 17 thousand
-// tokens of 28 / 4 heads 0.68 ms, 1.2 PFLOP/s of the visible pairs; 300 to 700 queries of two sequences
-// on 4.9 to 9.7 thousand tokens of 32 / 8 heads 0.10 ms; 5 queries of eight sequences on 6.5 thousand 65 us.
+// What bounds it: no unit alone.  A block pair takes 2048 cycles of products and 3.8 thousand in all; issue slots are 55 % used
+// and the tensor pipe 50 %.  Next to the exponentials of 256 rows the converting warps issue 3 thousand instructions for its
+// 32768 codes, and a tile's softmax, 950 cycles alone, takes 1.9 thousand beside them; the twelve roles' loops share
+// instruction caches (with 200 instructions more between them a block took 15 % longer).  Measured at 128 columns: 4001 queries
+// on 16 to 17 thousand tokens of 28 / 4 heads 0.70 ms, 1.2 PFLOP/s of the visible pairs (2.3 ms if every block is
+// block_apart's); 300 to 700 queries of two sequences on 4.9 to 9.7 thousand tokens of 32 / 8 heads 0.10 ms; 5 queries of
+// eight sequences on 6.5 thousand 63 us.  At 128 columns the kernel spills 172 bytes a thread at its launch's 96 registers.
 //
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1, 8 copies, 9 and 10 MMA issuers of tile 0 and 1,
 // 11 scales, 12-19 conversion.  Every wait is bounded (tcgen.cuh); a CTA that gives up drains and exits.
@@ -109,7 +110,8 @@ template <int N> constexpr uint32_t idesc() {     // fp32 D, f16 A and B, M = 12
 
 // tcgen's waits, with what follows a first try that fails out of the way: twelve roles' loops share the instruction caches,
 // and with the waits' own loops among them a block took 15 % longer.
-__device__ __forceinline__ bool wait_long(int32_t* err, volatile int* abort, long long timeout, uint32_t bar, uint32_t parity, int code) {
+__device__ __forceinline__ bool wait_long(int32_t* err, volatile int* abort, long long timeout, uint32_t bar, uint32_t parity,
+                                          int code) {
   const Ctl ctl{err, abort, timeout};
   return wait_bar(ctl, bar, parity, code);
 }
@@ -307,7 +309,8 @@ __device__ __forceinline__ int scale_half(uint8_t* half0, uint8_t* half1, int le
         r.w = max(r.w, __shfl_xor_sync(0xffffffffu, r.w, 16));
       }
       const int4 e = make_int4(exponent_of(r.x, floor), exponent_of(r.y, floor), exponent_of(r.z, floor), exponent_of(r.w, floor));
-      by = make_float4(power_of_two(kTopExp - e.x), power_of_two(kTopExp - e.y), power_of_two(kTopExp - e.z), power_of_two(kTopExp - e.w));
+      by = make_float4(power_of_two(kTopExp - e.x), power_of_two(kTopExp - e.y), power_of_two(kTopExp - e.z),
+                       power_of_two(kTopExp - e.w));
       *(char4*)(exps + token) = make_char4(e.x, e.y, e.z, e.w);
     }
     *to = scale_four(w, by, pairs);
@@ -451,7 +454,8 @@ constexpr int kParts = kConvert / 2;
 template <int ND> constexpr int kTiles = 4 * ND / kParts;
 template <int ND> __device__ __forceinline__ int group_of(int w) { return (w >> 1) * kTiles<ND> / 4; }
 
-// Keys of one page, a warp's share of its tokens (from `first` on; their steps already scaled f16), into rows of 64 columns (128 bytes, 16-byte pieces swizzled).
+// Keys of one page, a warp's share of its tokens (from `first` on; their steps already scaled f16), into rows of 64 columns
+// (128 bytes, 16-byte pieces swizzled).
 template <int ND>
 __device__ __forceinline__ void expand_keys(const uint8_t* page, uint8_t* tile, int page_row, int first, int lane) {
 #pragma unroll 1

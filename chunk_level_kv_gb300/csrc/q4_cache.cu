@@ -116,10 +116,12 @@ struct Q4AppendArgs {
 // One CTA writes the part of one page that a row's new tokens fill, of the keys
 // (blockIdx.z 0) or of the values (1).  Four lanes hold a group of a token, 16 columns
 // each, and find its smallest and largest value by shuffles (with eight lanes, what a group
-// costs once was two thirds of the instructions).  A lane's codes are two words of the keys' part; values go through shared memory, a byte a code, and leave as words of
-// eight tokens of a column (bytes paired into nibbles and transposed 4 x 4 in registers),
-// merged with the older tokens' codes where a word is shared.
-// Instructions bound it: 32 rows of 13164 bf16 tokens of 128 columns (276 MB) 74 us, 3.7 TB/s.
+// costs once was two thirds of the instructions).  A lane's codes are two words of the keys'
+// part; values go through shared memory, a byte a code, and leave as words of eight tokens of a
+// column (bytes paired into nibbles and transposed 4 x 4 in registers), merged with the older
+// tokens' codes where a word is shared.
+// Instructions bound it (630 a warp, issue slots 83 %): 32 rows of 13164 tokens of 128 columns in bf16
+// (276 MB) 74 us, 3.7 TB/s; in fp32 (492 MB) 95 us, 5.2 TB/s.
 template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 q4_append_kernel(Q4Geom g, Q4AppendArgs a, const int32_t* __restrict__ counts, const int64_t* __restrict__ slots,
@@ -251,8 +253,9 @@ struct Q4LoadArgs {
 
 // One CTA reads one page of a row: s c + m, rounded once to the output's type.  The values'
 // codes come through shared memory (blocks of 16 columns 528 bytes apart: their words of
-// the same tokens lie in different banks).  HBM bounds it: the rows of q4_append_kernel's
-// figure 56 us, 4.9 TB/s.
+// the same tokens lie in different banks).  Latency bounds it (a CTA's length, start, table entry, steps
+// and codes come one after another; writing the same bytes alone takes 33 us): the rows of
+// q4_append_kernel's figure 56 us, 4.9 TB/s; in fp32 99 us, 5.0 TB/s.
 template <int ND, typename T>
 __global__ void __launch_bounds__(kIoThreads)
 q4_load_kernel(Q4Geom g, Q4LoadArgs a, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,

@@ -1,9 +1,10 @@
 // The softmax of the tensor-core attention kernels: one query row per thread, its 128 logits
-// of a block in TMEM, probabilities written over them as bf16 pairs.
+// of a block in TMEM, probabilities written over them as pairs of bf16 (the prompts' kernel)
+// or of f16 (the 4-bit cache's, whose references are its own).
 //
-// The reference m of a row is the maximum of some of its first logits and stays while the
-// row's sum is below kBig: a common factor of P, O and the sum costs no precision (bf16 and
-// fp32 have the same exponents) and the final division removes it.  So a block has no
+// In the prompts' kernel the reference m of a row is the maximum of some of its first logits and stays
+// while the row's sum is below kBig: a common factor of P, O and the sum costs no precision (bf16
+// and fp32 have the same exponents) and the final division removes it.  So a block has no
 // maximum to find before its exponentials.  A block that passes the bound is done over with
 // its maximum as the reference, O and the sum rescaled; S is still there, since P replaces it
 // only after that test.
