@@ -234,3 +234,28 @@ def test_repeated_axes_take_the_kernel_for_few_rows(ckv, n_q):  # noqa: F811
                 n = int(cache.lens[r]) - n_q + 1 + i
                 heads = slice(4 * h, 4 * h + 4)
                 check_query(ckv, cache, r, q[b, i, heads], out[b, i, heads], n, 1 / 8, 0)
+
+
+# ------------------------------------------------------------------ long sums in fp32
+
+@pytest.mark.parametrize("d,G,n_q", [(128, 3, 1), (64, 4, 1), (128, 2, 2), (192, 2, 1)])
+def test_long_fp32_sums_keep_fp32(ckv, d, G, n_q):  # noqa: F811
+    # rows that one CTA sums over a hundred pages: the output's error as a whole, relative.  Three sources, independent from
+    # token to token like the values that they weigh, each of about 2^-21 and of 2^-20 at most: a logit's rounding (d
+    # products under partial sums of 3, 2^-25 each: sqrt(128) 3 2^-25), a weight's (22 bits, the exponential's 2 ulp),
+    # and a page's sum (8 products whose sums are cut off, not rounded: 8 2^-24); adding the pages is rounded and less
+    rows, n = 128, 8000
+    cache, g = random_cache(ckv, rows // 2, 2, d, [n] * rows, seed=d, dtype=F32)
+    q = torch.randn(rows // 2, n_q, 2 * G, d, generator=g, device=DEV)
+    out = ckv.q4_attention(cache, 0, q).double()
+    err = size = 0.0
+    for r in range(0, rows, 5):
+        b, h = divmod(r, 2)
+        (ks, km), (vs, vm) = held(cache, r, 0), held(cache, r, 1)
+        hidden = torch.arange(n, device=DEV)[None] > n - n_q + torch.arange(n_q, device=DEV)[:, None]
+        for i in range(h * G, (h + 1) * G):
+            t = (q[b, :, i].double() @ (ks + km).T / math.sqrt(d)).masked_fill(hidden, -math.inf)
+            want = torch.softmax(t, -1) @ (vs + vm)
+            err += float((out[b, :, i] - want).square().sum())
+            size += float(want.square().sum())
+    assert math.sqrt(err / size) <= 3 * 2.0 ** -20, math.sqrt(err / size)
